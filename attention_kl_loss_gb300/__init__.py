@@ -41,5 +41,11 @@ from .binding import (  # noqa: F401
     streamkl_fwd_workspace_size,
     streamkl_workspace_size,
 )
+from .ops import (  # noqa: F401
+    streamkl_paged_append,
+    streamkl_qk_norm_rope_bwd,
+    streamkl_qk_norm_rope_bwd_workspace_size,
+    streamkl_qk_norm_rope_fwd,
+)
 
 __version__ = "0.2.0"

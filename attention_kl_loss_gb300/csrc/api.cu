@@ -15,11 +15,20 @@
 #include <mutex>
 
 #include "streamkl.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace {
 
 thread_local char g_err[512] = "";
+
+}  // namespace
+
+// Host helpers shared by the C-ABI files (host.h).
+namespace skl {
+namespace host {
+
+void clear_error() { g_err[0] = '\0'; }
 
 streamkl_status fail(streamkl_status s, const char* fmt, ...) {
   va_list ap;
@@ -33,8 +42,8 @@ streamkl_status cuda_fail(cudaError_t e, const char* what) {
   return fail(STREAMKL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::once_flag g_encode_once;
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   std::call_once(g_encode_once, [] {
@@ -76,6 +85,13 @@ int num_sms() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace host
+}  // namespace skl
+
+namespace {
+
+using namespace skl::host;
 
 streamkl_status check_sizes(int B, int H, int NQ, int NK, int d, int causal) {
   if (B < 1 || H < 1 || NQ < 1 || NK < 1)

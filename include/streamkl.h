@@ -331,6 +331,98 @@ streamkl_status streamkl_bwd_varlen(const void* q1, const void* k1, const void* 
                                     void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Operators around the KL: what a model computes before the call (norm and
+ * rotation of its queries and keys, with the way back for the gradients) and
+ * what a trained student is run with (a paged key/value cache, its append and
+ * the attention of new tokens over it). The paper has no counterpart. The
+ * conventions above hold, with these additions:
+ * - dtype is the element type of q, k, v, caches and outputs; sums, norms,
+ *   softmax statistics and weights are fp32.
+ * - strides is a HOST array of element strides; the last dimension (d) is
+ *   contiguous, every stride and base a multiple of 16 bytes.
+ * - Outputs must not overlap inputs.
+ * - Values that only the device knows (positions, lengths, page numbers) are
+ *   checked by the kernels: a bad one sets STREAMKL_ERR_INVALID_ARG in
+ *   *dev_status and is never used as an address.
+ */
+typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamkl_dtype;
+
+/*
+ * Norm and rotation of queries and keys, one pass over both. Each row x (one
+ * token, one head, d elements) becomes R(p) (w * x / sqrt(mean(x^2) + eps)):
+ * R(p) turns the pairs of the first `rot` elements by the angles of position
+ * p, (a, b) -> (a cos - b sin, b cos + a sin); pairs are (i, i + rot / 2), or
+ * (2i, 2i + 1) with interleaved = 1.
+ *   in : q [B, NQ, HQ, d], k [B, NK, HK, d] (either may be NULL to skip it);
+ *        cos, sin fp32 [table_len, rot / 2]; rot a multiple of 16 up to d;
+ *        q_positions, k_positions: device int32, token (b, n) at
+ *        [b * pos_stride + n] (0: the same for each b); NULL: key n is at
+ *        position n, query n at n + max(NK - NQ, 0) (needs NQ <= NK);
+ *        q_weight, k_weight: fp32 [d], NULL for rotation without norm.
+ *   out: q_out [B, HQ, NQ, d] and k_out [B, HK * k_repeat, NK, d], placed by
+ *        their strides: head h of k stands k_repeat times, from h * k_repeat
+ *        on, so that grouped heads give streamkl_fwd its equal head counts.
+ *   strides: batch, token, head of q, k, q_out, k_out (12 values). A packed
+ *        batch [total, H, d] is B = 1.
+ * A row whose position lies outside the tables is reported and not written.
+ * dtype: any of streamkl_dtype. d is 64 or 128.
+ */
+streamkl_status streamkl_qk_norm_rope_fwd(const void* q, const void* k, int dtype, int B, int NQ, int NK, int HQ,
+                                          int HK, int d, int rot, const long long* strides, const float* cos,
+                                          const float* sin, int table_len, const int* q_positions,
+                                          long long q_pos_stride, const int* k_positions, long long k_pos_stride,
+                                          const float* q_weight, const float* k_weight, float eps, int interleaved,
+                                          int k_repeat, void* q_out, void* k_out, int* dev_status, void* stream);
+
+/*
+ * Its backward: arguments as above, with the outer gradients dq_out, dk_out
+ * in the place of the outputs (the gradients of a key head's repeats are
+ * summed). dq, dk: gradients of q and k; dq_weight, dk_weight: fp32 [d],
+ * written where the weight is given. strides: the 12 above (dq_out, dk_out
+ * for q_out, k_out), then batch, token, head of dq and dk (18 values).
+ * workspace: ws_bytes >= streamkl_qk_norm_rope_bwd_workspace_size(...) (sizes
+ * of an absent side 0; may be NULL without weights); no initialisation. The
+ * weight gradients are summed in a fixed order: the same in every run. Rows
+ * that the forward does not write get no gradient and add none.
+ */
+size_t streamkl_qk_norm_rope_bwd_workspace_size(int B, int NQ, int NK, int HQ, int HK, int d);
+streamkl_status streamkl_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                          int dtype, int B, int NQ, int NK, int HQ, int HK, int d, int rot,
+                                          const long long* strides, const float* cos, const float* sin,
+                                          int table_len, const int* q_positions, long long q_pos_stride,
+                                          const int* k_positions, long long k_pos_stride, const float* q_weight,
+                                          const float* k_weight, float eps, int interleaved, int k_repeat, void* dq,
+                                          void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                          size_t ws_bytes, int* dev_status, void* stream);
+
+/*
+ * Append new keys and values to a paged cache, the keys normed (k_weight) and
+ * rotated (cos, sin) on the way as above; NULL leaves either out.
+ *   in : k, v [T, HK, d], the new tokens of B sequences packed one after the
+ *        other: cu_seqlens int32 [B + 1] on the device, tokens from
+ *        cu_seqlens[B] on are padding and ignored; NULL: T = B, one token a
+ *        sequence. kv_lens int32 [B]: length of each sequence with its new
+ *        tokens, which stand at its end. block_table int32 [B, max_pages],
+ *        rows table_stride apart: position p of sequence b lies in slot
+ *        p % page_size of page block_table[b][p / page_size].
+ *   in/out: k_cache, v_cache [num_pages, HK, page_size, d], placed by their
+ *        strides; page_size a power of two from 16 to 1024. Only the new
+ *        tokens' slots are written. Two tokens of one call must not share a
+ *        slot (one of them would be left there, no more is said).
+ *   strides: page, head, slot of k_cache and of v_cache, then token, head of
+ *        k and of v (10 values).
+ * A token with a bad position or page is reported and not written. dtype:
+ * STREAMKL_BF16 or STREAMKL_FP16.
+ */
+streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                                      const int* block_table, long long table_stride, const int* kv_lens,
+                                      const int* cu_seqlens, int dtype, int B, int T, int HK, int d, int page_size,
+                                      int num_pages, int max_pages, const long long* strides, int rot,
+                                      const float* cos, const float* sin, int table_len, const float* k_weight,
+                                      float eps, int interleaved, int* dev_status, void* stream);
+
+/*
  * Self-test of the bounded-wait path: launches one tiny kernel that waits on
  * a barrier nothing arrives on, for timeout_us microseconds, then records
  * STREAMKL_ERR_TIMEOUT in *dev_status and returns. No other state is touched.
