@@ -43,6 +43,9 @@ from .binding import (  # noqa: F401
 )
 from .ops import (  # noqa: F401
     streamkl_paged_append,
+    streamkl_paged_attn,
+    streamkl_paged_attn_splits,
+    streamkl_paged_attn_workspace_size,
     streamkl_qk_norm_rope_bwd,
     streamkl_qk_norm_rope_bwd_workspace_size,
     streamkl_qk_norm_rope_fwd,

@@ -76,6 +76,10 @@ _SIGNATURES = {
                                        _Z, _P, _P]),
     "streamkl_paged_append": (_I, [_P, _P, _P, _P, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                    _P, _I, _P, _P, _I, _P, _F, _I, _P, _P]),
+    "streamkl_paged_attn_splits": (_I, [_I, _I, _I, _I, _I, _I, _I]),
+    "streamkl_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "streamkl_paged_attn": (_I, [_P, _P, _P, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                                 _P, _I, _I, _F, _I, _I, _P, _P, _P, _Z, _P, _P]),
 }
 
 

@@ -134,6 +134,86 @@ streamkl_status check_cache(const void* kc, const void* vc, const int* table, lo
   return STREAMKL_OK;
 }
 
+// Key split of the attention over the cache: with few query tiles against
+// long sequences the keys are cut into `splits` ranges of split_tiles 128-key
+// tiles (counted from a sequence's start, so a short one uses fewer ranges).
+struct AttnPlan {
+  int row_tiles, q_tiles, splits, split_tiles;
+};
+
+AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, int requested) {
+  AttnPlan p;
+  const long long rows = static_cast<long long>(max_q) * (HQ / HK);
+  p.row_tiles = rows > 128 ? 2 : 1;
+  p.q_tiles = static_cast<int>((rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles));
+  const int tiles = std::max(1, (max_kv + 127) / 128);
+  int s = requested;
+  if (s <= 0) {
+    const int sms = num_sms();
+    const long long ctas = static_cast<long long>(p.q_tiles) * B * HK;
+    const double tile_us = (p.row_tiles == 2 ? 1.2 : 0.7) * (d == 128 ? 1.0 : 0.6), cta_us = 4.0;
+    const double part_us = static_cast<double>(T) * HQ * (d + 1) * 8.0 / 4.0e12 * 1e6;
+    auto cost = [&](int n) {
+      const long long waves = (ctas * n + sms - 1) / sms;
+      const int per = (tiles + n - 1) / n;
+      return waves * (per * tile_us + cta_us) + (n > 1 ? 3.0 + n * part_us : 0.0);
+    };
+    s = 1;
+    double best = cost(1);
+    for (int n = 2; n <= std::min(64, tiles); ++n)
+      if (cost(n) < best) {
+        best = cost(n);
+        s = n;
+      }
+  }
+  s = std::max(1, std::min(s, tiles));
+  p.split_tiles = (tiles + s - 1) / s;
+  p.splits = (tiles + p.split_tiles - 1) / p.split_tiles;
+  return p;
+}
+
+size_t attn_part_bytes(int splits, int T, int HQ, int d) {
+  if (splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(splits) * T * HQ;
+  return (rows * (d + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+
+// 4-D map {d, page size, HK, pages} of a cache, 64-column boxes of one page's
+// slots (at most one key tile of them), 128-byte swizzle.
+streamkl_status make_map_cache(CUtensorMap* m, const void* ptr, int dtype, int d, int page_size, int HK,
+                               int num_pages, const long long* strides, const char* name) {
+  auto enc = encode_fn();
+  if (!enc) return fail(STREAMKL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+  const cuuint64_t gdim[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(HK), static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t gstride[3] = {static_cast<cuuint64_t>(strides[2]) * 2, static_cast<cuuint64_t>(strides[1]) * 2,
+                                 static_cast<cuuint64_t>(strides[0]) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(std::min(page_size, 128)), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type =
+      dtype == STREAMKL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = enc(m, type, 4, const_cast<void*>(ptr), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(STREAMKL_ERR_CUDA, "tensor map for %s failed (CUresult %d)", name, static_cast<int>(r));
+  return STREAMKL_OK;
+}
+
+streamkl_status check_attn_sizes(int B, int T, int HQ, int HK, int d, int max_q, int max_kv) {
+  if (B < 1 || T < 1 || HQ < 1 || HK < 1 || max_q < 1 || max_kv < 0)
+    return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (B=%d T=%d HQ=%d HK=%d max_seqlen_q=%d max_kv_len=%d)",
+                B, T, HQ, HK, max_q, max_kv);
+  if (HQ % HK) return fail(STREAMKL_ERR_INVALID_ARG, "query heads %d are not a multiple of key heads %d", HQ, HK);
+  if (d != 64 && d != 128) return fail(STREAMKL_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
+  if (static_cast<long long>(B) * HK > 65535)
+    return fail(STREAMKL_ERR_UNSUPPORTED, "B*HK=%lld exceeds 65535", static_cast<long long>(B) * HK);
+  if (max_q > T) return fail(STREAMKL_ERR_INVALID_ARG, "max_seqlen_q %d above the %d tokens", max_q, T);
+  if (static_cast<long long>(T) * HQ > (1LL << 30) || max_kv > (1 << 30))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "more than 2^30 rows or keys");
+  return STREAMKL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -251,6 +331,88 @@ streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cach
   a.dev_status = dev_status;
   cudaError_t e = skl::launch_append(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "append launch");
+}
+
+int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len) {
+  if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK) return 0;
+  return attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, 0).splits;
+}
+
+size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
+                                          int num_splits) {
+  if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK || num_splits < 0) return 0;
+  return attn_part_bytes(attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits).splits, T, HQ, d);
+}
+
+streamkl_status streamkl_paged_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                                    long long table_stride, const int* kv_lens, const int* cu_seqlens, int dtype,
+                                    int B, int T, int HQ, int HK, int d, int page_size, int num_pages, int max_pages,
+                                    const long long* strides, int max_seqlen_q, int max_kv_len, float scale,
+                                    int causal, int num_splits, void* out, float* lse, void* workspace,
+                                    size_t ws_bytes, int* dev_status, void* stream) {
+  clear_error();
+  if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
+  streamkl_status st = check_cache(k_cache, v_cache, block_table, table_stride, kv_lens, dtype, B, T, HK, d,
+                                   page_size, num_pages, max_pages, strides);
+  if (st != STREAMKL_OK) return st;
+  if ((st = check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len)) != STREAMKL_OK) return st;
+  if (!cu_seqlens && T != B)
+    return fail(STREAMKL_ERR_INVALID_ARG, "without cu_seqlens each sequence has one token (T=%d B=%d)", T, B);
+  if (max_kv_len > static_cast<long long>(max_pages) * page_size)
+    return fail(STREAMKL_ERR_INVALID_ARG, "max_kv_len %d above %d pages of %d", max_kv_len, max_pages, page_size);
+  if ((st = check_tensor("q", q, strides + 6, 2, dtype)) != STREAMKL_OK) return st;
+  if ((st = check_tensor("out", out, strides + 8, 2, dtype)) != STREAMKL_OK) return st;
+  if (!lse) return fail(STREAMKL_ERR_INVALID_ARG, "lse must be non-NULL");
+  if (causal != 0 && causal != 1) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (num_splits < 0) return fail(STREAMKL_ERR_INVALID_ARG, "num_splits must be >= 0");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(STREAMKL_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
+  const AttnPlan p = attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits);
+  if (p.splits > 65535) return fail(STREAMKL_ERR_UNSUPPORTED, "%d key splits (at most 65535)", p.splits);
+  const size_t need = attn_part_bytes(p.splits, T, HQ, d);
+  if (need && (!workspace || ws_bytes < need))
+    return fail(STREAMKL_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  if (need && !aligned16(workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  CUtensorMap mk, mv;
+  if ((st = make_map_cache(&mk, k_cache, dtype, d, page_size, HK, num_pages, strides, "k_cache")) != STREAMKL_OK)
+    return st;
+  if ((st = make_map_cache(&mv, v_cache, dtype, d, page_size, HK, num_pages, strides + 3, "v_cache")) != STREAMKL_OK)
+    return st;
+  skl::PagedAttnArgs a{};
+  a.tm_k = &mk;
+  a.tm_v = &mv;
+  a.q = q;
+  a.q_sn = strides[6], a.q_sh = strides[7];
+  a.o = out;
+  a.o_sn = strides[8], a.o_sh = strides[9];
+  a.lse = lse;
+  a.table = block_table;
+  a.table_sb = table_stride;
+  a.kv_lens = kv_lens;
+  a.cu = cu_seqlens;
+  a.B = B;
+  a.T = T;
+  a.HQ = HQ;
+  a.HK = HK;
+  a.d = d;
+  a.type = dtype;
+  a.causal = causal;
+  a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.max_q = max_seqlen_q;
+  a.max_kv = max_kv_len;
+  a.scale = scale;
+  a.q_tiles = p.q_tiles;
+  a.row_tiles = p.row_tiles;
+  a.splits = p.splits;
+  a.split_tiles = p.split_tiles;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o ? a.part_o + static_cast<size_t>(p.splits) * T * HQ * d : nullptr;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  cudaError_t e = skl::launch_paged_attn(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "paged attention launch");
 }
 
 }  // extern "C"

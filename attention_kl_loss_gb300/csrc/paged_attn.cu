@@ -1,0 +1,559 @@
+// Attention of new tokens over a paged cache: for query row i of a sequence
+// (its last n tokens), o_i = sum_j p_ij v_j with p = softmax(scale q K^T) over
+// the keys j it sees (causal: j <= len - n + i), and lse_i for merging.
+//
+// Rows. The G = HQ / HK query heads of a key head read the same keys, so a row
+// tile packs (token, head of the group) pairs, row r = token r / G, head r % G:
+// a single new token of a grouped model is G rows of one tile and the keys are
+// read once for all of them.
+//
+// One pass over the key tiles (128 keys) with the running reference and sum
+// of the softmax, S = Q K^T and O += P V as tcgen05 MMAs:
+//   S (fp32, TMEM) -> registers -> P = 2^(c s - ref) in the inputs' type,
+//   written over S's columns, from where it is the PV product's A operand.
+// P has 8 (bf16) or 11 (fp16) bits: its rounding is the size of the output's
+// own. ref, the sum (of unrounded terms) and O are fp32. The reference moves
+// only when a tile's maximum exceeds it by more than 2^8, so O is seldom
+// rescaled; the results do not depend on it.
+//
+// CTA: warp 0 loads (each lane one page's box of a tile; pages are found
+// through the block table), warp 1 issues MMAs, warps 4.. are one softmax
+// warpgroup per row tile, thread = row.
+// Two row tiles (NT = 2) share each K and V tile and the tensor pipe works on
+// one while the other's softmax runs. With at most 128 rows (NT = 1) the keys
+// are what costs; S is then double-buffered. Few rows against many keys are
+// split over the keys; a combine kernel joins the splits by their lse.
+#include <algorithm>
+
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace skl {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTau = 8.0f;  // log2 units
+constexpr int kTileM = 128, kTileN = 128;
+
+template <int D, int NT>
+struct AttnLayout {
+  static constexpr int KB = D / 64;               // 64-column (128-byte) boxes per row
+  static constexpr int BOX = kTileN * 128;        // 128 rows of one box
+  static constexpr int TILE = kTileN * D * 2;
+  static constexpr int STAGES = D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 10 : 12);
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = NT * TILE;
+  static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
+  // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], drain
+  static constexpr int NBAR = 2 + 2 * STAGES + 6 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int ALLOC = BYTES + 1024;
+  static_assert(ALLOC <= 232448, "shared memory budget");
+  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int COL_O = 256;
+};
+
+// What a CTA works on: one sequence's rows of one key head, a range of keys.
+struct Work {
+  int n, len;          // new tokens, length
+  int tok0;            // first token of the sequence
+  int rows;            // rows of the sequence: n * G
+  int row0;            // first row of this CTA
+  int t0, n_iter;      // key tiles [t0, t0 + n_iter)
+  int klim;            // keys any row of this CTA sees: [0, klim)
+  bool ok;             // the sequence's numbers are sound
+};
+
+__device__ __forceinline__ Work find_work(const PagedAttnArgs& a, int b, int G, int rows_cta) {
+  Work w;
+  const int c0 = a.cu != nullptr ? __ldg(a.cu + b) : b;
+  const int c1 = a.cu != nullptr ? __ldg(a.cu + b + 1) : b + 1;
+  w.len = __ldg(a.kv_lens + b);
+  w.n = c1 - c0;
+  w.tok0 = c0;
+  w.ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && w.n <= a.max_q && w.len >= 0 && w.len <= a.max_kv;
+  w.rows = w.ok ? w.n * G : 0;
+  // the last rows see the most keys: their tiles first
+  const int tiles = (w.rows + rows_cta - 1) / rows_cta;
+  const int x = a.causal ? tiles - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+  w.row0 = x >= 0 && x < tiles ? x * rows_cta : w.rows;  // no rows: nothing to do
+  const int last = min(w.rows, w.row0 + rows_cta) - 1;
+  w.klim = a.causal && w.rows > 0 ? min(w.len, w.len - w.n + last / G + 1) : w.len;
+  const int n_tiles = (max(0, w.klim) + kTileN - 1) / kTileN;
+  w.t0 = min(n_tiles, static_cast<int>(blockIdx.y) * a.split_tiles);
+  w.n_iter = min(n_tiles, w.t0 + a.split_tiles) - w.t0;
+  return w;
+}
+
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+}
+
+// A bounded wait of a whole warp: false for all lanes where any gave up, so
+// that the warp stays together for its .aligned instructions.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
+  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, wc));
+}
+
+// One row of the output: finished (o, lse) or a split's partial.
+template <int TYPE, int D>
+__device__ __forceinline__ void store_empty_row(const PagedAttnArgs& a, int token, int head) {
+  const long long e = static_cast<long long>(token) * a.HQ + head;
+  if (a.splits > 1) {
+    a.part_lse[static_cast<long long>(blockIdx.y) * a.T * a.HQ + e] = -INFINITY;
+    return;
+  }
+  uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+  a.lse[e] = -INFINITY;
+}
+
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
+    streamkl_paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
+                               const __grid_constant__ CUtensorMap tm_v,
+                               const __grid_constant__ PagedAttnArgs a) {
+  using L = AttnLayout<D, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* gb = smem_raw + (sb - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.HQ / a.HK;
+  const int b = static_cast<int>(blockIdx.z) / a.HK, hk = static_cast<int>(blockIdx.z) - b * a.HK;
+  const Work w = find_work(a, b, G, kTileM * NT);
+  if (!w.ok && threadIdx.x == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+  if (w.row0 >= w.rows) return;
+  if (w.n_iter == 0) {  // no key in this range is seen
+    for (int r = w.row0 + threadIdx.x; r < min(w.rows, w.row0 + kTileM * NT); r += blockDim.x)
+      store_empty_row<TYPE, D>(a, w.tok0 + r / G, hk * G + r % G);
+    return;
+  }
+
+  const uint32_t bar0 = sb + L::OFF_BAR;
+  const uint32_t q_full = bar0, v_fixed = bar0 + 8;
+  auto kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (2 + L::STAGES + s); };
+  auto s_full = [&](int k) { return bar0 + 8u * (2 + 2 * L::STAGES + k); };
+  auto p_full = [&](int k) { return bar0 + 8u * (4 + 2 * L::STAGES + k); };
+  auto o_full = [&](int k) { return bar0 + 8u * (6 + 2 * L::STAGES + k); };
+  const uint32_t drain = bar0 + 8u * (8 + 2 * L::STAGES);
+  static_assert(2 + 2 * L::STAGES + 6 + 1 == L::NBAR, "barrier region holds every barrier");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
+  volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
+
+  CheckCtx ck{sb, sb + L::OFF_BAR, sb + L::OFF_BAR, sb + L::OFF_BAR + L::NBAR * 8, 0, 0,
+              abort_flag, a.dev_status};
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    bool lay_ok = true;
+    if (kDeviceChecks)
+      for (int i = 0; i < L::NBAR; ++i) lay_ok = lay_ok && check_bar(ck, bar0 + 8u * i, __LINE__);
+    if (lay_ok) {
+      mbar_init(q_full, 4 * NT);  // one arrival per softmax warp
+      mbar_init(v_fixed, 1);
+      for (int s = 0; s < L::STAGES; ++s) {
+        mbar_init(kv_full(s), 1);
+        mbar_init(kv_empty(s), 1);
+      }
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(s_full(k), 1);
+        mbar_init(p_full(k), 4);
+        mbar_init(o_full(k), 1);
+      }
+      mbar_init(drain, 1);
+    }
+    // a failure recorded earlier, or a failed layout check, skips the work
+    *skip_flag = !lay_ok || *reinterpret_cast<volatile int*>(a.dev_status) != 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ck.tmem = tmem;
+  ck.tmem_cols = 512;
+  const WaitCtx wc{abort_flag, a.dev_status, a.timeout_ns};
+  const int n_iter = *skip_flag ? 0 : w.n_iter;
+  // row tiles of this CTA that have rows
+  const int nt = (NT == 2 && w.rows - w.row0 > kTileM) ? 2 : 1;
+  // keys of the last tile that are there; the rest of its V rows are cleared
+  const int last_valid = min(kTileN, w.klim - (w.t0 + w.n_iter - 1) * kTileN);
+
+  // Place of key tile j's K and V among the loads, in the order in which the
+  // MMAs use them. NT = 2: K0 V0 K1 V1 ..; NT = 1: K0 K1 V0 K2 V1 ..
+  auto idx_k = [&](int j) { return NT == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+  auto idx_v = [&](int j) { return NT == 2 ? 2 * j + 1 : (j + 1 < w.n_iter ? 2 * j + 2 : 2 * j + 1); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const int page = 1 << a.page_shift;
+    const int box_rows = min(page, kTileN);
+    const int* table = a.table + static_cast<long long>(b) * a.table_sb;
+    int issued = 0;
+    bool ok = true;
+    // the page this lane loads of tile j; a number that is none is reported
+    // and page 0 read in its place
+    auto page_of = [&](int j) {
+      const int key = (w.t0 + j) * kTileN + lane * box_rows;
+      if (j >= n_iter || lane * box_rows >= kTileN || key >= w.klim) return -1;
+      int p = __ldg(table + (key >> a.page_shift));
+      if (p < 0 || p >= a.num_pages) {
+        atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+        p = 0;
+      }
+      return p;
+    };
+    auto load = [&](const CUtensorMap* map, int j, int pg) {
+      const int s = issued % L::STAGES;
+      if (!warp_wait(kv_empty(s), ((issued / L::STAGES) & 1) ^ 1, wc)) return false;
+      const int key0 = (w.t0 + j) * kTileN;
+      const int pages = (min(kTileN, w.klim - key0) + box_rows - 1) / box_rows;
+      const uint32_t dst = sb + L::OFF_KV + s * L::TILE + lane * box_rows * 128;
+      if (lane == 0) mbar_arrive_expect_tx(kv_full(s), static_cast<uint32_t>(pages * box_rows * D * 2));
+      __syncwarp();
+      if (lane < pages) {
+        const int slot = key0 & (page - 1);  // 0 below 128-slot pages
+#pragma unroll
+        for (int kb = 0; kb < L::KB; ++kb)
+          if (check_tma(ck, dst + kb * L::BOX, box_rows * 128, kv_full(s), kb * 64, D, slot, page, 0, hk,
+                        a.HK, __LINE__))
+            tma_load_4d(dst + kb * L::BOX, map, kv_full(s), kb * 64, slot, hk, pg);
+      }
+      ++issued;
+      return true;
+    };
+    int pg = page_of(0), pg_next = page_of(1);
+    if (NT == 2) {
+      for (int j = 0; ok && j < n_iter; ++j) {
+        ok = load(&tm_k, j, pg) && load(&tm_v, j, pg);
+        pg = pg_next;
+        pg_next = page_of(j + 2);
+      }
+    } else {
+      if (n_iter > 0) ok = load(&tm_k, 0, pg);
+      for (int j = 0; ok && j < n_iter; ++j) {
+        if (j + 1 < n_iter) ok = load(&tm_k, j + 1, pg_next);
+        if (ok) ok = load(&tm_v, j, pg);
+        pg = pg_next;
+        pg_next = page_of(j + 2);
+      }
+    }
+    // the last load is the last tile's V: clear its rows past the last key
+    // (the slots there hold anything, and 0 x NaN is NaN)
+    if (ok && n_iter > 0 && last_valid < kTileN) {
+      const int i = issued - 1;
+      if (warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc)) {
+        uint8_t* v = gb + L::OFF_KV + (i % L::STAGES) * L::TILE;
+        for (int e = last_valid * 8 + lane; e < kTileN * 8; e += 32)  // 16 bytes each
+#pragma unroll
+          for (int kb = 0; kb < L::KB; ++kb)
+            *reinterpret_cast<uint4*>(v + kb * L::BOX + e * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_fixed);
+      }
+    }
+    // let every copy land before the CTA can exit
+    for (int i = max(0, issued - L::STAGES); i < issued; ++i)
+      wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && n_iter > 0) {
+      constexpr uint32_t id_s = TYPE == kTypeBf16 ? idesc_bf16(kTileM, kTileN, 0, 0) : idesc_f16(kTileM, kTileN, 0, 0);
+      constexpr uint32_t id_o = TYPE == kTypeBf16 ? idesc_bf16(kTileM, D, 0, 1) : idesc_f16(kTileM, D, 0, 1);
+      auto stage = [&](int i) { return sb + L::OFF_KV + (i % L::STAGES) * L::TILE; };
+      auto full = [&](int i) { return wait_bounded(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc); };
+      auto mma_s = [&](int t, int col, int j) {  // S = Q_t K_j^T
+        const uint32_t q = sb + L::OFF_Q + t * L::TILE, k = stage(idx_k(j));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = (i >> 2) * L::BOX + (i & 3) * 32;
+          mma_bf16(tmem + col, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), id_s, i > 0);
+        }
+      };
+      auto mma_o = [&](int t, int col, int j) {  // O_t += P V_j
+        const uint32_t v = stage(idx_v(j));
+#pragma unroll
+        for (int i = 0; i < kTileN / 16; ++i)
+          mma_bf16_ts(tmem + L::COL_O + t * D, tmem + col + 8 * i, smem_desc_sw128(v + i * 2048, L::BOX, 1024),
+                      id_o, j > 0 || i > 0);
+      };
+      auto v_ready = [&](int j) {
+        return full(idx_v(j)) && (j + 1 < n_iter || last_valid == kTileN || wait_bounded(v_fixed, 0, wc));
+      };
+      bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && full(idx_k(0));
+      tc_fence_after();
+      if (NT == 2) {
+        if (ok) {
+          for (int t = 0; t < nt; ++t) {
+            mma_s(t, t * 128, 0);
+            mma_commit(s_full(t));
+          }
+          mma_commit(kv_empty(idx_k(0) % L::STAGES));
+        }
+        for (int j = 0; ok && j < n_iter; ++j) {
+          const bool more = j + 1 < n_iter;
+          if (!(ok = v_ready(j))) break;
+          for (int t = 0; ok && t < nt; ++t) {
+            if (!(ok = wait_bounded(p_full(t), j & 1, wc))) break;
+            if (t == 0 && more && !(ok = full(idx_k(j + 1)))) break;
+            tc_fence_after();
+            mma_o(t, t * 128, j);
+            if (more) {
+              mma_s(t, t * 128, j + 1);
+              mma_commit(s_full(t));
+            } else {
+              mma_commit(o_full(t));
+            }
+          }
+          if (!ok) break;
+          mma_commit(kv_empty(idx_v(j) % L::STAGES));
+          if (more) mma_commit(kv_empty(idx_k(j + 1) % L::STAGES));
+        }
+      } else {
+        if (ok) {
+          mma_s(0, 0, 0);
+          mma_commit(s_full(0));
+          mma_commit(kv_empty(idx_k(0) % L::STAGES));
+        }
+        for (int j = 0; ok && j < n_iter; ++j) {
+          if (j + 1 < n_iter) {
+            if (!(ok = full(idx_k(j + 1)))) break;
+            tc_fence_after();
+            mma_s(0, ((j + 1) & 1) * 128, j + 1);
+            mma_commit(s_full((j + 1) & 1));
+            mma_commit(kv_empty(idx_k(j + 1) % L::STAGES));
+          }
+          if (!(ok = v_ready(j) && wait_bounded(p_full(j & 1), (j >> 1) & 1, wc))) break;
+          tc_fence_after();
+          mma_o(0, (j & 1) * 128, j);
+          mma_commit(o_full(0));
+          mma_commit(kv_empty(idx_v(j) % L::STAGES));
+        }
+      }
+      mma_commit(drain);
+      wait_drain(drain, 0, a.timeout_ns);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                    // row tile
+    const int r_tile = (warp & 3) * 32 + lane;        // TMEM lane
+    const int row = w.row0 + t * kTileM + r_tile;     // row of the sequence
+    const bool live = row < w.rows;
+    const int tok = live ? row / G : 0;
+    const int token = w.tok0 + tok, head = hk * G + (live ? row - tok * G : 0);
+    if (n_iter > 0) {
+      // this row of Q, 128-byte swizzled as TMA would place it; rows that are
+      // not there are zero
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + token * a.q_sn + head * a.q_sh);
+      const uint32_t dst = sb + L::OFF_Q + t * L::TILE + r_tile * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = __ldg(src + c);
+        st_shared_v4(dst + (c >> 3) * L::BOX + (((c & 7) ^ (r_tile & 7)) << 4), v.x, v.y, v.z, v.w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const float c = a.scale * kLog2e;
+    // keys < lim are seen by this row
+    const int lim = !live ? 0 : a.causal ? min(w.len, w.len - w.n + tok + 1) : w.len;
+    const bool warp_live = w.row0 + t * kTileM + (warp & 3) * 32 < w.rows;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t to = tmem + L::COL_O + t * D + lanes;
+    float ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; t < nt && j < n_iter; ++j) {
+      const int slot = NT == 2 ? t : (j & 1);
+      if (!(ok = warp_wait(s_full(slot), NT == 2 ? (j & 1) : ((j >> 1) & 1), wc))) break;
+      tc_fence_after();
+      if (warp_live) {
+        const uint32_t ts = tmem + slot * 128 + lanes;
+        if (!(ok = check_tmem(ck, ts, 32, 128, __LINE__))) break;
+        float s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+        tmem_wait_ld();
+        const int seen = lim - (w.t0 + j) * kTileN;  // of this tile's keys
+        if (seen < kTileN) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k >= seen) s[k] = -INFINITY;
+        }
+        float m0 = s[0], m1 = s[1];
+#pragma unroll
+        for (int k = 2; k < 126; k += 4) {
+          m0 = max3(m0, s[k], s[k + 1]);
+          m1 = max3(m1, s[k + 2], s[k + 3]);
+        }
+        const float top = max3(m0, m1, fmaxf(s[126], s[127])) * c;
+        const bool move = top > ref + kTau || (ref == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float alpha = move ? ex2(ref - top) : 1.f;
+          if (move) {
+            ref = top;
+            l *= alpha;
+          }
+          if (j > 0) {
+            // O holds the tiles before this one: with two row tiles their
+            // products ended before this S; with one, wait for the last
+            if (NT == 1 && !(ok = warp_wait(o_full(0), (j - 1) & 1, wc))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              float o[16];
+              tmem_ld16(to + 16 * q, o);
+              tmem_wait_ld();
+              uint32_t r[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * alpha);
+              tmem_st16(to + 16 * q, r);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float r0 = ref == -INFINITY ? 0.f : ref;
+        const float2 c2 = make_float2(c, c), nr = make_float2(-r0, -r0);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = __ffma2_rn(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), c2, nr);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+            p[k] = pack2<TYPE>(e.x, e.y);
+          }
+          tmem_st16(ts + 16 * q, p);
+        }
+        const float2 f = __fadd2_rn(sum[0], sum[1]);
+        l += f.x + f.y;
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(slot));
+    }
+    // ------------------------------------------------------------ output
+    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(t), NT == 2 ? 0 : ((n_iter - 1) & 1), wc) && warp_live) {
+      tc_fence_after();
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (NaN stays NaN)
+      const bool none = l == 0.f;
+      const long long e = static_cast<long long>(token) * a.HQ + head;
+      const long long plane = static_cast<long long>(blockIdx.y) * a.T * a.HQ;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tmem_ld32(to + 32 * q, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = none ? 0.f : o[k] * inv;
+        if (live) {
+          if (a.splits > 1) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (plane + e) * D + 32 * q);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + 32 * q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(pack2<TYPE>(o[8 * k], o[8 * k + 1]), pack2<TYPE>(o[8 * k + 2], o[8 * k + 3]),
+                                  pack2<TYPE>(o[8 * k + 4], o[8 * k + 5]), pack2<TYPE>(o[8 * k + 6], o[8 * k + 7]));
+          }
+        }
+      }
+      if (live) {
+        const float lse2 = none ? -INFINITY : ref + log2f(l);
+        if (a.splits > 1)
+          a.part_lse[plane + e] = lse2;
+        else
+          a.lse[e] = lse2 * kLn2;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Join the splits of a row (token, head), one warp a row: with weights
+// 2^(lse_s - lse), o = sum_s w_s o_s.
+template <int TYPE, int D>
+__global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int V = D / 32;  // columns of a lane
+  const int lane = threadIdx.x & 31;
+  const long long e = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const long long rows = static_cast<long long>(a.T) * a.HQ;
+  const int end = a.cu != nullptr ? __ldg(a.cu + a.B) : a.B;  // tokens behind the last sequence stay
+  const int token = static_cast<int>(e / a.HQ), head = static_cast<int>(e - static_cast<long long>(token) * a.HQ);
+  if (e >= rows || token >= end) return;
+  float top = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + e]);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+  const float t0 = top == -INFINITY ? 0.f : top;
+  float total = 0.f, o[V] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const float wgt = ex2(a.part_lse[s * rows + e] - t0);
+    if (wgt == 0.f) continue;  // (the partial of an empty range is not written)
+    total += wgt;
+    const float* p = a.part_o + (s * rows + e) * D + lane * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = fmaf(wgt, p[k], o[k]);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) dst[k] = pack2<TYPE>(o[2 * k] * inv, o[2 * k + 1] * inv);
+  if (lane == 0) a.lse[e] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+template <int TYPE, int D, int NT>
+cudaError_t attn_t(const PagedAttnArgs& a, cudaStream_t stream) {
+  using L = AttnLayout<D, NT>;
+  auto kern = streamkl_paged_attn_kernel<TYPE, D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(a.q_tiles, a.splits, a.B * a.HK), L::THREADS, L::ALLOC, stream>>>(*a.tm_k, *a.tm_v, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const long long rows = static_cast<long long>(a.T) * a.HQ;
+  streamkl_paged_combine_kernel<TYPE, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int TYPE, int D>
+cudaError_t attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
+  return a.row_tiles == 2 ? attn_t<TYPE, D, 2>(a, stream) : attn_t<TYPE, D, 1>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
+  if (a.type == kTypeBf16) return a.d == 128 ? attn_d<kTypeBf16, 128>(a, stream) : attn_d<kTypeBf16, 64>(a, stream);
+  return a.d == 128 ? attn_d<kTypeF16, 128>(a, stream) : attn_d<kTypeF16, 64>(a, stream);
+}
+
+}  // namespace skl

@@ -4,18 +4,20 @@
 projection to the layout that ``streamkl_fwd`` reads (norm and rotation of
 every head in one pass, grouped key heads repeated on request) and the KL's
 gradients back. ``streamkl_paged_append`` puts a trained student's new keys
-and values into a paged cache. As in ``binding``: argument marshalling only,
+and values into a paged cache, ``streamkl_paged_attn`` is the attention of new
+tokens (one, or a chunk) over it. As in ``binding``: argument marshalling only,
 PyTorch provides device memory and the current stream.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from typing import Optional
 
 import torch
 
-from .binding import _check, _ptr, _workspace, load, new_status
+from .binding import _check, _ptr, load, new_status
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NO_GUARD = contextlib.nullcontext()
@@ -68,6 +70,18 @@ def _status(dev_status, device):
     if dev_status.dtype != torch.int32 or dev_status.device != device or dev_status.numel() < 1:
         raise ValueError(f"dev_status must be an int32 tensor on {device}")
     return dev_status
+
+
+def _workspace(need, device, workspace):
+    if need == 0:
+        return None
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace too small: need {need} bytes")
+    return workspace
 
 
 def _tables(cos, sin, device):
@@ -308,3 +322,63 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     if st:
         _check(st, "streamkl_paged_append")
     return k_cache, v_cache
+
+
+def streamkl_paged_attn_splits(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) -> int:
+    """Key splits of ``streamkl_paged_attn`` for these sizes."""
+    return int(load().streamkl_paged_attn_splits(B, T, HQ, HK, d, max_seqlen_q, max_kv_len))
+
+
+def streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits=0) -> int:
+    return int(load().streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits))
+
+
+def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None,
+                        max_seqlen_q: Optional[int] = None, max_kv_len: Optional[int] = None,
+                        scale: Optional[float] = None, causal: bool = True, num_splits: int = 0, out=None,
+                        workspace=None, dev_status=None, stream=None):
+    """Attention of new tokens over a paged cache: (out [total, H, d], lse
+    fp32 [total, H]).
+
+    q [total, H, d]: the new tokens of B sequences (cu_seqlens int32 [B + 1];
+    None: one token a sequence), the last ones of kv_lens int32 [B] keys, which
+    lie in the caches as ``streamkl_paged_append`` puts them (append first).
+    H is a multiple of the caches' heads. max_seqlen_q, max_kv_len: bounds of
+    the sequences' new tokens and lengths (default: every token, every page of
+    block_table); close ones give a better grid. Rows that see no key get
+    zeros and -inf; rows behind the last sequence stay as they were."""
+    _rows("q", q, 3, k_cache.dtype, k_cache.device)
+    dev = q.device
+    total, HQ, d = q.shape
+    B, _, HK, dk, page, pages, width = sizes = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
+    if dk != d or HK < 1 or HQ % HK:
+        raise ValueError(f"q [total, H, d] needs d = {dk} and H a multiple of {HK}, got {list(q.shape)}")
+    max_q = int(max_seqlen_q) if max_seqlen_q is not None else (1 if cu_seqlens is None else total)
+    max_kv = int(max_kv_len) if max_kv_len is not None else page * width
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if out is None:
+        o, lse = torch.empty((total, HQ, d), dtype=q.dtype, device=dev), None
+    else:
+        o, lse = out
+        if _rows("out[0]", o, 3, q.dtype, dev).shape != q.shape:
+            raise ValueError(f"out[0] must be {list(q.shape)}, got {list(o.shape)}")
+    if lse is None:
+        lse = torch.empty((total, HQ), dtype=torch.float32, device=dev)
+    elif lse.shape != (total, HQ) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise ValueError(f"out[1] must be contiguous fp32 [{total}, {HQ}] on {dev}")
+    status = _status(dev_status, dev)
+    if q.numel() == 0:
+        return o, lse
+    lib = load()
+    strides = _strides(*k_cache.stride()[:3], *v_cache.stride()[:3], *q.stride()[:2], *o.stride()[:2])
+    with _guard(dev):
+        need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, int(num_splits))
+        ws = _workspace(need, dev, workspace)
+        st = lib.streamkl_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                     block_table.stride(0), kv_lens.data_ptr(), _ptr(cu_seqlens), _DTYPES[q.dtype],
+                                     B, total, HQ, *sizes[2:], strides, max_q, max_kv, scale, int(bool(causal)),
+                                     int(num_splits), o.data_ptr(), lse.data_ptr(), _ptr(ws), need,
+                                     status.data_ptr(), _stream(stream, dev))
+    if st:
+        _check(st, "streamkl_paged_attn")
+    return o, lse

@@ -423,6 +423,43 @@ streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cach
                                       float eps, int interleaved, int* dev_status, void* stream);
 
 /*
+ * Attention of new tokens over a paged cache: row i of a sequence's n new
+ * tokens gives o = softmax(scale q K^T) V over the keys it sees, all of the
+ * sequence, or with causal = 1 those up to its own position (bottom-right
+ * aligned as above: key j <= i + length - n).
+ *   in : q [T, HQ, d] packed as k of streamkl_paged_append; caches,
+ *        block_table, kv_lens, cu_seqlens as there (cu_seqlens NULL: T = B,
+ *        one new token a sequence); HQ a multiple of HK, query head h reads
+ *        key head h / (HQ / HK); max_seqlen_q, max_kv_len: upper bounds of
+ *        the sequences' new tokens and lengths (they size the grid and the
+ *        key split); num_splits: 0 = automatic, >= 1 forces that many key
+ *        splits (clamped to the number of 128-key tiles).
+ *   out: out [T, HQ, d] and lse [T, HQ] (fp32, contiguous, the log of the
+ *        softmax's sum, as streamkl_fwd's). A row that sees no key (length 0,
+ *        or causal with more new tokens than keys) gets zeros and -inf. Rows
+ *        behind the last sequence are left as they were.
+ *   strides: page, head, slot of k_cache and of v_cache, then token, head of
+ *        q and of out (10 values).
+ *   workspace: ws_bytes >= streamkl_paged_attn_workspace_size(...) of the
+ *        same sizes and num_splits (may be NULL when that is 0); contents
+ *        need no initialisation; calls that may overlap need one each.
+ * Slots past a sequence's length and page numbers past its last page are
+ * never used, whatever they hold. A value of V that is not finite reaches
+ * every row whose key tile it lies in. Offsets or lengths out of range or
+ * above their bounds, and bad page numbers, are reported in *dev_status.
+ * Results are the same in every run for the same sizes.
+ */
+int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len);
+size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
+                                          int num_splits);
+streamkl_status streamkl_paged_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                                    long long table_stride, const int* kv_lens, const int* cu_seqlens, int dtype,
+                                    int B, int T, int HQ, int HK, int d, int page_size, int num_pages, int max_pages,
+                                    const long long* strides, int max_seqlen_q, int max_kv_len, float scale,
+                                    int causal, int num_splits, void* out, float* lse, void* workspace,
+                                    size_t ws_bytes, int* dev_status, void* stream);
+
+/*
  * Self-test of the bounded-wait path: launches one tiny kernel that waits on
  * a barrier nothing arrives on, for timeout_us microseconds, then records
  * STREAMKL_ERR_TIMEOUT in *dev_status and returns. No other state is touched.

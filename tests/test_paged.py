@@ -174,6 +174,298 @@ def test_append_reports_what_does_not_fit_and_writes_the_rest(what):
         assert torch.equal(now.view(torch.int16), old.view(torch.int16))
 
 
+# ---------------------------------------------------------------- attention
+def _check_attn(o, lse, q, c, new, lens, scale, causal, dt):
+    """Per element: a score of d fp32-accumulated products is within
+    (d + 4) 2^-23 of S = scale sum |q k|, its exponent's product and difference
+    add 8 x 2^-23 of it and ex2 2^-22, so a term of the softmax and its sum are
+    each within D = (d + 12) 2^-23 S + 2^-21, the sums over L keys within
+    L 2^-23 more; P is rounded to the type, half a step, and so is o: eps / 2
+    of sum p |v| and of |o|. fp16 terms below 2^-14 of a row's reference lose
+    up to 2^-25 each instead, of at most the largest |v|."""
+    at = 0
+    half = torch.finfo(dt).eps / 2
+    for b, n in enumerate(new):
+        k, v = (_np(torch.stack(list(t)).transpose(0, 1)) if len(t) else np.zeros((q.shape[1], 0, q.shape[2]))
+                for t in (c.rows[b][0][:lens[b]], c.rows[b][1][:lens[b]]))
+        x = _np(q[at:at + n])
+        ref, ref_lse, mag = orc.paged_attn(x, k, v, scale, causal)
+        got, got_lse = _np(o[at:at + n]), _np(lse[at:at + n])
+        at += n
+        if n == 0 or lens[b] == 0:
+            assert np.all(got == 0) and np.all(np.isneginf(got_lse))
+            continue
+        G = x.shape[1] // k.shape[0]
+        S = scale * max(np.max(np.abs(x[:, h]) @ np.abs(k[h // G]).T) for h in range(x.shape[1]))
+        D = (x.shape[2] + 12) * 2.0 ** -23 * S + 2.0 ** -21
+        E = 2 * D + lens[b] * 2.0 ** -23
+        tol = half * np.abs(ref) + (half + E) * mag
+        if dt == torch.float16:
+            tol = tol + lens[b] * 2.0 ** -25 * np.abs(v).max() + 2.0 ** -25
+        empty = np.isneginf(ref_lse)
+        assert np.array_equal(empty, np.isneginf(got_lse))
+        assert np.all(got[empty] == 0)
+        err = np.abs(got - ref)
+        assert np.all(err <= tol), (b, float((err / tol).max()))
+        fin = ~empty
+        assert np.all(np.abs(got_lse - ref_lse)[fin] <= E + 2.0 ** -22 * np.abs(ref_lse[fin]))
+
+
+ATTN = [
+    # new, lens, HQ, HK, d, page, type, causal, splits, layout
+    ([1], [1], 1, 1, 64, 16, "bf16", True, 0, "heads"),
+    ([1], [200], 4, 1, 128, 16, "bf16", True, 0, "heads"),
+    ([1, 1, 1, 1], [1, 128, 129, 700], 8, 2, 128, 32, "bf16", True, 0, "heads"),
+    ([1, 1, 1], [700, 2, 300], 6, 2, 64, 64, "fp16", False, 3, "slots"),
+    ([3, 0, 5, 1], [3, 40, 600, 257], 3, 3, 128, 16, "bf16", True, 1, "slots"),
+    ([40, 1, 17], [300, 1000, 17], 10, 2, 128, 128, "fp16", True, 2, "heads"),
+    ([128], [128], 1, 1, 64, 256, "bf16", True, 0, "heads"),
+    ([129, 2], [129, 513], 2, 1, 128, 64, "bf16", True, 0, "heads"),
+    ([300, 77], [300, 1111], 3, 1, 64, 16, "bf16", True, 1, "heads"),
+    ([257, 130], [700, 130], 4, 4, 128, 1024, "bf16", True, 3, "slots"),
+    ([65], [900], 21, 3, 128, 32, "fp16", False, 0, "heads"),
+    ([2, 9], [0, 5], 4, 2, 64, 16, "bf16", True, 0, "heads"),       # rows without a key
+    ([300], [140], 1, 1, 128, 16, "bf16", True, 2, "heads"),
+    ([4, 4], [0, 0], 2, 2, 128, 16, "fp16", False, 0, "heads"),
+    ([6], [33], 160, 1, 64, 32, "bf16", True, 0, "heads"),          # one token's group wider than a tile
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,lens,HQ,HK,d,page,dtype,causal,splits,layout", ATTN)
+def test_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, causal, splits, layout):
+    dt = TYPES[dtype]
+    c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
+    g = torch.Generator().manual_seed(HQ + d)
+    total, pad = sum(new), 2
+    # strided queries: the first heads of a wider projection
+    q = torch.randn(total + pad, HQ + 2, d, generator=g).to(dt).cuda()[:, :HQ]
+    o = torch.full((total + pad, HQ, d), 3.0, dtype=dt, device="cuda")
+    lse = torch.full((total + pad, HQ), 3.0, device="cuda")
+    st = binding.new_status()
+    scale = d ** -0.5
+    cu = _cu(new)
+    ret = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=cu, max_seqlen_q=max(new),
+                                  max_kv_len=max(lens), causal=causal, num_splits=splits, out=(o, lse), dev_status=st)
+    binding.raise_on_device_status(st)
+    assert ret[0] is o and ret[1] is lse
+    assert torch.all(o[total:] == 3) and torch.all(lse[total:] == 3)  # rows behind the last sequence
+    _check_attn(o, lse, q, c, new, lens, scale, causal, dt)
+    # bounds left at their defaults, outputs made by the call: the same rows
+    o2, lse2 = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=cu, causal=causal, dev_status=st)
+    binding.raise_on_device_status(st)
+    _check_attn(o2, lse2, q, c, new, lens, scale, causal, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_large_logits_move_the_reference(dtype):
+    """Keys that grow along the sequence raise the running maximum far past the
+    2^8 that leaves the reference alone, and a last key decides some rows."""
+    dt = TYPES[dtype]
+    lens, HQ, HK, d = [700], 4, 2, 64
+    c = Cache(lens, HK, d, 16, dt, seed=4)
+    ramp = torch.linspace(0.1, 6.0, 700)
+    k = (c.rows[0][0].float() * ramp[:, None, None]).to(dt)
+    k[-1] *= 2
+    c.rows[0] = (k, c.rows[0][1])
+    pos = torch.arange(700)
+    c.k[c.table[0, pos // 16].long(), :, (pos % 16).cuda()] = k.cuda()
+    for n in (1, 60, 140):
+        q = 3 * torch.randn(n, HQ, d, generator=torch.Generator().manual_seed(n))
+        q = q.to(dt).cuda()
+        for splits in (1, 3):
+            o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), num_splits=splits)
+            _check_attn(o, lse, q, c, [n], lens, d ** -0.5, True, dt)
+
+
+@pytest.mark.gpu
+def test_single_tokens_without_offsets():
+    lens = [5, 300, 64]
+    c = Cache(lens, 2, 128, 16, torch.bfloat16)
+    q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    a = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens)
+    b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([1, 1, 1]), max_seqlen_q=1)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    _check_attn(*a, q, c, [1, 1, 1], lens, 128 ** -0.5, True, torch.bfloat16)
+
+
+@pytest.mark.gpu
+def test_nan_in_one_sequence_stays_there():
+    lens = [200, 200]
+    c = Cache(lens, 1, 64, 16, torch.bfloat16)
+    c.k[c.table[0, 3].long(), 0, 5] = float("nan")
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    q[1, 2, 9] = float("inf")
+    o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens)
+    assert torch.all(torch.isnan(o[0])) and torch.all(torch.isnan(lse[0]))
+    assert torch.all(torch.isnan(o[1, 2])) and torch.all(torch.isfinite(o[1, [0, 1, 3]]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 1], [70, 40]])
+def test_pages_past_32_bits(new):
+    """Caches of more than 2^31 elements each, the sequences in the last pages."""
+    HK, d, page, dt = 8, 128, 128, torch.bfloat16
+    pages = (1 << 31) // (HK * page * d) + 40
+    small = Cache([300, 1000], HK, d, page, dt, spare=0)
+    big = []
+    for t in (small.k, small.v):
+        x = torch.empty(pages, HK, page, d, dtype=dt, device="cuda")
+        x[pages - t.shape[0]:] = t
+        big.append(x)
+    table = torch.where(small.table < small.k.shape[0], small.table + (pages - small.k.shape[0]), small.table)
+    q = torch.randn(sum(new), 16, d, generator=torch.Generator().manual_seed(0)).to(dt).cuda()
+    kw = dict(cu_seqlens=_cu(new), max_seqlen_q=max(new), max_kv_len=1000)
+    a = skl.streamkl_paged_attn(q, *big, table, small.lens, **kw)
+    b = skl.streamkl_paged_attn(q, small.k, small.v, small.table, small.lens, **kw)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    k, v = (torch.randn(sum(new), HK, d, generator=torch.Generator().manual_seed(i)).to(dt).cuda() for i in (1, 2))
+    skl.streamkl_paged_append(k, v, *big, table, small.lens, cu_seqlens=kw["cu_seqlens"])
+    skl.streamkl_paged_append(k, v, small.k, small.v, small.table, small.lens, cu_seqlens=kw["cu_seqlens"])
+    for x, y in zip(big, (small.k, small.v)):
+        assert torch.equal(x[pages - y.shape[0]:].view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["page", "length", "new tokens", "offsets"])
+def test_attention_reports_what_does_not_fit(what):
+    lens, new = [40, 300], [3, 3]
+    c = Cache(lens, 2, 64, 16, torch.bfloat16)
+    q = torch.randn(6, 4, 64, device="cuda").to(torch.bfloat16)
+    cu = _cu(new)
+    kw = dict(max_seqlen_q=3, max_kv_len=300)
+    if what == "page":
+        c.table[1, 5] = c.k.shape[0]
+    elif what == "length":
+        kw["max_kv_len"] = 299
+    elif what == "new tokens":
+        kw["max_seqlen_q"] = 2
+    else:
+        cu[2] = 7
+    st = binding.new_status()
+    skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=cu, dev_status=st, **kw)
+    with pytest.raises(binding.StreamKLError) as e:
+        binding.raise_on_device_status(st)
+    assert e.value.status == binding.STREAMKL_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_cache_lives_through_prefill_and_captured_decode_steps():
+    """A chunk of new tokens, then single tokens: norm + rotation of the
+    queries, append, attention. The decode step is captured once and replayed,
+    lengths advancing on the device; each step equals the eager calls bit for
+    bit, and the whole the definition in fp64: rounding q and k to bf16 moves a
+    logit by at most 2^-8 S each (S = scale sum |q k|, about 8 for these
+    normal rows), so terms by 2 x 2^-8 S and the sums of terms and values by
+    twice that; o differs by at most that share of sum p |v|."""
+    dt, HQ, HK, d, page, eps = torch.bfloat16, 4, 2, 64, 16, 1e-6
+    g = torch.Generator().manual_seed(0)
+    start, steps = [37, 5, 300], 6
+    B, width = len(start), 32
+    dev = torch.device("cuda")
+    cos, sin = _tables(width * page, d, dev)
+    wq, wk = (1 + 0.2 * torch.randn(2, d, generator=g)).to(dev)
+    table = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width).to(dev)
+
+    def fresh():
+        return [torch.full((B * width, HK, page, d), float("nan"), dtype=dt, device=dev) for _ in range(2)]
+
+    pre = torch.randn(sum(start), HQ + 2 * HK, d, generator=g).to(dt).to(dev)
+    dec = torch.randn(steps, B, HQ + 2 * HK, d, generator=g).to(dt).to(dev)
+    cu = _cu(start)
+    st = binding.new_status(dev)
+
+    def forward(x, positions, caches, lens, cu_seqlens, n, ws, out=None):
+        q, k, v = x[:, :HQ], x[:, HQ:HQ + HK], x[:, HQ + HK:]
+        q, _ = skl.streamkl_qk_norm_rope_fwd(q, None, cos, sin, positions=positions, q_weight=wq, eps=eps, dev_status=st)
+        skl.streamkl_paged_append(k, v, *caches, table, lens, cu_seqlens=cu_seqlens, cos=cos, sin=sin, k_weight=wk,
+                                  eps=eps, dev_status=st)
+        return skl.streamkl_paged_attn(q, *caches, table, lens, cu_seqlens=cu_seqlens, max_seqlen_q=n,
+                                       num_splits=2, out=out, workspace=ws, dev_status=st)
+
+    pos = torch.cat([torch.arange(n) for n in start]).to(torch.int32).to(dev)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+
+    def prefill(caches):
+        lens = torch.tensor(start, dtype=torch.int32, device=dev)
+        return lens, forward(pre, pos, caches, lens, cu, max(start), ws)
+
+    eager, eager_out = fresh(), []
+    lens, first = prefill(eager)
+    for i in range(steps):
+        lens += 1
+        eager_out.append([t.clone() for t in forward(dec[i], lens - 1, eager, lens, None, 1, ws)])
+
+    caches = fresh()
+    lens, again = prefill(caches)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    x = torch.empty_like(dec[0])
+    out = (torch.empty(B, HQ, d, dtype=dt, device=dev), torch.empty(B, HQ, device=dev))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lens.add_(1)
+        forward(x, lens - 1, caches, lens, None, 1, ws, out)
+    for i in range(steps):
+        x.copy_(dec[i])
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager_out[i]))
+    for a, b in zip(eager, caches):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    binding.raise_on_device_status(st)
+
+    tables = [_np(t) for t in (cos, sin)]
+    for b in range(B):
+        rows = torch.cat([pre[cu[b]:cu[b + 1]]] + [dec[i, b:b + 1] for i in range(steps)])
+        n = rows.shape[0]
+        c, s = (t[:n, None] for t in tables)
+        q, _ = orc.norm_rope(_np(rows[:, :HQ]), _np(wq), c, s, eps, False)
+        k, _ = orc.norm_rope(_np(rows[:, HQ:HQ + HK]), _np(wk), c, s, eps, False)
+        k, v = (np.swapaxes(t, 0, 1) for t in (k, _np(rows[:, HQ + HK:])))
+        ref, ref_lse, mag = orc.paged_attn(q, k, v, d ** -0.5, True)
+        got = torch.cat([first[0][cu[b]:cu[b + 1]]] + [o[0][b:b + 1] for o in eager_out])
+        got_lse = torch.cat([first[1][cu[b]:cu[b + 1]]] + [o[1][b:b + 1] for o in eager_out])
+        S = d ** -0.5 * max(np.max(np.abs(q[:, h]) @ np.abs(k[h // 2]).T) for h in range(HQ))
+        move = 2 * 2.0 ** -8 * S
+        assert np.all(np.abs(_np(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * move) * mag)
+        assert np.all(np.abs(_np(got_lse) - ref_lse) <= 1.1 * move)
+
+
+@pytest.mark.gpu
+def test_on_another_stream_and_the_same_in_every_run():
+    lens, new = [900, 300], [40, 20]
+    c = Cache(lens, 2, 128, 32, torch.bfloat16)
+    q = torch.randn(60, 8, 128, device="cuda").to(torch.bfloat16)
+    kw = dict(cu_seqlens=_cu(new), max_seqlen_q=40, max_kv_len=900, num_splits=3)
+    a = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, stream=side,
+                                workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for _ in range(3):
+        b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_debug_build_finds_nothing_and_gives_the_same():
+    """Every TMA copy, TMEM access and barrier range-checked: no check fails
+    and the results are the release build's."""
+    for new, lens, HQ, HK, d, page, dtype, causal, splits, layout in ATTN:
+        dt = TYPES[dtype]
+        c = Cache(lens, HK, d, page, dt, layout=layout)
+        q = torch.randn(sum(new), HQ, d, device="cuda").to(dt)
+        kw = dict(cu_seqlens=_cu(new), max_seqlen_q=max(new), max_kv_len=max(lens), causal=causal, num_splits=splits)
+        st = binding.new_status()
+        a = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, dev_status=st, **kw)
+        with binding.use_debug_library():
+            b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, dev_status=st, **kw)
+        binding.raise_on_device_status(st)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
@@ -228,3 +520,63 @@ def test_append_python_call_refuses():
     ]:
         with pytest.raises(ValueError, match=match):
             call(*args, **kw)
+
+
+ATTN_C = dict(q=4096, kc=4096, vc=4096, table=4096, ts=4, lens=4096, cu=4096, dtype=0, B=2, T=5, HQ=4, HK=2, d=64,
+              page=16, pages=9, most=4, strides=[2048, 1024, 64] * 2 + [256, 64] * 2, mq=4, mk=64, scale=0.1, causal=1,
+              splits=1, out=4096, lse=4096, ws=None, wsb=0, st=4096)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=2), 2), (dict(d=80), 2), (dict(B=0), 1), (dict(T=0), 1), (dict(HQ=0), 1), (dict(HQ=3), 1),
+    (dict(mq=0), 1), (dict(mq=6), 1), (dict(mk=-1), 1), (dict(mk=65), 1), (dict(cu=None), 1), (dict(q=4104), 1),
+    (dict(out=None), 1), (dict(out=4104), 1), (dict(lse=None), 1), (dict(causal=2), 1), (dict(splits=-1), 1),
+    (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(st=None), 1), (dict(page=24), 2),
+    (dict(strides=[2048, 1024, 64] * 2 + [256, 60] + [256, 64]), 1), (dict(strides=None), 1),
+    (dict(B=40000, HK=2, T=40000, cu=None, mq=1), 2), (dict(splits=2, most=40, ts=40, mk=640), 1),
+])
+def test_attention_c_call_refuses(lib, over, status):
+    a = {**ATTN_C, **over}
+    if a["strides"] is not None:
+        a["strides"] = (ctypes.c_longlong * 10)(*a["strides"])
+    got = lib.streamkl_paged_attn(*[a[n] for n in ("q", "kc", "vc", "table", "ts", "lens", "cu", "dtype", "B", "T", "HQ",
+                                                   "HK", "d", "page", "pages", "most", "strides", "mq", "mk", "scale",
+                                                   "causal", "splits", "out", "lse", "ws", "wsb", "st")], None)
+    assert got == status and lib.streamkl_last_error()
+
+
+def test_attention_splits_on_the_host(lib):
+    assert skl.streamkl_paged_attn_splits(1, 1, 32, 8, 128, 1, 4096) > 1      # few tiles, long keys
+    assert skl.streamkl_paged_attn_splits(64, 64 * 512, 32, 8, 128, 512, 4096) == 1
+    assert skl.streamkl_paged_attn_splits(1, 1, 32, 8, 128, 1, 100) == 1
+    assert skl.streamkl_paged_attn_splits(1, 1, 32, 5, 128, 1, 100) == 0
+    for args in ((1, 1, 32, 8, 128, 1, 4096), (3, 700, 8, 8, 64, 512, 131072)):
+        s = skl.streamkl_paged_attn_splits(*args)
+        need = s * args[1] * args[2] * (args[4] + 1) * 4 if s > 1 else 0
+        got = skl.streamkl_paged_attn_workspace_size(*args)
+        assert need <= got < need + 256
+    assert skl.streamkl_paged_attn_workspace_size(1, 1, 32, 8, 128, 1, 4096, 1) == 0
+
+
+@pytest.mark.gpu
+def test_attention_python_call_refuses():
+    c = Cache([20, 40], 2, 64, 16, torch.bfloat16)
+    q = torch.ones(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    call = skl.streamkl_paged_attn
+    for match, args, kw in [
+        ("q must be", (q.half(), c.k, c.v, c.table, c.lens), {}),
+        ("multiple of 2", (q[:, :3], c.k, c.v, c.table, c.lens), {}),
+        ("d = 64", (q[..., :32], c.k, c.v, c.table, c.lens), {}),
+        ("one token", (q[:1], c.k, c.v, c.table, c.lens), {}),
+        (r"out\[0\]", (q, c.k, c.v, c.table, c.lens), dict(out=(q[:1], None))),
+        (r"out\[1\]", (q, c.k, c.v, c.table, c.lens), dict(out=(q, torch.zeros(2, 3, device="cuda")))),
+        ("workspace", (q, c.k, c.v, c.table, c.lens),
+         dict(num_splits=2, max_kv_len=48, workspace=torch.empty(9, device="cuda"))),
+    ]:
+        if match == "workspace":
+            kw["num_splits"], kw["max_kv_len"] = 2, None
+            args = (q, c.k, c.v, c.table.repeat(1, 8), c.lens)
+        with pytest.raises(ValueError, match=match):
+            call(*args, **kw)
+    o, lse = call(q[:0], c.k, c.v, c.table[:0], c.lens[:0], cu_seqlens=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
