@@ -342,7 +342,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           if (!(ok = v_ready(j) && wait_bounded(p_full(j & 1), (j >> 1) & 1, wc))) break;
           tc_fence_after();
           mma_o(0, (j & 1) * 128, j);
-          mma_commit(o_full(0));
+          // o_full(0) counts the tiles (a rescale waits for the one before);
+          // the end has a barrier of its own: a wait by parity cannot tell
+          // the last product from the one two before it
+          mma_commit(j + 1 < n_iter ? o_full(0) : o_full(1));
           mma_commit(kv_empty(idx_v(j) % L::STAGES));
         }
       }
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       if (lane == 0) mbar_arrive(p_full(slot));
     }
     // ------------------------------------------------------------ output
-    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(t), NT == 2 ? 0 : ((n_iter - 1) & 1), wc) && warp_live) {
+    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(NT == 2 ? t : 1), 0, wc) && warp_live) {
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (NaN stays NaN)
       const bool none = l == 0.f;

@@ -208,7 +208,7 @@ def _check_attn(o, lse, q, c, new, lens, scale, causal, dt):
         err = np.abs(got - ref)
         assert np.all(err <= tol), (b, float((err / tol).max()))
         fin = ~empty
-        assert np.all(np.abs(got_lse - ref_lse)[fin] <= E + 2.0 ** -22 * np.abs(ref_lse[fin]))
+        assert np.all(np.abs(got_lse[fin] - ref_lse[fin]) <= E + 2.0 ** -22 * np.abs(ref_lse[fin]))
 
 
 ATTN = [
@@ -277,6 +277,43 @@ def test_large_logits_move_the_reference(dtype):
         for splits in (1, 3):
             o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), num_splits=splits)
             _check_attn(o, lse, q, c, [n], lens, d ** -0.5, True, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,n,L,HQ,HK,page,splits", [(32, 1, 9000, 8, 8, 16, 1), (16, 1, 20000, 16, 4, 32, 0),
+                                                     (4, 300, 5000, 8, 4, 128, 0), (2, 40, 30000, 8, 4, 64, 3)])
+def test_long_sequences_that_wait_for_memory(B, n, L, HQ, HK, page, splits):
+    """More keys than the caches hold on chip, so that loads arrive late: every
+    wait of the kernel is needed. Against torch in fp64 on the device, bounds
+    as in _check_attn with the relative 2-norm: the term (eps / 2) sum p |v| is
+    there a sum of L independent roundings, at most eps / 2 of the norm of p v,
+    and o's own rounding eps / 2 of o; E adds under 2e-3: 2^-8 + 2^-8 + 2e-3."""
+    d, dt = 128, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(L)
+    per = -(-L // page)
+    k, v = (torch.randn(B * per, HK, page, d, generator=g, device="cuda").to(dt) for _ in range(2))
+    table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+    lens = torch.randint(L // 2, L + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    q = torch.randn(B * n, HQ, d, generator=g, device="cuda").to(dt)
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_attn(q, k, v, table, lens, cu_seqlens=_cu([n] * B), max_seqlen_q=n, max_kv_len=L,
+                                     num_splits=splits, dev_status=st)
+    binding.raise_on_device_status(st)
+    for b in range(B):
+        length = int(lens[b])
+        ks, vs = (t[table[b].long()].transpose(0, 1).reshape(HK, -1, d)[:, :length].double() for t in (k, v))
+        x = q[b * n:(b + 1) * n].double().transpose(0, 1).reshape(HK, -1, d)  # [HK, G n, d]
+        s = x @ ks.transpose(1, 2) * d ** -0.5
+        keys = torch.arange(length, device="cuda")
+        row = torch.arange(n, device="cuda").repeat(HQ // HK)
+        s = s.masked_fill(keys > (length - n + row)[:, None], -float("inf"))
+        z = torch.logsumexp(s, -1, keepdim=True)
+        ref = ((s - z).exp() @ vs).view(HQ, n, d).transpose(0, 1)
+        got = o[b * n:(b + 1) * n].double()
+        rel = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).max()
+        assert float(rel) <= 2.0 ** -7 + 2e-3, (b, float(rel))
+        dl = (lse[b * n:(b + 1) * n].double() - z.view(HQ, n).T).abs().max()
+        assert float(dl) <= 1e-3
 
 
 @pytest.mark.gpu
