@@ -24,12 +24,20 @@ constexpr long long kMaxRows = 1LL << 31;  // rows (tokens x heads) of one tenso
 
 size_t elem_size(int dtype) { return dtype == STREAMKL_FP32 ? 4 : 2; }
 
-streamkl_status check_tensor(const char* name, const void* p, const long long* strides, int n, int dtype) {
+// A tensor of n strided dimensions over rows of d contiguous elements. The
+// stride of a dimension of size 1 says nothing and becomes d. `own_rows`: the
+// rows must be apart (outputs, caches); inputs may repeat rows (stride 0).
+streamkl_status check_tensor(const char* name, const void* p, long long* strides, const int* sizes, int n, int d,
+                             int dtype, bool own_rows) {
   if (!p) return fail(STREAMKL_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned16(p)) return fail(STREAMKL_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
-  for (int i = 0; i < n; ++i)
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 1) strides[i] = d;
     if (strides[i] < 0 || strides[i] * static_cast<long long>(elem_size(dtype)) % 16)
       return fail(STREAMKL_ERR_INVALID_ARG, "%s: stride %lld is not a multiple of 16 bytes", name, strides[i]);
+    if (own_rows && strides[i] < d)
+      return fail(STREAMKL_ERR_INVALID_ARG, "%s: stride %lld below one row of %d", name, strides[i], d);
+  }
   return STREAMKL_OK;
 }
 
@@ -52,13 +60,11 @@ skl::RowStrides row_strides(const long long* s) { return skl::RowStrides{s[0], s
 // The part of a norm + rotation call that both directions share: the
 // arguments' checks and a's sides without their outer rows.
 streamkl_status rope_common(skl::RopeArgs* a, const void* q, const void* k, int dtype, int B, int NQ, int NK,
-                            int HQ, int HK, int d, int rot, const long long* strides, const float* cos,
+                            int HQ, int HK, int d, int rot, long long* strides, const float* cos,
                             const float* sin, int table_len, const int* q_pos, long long q_pos_stride,
                             const int* k_pos, long long k_pos_stride, const float* q_weight,
                             const float* k_weight, float eps, int interleaved, int k_repeat, int* dev_status) {
-  clear_error();
   if (!q && !k) return fail(STREAMKL_ERR_INVALID_ARG, "q and k are both NULL");
-  if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
   if (dtype != STREAMKL_BF16 && dtype != STREAMKL_FP16 && dtype != STREAMKL_FP32)
     return fail(STREAMKL_ERR_UNSUPPORTED, "element type %d", dtype);
   streamkl_status st = check_rope(d, rot, cos, sin, table_len, eps, interleaved);
@@ -72,8 +78,9 @@ streamkl_status rope_common(skl::RopeArgs* a, const void* q, const void* k, int 
   if (q && k && !q_pos && NQ > NK)
     return fail(STREAMKL_ERR_INVALID_ARG, "more queries than keys (%d > %d) need q_positions", NQ, NK);
   if (!dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
-  if (q && (st = check_tensor("q", q, strides, 3, dtype)) != STREAMKL_OK) return st;
-  if (k && (st = check_tensor("k", k, strides + 3, 3, dtype)) != STREAMKL_OK) return st;
+  const int sq[3] = {B, NQ, HQ}, sk[3] = {B, NK, HK};
+  if (q && (st = check_tensor("q", q, strides, sq, 3, d, dtype, false)) != STREAMKL_OK) return st;
+  if (k && (st = check_tensor("k", k, strides + 3, sk, 3, d, dtype, false)) != STREAMKL_OK) return st;
   *a = skl::RopeArgs{};
   a->side[0].x = q;
   a->side[0].xs = row_strides(strides);
@@ -93,7 +100,7 @@ streamkl_status rope_common(skl::RopeArgs* a, const void* q, const void* k, int 
   a->side[1].H = HK;
   a->side[1].rep = k_repeat;
   for (int i = 0; i < 2; ++i) {
-    a->side[i].ys = row_strides(strides + 6 + 3 * i);
+    a->side[i].ys = skl::RowStrides{0, 0, 0};
     a->side[i].dxs = skl::RowStrides{0, 0, 0};
   }
   a->B = B;
@@ -111,7 +118,7 @@ streamkl_status rope_common(skl::RopeArgs* a, const void* q, const void* k, int 
 
 streamkl_status check_cache(const void* kc, const void* vc, const int* table, long long table_stride,
                             const int* kv_lens, int dtype, int B, int T, int HK, int d, int page_size,
-                            int num_pages, int max_pages, const long long* strides) {
+                            int num_pages, int max_pages, long long* strides) {
   if (dtype != STREAMKL_BF16 && dtype != STREAMKL_FP16)
     return fail(STREAMKL_ERR_UNSUPPORTED, "cache element type %d (supported: bf16, fp16)", dtype);
   if (d != 64 && d != 128) return fail(STREAMKL_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
@@ -125,13 +132,10 @@ streamkl_status check_cache(const void* kc, const void* vc, const int* table, lo
   if (!table || !kv_lens) return fail(STREAMKL_ERR_INVALID_ARG, "block_table and kv_lens must be non-NULL");
   if (table_stride < max_pages && B > 1)
     return fail(STREAMKL_ERR_INVALID_ARG, "block_table rows overlap (stride %lld, %d pages)", table_stride, max_pages);
-  streamkl_status st = check_tensor("k_cache", kc, strides, 3, dtype);
+  const int sizes[3] = {num_pages, HK, page_size};
+  streamkl_status st = check_tensor("k_cache", kc, strides, sizes, 3, d, dtype, true);
   if (st != STREAMKL_OK) return st;
-  if ((st = check_tensor("v_cache", vc, strides + 3, 3, dtype)) != STREAMKL_OK) return st;
-  for (int i = 0; i < 6; ++i)
-    if (strides[i] < d)
-      return fail(STREAMKL_ERR_INVALID_ARG, "cache stride %lld below one row of %d", strides[i], d);
-  return STREAMKL_OK;
+  return check_tensor("v_cache", vc, strides + 3, sizes, 3, d, dtype, true);
 }
 
 // Key split of the attention over the cache: with few query tiles against
@@ -224,15 +228,22 @@ streamkl_status streamkl_qk_norm_rope_fwd(const void* q, const void* k, int dtyp
                                           long long q_pos_stride, const int* k_positions, long long k_pos_stride,
                                           const float* q_weight, const float* k_weight, float eps, int interleaved,
                                           int k_repeat, void* q_out, void* k_out, int* dev_status, void* stream) {
+  clear_error();
+  if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
+  long long s[12];
+  std::copy(strides, strides + 12, s);
   skl::RopeArgs a;
-  streamkl_status st = rope_common(&a, q, k, dtype, B, NQ, NK, HQ, HK, d, rot, strides, cos, sin, table_len,
+  streamkl_status st = rope_common(&a, q, k, dtype, B, NQ, NK, HQ, HK, d, rot, s, cos, sin, table_len,
                                    q_positions, q_pos_stride, k_positions, k_pos_stride, q_weight, k_weight, eps,
                                    interleaved, k_repeat, dev_status);
   if (st != STREAMKL_OK) return st;
-  if (q && (st = check_tensor("q_out", q_out, strides + 6, 3, dtype)) != STREAMKL_OK) return st;
-  if (k && (st = check_tensor("k_out", k_out, strides + 9, 3, dtype)) != STREAMKL_OK) return st;
+  const int oq[3] = {B, NQ, HQ}, ok[3] = {B, NK, HK * k_repeat};
+  if (q && (st = check_tensor("q_out", q_out, s + 6, oq, 3, d, dtype, true)) != STREAMKL_OK) return st;
+  if (k && (st = check_tensor("k_out", k_out, s + 9, ok, 3, d, dtype, true)) != STREAMKL_OK) return st;
   a.side[0].y_out = q_out;
   a.side[1].y_out = k_out;
+  a.side[0].ys = row_strides(s + 6);
+  a.side[1].ys = row_strides(s + 9);
   cudaError_t e = skl::launch_rope_fwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "norm + rotation launch");
 }
@@ -250,15 +261,20 @@ streamkl_status streamkl_qk_norm_rope_bwd(const void* q, const void* k, const vo
                                           const float* k_weight, float eps, int interleaved, int k_repeat, void* dq,
                                           void* dk, float* dq_weight, float* dk_weight, void* workspace,
                                           size_t ws_bytes, int* dev_status, void* stream) {
+  clear_error();
+  if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
+  long long s[18];
+  std::copy(strides, strides + 18, s);
   skl::RopeArgs a;
-  streamkl_status st = rope_common(&a, q, k, dtype, B, NQ, NK, HQ, HK, d, rot, strides, cos, sin, table_len,
+  streamkl_status st = rope_common(&a, q, k, dtype, B, NQ, NK, HQ, HK, d, rot, s, cos, sin, table_len,
                                    q_positions, q_pos_stride, k_positions, k_pos_stride, q_weight, k_weight, eps,
                                    interleaved, k_repeat, dev_status);
   if (st != STREAMKL_OK) return st;
-  if (q && (st = check_tensor("dq_out", dq_out, strides + 6, 3, dtype)) != STREAMKL_OK) return st;
-  if (k && (st = check_tensor("dk_out", dk_out, strides + 9, 3, dtype)) != STREAMKL_OK) return st;
-  if (q && (st = check_tensor("dq", dq, strides + 12, 3, dtype)) != STREAMKL_OK) return st;
-  if (k && (st = check_tensor("dk", dk, strides + 15, 3, dtype)) != STREAMKL_OK) return st;
+  const int sq[3] = {B, NQ, HQ}, sk[3] = {B, NK, HK}, ok[3] = {B, NK, HK * k_repeat};
+  if (q && (st = check_tensor("dq_out", dq_out, s + 6, sq, 3, d, dtype, false)) != STREAMKL_OK) return st;
+  if (k && (st = check_tensor("dk_out", dk_out, s + 9, ok, 3, d, dtype, false)) != STREAMKL_OK) return st;
+  if (q && (st = check_tensor("dq", dq, s + 12, sq, 3, d, dtype, true)) != STREAMKL_OK) return st;
+  if (k && (st = check_tensor("dk", dk, s + 15, sk, 3, d, dtype, true)) != STREAMKL_OK) return st;
   const bool nq = q && q_weight, nk = k && k_weight;
   if ((nq && !dq_weight) || (nk && !dk_weight))
     return fail(STREAMKL_ERR_INVALID_ARG, "a norm weight needs its gradient's buffer");
@@ -269,10 +285,12 @@ streamkl_status streamkl_qk_norm_rope_bwd(const void* q, const void* k, const vo
   if (need && !aligned16(workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
   a.side[0].y_in = dq_out;
   a.side[0].dx = dq;
-  a.side[0].dxs = row_strides(strides + 12);
+  a.side[0].ys = row_strides(s + 6);
+  a.side[0].dxs = row_strides(s + 12);
   a.side[1].y_in = dk_out;
   a.side[1].dx = dk;
-  a.side[1].dxs = row_strides(strides + 15);
+  a.side[1].ys = row_strides(s + 9);
+  a.side[1].dxs = row_strides(s + 15);
   a.part = static_cast<float*>(workspace);
   cudaError_t e = skl::launch_rope_bwd(a, blocks, nq ? dq_weight : nullptr, nk ? dk_weight : nullptr,
                                        static_cast<cudaStream_t>(stream));
@@ -287,14 +305,17 @@ streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cach
                                       float eps, int interleaved, int* dev_status, void* stream) {
   clear_error();
   if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
+  long long s[10];
+  std::copy(strides, strides + 10, s);
   streamkl_status st = check_cache(k_cache, v_cache, block_table, table_stride, kv_lens, dtype, B, T, HK, d,
-                                   page_size, num_pages, max_pages, strides);
+                                   page_size, num_pages, max_pages, s);
   if (st != STREAMKL_OK) return st;
   if (!cu_seqlens && T != B)
     return fail(STREAMKL_ERR_INVALID_ARG, "without cu_seqlens each sequence has one token (T=%d B=%d)", T, B);
   if (static_cast<long long>(T) * HK > kMaxRows) return fail(STREAMKL_ERR_UNSUPPORTED, "rows x heads above 2^31");
-  if ((st = check_tensor("k", k, strides + 6, 2, dtype)) != STREAMKL_OK) return st;
-  if ((st = check_tensor("v", v, strides + 8, 2, dtype)) != STREAMKL_OK) return st;
+  const int sizes[2] = {T, HK};
+  if ((st = check_tensor("k", k, s + 6, sizes, 2, d, dtype, false)) != STREAMKL_OK) return st;
+  if ((st = check_tensor("v", v, s + 8, sizes, 2, d, dtype, false)) != STREAMKL_OK) return st;
   if ((cos == nullptr) != (sin == nullptr))
     return fail(STREAMKL_ERR_INVALID_ARG, "cos and sin must be both NULL or both non-NULL");
   if (cos && (st = check_rope(d, rot, cos, sin, table_len, eps, interleaved)) != STREAMKL_OK) return st;
@@ -303,12 +324,12 @@ streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cach
   skl::AppendArgs a{};
   a.k = k;
   a.v = v;
-  a.ks = skl::RowStrides{0, strides[6], strides[7]};
-  a.vs = skl::RowStrides{0, strides[8], strides[9]};
+  a.ks = skl::RowStrides{0, s[6], s[7]};
+  a.vs = skl::RowStrides{0, s[8], s[9]};
   a.kc = k_cache;
   a.vc = v_cache;
-  a.kc_sp = strides[0], a.kc_sh = strides[1], a.kc_ss = strides[2];
-  a.vc_sp = strides[3], a.vc_sh = strides[4], a.vc_ss = strides[5];
+  a.kc_sp = s[0], a.kc_sh = s[1], a.kc_ss = s[2];
+  a.vc_sp = s[3], a.vc_sh = s[4], a.vc_ss = s[5];
   a.table = block_table;
   a.table_sb = table_stride;
   a.kv_lens = kv_lens;
@@ -352,16 +373,19 @@ streamkl_status streamkl_paged_attn(const void* q, const void* k_cache, const vo
                                     size_t ws_bytes, int* dev_status, void* stream) {
   clear_error();
   if (!strides) return fail(STREAMKL_ERR_INVALID_ARG, "strides is NULL");
+  long long s[10];
+  std::copy(strides, strides + 10, s);
   streamkl_status st = check_cache(k_cache, v_cache, block_table, table_stride, kv_lens, dtype, B, T, HK, d,
-                                   page_size, num_pages, max_pages, strides);
+                                   page_size, num_pages, max_pages, s);
   if (st != STREAMKL_OK) return st;
   if ((st = check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len)) != STREAMKL_OK) return st;
   if (!cu_seqlens && T != B)
     return fail(STREAMKL_ERR_INVALID_ARG, "without cu_seqlens each sequence has one token (T=%d B=%d)", T, B);
   if (max_kv_len > static_cast<long long>(max_pages) * page_size)
     return fail(STREAMKL_ERR_INVALID_ARG, "max_kv_len %d above %d pages of %d", max_kv_len, max_pages, page_size);
-  if ((st = check_tensor("q", q, strides + 6, 2, dtype)) != STREAMKL_OK) return st;
-  if ((st = check_tensor("out", out, strides + 8, 2, dtype)) != STREAMKL_OK) return st;
+  const int sizes[2] = {T, HQ};
+  if ((st = check_tensor("q", q, s + 6, sizes, 2, d, dtype, false)) != STREAMKL_OK) return st;
+  if ((st = check_tensor("out", out, s + 8, sizes, 2, d, dtype, true)) != STREAMKL_OK) return st;
   if (!lse) return fail(STREAMKL_ERR_INVALID_ARG, "lse must be non-NULL");
   if (causal != 0 && causal != 1) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0 or 1");
   if (num_splits < 0) return fail(STREAMKL_ERR_INVALID_ARG, "num_splits must be >= 0");
@@ -374,17 +398,17 @@ streamkl_status streamkl_paged_attn(const void* q, const void* k_cache, const vo
     return fail(STREAMKL_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
   if (need && !aligned16(workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
   CUtensorMap mk, mv;
-  if ((st = make_map_cache(&mk, k_cache, dtype, d, page_size, HK, num_pages, strides, "k_cache")) != STREAMKL_OK)
+  if ((st = make_map_cache(&mk, k_cache, dtype, d, page_size, HK, num_pages, s, "k_cache")) != STREAMKL_OK)
     return st;
-  if ((st = make_map_cache(&mv, v_cache, dtype, d, page_size, HK, num_pages, strides + 3, "v_cache")) != STREAMKL_OK)
+  if ((st = make_map_cache(&mv, v_cache, dtype, d, page_size, HK, num_pages, s + 3, "v_cache")) != STREAMKL_OK)
     return st;
   skl::PagedAttnArgs a{};
   a.tm_k = &mk;
   a.tm_v = &mv;
   a.q = q;
-  a.q_sn = strides[6], a.q_sh = strides[7];
+  a.q_sn = s[6], a.q_sh = s[7];
   a.o = out;
-  a.o_sn = strides[8], a.o_sh = strides[9];
+  a.o_sn = s[8], a.o_sh = s[9];
   a.lse = lse;
   a.table = block_table;
   a.table_sb = table_stride;

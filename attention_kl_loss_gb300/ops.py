@@ -10,58 +10,61 @@ PyTorch provides device memory and the current stream.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
 
-from .binding import _check, _ptr, load, new_status
+from .binding import _check, load, new_status
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_NO_GUARD = contextlib.nullcontext()
+# the current stream's handle without making a Stream object (2 us of a call
+# whose kernel takes 3)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_pack10, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (10, 12, 18))
+_NONE = (0, 0, 0)
 
 
-def _guard(device):
-    """Make ``device`` the current one for a call (launches and tensor maps go
-    to the current device)."""
-    if device.index == torch.cuda.current_device():
-        return _NO_GUARD
-    return torch.cuda.device(device)
+def _on_device(call, device, kwargs):
+    """Run ``call`` with ``device`` current: launches and tensor maps go to
+    the current device."""
+    with torch.cuda.device(device):
+        return call(**kwargs)
 
 
 def _stream(stream, device):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"stream of {s.device} for tensors on {device}")
-    return s.cuda_stream
+    if stream is None:
+        return _raw_stream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    return stream.cuda_stream
 
 
-def _strides(*values):
-    return (ctypes.c_longlong * len(values))(*values)
-
-
-def _rows(name, t, dim, dtype=None, device=None):
-    """A CUDA tensor of ``dim`` dimensions whose last one is contiguous."""
+def _rows(name, t, dim, dtype, device):
+    """A CUDA tensor of ``dim`` dimensions whose last one is contiguous; its
+    strides."""
     if not isinstance(t, torch.Tensor) or t.dim() != dim:
         raise ValueError(f"{name} must be a {dim}-D tensor")
-    if not t.is_cuda or t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor with a contiguous last dimension")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
+    return strides
 
 
 def _vector(name, t, n, dtype, device):
+    """The address of a contiguous vector, 0 for None."""
     if t is None:
-        return None
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.dim() != 1
-            or t.shape[0] != n or not t.is_contiguous()):
+        return 0
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != (n,)
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} vector [{n}] on {device}")
-    return t
+    return t.data_ptr()
 
 
 def _status(dev_status, device):
@@ -89,56 +92,12 @@ def _tables(cos, sin, device):
     _rows("sin", sin, 2, torch.float32, device)
     if cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
         raise ValueError("cos and sin must be contiguous and of one shape [positions, rot / 2]")
-    return cos.shape[0], 2 * cos.shape[1]
+    n, half = cos.shape
+    return n, 2 * half
 
 
-class _RopeSide:
-    """One of q, k of a call: its tensor, sizes and the shape of its outer rows."""
-
-    def __init__(self, name, x, positions, weight, repeat):
-        packed = x.dim() == 3
-        self.name, self.x, self.packed, self.repeat = name, x, packed, repeat
-        if packed:
-            self.B, (self.N, self.H, self.d) = 1, x.shape
-            self.outer = (self.N, self.H * repeat, self.d)
-        else:
-            self.B, self.N, self.H, self.d = x.shape
-            self.outer = (self.B, self.H * repeat, self.N, self.d)
-        self.weight = _vector(f"{name}_weight", weight, self.d, torch.float32, x.device)
-        self.pos, self.pos_stride = positions, 0
-        if positions is not None:
-            p = positions
-            if not isinstance(p, torch.Tensor) or p.dtype != torch.int32 or p.device != x.device:
-                raise ValueError(f"positions of {name} must be an int32 tensor on {x.device}")
-            if p.shape == (self.N,) and (self.N == 1 or p.stride(0) == 1):
-                return
-            if packed or p.shape != (self.B, self.N) or (self.N > 1 and p.stride(1) != 1) or p.stride(0) < 0:
-                raise ValueError(f"positions of {name} must be [{self.N}]"
-                                 + ("" if packed else f" or [{self.B}, {self.N}]") + ", tokens contiguous")
-            self.pos_stride = p.stride(0)
-
-    def inner_strides(self, t):
-        s = t.stride()
-        return (0, s[0], s[1]) if self.packed else (s[0], s[1], s[2])
-
-    def outer_strides(self, t):
-        s = t.stride()
-        return (0, s[0], s[1]) if self.packed else (s[0], s[2], s[1])
-
-    def check_outer(self, name, t):
-        _rows(name, t, len(self.outer), self.x.dtype, self.x.device)
-        if t.shape != self.outer:
-            raise ValueError(f"{name} must be {list(self.outer)}, got {list(t.shape)}")
-        return t
-
-    def check_inner(self, name, t):
-        _rows(name, t, self.x.dim(), self.x.dtype, self.x.device)
-        if t.shape != self.x.shape:
-            raise ValueError(f"{name} must be {list(self.x.shape)}, got {list(t.shape)}")
-        return t
-
-
-def _rope_sides(q, k, positions, k_positions, q_weight, k_weight, k_repeat):
+def _rope_sizes(q, k, positions, k_positions, k_repeat):
+    """(a given tensor, packed, positions of q and of k)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
@@ -146,36 +105,49 @@ def _rope_sides(q, k, positions, k_positions, q_weight, k_weight, k_repeat):
         raise ValueError("q and k must be [B, N, H, d] or packed [total, H, d]")
     if x.dtype not in _DTYPES:
         raise ValueError(f"unsupported type {x.dtype} (bf16, fp16, fp32)")
-    if int(k_repeat) < 1:
+    if k_repeat < 1:
         raise ValueError("k_repeat must be >= 1")
-    if k_positions is None and (q is None or k is None or q.shape[-3] == k.shape[-3]):
+    packed = x.dim() == 3
+    if k_positions is None and positions is not None and k is not None:
+        if q is not None and q.shape[-3] != k.shape[-3]:
+            raise ValueError("q and k of different lengths need k_positions beside positions")
         k_positions = positions
-    elif k is not None and positions is not None and k_positions is None:
-        raise ValueError("q and k of different lengths need k_positions beside positions")
-    sides = []
-    for name, t, p, w, r in (("q", q, positions, q_weight, 1), ("k", k, k_positions, k_weight, int(k_repeat))):
-        if t is None:
-            sides.append(None)
-            continue
-        _rows(name, t, x.dim(), x.dtype, x.device)
-        sides.append(_RopeSide(name, t, p, w, r))
-    sq, sk = sides
-    if sq and sk and (sq.B != sk.B or sq.d != sk.d):
-        raise ValueError("q and k differ in batch size or head dim")
-    if x.dim() == 3 and ((sq and positions is None) or (sk and k_positions is None)):
+    if packed and ((q is not None and positions is None) or (k is not None and k_positions is None)):
         raise ValueError("a packed batch needs the positions of its tokens")
-    return x, sq, sk
+    return x, packed, positions, k_positions
 
 
-def _rope_args(x, sq, sk, strides, cos, sin, eps, interleaved, k_repeat):
-    length, rot = _tables(cos, sin, x.device)
-    a = sq or sk
-    return (_DTYPES[x.dtype], a.B, sq.N if sq else 0, sk.N if sk else 0, sq.H if sq else 0, sk.H if sk else 0,
-            a.d, rot, _strides(*strides), cos.data_ptr(), sin.data_ptr(), length,
-            _ptr(sq.pos) if sq else None, sq.pos_stride if sq else 0,
-            _ptr(sk.pos) if sk else None, sk.pos_stride if sk else 0,
-            _ptr(sq.weight) if sq else None, _ptr(sk.weight) if sk else None, float(eps),
-            int(bool(interleaved)), int(k_repeat))
+def _rope_side(name, t, x, packed, pos, weight, repeat):
+    """Checks of q or k: (B, N, H, d, strides, shape of the outer rows,
+    positions and their batch stride, weight)."""
+    s = _rows(name, t, 3 if packed else 4, x.dtype, x.device)
+    if packed:
+        N, H, d = t.shape
+        B, inner, outer = 1, (0, s[0], s[1]), (N, H * repeat, d)
+    else:
+        B, N, H, d = t.shape
+        inner, outer = s[:3], (B, H * repeat, N, d)
+    w = _vector("q_weight" if name == "q" else "k_weight", weight, d, torch.float32, x.device)
+    at, stride = 0, 0
+    if pos is not None:
+        if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or pos.device != x.device:
+            raise ValueError(f"positions of {name} must be an int32 tensor on {x.device}")
+        ps, pst = pos.shape, pos.stride()
+        if ps == (B, N) and not packed and pst[0] >= 0 and (N <= 1 or pst[1] == 1):
+            stride = pst[0]
+        elif ps != (N,) or (N > 1 and pst[0] != 1):
+            raise ValueError(f"positions of {name} must be [{N}]" + ("" if packed else f" or [{B}, {N}]")
+                             + ", tokens contiguous")
+        at = pos.data_ptr()
+    return B, N, H, d, inner, outer, at, stride, w
+
+
+def _rope_rows(name, t, shape, x, packed):
+    """Strides (batch, token, head) of an outer tensor."""
+    s = _rows(name, t, len(shape), x.dtype, x.device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return (0, s[0], s[1]) if packed else (s[0], s[2], s[1])
 
 
 def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, q_weight=None,
@@ -192,29 +164,45 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
     k_positions is given); without them key n stands at position n and the
     queries at the last N positions of the keys. Weights: fp32 [d], None for
     rotation without norm."""
-    x, sq, sk = _rope_sides(q, k, positions, k_positions, q_weight, k_weight, k_repeat)
-    outs, inner, outer = [], [], []
-    for i, s in enumerate((sq, sk)):
-        if s is None:
-            outs.append(None)
-            inner += (0, 0, 0)
-            outer += (0, 0, 0)
-            continue
-        y = out[i] if out is not None else None
-        y = s.check_outer(f"out[{i}]", y) if y is not None else torch.empty(s.outer, dtype=x.dtype, device=x.device)
-        outs.append(y)
-        inner += s.inner_strides(s.x)
-        outer += s.outer_strides(y)
-    if all(s is None or s.x.numel() == 0 for s in (sq, sk)):
-        return tuple(outs)
-    status = _status(dev_status, x.device)
-    args = _rope_args(x, sq, sk, inner + outer, cos, sin, eps, interleaved, k_repeat)
-    with _guard(x.device):
-        st = load().streamkl_qk_norm_rope_fwd(_ptr(q), _ptr(k), *args, _ptr(outs[0]), _ptr(outs[1]),
-                                              status.data_ptr(), _stream(stream, x.device))
+    k_repeat = int(k_repeat)
+    x, packed, q_pos, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
+    dev, dtype = x.device, x.dtype
+    if x.is_cuda and dev.index != torch.cuda.current_device():
+        return _on_device(streamkl_qk_norm_rope_fwd, dev, dict(
+            q=q, k=k, cos=cos, sin=sin, positions=positions, k_positions=k_positions, q_weight=q_weight,
+            k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out, dev_status=dev_status,
+            stream=stream))
+    yq = yk = None
+    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = q_at = k_at = yq_at = yk_at = 0
+    iq = ik = oq = ok = _NONE
+    if q is not None:
+        B, NQ, HQ, d, iq, shape, pq, sq, wq = _rope_side("q", q, x, packed, q_pos, q_weight, 1)
+        yq = out[0] if out is not None else None
+        if yq is None:
+            yq = torch.empty(shape, dtype=dtype, device=dev)
+        oq = _rope_rows("out[0]", yq, shape, x, packed)
+        q_at, yq_at = q.data_ptr(), yq.data_ptr()
+    if k is not None:
+        Bk, NK, HK, dk, ik, shape, pk, sk, wk = _rope_side("k", k, x, packed, k_pos, k_weight, k_repeat)
+        if q is not None and (Bk != B or dk != d):
+            raise ValueError("q and k differ in batch size or head dim")
+        B, d = Bk, dk
+        yk = out[1] if out is not None else None
+        if yk is None:
+            yk = torch.empty(shape, dtype=dtype, device=dev)
+        ok = _rope_rows("out[1]", yk, shape, x, packed)
+        k_at, yk_at = k.data_ptr(), yk.data_ptr()
+    length, rot = _tables(cos, sin, dev)
+    status = _status(dev_status, dev)
+    if B * (NQ * HQ + NK * HK) == 0:
+        return yq, yk
+    st = load().streamkl_qk_norm_rope_fwd(q_at, k_at, _DTYPES[dtype], B, NQ, NK, HQ, HK, d, rot,
+                                          _pack12(*iq, *ik, *oq, *ok), cos.data_ptr(), sin.data_ptr(), length, pq, sq,
+                                          pk, sk, wq, wk, eps, bool(interleaved), k_repeat, yq_at, yk_at,
+                                          status.data_ptr(), _stream(stream, dev))
     if st:
         _check(st, "streamkl_qk_norm_rope_fwd")
-    return tuple(outs)
+    return yq, yk
 
 
 def streamkl_qk_norm_rope_bwd_workspace_size(B, NQ, NK, HQ, HK, d) -> int:
@@ -229,62 +217,97 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     the shapes of q, k (``out`` = (dq, dk) may be slices of one buffer); the
     gradients of a key head's repeats are summed; weight gradients are fp32
     [d], None where there is no weight."""
-    x, sq, sk = _rope_sides(q, k, positions, k_positions, q_weight, k_weight, k_repeat)
-    dev = x.device
-    grads, dws, ins, inner, outer, back = [], [], [], [], [], []
-    for i, (s, g) in enumerate(((sq, dq_out), (sk, dk_out))):
-        if s is None:
-            for to in (inner, outer, back):
-                to += (0, 0, 0)
-            for to in (grads, dws, ins):
-                to.append(None)
-            continue
-        ins.append(s.check_outer(f"d{s.name}_out", g))
-        t = out[i] if out is not None else None
-        t = s.check_inner(f"out[{i}]", t) if t is not None else torch.empty(s.x.shape, dtype=x.dtype, device=dev)
-        grads.append(t)
-        dws.append(None if s.weight is None else torch.empty(s.d, dtype=torch.float32, device=dev))
-        inner += s.inner_strides(s.x)
-        outer += s.outer_strides(g)
-        back += s.inner_strides(t)
-    if all(s is None or s.x.numel() == 0 for s in (sq, sk)):
-        return (*grads, *(w if w is None else w.zero_() for w in dws))
+    k_repeat = int(k_repeat)
+    x, packed, q_pos, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
+    dev, dtype = x.device, x.dtype
+    if x.is_cuda and dev.index != torch.cuda.current_device():
+        return _on_device(streamkl_qk_norm_rope_bwd, dev, dict(
+            q=q, k=k, dq_out=dq_out, dk_out=dk_out, cos=cos, sin=sin, positions=positions, k_positions=k_positions,
+            q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out,
+            workspace=workspace, dev_status=dev_status, stream=stream))
+    dq = dk = dwq = dwk = None
+    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = 0
+    q_at = k_at = yq_at = yk_at = dq_at = dk_at = dwq_at = dwk_at = 0
+    iq = ik = oq = ok = gq = gk = _NONE
+    if q is not None:
+        B, NQ, HQ, d, iq, shape, pq, sq, wq = _rope_side("q", q, x, packed, q_pos, q_weight, 1)
+        oq = _rope_rows("dq_out", dq_out, shape, x, packed)
+        dq = out[0] if out is not None else None
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=dtype, device=dev)
+        gq = _rope_grad("out[0]", dq, q, packed)
+        q_at, yq_at, dq_at = q.data_ptr(), dq_out.data_ptr(), dq.data_ptr()
+        if wq:
+            dwq = torch.empty(d, dtype=torch.float32, device=dev)
+            dwq_at = dwq.data_ptr()
+    if k is not None:
+        Bk, NK, HK, dim, ik, shape, pk, sk, wk = _rope_side("k", k, x, packed, k_pos, k_weight, k_repeat)
+        if q is not None and (Bk != B or dim != d):
+            raise ValueError("q and k differ in batch size or head dim")
+        B, d = Bk, dim
+        ok = _rope_rows("dk_out", dk_out, shape, x, packed)
+        dk = out[1] if out is not None else None
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=dtype, device=dev)
+        gk = _rope_grad("out[1]", dk, k, packed)
+        k_at, yk_at, dk_at = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
+        if wk:
+            dwk = torch.empty(d, dtype=torch.float32, device=dev)
+            dwk_at = dwk.data_ptr()
+    length, rot = _tables(cos, sin, dev)
     status = _status(dev_status, dev)
-    args = _rope_args(x, sq, sk, inner + outer + back, cos, sin, eps, interleaved, k_repeat)
-    with _guard(dev):
-        need = 0
-        if dws[0] is not None or dws[1] is not None:
-            need = streamkl_qk_norm_rope_bwd_workspace_size(*args[1:7])
-        ws = _workspace(need, dev, workspace)
-        st = load().streamkl_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(ins[0]), _ptr(ins[1]), *args,
-                                              _ptr(grads[0]), _ptr(grads[1]), _ptr(dws[0]), _ptr(dws[1]),
-                                              _ptr(ws), need, status.data_ptr(), _stream(stream, dev))
+    if B * (NQ * HQ + NK * HK) == 0:
+        for w in (dwq, dwk):
+            if w is not None:
+                w.zero_()
+        return dq, dk, dwq, dwk
+    lib = load()
+    need = lib.streamkl_qk_norm_rope_bwd_workspace_size(B, NQ, NK, HQ, HK, d) if wq or wk else 0
+    ws = _workspace(need, dev, workspace)
+    st = lib.streamkl_qk_norm_rope_bwd(q_at, k_at, yq_at, yk_at, _DTYPES[dtype], B, NQ, NK, HQ, HK, d, rot,
+                                       _pack18(*iq, *ik, *oq, *ok, *gq, *gk), cos.data_ptr(), sin.data_ptr(), length,
+                                       pq, sq, pk, sk, wq, wk, eps, bool(interleaved), k_repeat, dq_at, dk_at, dwq_at,
+                                       dwk_at, ws.data_ptr() if need else 0, need, status.data_ptr(),
+                                       _stream(stream, dev))
     if st:
         _check(st, "streamkl_qk_norm_rope_bwd")
-    return (*grads, *dws)
+    return dq, dk, dwq, dwk
+
+
+def _rope_grad(name, t, x, packed):
+    """Strides (batch, token, head) of an output in the place of x."""
+    s = _rows(name, t, 3 if packed else 4, x.dtype, x.device)
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must be {list(x.shape)}, got {list(t.shape)}")
+    return (0, s[0], s[1]) if packed else s[:3]
 
 
 def _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total):
-    """Checks of the paged cache; (B, total, HK, d, page_size, num_pages, max_pages)."""
-    dev = k_cache.device
-    _rows("k_cache", k_cache, 4)
-    if k_cache.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"unsupported cache type {k_cache.dtype} (bf16, fp16)")
-    _rows("v_cache", v_cache, 4, k_cache.dtype, dev)
-    if v_cache.shape != k_cache.shape:
+    """Checks of the paged cache: (B, HK, d, page size, pages, pages of a
+    sequence, stride of block_table, strides of the caches, addresses of
+    block_table, kv_lens, cu_seqlens)."""
+    dev, dtype = k_cache.device, k_cache.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"unsupported cache type {dtype} (bf16, fp16)")
+    ks = _rows("k_cache", k_cache, 4, dtype, dev)
+    vs = _rows("v_cache", v_cache, 4, dtype, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [pages, heads, page size, d]")
-    if (block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError(f"block_table must be int32 [B, pages of a sequence] on {dev}, rows contiguous")
-    B = block_table.shape[0]
-    _vector("kv_lens", kv_lens, B, torch.int32, dev)
+    if block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2:
+        raise ValueError(f"block_table must be int32 [B, pages of a sequence] on {dev}")
+    B, width = block_table.shape
+    bs = block_table.stride()
+    if width > 1 and bs[1] != 1:
+        raise ValueError("block_table rows must be contiguous")
     if kv_lens is None:
         raise ValueError("kv_lens must be given")
-    _vector("cu_seqlens", cu_seqlens, B + 1, torch.int32, dev)
+    lens = _vector("kv_lens", kv_lens, B, torch.int32, dev)
+    cu = _vector("cu_seqlens", cu_seqlens, B + 1, torch.int32, dev)
     if cu_seqlens is None and total != B:
         raise ValueError(f"without cu_seqlens each of the {B} sequences has one token, got {total}")
-    pages, heads, page, d = k_cache.shape
-    return B, total, heads, d, page, pages, block_table.shape[1]
+    pages, heads, page, d = shape
+    return B, heads, d, page, pages, width, bs[0], ks[:3] + vs[:3], block_table.data_ptr(), lens, cu
 
 
 def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None,
@@ -299,26 +322,31 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     bf16 or fp16, any strides with d contiguous. cos, sin, k_weight as in
     ``streamkl_qk_norm_rope_fwd``, None to leave out the rotation or the norm.
     Writes the caches in place and returns them."""
-    _rows("k", k, 3, k_cache.dtype, k_cache.device)
-    _rows("v", v, 3, k_cache.dtype, k_cache.device)
-    sizes = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, k.shape[0])
-    if k.shape != v.shape or k.shape[1:] != (sizes[2], sizes[3]):
-        raise ValueError(f"k and v must both be [total, {sizes[2]}, {sizes[3]}]")
+    dev, dtype = k_cache.device, k_cache.dtype
+    if k_cache.is_cuda and dev.index != torch.cuda.current_device():
+        return _on_device(streamkl_paged_append, dev, dict(
+            k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens,
+            cu_seqlens=cu_seqlens, cos=cos, sin=sin, k_weight=k_weight, eps=eps, interleaved=interleaved,
+            dev_status=dev_status, stream=stream))
+    ks = _rows("k", k, 3, dtype, dev)
+    vs = _rows("v", v, 3, dtype, dev)
+    total, HK, d = k.shape
+    B, heads, dim, page, pages, width, table_stride, strides, table, lens, cu = _cache(
+        k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
+    if k.shape != v.shape or HK != heads or d != dim:
+        raise ValueError(f"k and v must both be [total, {heads}, {dim}]")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin must be given together")
-    dev = k.device
     length, rot = _tables(cos, sin, dev) if cos is not None else (0, 0)
-    _vector("k_weight", k_weight, sizes[3], torch.float32, dev)
+    w = _vector("k_weight", k_weight, d, torch.float32, dev)
     status = _status(dev_status, dev)
-    if k.numel() == 0:
+    if total == 0 or HK == 0:
         return k_cache, v_cache
-    strides = _strides(*k_cache.stride()[:3], *v_cache.stride()[:3], *k.stride()[:2], *v.stride()[:2])
-    with _guard(dev):
-        st = load().streamkl_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                          block_table.data_ptr(), block_table.stride(0), kv_lens.data_ptr(),
-                                          _ptr(cu_seqlens), _DTYPES[k.dtype], *sizes, strides, rot, _ptr(cos),
-                                          _ptr(sin), length, _ptr(k_weight), float(eps), int(bool(interleaved)),
-                                          status.data_ptr(), _stream(stream, dev))
+    st = load().streamkl_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table,
+                                      table_stride, lens, cu, _DTYPES[dtype], B, total, HK, d, page, pages, width,
+                                      _pack10(*strides, ks[0], ks[1], vs[0], vs[1]), rot,
+                                      cos.data_ptr() if rot else 0, sin.data_ptr() if rot else 0, length, w, eps,
+                                      bool(interleaved), status.data_ptr(), _stream(stream, dev))
     if st:
         _check(st, "streamkl_paged_append")
     return k_cache, v_cache
@@ -347,38 +375,43 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     the sequences' new tokens and lengths (default: every token, every page of
     block_table); close ones give a better grid. Rows that see no key get
     zeros and -inf; rows behind the last sequence stay as they were."""
-    _rows("q", q, 3, k_cache.dtype, k_cache.device)
-    dev = q.device
-    total, HQ, d = q.shape
-    B, _, HK, dk, page, pages, width = sizes = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
-    if dk != d or HK < 1 or HQ % HK:
-        raise ValueError(f"q [total, H, d] needs d = {dk} and H a multiple of {HK}, got {list(q.shape)}")
-    max_q = int(max_seqlen_q) if max_seqlen_q is not None else (1 if cu_seqlens is None else total)
-    max_kv = int(max_kv_len) if max_kv_len is not None else page * width
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    if out is None:
-        o, lse = torch.empty((total, HQ, d), dtype=q.dtype, device=dev), None
-    else:
-        o, lse = out
-        if _rows("out[0]", o, 3, q.dtype, dev).shape != q.shape:
-            raise ValueError(f"out[0] must be {list(q.shape)}, got {list(o.shape)}")
+    dev, dtype = k_cache.device, k_cache.dtype
+    if k_cache.is_cuda and dev.index != torch.cuda.current_device():
+        return _on_device(streamkl_paged_attn, dev, dict(
+            q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
+            max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, causal=causal, num_splits=num_splits,
+            out=out, workspace=workspace, dev_status=dev_status, stream=stream))
+    qs = _rows("q", q, 3, dtype, dev)
+    shape = q.shape
+    total, HQ, d = shape
+    B, HK, dim, page, pages, width, table_stride, strides, table, lens, cu = _cache(
+        k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
+    if dim != d or HK < 1 or HQ % HK:
+        raise ValueError(f"q [total, H, d] needs d = {dim} and H a multiple of {HK}, got {list(shape)}")
+    max_q = (total if cu else 1) if max_seqlen_q is None else max_seqlen_q
+    max_kv = page * width if max_kv_len is None else max_kv_len
+    o, lse = (None, None) if out is None else out
+    if o is None:
+        o = torch.empty(shape, dtype=dtype, device=dev)
+    os = _rows("out[0]", o, 3, dtype, dev)
+    if o.shape != shape:
+        raise ValueError(f"out[0] must be {list(shape)}, got {list(o.shape)}")
     if lse is None:
         lse = torch.empty((total, HQ), dtype=torch.float32, device=dev)
     elif lse.shape != (total, HQ) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError(f"out[1] must be contiguous fp32 [{total}, {HQ}] on {dev}")
     status = _status(dev_status, dev)
-    if q.numel() == 0:
+    if total == 0 or HQ == 0:
         return o, lse
     lib = load()
-    strides = _strides(*k_cache.stride()[:3], *v_cache.stride()[:3], *q.stride()[:2], *o.stride()[:2])
-    with _guard(dev):
-        need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, int(num_splits))
-        ws = _workspace(need, dev, workspace)
-        st = lib.streamkl_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                     block_table.stride(0), kv_lens.data_ptr(), _ptr(cu_seqlens), _DTYPES[q.dtype],
-                                     B, total, HQ, *sizes[2:], strides, max_q, max_kv, scale, int(bool(causal)),
-                                     int(num_splits), o.data_ptr(), lse.data_ptr(), _ptr(ws), need,
-                                     status.data_ptr(), _stream(stream, dev))
+    need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+    ws = _workspace(need, dev, workspace)
+    st = lib.streamkl_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, table_stride, lens, cu,
+                                 _DTYPES[dtype], B, total, HQ, HK, d, page, pages, width,
+                                 _pack10(*strides, qs[0], qs[1], os[0], os[1]), max_q, max_kv,
+                                 1.0 / math.sqrt(d) if scale is None else scale, bool(causal), num_splits,
+                                 o.data_ptr(), lse.data_ptr(), ws.data_ptr() if need else 0, need, status.data_ptr(),
+                                 _stream(stream, dev))
     if st:
         _check(st, "streamkl_paged_attn")
     return o, lse
