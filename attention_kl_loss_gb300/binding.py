@@ -35,7 +35,6 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
-_L = ctypes.c_longlong
 
 _SIGNATURES = {
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
@@ -68,18 +67,13 @@ _SIGNATURES = {
                                  _P, _P, _P, _P, _P]),
     "streamkl_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
                                  _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
-    "streamkl_qk_norm_rope_fwd": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P,
-                                       _L, _P, _L, _P, _P, _F, _I, _I, _P, _P, _P, _P]),
+    "streamkl_qk_norm_rope_fwd": (_I, [_P, _P]),
     "streamkl_qk_norm_rope_bwd_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
-    "streamkl_qk_norm_rope_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
-                                       _I, _P, _L, _P, _L, _P, _P, _F, _I, _I, _P, _P, _P, _P, _P,
-                                       _Z, _P, _P]),
-    "streamkl_paged_append": (_I, [_P, _P, _P, _P, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
-                                   _P, _I, _P, _P, _I, _P, _F, _I, _P, _P]),
+    "streamkl_qk_norm_rope_bwd": (_I, [_P, _P]),
+    "streamkl_paged_append": (_I, [_P, _P]),
     "streamkl_paged_attn_splits": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
-    "streamkl_paged_attn": (_I, [_P, _P, _P, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
-                                 _P, _I, _I, _F, _I, _I, _P, _P, _P, _Z, _P, _P]),
+    "streamkl_paged_attn": (_I, [_P, _P]),
 }
 
 

@@ -97,9 +97,9 @@ struct PagedAttnArgs {
 // Blocks of the backward's persistent grid (its partials' row count).
 int rope_bwd_blocks(int B, int NQ, int HQ, int NK, int HK, int d, int sms);
 
-cudaError_t launch_rope_fwd(RopeArgs& a, cudaStream_t stream);
-cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, float* dw_q, float* dw_k, cudaStream_t stream);
-cudaError_t launch_append(AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_fwd(RopeArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, int sms, float* dw_q, float* dw_k, cudaStream_t stream);
+cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 
 }  // namespace skl

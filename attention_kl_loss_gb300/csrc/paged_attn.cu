@@ -24,6 +24,7 @@
 // are what costs; S is then double-buffered. Few rows against many keys are
 // split over the keys; a combine kernel joins the splits by their lse.
 #include <algorithm>
+#include <atomic>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     }
   }
 
+  if (a.splits > 1) grid_launch_dependents();  // the combine kernel may be launched
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -506,6 +508,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
 template <int TYPE, int D>
 __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
+  grid_dependency_wait();  // launched while the attention kernel ends
   const int lane = threadIdx.x & 31;
   const long long e = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const long long rows = static_cast<long long>(a.T) * a.HQ;
@@ -518,13 +521,32 @@ __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __gri
   for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
   const float t0 = top == -INFINITY ? 0.f : top;
   float total = 0.f, o[V] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float wgt = ex2(a.part_lse[s * rows + e] - t0);
-    if (wgt == 0.f) continue;  // (the partial of an empty range is not written)
-    total += wgt;
-    const float* p = a.part_o + (s * rows + e) * D + lane * V;
+  for (int s0 = 0; s0 < a.splits; s0 += 32) {
+    const float mine = s0 + lane < a.splits ? ex2(a.part_lse[(s0 + lane) * rows + e] - t0) : 0.f;
+    const int end_s = min(32, a.splits - s0);
+    for (int s1 = 0; s1 < end_s; s1 += 8) {  // 8 splits' loads in flight
+      float w[8], p[8][V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = fmaf(wgt, p[k], o[k]);
+      for (int i = 0; i < 8; ++i) {
+        w[i] = __shfl_sync(0xFFFFFFFFu, mine, s1 + i);  // 0 past the last split
+        if (w[i] != 0.f) {  // (the partial of an empty range is not written)
+          const float* src = a.part_o + ((s0 + s1 + i) * rows + e) * D + lane * V;
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(p[i]) = *reinterpret_cast<const float2*>(src);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) p[i][k] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        total += w[i];
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = fmaf(w[i], p[i][k], o[k]);
+      }
+    }
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
@@ -537,14 +559,31 @@ template <int TYPE, int D, int NT>
 cudaError_t attn_t(const PagedAttnArgs& a, cudaStream_t stream) {
   using L = AttnLayout<D, NT>;
   auto kern = streamkl_paged_attn_kernel<TYPE, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  // the shared-memory attribute, once per device
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
   kern<<<dim3(a.q_tiles, a.splits, a.B * a.HK), L::THREADS, L::ALLOC, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   const long long rows = static_cast<long long>(a.T) * a.HQ;
-  streamkl_paged_combine_kernel<TYPE, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, streamkl_paged_combine_kernel<TYPE, D>, a);
 }
 
 template <int TYPE, int D>

@@ -23,8 +23,13 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 # whose kernel takes 3)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_pack10, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (10, 12, 18))
-_NONE = (0, 0, 0)
+_NONE = (0, 0, 0, 0)
+
+# The argument structs of the C ABI, field by field (native alignment)
+_ROWS = "Pqqq"
+_ROPE = struct.Struct("N" + 6 * _ROWS + "PPPqPqPPPPPNP11if")
+_APPEND = struct.Struct("N" + 4 * _ROWS + "PqPPPPPP11if")
+_ATTN = struct.Struct("N" + 4 * _ROWS + "PqPPPPNP13if")
 
 
 def _on_device(call, device, kwargs):
@@ -118,15 +123,15 @@ def _rope_sizes(q, k, positions, k_positions, k_repeat):
 
 
 def _rope_side(name, t, x, packed, pos, weight, repeat):
-    """Checks of q or k: (B, N, H, d, strides, shape of the outer rows,
+    """Checks of q or k: (B, N, H, d, its rows, shape of the outer rows,
     positions and their batch stride, weight)."""
     s = _rows(name, t, 3 if packed else 4, x.dtype, x.device)
     if packed:
         N, H, d = t.shape
-        B, inner, outer = 1, (0, s[0], s[1]), (N, H * repeat, d)
+        B, inner, outer = 1, (t.data_ptr(), 0, s[0], s[1]), (N, H * repeat, d)
     else:
         B, N, H, d = t.shape
-        inner, outer = s[:3], (B, H * repeat, N, d)
+        inner, outer = (t.data_ptr(), s[0], s[1], s[2]), (B, H * repeat, N, d)
     w = _vector("q_weight" if name == "q" else "k_weight", weight, d, torch.float32, x.device)
     at, stride = 0, 0
     if pos is not None:
@@ -143,11 +148,11 @@ def _rope_side(name, t, x, packed, pos, weight, repeat):
 
 
 def _rope_rows(name, t, shape, x, packed):
-    """Strides (batch, token, head) of an outer tensor."""
+    """Address and strides (batch, token, head) of an outer tensor."""
     s = _rows(name, t, len(shape), x.dtype, x.device)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return (0, s[0], s[1]) if packed else (s[0], s[2], s[1])
+    return (t.data_ptr(), 0, s[0], s[1]) if packed else (t.data_ptr(), s[0], s[2], s[1])
 
 
 def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, q_weight=None,
@@ -173,7 +178,7 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
             k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out, dev_status=dev_status,
             stream=stream))
     yq = yk = None
-    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = q_at = k_at = yq_at = yk_at = 0
+    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = 0
     iq = ik = oq = ok = _NONE
     if q is not None:
         B, NQ, HQ, d, iq, shape, pq, sq, wq = _rope_side("q", q, x, packed, q_pos, q_weight, 1)
@@ -181,7 +186,6 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
         if yq is None:
             yq = torch.empty(shape, dtype=dtype, device=dev)
         oq = _rope_rows("out[0]", yq, shape, x, packed)
-        q_at, yq_at = q.data_ptr(), yq.data_ptr()
     if k is not None:
         Bk, NK, HK, dk, ik, shape, pk, sk, wk = _rope_side("k", k, x, packed, k_pos, k_weight, k_repeat)
         if q is not None and (Bk != B or dk != d):
@@ -191,15 +195,14 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
         if yk is None:
             yk = torch.empty(shape, dtype=dtype, device=dev)
         ok = _rope_rows("out[1]", yk, shape, x, packed)
-        k_at, yk_at = k.data_ptr(), yk.data_ptr()
     length, rot = _tables(cos, sin, dev)
     status = _status(dev_status, dev)
     if B * (NQ * HQ + NK * HK) == 0:
         return yq, yk
-    st = load().streamkl_qk_norm_rope_fwd(q_at, k_at, _DTYPES[dtype], B, NQ, NK, HQ, HK, d, rot,
-                                          _pack12(*iq, *ik, *oq, *ok), cos.data_ptr(), sin.data_ptr(), length, pq, sq,
-                                          pk, sk, wq, wk, eps, bool(interleaved), k_repeat, yq_at, yk_at,
-                                          status.data_ptr(), _stream(stream, dev))
+    args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *_NONE, *_NONE, cos.data_ptr(), sin.data_ptr(), pq, sq, pk, sk,
+                      wq, wk, 0, 0, 0, 0, status.data_ptr(), _DTYPES[dtype], B, NQ, NK, HQ, HK, d, rot, length,
+                      bool(interleaved), k_repeat, eps)
+    st = load().streamkl_qk_norm_rope_fwd(args, _stream(stream, dev))
     if st:
         _check(st, "streamkl_qk_norm_rope_fwd")
     return yq, yk
@@ -226,8 +229,7 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
             q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out,
             workspace=workspace, dev_status=dev_status, stream=stream))
     dq = dk = dwq = dwk = None
-    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = 0
-    q_at = k_at = yq_at = yk_at = dq_at = dk_at = dwq_at = dwk_at = 0
+    B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = dwq_at = dwk_at = 0
     iq = ik = oq = ok = gq = gk = _NONE
     if q is not None:
         B, NQ, HQ, d, iq, shape, pq, sq, wq = _rope_side("q", q, x, packed, q_pos, q_weight, 1)
@@ -236,7 +238,6 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
         if dq is None:
             dq = torch.empty(q.shape, dtype=dtype, device=dev)
         gq = _rope_grad("out[0]", dq, q, packed)
-        q_at, yq_at, dq_at = q.data_ptr(), dq_out.data_ptr(), dq.data_ptr()
         if wq:
             dwq = torch.empty(d, dtype=torch.float32, device=dev)
             dwq_at = dwq.data_ptr()
@@ -250,7 +251,6 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
         if dk is None:
             dk = torch.empty(k.shape, dtype=dtype, device=dev)
         gk = _rope_grad("out[1]", dk, k, packed)
-        k_at, yk_at, dk_at = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
         if wk:
             dwk = torch.empty(d, dtype=torch.float32, device=dev)
             dwk_at = dwk.data_ptr()
@@ -264,28 +264,26 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     lib = load()
     need = lib.streamkl_qk_norm_rope_bwd_workspace_size(B, NQ, NK, HQ, HK, d) if wq or wk else 0
     ws = _workspace(need, dev, workspace)
-    st = lib.streamkl_qk_norm_rope_bwd(q_at, k_at, yq_at, yk_at, _DTYPES[dtype], B, NQ, NK, HQ, HK, d, rot,
-                                       _pack18(*iq, *ik, *oq, *ok, *gq, *gk), cos.data_ptr(), sin.data_ptr(), length,
-                                       pq, sq, pk, sk, wq, wk, eps, bool(interleaved), k_repeat, dq_at, dk_at, dwq_at,
-                                       dwk_at, ws.data_ptr() if need else 0, need, status.data_ptr(),
-                                       _stream(stream, dev))
+    args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *gq, *gk, cos.data_ptr(), sin.data_ptr(), pq, sq, pk, sk, wq, wk,
+                      dwq_at, dwk_at, ws.data_ptr() if need else 0, need, status.data_ptr(), _DTYPES[dtype], B, NQ, NK,
+                      HQ, HK, d, rot, length, bool(interleaved), k_repeat, eps)
+    st = lib.streamkl_qk_norm_rope_bwd(args, _stream(stream, dev))
     if st:
         _check(st, "streamkl_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
 def _rope_grad(name, t, x, packed):
-    """Strides (batch, token, head) of an output in the place of x."""
+    """Address and strides (batch, token, head) of an output in the place of x."""
     s = _rows(name, t, 3 if packed else 4, x.dtype, x.device)
     if t.shape != x.shape:
         raise ValueError(f"{name} must be {list(x.shape)}, got {list(t.shape)}")
-    return (0, s[0], s[1]) if packed else s[:3]
+    return (t.data_ptr(), 0, s[0], s[1]) if packed else (t.data_ptr(), s[0], s[1], s[2])
 
 
 def _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total):
-    """Checks of the paged cache: (B, HK, d, page size, pages, pages of a
-    sequence, stride of block_table, strides of the caches, addresses of
-    block_table, kv_lens, cu_seqlens)."""
+    """Checks of the paged cache: (HK, d, (page size, pages, pages of a
+    sequence), B, cu_seqlens given, the caches' and the tables' fields)."""
     dev, dtype = k_cache.device, k_cache.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"unsupported cache type {dtype} (bf16, fp16)")
@@ -307,7 +305,9 @@ def _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total):
     if cu_seqlens is None and total != B:
         raise ValueError(f"without cu_seqlens each of the {B} sequences has one token, got {total}")
     pages, heads, page, d = shape
-    return B, heads, d, page, pages, width, bs[0], ks[:3] + vs[:3], block_table.data_ptr(), lens, cu
+    return heads, d, (page, pages, width), B, cu != 0, (
+        k_cache.data_ptr(), ks[0], ks[1], ks[2], v_cache.data_ptr(), vs[0], vs[1], vs[2], block_table.data_ptr(), bs[0],
+        lens, cu)
 
 
 def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None,
@@ -331,8 +331,7 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     ks = _rows("k", k, 3, dtype, dev)
     vs = _rows("v", v, 3, dtype, dev)
     total, HK, d = k.shape
-    B, heads, dim, page, pages, width, table_stride, strides, table, lens, cu = _cache(
-        k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
+    heads, dim, pages, B, _, cache = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
     if k.shape != v.shape or HK != heads or d != dim:
         raise ValueError(f"k and v must both be [total, {heads}, {dim}]")
     if (cos is None) != (sin is None):
@@ -342,11 +341,10 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     status = _status(dev_status, dev)
     if total == 0 or HK == 0:
         return k_cache, v_cache
-    st = load().streamkl_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table,
-                                      table_stride, lens, cu, _DTYPES[dtype], B, total, HK, d, page, pages, width,
-                                      _pack10(*strides, ks[0], ks[1], vs[0], vs[1]), rot,
-                                      cos.data_ptr() if rot else 0, sin.data_ptr() if rot else 0, length, w, eps,
-                                      bool(interleaved), status.data_ptr(), _stream(stream, dev))
+    args = _APPEND.pack(_APPEND.size, k.data_ptr(), 0, ks[0], ks[1], v.data_ptr(), 0, vs[0], vs[1], *cache,
+                        cos.data_ptr() if rot else 0, sin.data_ptr() if rot else 0, w, status.data_ptr(),
+                        _DTYPES[dtype], B, total, HK, d, *pages, rot, length, bool(interleaved), eps)
+    st = load().streamkl_paged_append(args, _stream(stream, dev))
     if st:
         _check(st, "streamkl_paged_append")
     return k_cache, v_cache
@@ -384,12 +382,11 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     qs = _rows("q", q, 3, dtype, dev)
     shape = q.shape
     total, HQ, d = shape
-    B, HK, dim, page, pages, width, table_stride, strides, table, lens, cu = _cache(
-        k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
+    HK, dim, pages, B, offsets, cache = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total)
     if dim != d or HK < 1 or HQ % HK:
         raise ValueError(f"q [total, H, d] needs d = {dim} and H a multiple of {HK}, got {list(shape)}")
-    max_q = (total if cu else 1) if max_seqlen_q is None else max_seqlen_q
-    max_kv = page * width if max_kv_len is None else max_kv_len
+    max_q = (total if offsets else 1) if max_seqlen_q is None else max_seqlen_q
+    max_kv = pages[0] * pages[2] if max_kv_len is None else max_kv_len
     o, lse = (None, None) if out is None else out
     if o is None:
         o = torch.empty(shape, dtype=dtype, device=dev)
@@ -406,12 +403,11 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     lib = load()
     need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
     ws = _workspace(need, dev, workspace)
-    st = lib.streamkl_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, table_stride, lens, cu,
-                                 _DTYPES[dtype], B, total, HQ, HK, d, page, pages, width,
-                                 _pack10(*strides, qs[0], qs[1], os[0], os[1]), max_q, max_kv,
-                                 1.0 / math.sqrt(d) if scale is None else scale, bool(causal), num_splits,
-                                 o.data_ptr(), lse.data_ptr(), ws.data_ptr() if need else 0, need, status.data_ptr(),
-                                 _stream(stream, dev))
+    args = _ATTN.pack(_ATTN.size, q.data_ptr(), 0, qs[0], qs[1], o.data_ptr(), 0, os[0], os[1], *cache, lse.data_ptr(),
+                      ws.data_ptr() if need else 0, need, status.data_ptr(), _DTYPES[dtype], B, total, HQ, HK, d,
+                      *pages, max_q, max_kv, bool(causal), num_splits,
+                      1.0 / math.sqrt(d) if scale is None else scale)
+    st = lib.streamkl_paged_attn(args, _stream(stream, dev))
     if st:
         _check(st, "streamkl_paged_attn")
     return o, lse

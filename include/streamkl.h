@@ -337,16 +337,24 @@ streamkl_status streamkl_bwd_varlen(const void* q1, const void* k1, const void* 
  * what a trained student is run with (a paged key/value cache, its append and
  * the attention of new tokens over it). The paper has no counterpart. The
  * conventions above hold, with these additions:
+ * - Arguments come in one struct that lives on the host for the length of the
+ *   call; struct_size is its sizeof (a call with another size is refused).
  * - dtype is the element type of q, k, v, caches and outputs; sums, norms,
  *   softmax statistics and weights are fp32.
- * - strides is a HOST array of element strides; the last dimension (d) is
- *   contiguous, every stride and base a multiple of 16 bytes.
- * - Outputs must not overlap inputs.
+ * - A tensor of rows of d contiguous elements is its address and the element
+ *   strides of its other dimensions, address and strides multiples of 16
+ *   bytes (the stride of a dimension of one element is ignored).
+ * - Outputs must not overlap inputs, nor their own rows each other.
  * - Values that only the device knows (positions, lengths, page numbers) are
  *   checked by the kernels: a bad one sets STREAMKL_ERR_INVALID_ARG in
  *   *dev_status and is never used as an address.
  */
 typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamkl_dtype;
+
+typedef struct {
+  void* data; /* not written through for an input */
+  long long stride[3];
+} streamkl_rows;
 
 /*
  * Norm and rotation of queries and keys, one pass over both. Each row x (one
@@ -354,110 +362,117 @@ typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamk
  * R(p) turns the pairs of the first `rot` elements by the angles of position
  * p, (a, b) -> (a cos - b sin, b cos + a sin); pairs are (i, i + rot / 2), or
  * (2i, 2i + 1) with interleaved = 1.
- *   in : q [B, NQ, HQ, d], k [B, NK, HK, d] (either may be NULL to skip it);
- *        cos, sin fp32 [table_len, rot / 2]; rot a multiple of 16 up to d;
- *        q_positions, k_positions: device int32, token (b, n) at
- *        [b * pos_stride + n] (0: the same for each b); NULL: key n is at
- *        position n, query n at n + max(NK - NQ, 0) (needs NQ <= NK);
- *        q_weight, k_weight: fp32 [d], NULL for rotation without norm.
- *   out: q_out [B, HQ, NQ, d] and k_out [B, HK * k_repeat, NK, d], placed by
- *        their strides: head h of k stands k_repeat times, from h * k_repeat
- *        on, so that grouped heads give streamkl_fwd its equal head counts.
- *   strides: batch, token, head of q, k, q_out, k_out (12 values). A packed
- *        batch [total, H, d] is B = 1.
- * A row whose position lies outside the tables is reported and not written.
- * dtype: any of streamkl_dtype. d is 64 or 128.
- */
-streamkl_status streamkl_qk_norm_rope_fwd(const void* q, const void* k, int dtype, int B, int NQ, int NK, int HQ,
-                                          int HK, int d, int rot, const long long* strides, const float* cos,
-                                          const float* sin, int table_len, const int* q_positions,
-                                          long long q_pos_stride, const int* k_positions, long long k_pos_stride,
-                                          const float* q_weight, const float* k_weight, float eps, int interleaved,
-                                          int k_repeat, void* q_out, void* k_out, int* dev_status, void* stream);
-
-/*
- * Its backward: arguments as above, with the outer gradients dq_out, dk_out
- * in the place of the outputs (the gradients of a key head's repeats are
- * summed). dq, dk: gradients of q and k; dq_weight, dk_weight: fp32 [d],
- * written where the weight is given. strides: the 12 above (dq_out, dk_out
- * for q_out, k_out), then batch, token, head of dq and dk (18 values).
+ *   q [B, NQ, HQ, d], k [B, NK, HK, d] -> q_out [B, HQ, NQ, d],
+ *   k_out [B, HK * k_repeat, NK, d]: head h of k stands k_repeat times, from
+ *   h * k_repeat on, so that grouped heads give streamkl_fwd its equal head
+ *   counts. Strides of all: batch, token, head. A packed batch [total, H, d]
+ *   is B = 1. A row whose position lies outside the tables is reported and
+ *   not written. dtype: any; d is 64 or 128.
+ * Backward: q_out, k_out are the gradients of the outputs (those of a key
+ * head's repeats are summed), dq, dk and dq_weight, dk_weight are written.
  * workspace: ws_bytes >= streamkl_qk_norm_rope_bwd_workspace_size(...) (sizes
  * of an absent side 0; may be NULL without weights); no initialisation. The
  * weight gradients are summed in a fixed order: the same in every run. Rows
  * that the forward does not write get no gradient and add none.
  */
+typedef struct {
+  size_t struct_size;
+  streamkl_rows q, k;         /* data NULL skips q or k */
+  streamkl_rows q_out, k_out; /* forward: outputs; backward: their gradients */
+  streamkl_rows dq, dk;       /* backward only */
+  const float *cos, *sin;     /* [table_len, rot / 2] */
+  const int* q_positions;     /* device; token (b, n) at [b * q_pos_stride + n] (0: the same for each b);
+                                 NULL: query n at position n + max(NK - NQ, 0) (needs NQ <= NK) */
+  long long q_pos_stride;
+  const int* k_positions;     /* likewise; NULL: key n at position n */
+  long long k_pos_stride;
+  const float *q_weight, *k_weight; /* [d], 16-byte aligned; NULL: rotation without norm */
+  float *dq_weight, *dk_weight;     /* backward: [d], needed where the weight is given */
+  void* workspace;                  /* backward */
+  size_t ws_bytes;
+  int* dev_status;
+  int dtype, B, NQ, NK, HQ, HK, d;
+  int rot; /* a multiple of 16 up to d */
+  int table_len, interleaved, k_repeat;
+  float eps;
+} streamkl_rope_args;
+
+streamkl_status streamkl_qk_norm_rope_fwd(const streamkl_rope_args* args, void* stream);
 size_t streamkl_qk_norm_rope_bwd_workspace_size(int B, int NQ, int NK, int HQ, int HK, int d);
-streamkl_status streamkl_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
-                                          int dtype, int B, int NQ, int NK, int HQ, int HK, int d, int rot,
-                                          const long long* strides, const float* cos, const float* sin,
-                                          int table_len, const int* q_positions, long long q_pos_stride,
-                                          const int* k_positions, long long k_pos_stride, const float* q_weight,
-                                          const float* k_weight, float eps, int interleaved, int k_repeat, void* dq,
-                                          void* dk, float* dq_weight, float* dk_weight, void* workspace,
-                                          size_t ws_bytes, int* dev_status, void* stream);
+streamkl_status streamkl_qk_norm_rope_bwd(const streamkl_rope_args* args, void* stream);
 
 /*
  * Append new keys and values to a paged cache, the keys normed (k_weight) and
  * rotated (cos, sin) on the way as above; NULL leaves either out.
- *   in : k, v [T, HK, d], the new tokens of B sequences packed one after the
- *        other: cu_seqlens int32 [B + 1] on the device, tokens from
- *        cu_seqlens[B] on are padding and ignored; NULL: T = B, one token a
- *        sequence. kv_lens int32 [B]: length of each sequence with its new
- *        tokens, which stand at its end. block_table int32 [B, max_pages],
- *        rows table_stride apart: position p of sequence b lies in slot
- *        p % page_size of page block_table[b][p / page_size].
- *   in/out: k_cache, v_cache [num_pages, HK, page_size, d], placed by their
- *        strides; page_size a power of two from 16 to 1024. Only the new
- *        tokens' slots are written. Two tokens of one call must not share a
- *        slot (one of them would be left there, no more is said).
- *   strides: page, head, slot of k_cache and of v_cache, then token, head of
- *        k and of v (10 values).
- * A token with a bad position or page is reported and not written. dtype:
- * STREAMKL_BF16 or STREAMKL_FP16.
+ *   k, v [T, HK, d]: the new tokens of B sequences packed one after the other;
+ *   those from cu_seqlens[B] on are padding and ignored. Position p of
+ *   sequence b lies in slot p % page_size of page block_table[b][p / page_size]
+ *   of k_cache, v_cache [num_pages, HK, page_size, d]. Only the new tokens'
+ *   slots are written. Two tokens of one call must not share a slot (one of
+ *   them would be left there, no more is said). A token with a bad position
+ *   or page is reported and not written. dtype: STREAMKL_BF16 or STREAMKL_FP16.
  */
-streamkl_status streamkl_paged_append(const void* k, const void* v, void* k_cache, void* v_cache,
-                                      const int* block_table, long long table_stride, const int* kv_lens,
-                                      const int* cu_seqlens, int dtype, int B, int T, int HK, int d, int page_size,
-                                      int num_pages, int max_pages, const long long* strides, int rot,
-                                      const float* cos, const float* sin, int table_len, const float* k_weight,
-                                      float eps, int interleaved, int* dev_status, void* stream);
+typedef struct {
+  size_t struct_size;
+  streamkl_rows k, v;             /* strides: (unused), token, head */
+  streamkl_rows k_cache, v_cache; /* strides: page, head, slot */
+  const int* block_table;         /* device [B, max_pages], rows table_stride apart */
+  long long table_stride;
+  const int* kv_lens;             /* device [B]: length of each sequence with its new tokens, which end it */
+  const int* cu_seqlens;          /* device [B + 1]: first token of each sequence; NULL: T = B, one token each */
+  const float *cos, *sin;
+  const float* k_weight;
+  int* dev_status;
+  int dtype, B, T, HK, d;
+  int page_size; /* a power of two from 16 to 1024 */
+  int num_pages, max_pages, rot, table_len, interleaved;
+  float eps;
+} streamkl_append_args;
+
+streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* stream);
 
 /*
  * Attention of new tokens over a paged cache: row i of a sequence's n new
  * tokens gives o = softmax(scale q K^T) V over the keys it sees, all of the
  * sequence, or with causal = 1 those up to its own position (bottom-right
  * aligned as above: key j <= i + length - n).
- *   in : q [T, HQ, d] packed as k of streamkl_paged_append; caches,
- *        block_table, kv_lens, cu_seqlens as there (cu_seqlens NULL: T = B,
- *        one new token a sequence); HQ a multiple of HK, query head h reads
- *        key head h / (HQ / HK); max_seqlen_q, max_kv_len: upper bounds of
- *        the sequences' new tokens and lengths (they size the grid and the
- *        key split); num_splits: 0 = automatic, >= 1 forces that many key
- *        splits (clamped to the number of 128-key tiles).
- *   out: out [T, HQ, d] and lse [T, HQ] (fp32, contiguous, the log of the
- *        softmax's sum, as streamkl_fwd's). A row that sees no key (length 0,
- *        or causal with more new tokens than keys) gets zeros and -inf. Rows
- *        behind the last sequence are left as they were.
- *   strides: page, head, slot of k_cache and of v_cache, then token, head of
- *        q and of out (10 values).
- *   workspace: ws_bytes >= streamkl_paged_attn_workspace_size(...) of the
- *        same sizes and num_splits (may be NULL when that is 0); contents
- *        need no initialisation; calls that may overlap need one each.
+ *   q [T, HQ, d] packed as k of streamkl_paged_append; caches, block_table,
+ *   kv_lens, cu_seqlens as there; query head h reads key head h / (HQ / HK).
+ *   out [T, HQ, d] and lse [T, HQ] (fp32, contiguous, the log of the softmax's
+ *   sum, as streamkl_fwd's). A row that sees no key (length 0, or causal with
+ *   more new tokens than keys) gets zeros and -inf. Rows behind the last
+ *   sequence are left as they were.
+ * workspace: ws_bytes >= streamkl_paged_attn_workspace_size(...) of the same
+ * sizes and num_splits (may be NULL when that is 0); contents need no
+ * initialisation; calls that may overlap need one each.
  * Slots past a sequence's length and page numbers past its last page are
  * never used, whatever they hold. A value of V that is not finite reaches
  * every row whose key tile it lies in. Offsets or lengths out of range or
  * above their bounds, and bad page numbers, are reported in *dev_status.
  * Results are the same in every run for the same sizes.
  */
+typedef struct {
+  size_t struct_size;
+  streamkl_rows q, out;           /* strides: (unused), token, head */
+  streamkl_rows k_cache, v_cache; /* strides: page, head, slot */
+  const int* block_table;
+  long long table_stride;
+  const int *kv_lens, *cu_seqlens;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int* dev_status;
+  int dtype, B, T, HQ, HK, d, page_size, num_pages, max_pages;
+  int max_seqlen_q, max_kv_len; /* upper bounds of the sequences' new tokens and lengths (grid, key split) */
+  int causal;
+  int num_splits; /* 0: automatic; >= 1: that many key splits (clamped to the 128-key tiles) */
+  float scale;
+} streamkl_paged_attn_args;
+
 int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len);
 size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
                                           int num_splits);
-streamkl_status streamkl_paged_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                                    long long table_stride, const int* kv_lens, const int* cu_seqlens, int dtype,
-                                    int B, int T, int HQ, int HK, int d, int page_size, int num_pages, int max_pages,
-                                    const long long* strides, int max_seqlen_q, int max_kv_len, float scale,
-                                    int causal, int num_splits, void* out, float* lse, void* workspace,
-                                    size_t ws_bytes, int* dev_status, void* stream);
+streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* stream);
 
 /*
  * Self-test of the bounded-wait path: launches one tiny kernel that waits on

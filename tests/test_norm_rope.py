@@ -9,6 +9,8 @@ mean of u x 16 u, r^2 22 u, the last products and difference 4 u: (64 + R) u of
 the absolute form. Weight gradients: at most one fma for each row and 64 u
 more. Then one rounding to the type, half a step: eps / 2 of the value, and
 for fp16 half of the smallest subnormal, 2^-25."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -328,33 +330,76 @@ def lib():
     return binding.load()
 
 
-def _raw_fwd(lib, **over):
-    """The C call with host-side arguments only: a refused call never uses its pointers."""
-    a = dict(q=4096, k=8192, dtype=0, B=1, NQ=4, NK=4, HQ=2, HK=2, d=64, rot=64, strides=None, cos=4096, sin=4096,
-             table=4, qp=None, qps=0, kp=None, kps=0, wq=None, wk=None, eps=1e-6, inter=0, rep=1, qo=4096, ko=4096,
-             st=4096)
-    strides = over.pop("strides_values", [512, 128, 64] * 4)
-    a.update(over)
-    import ctypes
-    if a["strides"] is None:
-        a["strides"] = (ctypes.c_longlong * 12)(*strides)
-    return lib.streamkl_qk_norm_rope_fwd(*[a[n] for n in (
-        "q", "k", "dtype", "B", "NQ", "NK", "HQ", "HK", "d", "rot", "strides", "cos", "sin", "table", "qp", "qps",
-        "kp", "kps", "wq", "wk", "eps", "inter", "rep", "qo", "ko", "st")], None)
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong * 3)]
+
+
+class RopeArgs(ctypes.Structure):
+    """streamkl_rope_args of the header."""
+    _fields_ = ([("struct_size", ctypes.c_size_t)] + [(n, Rows) for n in ("q", "k", "q_out", "k_out", "dq", "dk")]
+                + [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("q_positions", ctypes.c_void_p),
+                   ("q_pos_stride", ctypes.c_longlong), ("k_positions", ctypes.c_void_p),
+                   ("k_pos_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "dq_weight", "dk_weight", "workspace")]
+                + [("ws_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
+                + [(n, ctypes.c_int) for n in ("dtype", "B", "NQ", "NK", "HQ", "HK", "d", "rot", "table_len",
+                                               "interleaved", "k_repeat")] + [("eps", ctypes.c_float)])
+
+
+def _raw_args(**over):
+    """Arguments that only the host looks at: a refused call never uses its addresses."""
+    a = RopeArgs(ctypes.sizeof(RopeArgs), cos=4096, sin=4096, dev_status=4096, B=2, NQ=4, NK=4, HQ=2, HK=2, d=64, rot=64,
+                 table_len=4, k_repeat=1, eps=1e-6)
+    for n in ("q", "k", "q_out", "k_out", "dq", "dk"):
+        setattr(a, n, Rows(4096, (512, 128, 64)))
+    for n, v in over.items():
+        rows, _, field = n.partition("__")
+        if not field:
+            setattr(a, n, v)
+        elif field == "data":
+            getattr(a, rows).data = v
+        else:
+            getattr(a, rows).stride[:] = v
+    return a
+
+
+REFUSED = [
+    (dict(struct_size=8), 1), (dict(q__data=None, k__data=None), 1), (dict(dtype=3), 2), (dict(d=96), 2),
+    (dict(rot=0), 2), (dict(rot=80), 2), (dict(rot=24), 2), (dict(cos=None), 1), (dict(sin=4100), 1),
+    (dict(table_len=0), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
+    (dict(interleaved=2), 1), (dict(B=0), 1), (dict(NQ=0), 1), (dict(HK=0), 1), (dict(k_repeat=0), 1),
+    (dict(NQ=1 << 30, NK=1 << 30, HQ=4), 2), (dict(NQ=5), 1), (dict(dev_status=None), 1), (dict(q__data=4104), 1),
+    (dict(k__data=8193), 1), (dict(q_out__data=None), 1), (dict(k_out__data=4100), 1),
+    (dict(q__stride=(512, 128, 60)), 1), (dict(k_out__stride=(512, -128, 64)), 1), (dict(q_weight=4100), 1),
+    (dict(q_out__stride=(512, 128, 0)), 1), (dict(k_out__stride=(0, 128, 64)), 1),
+]
+
+
+@pytest.mark.parametrize("over,status", REFUSED)
+def test_c_call_refuses(lib, over, status):
+    if "k_out__stride" in over and over["k_out__stride"][0] == 0 or over.get("q_out__stride"):
+        backward = []  # there these are inputs, which may repeat rows
+    else:
+        backward = [lib.streamkl_qk_norm_rope_bwd]
+    for call in [lib.streamkl_qk_norm_rope_fwd] + backward:
+        assert call(ctypes.byref(_raw_args(**over)), None) == status
+        assert lib.streamkl_last_error()
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(q=None, k=None), 1), (dict(dtype=3), 2), (dict(d=96), 2), (dict(rot=0), 2), (dict(rot=80), 2),
-    (dict(rot=24), 2), (dict(cos=None), 1), (dict(sin=4100), 1), (dict(table=0), 1), (dict(eps=-1.0), 1),
-    (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(inter=2), 1), (dict(B=0), 1), (dict(NQ=0), 1),
-    (dict(HK=0), 1), (dict(rep=0), 1), (dict(NQ=1 << 30, NK=1 << 30, HQ=4), 2), (dict(NQ=5), 1), (dict(st=None), 1),
-    (dict(q=4104), 1), (dict(k=8193), 1), (dict(qo=None), 1), (dict(ko=4100), 1),
-    (dict(strides_values=[512, 128, 60] + [512, 128, 64] * 3), 1),
-    (dict(strides_values=[512, 128, 64] * 3 + [512, -128, 64]), 1),
+    (dict(dq__data=None), 1), (dict(dk__stride=(512, 0, 64)), 1), (dict(q_weight=4096), 1),
+    (dict(q_weight=4096, dq_weight=4096), 1), (dict(k_weight=4096, dk_weight=4096, workspace=4100, ws_bytes=1 << 20), 1),
+    (dict(k_weight=4096, dk_weight=4096, workspace=4096, ws_bytes=16), 1),
 ])
-def test_c_call_refuses(lib, over, status):
-    assert _raw_fwd(lib, **over) == status
+def test_c_backward_refuses(lib, over, status):
+    assert lib.streamkl_qk_norm_rope_bwd(ctypes.byref(_raw_args(**over)), None) == status
     assert lib.streamkl_last_error()
+
+
+def test_no_arguments_are_refused(lib):
+    for call in (lib.streamkl_qk_norm_rope_fwd, lib.streamkl_qk_norm_rope_bwd, lib.streamkl_paged_append,
+                 lib.streamkl_paged_attn):
+        assert call(None, None) == 1
 
 
 def test_workspace_size_on_the_host(lib):

@@ -511,29 +511,70 @@ def lib():
     return binding.load()
 
 
-APPEND = dict(k=4096, v=4096, kc=4096, vc=4096, table=4096, ts=4, lens=4096, cu=4096, dtype=0, B=2, T=5, HK=2, d=64,
-              page=16, pages=9, most=4, strides=[2048, 1024, 64] * 2 + [128, 64] * 2, rot=64, cos=4096, sin=4096, len=64,
-              w=None, eps=1e-6, inter=0, st=4096)
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong * 3)]
 
 
-@pytest.mark.parametrize("over,status", [
-    (dict(dtype=2), 2), (dict(d=80), 2), (dict(B=0), 1), (dict(T=0), 1), (dict(HK=0), 1), (dict(pages=0), 1),
-    (dict(page=8), 2), (dict(page=48), 2), (dict(page=2048), 2), (dict(most=1 << 27), 2), (dict(ts=3), 1),
-    (dict(table=None), 1), (dict(lens=None), 1), (dict(cu=None), 1), (dict(k=4104), 1), (dict(v=None), 1),
-    (dict(kc=None), 1), (dict(vc=4100), 1), (dict(strides=[2048, 1024, 60] + [2048, 1024, 64] + [128, 64] * 2), 1),
-    (dict(strides=[2048, 1024, 0] + [2048, 1024, 64] + [128, 64] * 2), 1),
-    (dict(strides=[2048, 1024, 64] * 2 + [-128, 64] * 2), 1), (dict(cos=None), 1), (dict(rot=8), 2), (dict(rot=72), 2),
-    (dict(len=0), 1), (dict(eps=-1.0), 1), (dict(eps=-1.0, cos=None, sin=None), 1), (dict(inter=2), 1), (dict(st=None), 1),
-    (dict(T=1 << 30, HK=4), 2), (dict(strides=None), 1),
+_TABLES = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("kv_lens", ctypes.c_void_p),
+           ("cu_seqlens", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    """streamkl_append_args of the header."""
+    _fields_ = ([("struct_size", ctypes.c_size_t)] + [(n, Rows) for n in ("k", "v", "k_cache", "v_cache")] + _TABLES
+                + [(n, ctypes.c_void_p) for n in ("cos", "sin", "k_weight", "dev_status")]
+                + [(n, ctypes.c_int) for n in ("dtype", "B", "T", "HK", "d", "page_size", "num_pages", "max_pages", "rot",
+                                               "table_len", "interleaved")] + [("eps", ctypes.c_float)])
+
+
+class AttnArgs(ctypes.Structure):
+    """streamkl_paged_attn_args of the header."""
+    _fields_ = ([("struct_size", ctypes.c_size_t)] + [(n, Rows) for n in ("q", "out", "k_cache", "v_cache")] + _TABLES
+                + [(n, ctypes.c_void_p) for n in ("lse", "workspace")] + [("ws_bytes", ctypes.c_size_t),
+                                                                          ("dev_status", ctypes.c_void_p)]
+                + [(n, ctypes.c_int) for n in ("dtype", "B", "T", "HQ", "HK", "d", "page_size", "num_pages", "max_pages",
+                                               "max_seqlen_q", "max_kv_len", "causal", "num_splits")]
+                + [("scale", ctypes.c_float)])
+
+
+def _raw(cls, over, **base):
+    """Arguments that only the host looks at: a refused call never uses its addresses."""
+    a = cls(ctypes.sizeof(cls), block_table=4096, table_stride=4, kv_lens=4096, cu_seqlens=4096, dev_status=4096, B=2,
+            T=5, HK=2, d=64, page_size=16, num_pages=9, max_pages=4, **base)
+    for n, s in (("k_cache", (2048, 1024, 64)), ("v_cache", (2048, 1024, 64)), ("k", (0, 128, 64)), ("v", (0, 128, 64)),
+                 ("q", (0, 256, 64)), ("out", (0, 256, 64))):
+        if hasattr(a, n):
+            setattr(a, n, Rows(4096, s))
+    for n, v in over.items():
+        rows, _, field = n.partition("__")
+        if not field:
+            setattr(a, n, v)
+        elif field == "data":
+            getattr(a, rows).data = v
+        else:
+            getattr(a, rows).stride[:] = v
+    return ctypes.byref(a)
+
+
+CACHE_REFUSED = [
+    (dict(struct_size=8), 1), (dict(dtype=2), 2), (dict(d=80), 2), (dict(B=0), 1), (dict(T=0), 1), (dict(HK=0), 1),
+    (dict(num_pages=0), 1), (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=2048), 2),
+    (dict(max_pages=1 << 27), 2), (dict(table_stride=3), 1), (dict(block_table=None), 1), (dict(kv_lens=None), 1),
+    (dict(cu_seqlens=None), 1), (dict(k_cache__data=None), 1), (dict(v_cache__data=4100), 1),
+    (dict(k_cache__stride=(2048, 1024, 60)), 1), (dict(k_cache__stride=(2048, 1024, 0)), 1),
+    (dict(v_cache__stride=(0, 1024, 64)), 1), (dict(dev_status=None), 1),
+]
+
+
+@pytest.mark.parametrize("over,status", CACHE_REFUSED + [
+    (dict(k__data=4104), 1), (dict(v__data=None), 1), (dict(k__stride=(0, -128, 64)), 1), (dict(cos=None), 1),
+    (dict(rot=8), 2), (dict(rot=72), 2), (dict(table_len=0), 1), (dict(eps=-1.0), 1),
+    (dict(eps=-1.0, cos=None, sin=None), 1), (dict(interleaved=2), 1), (dict(T=1 << 30, HK=4), 2),
+    (dict(k_weight=4104), 1),
 ])
 def test_append_c_call_refuses(lib, over, status):
-    a = {**APPEND, **over}
-    if a["strides"] is not None:
-        a["strides"] = (ctypes.c_longlong * 10)(*a["strides"])
-    got = lib.streamkl_paged_append(*[a[n] for n in ("k", "v", "kc", "vc", "table", "ts", "lens", "cu", "dtype", "B", "T",
-                                                     "HK", "d", "page", "pages", "most", "strides", "rot", "cos", "sin",
-                                                     "len", "w", "eps", "inter", "st")], None)
-    assert got == status and lib.streamkl_last_error()
+    a = _raw(AppendArgs, over, cos=4096, sin=4096, rot=64, table_len=64, eps=1e-6)
+    assert lib.streamkl_paged_append(a, None) == status and lib.streamkl_last_error()
 
 
 @pytest.mark.gpu
@@ -559,27 +600,18 @@ def test_append_python_call_refuses():
             call(*args, **kw)
 
 
-ATTN_C = dict(q=4096, kc=4096, vc=4096, table=4096, ts=4, lens=4096, cu=4096, dtype=0, B=2, T=5, HQ=4, HK=2, d=64,
-              page=16, pages=9, most=4, strides=[2048, 1024, 64] * 2 + [256, 64] * 2, mq=4, mk=64, scale=0.1, causal=1,
-              splits=1, out=4096, lse=4096, ws=None, wsb=0, st=4096)
-
-
-@pytest.mark.parametrize("over,status", [
-    (dict(dtype=2), 2), (dict(d=80), 2), (dict(B=0), 1), (dict(T=0), 1), (dict(HQ=0), 1), (dict(HQ=3), 1),
-    (dict(mq=0), 1), (dict(mq=6), 1), (dict(mk=-1), 1), (dict(mk=65), 1), (dict(cu=None), 1), (dict(q=4104), 1),
-    (dict(out=None), 1), (dict(out=4104), 1), (dict(lse=None), 1), (dict(causal=2), 1), (dict(splits=-1), 1),
-    (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(st=None), 1), (dict(page=24), 2),
-    (dict(strides=[2048, 1024, 64] * 2 + [256, 60] + [256, 64]), 1), (dict(strides=None), 1),
-    (dict(B=40000, HK=2, T=40000, cu=None, mq=1), 2), (dict(splits=2, most=40, ts=40, mk=640), 1),
+@pytest.mark.parametrize("over,status", CACHE_REFUSED + [
+    (dict(HQ=0), 1), (dict(HQ=3), 1), (dict(max_seqlen_q=0), 1), (dict(max_seqlen_q=6), 1), (dict(max_kv_len=-1), 1),
+    (dict(max_kv_len=65), 1), (dict(q__data=4104), 1), (dict(out__data=None), 1), (dict(out__data=4104), 1),
+    (dict(lse=None), 1), (dict(causal=2), 1), (dict(num_splits=-1), 1), (dict(scale=0.0), 1),
+    (dict(scale=float("inf")), 1), (dict(q__stride=(0, 256, 60)), 1), (dict(out__stride=(0, 256, 0)), 1),
+    (dict(B=40000, T=40000, cu_seqlens=None, max_seqlen_q=1), 2),
+    (dict(num_splits=2, max_pages=40, table_stride=40, max_kv_len=640), 1),
+    (dict(num_splits=2, max_pages=40, table_stride=40, max_kv_len=640, workspace=4100, ws_bytes=1 << 20), 1),
 ])
 def test_attention_c_call_refuses(lib, over, status):
-    a = {**ATTN_C, **over}
-    if a["strides"] is not None:
-        a["strides"] = (ctypes.c_longlong * 10)(*a["strides"])
-    got = lib.streamkl_paged_attn(*[a[n] for n in ("q", "kc", "vc", "table", "ts", "lens", "cu", "dtype", "B", "T", "HQ",
-                                                   "HK", "d", "page", "pages", "most", "strides", "mq", "mk", "scale",
-                                                   "causal", "splits", "out", "lse", "ws", "wsb", "st")], None)
-    assert got == status and lib.streamkl_last_error()
+    a = _raw(AttnArgs, over, HQ=4, max_seqlen_q=4, max_kv_len=64, scale=0.1, causal=1, num_splits=1, lse=4096)
+    assert lib.streamkl_paged_attn(a, None) == status and lib.streamkl_last_error()
 
 
 def test_attention_splits_on_the_host(lib):
