@@ -25,6 +25,7 @@
 // split over the keys; a combine kernel joins the splits by their lse.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -51,7 +52,7 @@ struct AttnLayout {
   static constexpr int NBAR = 2 + 2 * STAGES + 6 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
-  static constexpr int ALLOC = BYTES + 1024;
+  static constexpr int ALLOC = BYTES;  // (the base is declared 1024-byte aligned)
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int THREADS = 128 + 128 * NT;
   static constexpr int COL_O = 256;
@@ -120,10 +121,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
                                const __grid_constant__ CUtensorMap tm_v,
                                const __grid_constant__ PagedAttnArgs a) {
   using L = AttnLayout<D, NT>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sb = (raw + 1023u) & ~1023u;
-  uint8_t* gb = smem_raw + (sb - raw);
+  extern __shared__ __align__(1024) uint8_t gb[];
+  const uint32_t sb = smem_u32(gb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.HQ / a.HK;
   const int b = static_cast<int>(blockIdx.z) / a.HK, hk = static_cast<int>(blockIdx.z) - b * a.HK;
@@ -136,6 +135,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     return;
   }
 
+  // row tiles of this CTA that have rows
+  const int nt = (NT == 2 && w.rows - w.row0 > kTileM) ? 2 : 1;
   const uint32_t bar0 = sb + L::OFF_BAR;
   const uint32_t q_full = bar0, v_fixed = bar0 + 8;
   auto kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
               abort_flag, a.dev_status};
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    bool lay_ok = true;
+    bool lay_ok = (sb & 1023u) == 0;  // the swizzled tiles' alignment
+    if (!lay_ok) atomicCAS(a.dev_status, 0, kStatusDeviceCheck);
     if (kDeviceChecks)
       for (int i = 0; i < L::NBAR; ++i) lay_ok = lay_ok && check_bar(ck, bar0 + 8u * i, __LINE__);
     if (lay_ok) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       mbar_init(v_fixed, 1);
       for (int s = 0; s < L::STAGES; ++s) {
         mbar_init(kv_full(s), 1);
-        mbar_init(kv_empty(s), 1);
+        mbar_init(kv_empty(s), NT == 2 ? nt : 1);
       }
       for (int k = 0; k < 2; ++k) {
         mbar_init(s_full(k), 1);
@@ -190,8 +192,6 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   ck.tmem_cols = 512;
   const WaitCtx wc{abort_flag, a.dev_status, a.timeout_ns};
   const int n_iter = *skip_flag ? 0 : w.n_iter;
-  // row tiles of this CTA that have rows
-  const int nt = (NT == 2 && w.rows - w.row0 > kTileM) ? 2 : 1;
   // keys of the last tile that are there; the rest of its V rows are cleared
   const int last_valid = min(kTileN, w.klim - (w.t0 + w.n_iter - 1) * kTileN);
 
@@ -200,6 +200,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   auto idx_k = [&](int j) { return NT == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
   auto idx_v = [&](int j) { return NT == 2 ? 2 * j + 1 : (j + 1 < w.n_iter ? 2 * j + 2 : 2 * j + 1); };
 
+  if (warp < 4) {
+  // NT = 2: 128 threads with 88 registers and 256 with 208 make up the launch's
+  // 384 x 168; a softmax thread holds a row of S (128)
+  if (NT == 2) regs_dec<88>();
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     const int page = 1 << a.page_shift;
@@ -274,87 +278,96 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
+    // One thread issues every product, so its own instructions count: the
+    // descriptors are a constant high word and a running low word, the loads
+    // are consumed in the order of their ring, and the stages are released by
+    // the softmax warps (a commit for each would hold the issuer up).
     if (lane == 0 && n_iter > 0) {
       constexpr uint32_t id_s = TYPE == kTypeBf16 ? idesc_bf16(kTileM, kTileN, 0, 0) : idesc_f16(kTileM, kTileN, 0, 0);
       constexpr uint32_t id_o = TYPE == kTypeBf16 ? idesc_bf16(kTileM, D, 0, 1) : idesc_f16(kTileM, D, 0, 1);
-      auto stage = [&](int i) { return sb + L::OFF_KV + (i % L::STAGES) * L::TILE; };
-      auto full = [&](int i) { return wait_bounded(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc); };
-      auto mma_s = [&](int t, int col, int j) {  // S = Q_t K_j^T
-        const uint32_t q = sb + L::OFF_Q + t * L::TILE, k = stage(idx_k(j));
+      const uint64_t q0 = smem_desc_sw128(sb + L::OFF_Q, 16, 1024);
+      const uint64_t k0 = smem_desc_sw128(sb + L::OFF_KV, 16, 1024), v0 = smem_desc_sw128(sb + L::OFF_KV, L::BOX, 1024);
+      const uint32_t hi = static_cast<uint32_t>(k0 >> 32);  // the same in all three
+      const uint32_t q_lo = static_cast<uint32_t>(q0), k_lo = static_cast<uint32_t>(k0), v_lo = static_cast<uint32_t>(v0);
+      auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
+      int stage = 0;        // next stage of the ring to be waited for
+      uint32_t phase = 0;
+      auto next_full = [&](uint32_t& at) {  // ... once it has landed, its offset in descriptor units
+        const bool got = wait_bounded(kv_full(stage), phase, wc);
+        at = static_cast<uint32_t>(stage) * (L::TILE >> 4);
+        if (++stage == L::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+        return got;
+      };
+      auto mma_s = [&](uint32_t q, uint32_t k, uint32_t col) {  // S = Q_t K_j^T
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * L::BOX + (i & 3) * 32;
-          mma_bf16(tmem + col, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), id_s, i > 0);
+          const uint32_t off = ((i >> 2) * L::BOX + (i & 3) * 32) >> 4;
+          mma_bf16(tmem + col, desc(q + off), desc(k + off), id_s, i > 0);
         }
       };
-      auto mma_o = [&](int t, int col, int j) {  // O_t += P V_j
-        const uint32_t v = stage(idx_v(j));
+      auto mma_o = [&](uint32_t v, uint32_t col_p, uint32_t col_o, uint32_t add) {  // O_t += P V_j
 #pragma unroll
         for (int i = 0; i < kTileN / 16; ++i)
-          mma_bf16_ts(tmem + L::COL_O + t * D, tmem + col + 8 * i, smem_desc_sw128(v + i * 2048, L::BOX, 1024),
-                      id_o, j > 0 || i > 0);
+          mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * i, desc(v + i * (2048 >> 4)), id_o, i > 0 ? 1 : add);
       };
-      auto v_ready = [&](int j) {
-        return full(idx_v(j)) && (j + 1 < n_iter || last_valid == kTileN || wait_bounded(v_fixed, 0, wc));
-      };
-      bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && full(idx_k(0));
+      uint32_t k_at = 0, v_at = 0;
+      bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && next_full(k_at);
       tc_fence_after();
-      if (NT == 2) {
-        if (ok) {
-          for (int t = 0; t < nt; ++t) {
-            mma_s(t, t * 128, 0);
-            mma_commit(s_full(t));
-          }
-          mma_commit(kv_empty(idx_k(0) % L::STAGES));
+      if (ok) {
+        mma_s(q_lo, k_lo + k_at, 0);
+        mma_commit(s_full(0));
+        if (nt == 2) {
+          mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, 128);
+          mma_commit(s_full(1));
         }
-        for (int j = 0; ok && j < n_iter; ++j) {
-          const bool more = j + 1 < n_iter;
-          if (!(ok = v_ready(j))) break;
-          for (int t = 0; ok && t < nt; ++t) {
-            if (!(ok = wait_bounded(p_full(t), j & 1, wc))) break;
-            if (t == 0 && more && !(ok = full(idx_k(j + 1)))) break;
+      }
+      // the last tile's V has its rows past the last key cleared first
+      auto v_ready = [&](bool more) {
+        return next_full(v_at) && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc));
+      };
+#pragma unroll 1
+      for (int j = 0; ok && j < n_iter; ++j) {
+        const bool more = j + 1 < n_iter;
+        if (NT == 2) {
+          if (!(ok = v_ready(more) && (!more || next_full(k_at)))) break;
+          auto step = [&](auto tile) {
+            constexpr int t = decltype(tile)::value;
+            if (!(ok = wait_bounded(p_full(t), j & 1, wc))) return;
             tc_fence_after();
-            mma_o(t, t * 128, j);
+            mma_o(v_lo + v_at, t * 128, L::COL_O + t * D, j > 0);
             if (more) {
-              mma_s(t, t * 128, j + 1);
+              mma_s(q_lo + t * (L::TILE >> 4), k_lo + k_at, t * 128);
               mma_commit(s_full(t));
             } else {
               mma_commit(o_full(t));
             }
-          }
-          if (!ok) break;
-          mma_commit(kv_empty(idx_v(j) % L::STAGES));
-          if (more) mma_commit(kv_empty(idx_k(j + 1) % L::STAGES));
-        }
-      } else {
-        if (ok) {
-          mma_s(0, 0, 0);
-          mma_commit(s_full(0));
-          mma_commit(kv_empty(idx_k(0) % L::STAGES));
-        }
-        for (int j = 0; ok && j < n_iter; ++j) {
-          if (j + 1 < n_iter) {
-            if (!(ok = full(idx_k(j + 1)))) break;
+          };
+          step(std::integral_constant<int, 0>{});
+          if (ok && nt == 2) step(std::integral_constant<int, NT - 1>{});
+        } else {
+          if (more) {
+            if (!(ok = next_full(k_at))) break;
             tc_fence_after();
-            mma_s(0, ((j + 1) & 1) * 128, j + 1);
+            mma_s(q_lo, k_lo + k_at, ((j + 1) & 1) * 128);
             mma_commit(s_full((j + 1) & 1));
-            mma_commit(kv_empty(idx_k(j + 1) % L::STAGES));
           }
-          if (!(ok = v_ready(j) && wait_bounded(p_full(j & 1), (j >> 1) & 1, wc))) break;
+          if (!(ok = v_ready(more) && wait_bounded(p_full(j & 1), (j >> 1) & 1, wc))) break;
           tc_fence_after();
-          mma_o(0, (j & 1) * 128, j);
-          // o_full(0) counts the tiles (a rescale waits for the one before);
-          // the end has a barrier of its own: a wait by parity cannot tell
-          // the last product from the one two before it
-          mma_commit(j + 1 < n_iter ? o_full(0) : o_full(1));
-          mma_commit(kv_empty(idx_v(j) % L::STAGES));
+          mma_o(v_lo + v_at, (j & 1) * 128, L::COL_O, j > 0);
+          // (the release of V also tells a rescale that its product is done)
+          mma_commit(more ? kv_empty(idx_v(j) % L::STAGES) : o_full(0));
         }
       }
       mma_commit(drain);
       wait_drain(drain, 0, a.timeout_ns);
     }
-  } else if (warp >= 4) {
+  }
+  } else {
     // ------------------------------------------------------------ softmax
+    if (NT == 2) regs_inc<208>();
     const int t = (warp - 4) >> 2;                    // row tile
     const int r_tile = (warp & 3) * 32 + lane;        // TMEM lane
     const int row = w.row0 + t * kTileM + r_tile;     // row of the sequence
@@ -417,8 +430,12 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           }
           if (j > 0) {
             // O holds the tiles before this one: with two row tiles their
-            // products ended before this S; with one, wait for the last
-            if (NT == 1 && !(ok = warp_wait(o_full(0), (j - 1) & 1, wc))) break;
+            // products ended before this S; with one, wait for the last,
+            // which frees its V stage
+            if (NT == 1) {
+              const int i = idx_v(j - 1);
+              if (!(ok = warp_wait(kv_empty(i % L::STAGES), (i / L::STAGES) & 1, wc))) break;
+            }
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
@@ -454,10 +471,18 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(slot));
+      if (lane == 0) {
+        mbar_arrive(p_full(slot));
+        // S of this tile came from K's stage and, with two row tiles, after
+        // the product of the V before it: both are free
+        if ((warp & 3) == 0) {
+          if (NT == 2 && j > 0) mbar_arrive(kv_empty(idx_v(j - 1) % L::STAGES));
+          mbar_arrive(kv_empty(idx_k(j) % L::STAGES));
+        }
+      }
     }
     // ------------------------------------------------------------ output
-    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(NT == 2 ? t : 1), 0, wc) && warp_live) {
+    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(t), 0, wc) && warp_live) {
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (NaN stays NaN)
       const bool none = l == 0.f;
