@@ -25,7 +25,6 @@
 // split over the keys; a combine kernel joins the splits by their lse.
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -37,6 +36,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.0f;  // log2 units
+constexpr float kSumMax = 256.0f;  // 2^kTau
 constexpr int kTileM = 128, kTileN = 128;
 
 template <int D, int NT>
@@ -56,6 +56,18 @@ struct AttnLayout {
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int THREADS = 128 + 128 * NT;
   static constexpr int COL_O = 256;
+};
+
+// A place in the ring of K and V stages and the parity of its turn.
+struct RingPos {
+  int stage;
+  uint32_t phase;
+  __device__ __forceinline__ void step(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // What a CTA works on: one sequence's rows of one key head, a range of keys.
@@ -290,15 +302,15 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       const uint32_t hi = static_cast<uint32_t>(k0 >> 32);  // the same in all three
       const uint32_t q_lo = static_cast<uint32_t>(q0), k_lo = static_cast<uint32_t>(k0), v_lo = static_cast<uint32_t>(v0);
       auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
-      int stage = 0;        // next stage of the ring to be waited for
-      uint32_t phase = 0;
-      auto next_full = [&](uint32_t& at) {  // ... once it has landed, its offset in descriptor units
-        const bool got = wait_bounded(kv_full(stage), phase, wc);
-        at = static_cast<uint32_t>(stage) * (L::TILE >> 4);
-        if (++stage == L::STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
+      RingPos ring{0, 0};  // next stage to be used
+      auto next = [&]() {  // its offset in descriptor units
+        const uint32_t at = static_cast<uint32_t>(ring.stage) * (L::TILE >> 4);
+        ring.step(L::STAGES);
+        return at;
+      };
+      auto landed = [&]() {
+        const bool got = wait_bounded(kv_full(ring.stage), ring.phase, wc);
+        tc_fence_after();
         return got;
       };
       auto mma_s = [&](uint32_t q, uint32_t k, uint32_t col) {  // S = Q_t K_j^T
@@ -313,9 +325,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         for (int i = 0; i < kTileN / 16; ++i)
           mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * i, desc(v + i * (2048 >> 4)), id_o, i > 0 ? 1 : add);
       };
-      uint32_t k_at = 0, v_at = 0;
-      bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && next_full(k_at);
-      tc_fence_after();
+      bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && landed();
+      uint32_t k_at = next();
       if (ok) {
         mma_s(q_lo, k_lo + k_at, 0);
         mma_commit(s_full(0));
@@ -324,39 +335,37 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           mma_commit(s_full(1));
         }
       }
-      // the last tile's V has its rows past the last key cleared first
-      auto v_ready = [&](bool more) {
-        return next_full(v_at) && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc));
-      };
 #pragma unroll 1
       for (int j = 0; ok && j < n_iter; ++j) {
         const bool more = j + 1 < n_iter;
         if (NT == 2) {
-          if (!(ok = v_ready(more) && (!more || next_full(k_at)))) break;
-          auto step = [&](auto tile) {
-            constexpr int t = decltype(tile)::value;
-            if (!(ok = wait_bounded(p_full(t), j & 1, wc))) return;
+          // P of row tile 0 comes with V of this tile and K of the next
+          const uint32_t v_at = next();
+          if (more) k_at = next();
+          if (!(ok = wait_bounded(p_full(0), j & 1, wc))) break;
+          tc_fence_after();
+          mma_o(v_lo + v_at, 0, L::COL_O, j > 0);
+          if (more) mma_s(q_lo, k_lo + k_at, 0);
+          mma_commit(more ? s_full(0) : o_full(0));
+          if (nt == 2) {
+            if (!(ok = wait_bounded(p_full(1), j & 1, wc))) break;
             tc_fence_after();
-            mma_o(v_lo + v_at, t * 128, L::COL_O + t * D, j > 0);
-            if (more) {
-              mma_s(q_lo + t * (L::TILE >> 4), k_lo + k_at, t * 128);
-              mma_commit(s_full(t));
-            } else {
-              mma_commit(o_full(t));
-            }
-          };
-          step(std::integral_constant<int, 0>{});
-          if (ok && nt == 2) step(std::integral_constant<int, NT - 1>{});
+            mma_o(v_lo + v_at, 128, L::COL_O + D, j > 0);
+            if (more) mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, 128);
+            mma_commit(more ? s_full(1) : o_full(1));
+          }
         } else {
           if (more) {
-            if (!(ok = next_full(k_at))) break;
-            tc_fence_after();
-            mma_s(q_lo, k_lo + k_at, ((j + 1) & 1) * 128);
+            if (!(ok = landed())) break;
+            mma_s(q_lo, k_lo + next(), ((j + 1) & 1) * 128);
             mma_commit(s_full((j + 1) & 1));
           }
-          if (!(ok = v_ready(more) && wait_bounded(p_full(j & 1), (j >> 1) & 1, wc))) break;
+          // the last tile's V has its rows past the last key cleared first
+          if (!(ok = landed() && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc)) &&
+                     wait_bounded(p_full(j & 1), (j >> 1) & 1, wc)))
+            break;
           tc_fence_after();
-          mma_o(v_lo + v_at, (j & 1) * 128, L::COL_O, j > 0);
+          mma_o(v_lo + next(), (j & 1) * 128, L::COL_O, j > 0);
           // (the release of V also tells a rescale that its product is done)
           mma_commit(more ? kv_empty(idx_v(j) % L::STAGES) : o_full(0));
         }
@@ -397,6 +406,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     const uint32_t to = tmem + L::COL_O + t * D + lanes;
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
+    RingPos ring{1, 0};  // V of the first tile
     for (int j = 0; t < nt && j < n_iter; ++j) {
       const int slot = NT == 2 ? t : (j & 1);
       if (!(ok = warp_wait(s_full(slot), NT == 2 ? (j & 1) : ((j >> 1) & 1), wc))) break;
@@ -405,24 +415,48 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         const uint32_t ts = tmem + slot * 128 + lanes;
         if (!(ok = check_tmem(ck, ts, 32, 128, __LINE__))) break;
         float s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
-        tmem_wait_ld();
         const int seen = lim - (w.t0 + j) * kTileN;  // of this tile's keys
-        if (seen < kTileN) {
+        auto load_s = [&]() {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= seen) s[k] = -INFINITY;
-        }
-        float m0 = s[0], m1 = s[1];
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+          tmem_wait_ld();
+          if (seen < kTileN) {
 #pragma unroll
-        for (int k = 2; k < 126; k += 4) {
-          m0 = max3(m0, s[k], s[k + 1]);
-          m1 = max3(m1, s[k + 2], s[k + 3]);
-        }
-        const float top = max3(m0, m1, fmaxf(s[126], s[127])) * c;
-        const bool move = top > ref + kTau || (ref == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xFFFFFFFFu, move)) {
+            for (int k = 0; k < 128; ++k)
+              if (k >= seen) s[k] = -INFINITY;
+          }
+        };
+        uint32_t p[64];
+        auto terms = [&]() {  // P against ref, in the inputs' type; its fp32 sum
+          const float r0 = ref == -INFINITY ? 0.f : ref;
+          const float2 c2 = make_float2(c, c), nr = make_float2(-r0, -r0);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, nr);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+            p[k] = pack2<TYPE>(e.x, e.y);
+          }
+          const float2 f = __fadd2_rn(sum[0], sum[1]);
+          return f.x + f.y;
+        };
+        load_s();
+        float f = terms();
+        // Terms against the reference as it is, while their sum stays within
+        // 2^8; else (and in a row's first tile) the maximum is taken and moves
+        // the reference if it exceeds it by more than 2^8
+        const bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
+        if (__any_sync(0xFFFFFFFFu, again)) {
+          load_s();
+          float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k < 124; k += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
+          }
+          const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
+          const bool move = again && (top > ref + kTau || (ref == -INFINITY && top > -INFINITY));
           const float alpha = move ? ex2(ref - top) : 1.f;
           if (move) {
             ref = top;
@@ -449,25 +483,27 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             }
             tmem_wait_st();
           }
+          f = terms();
         }
-        const float r0 = ref == -INFINITY ? 0.f : ref;
-        const float2 c2 = make_float2(c, c), nr = make_float2(-r0, -r0);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 x = __ffma2_rn(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), c2, nr);
-            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-            p[k] = pack2<TYPE>(e.x, e.y);
-          }
-          tmem_st16(ts + 16 * q, p);
-        }
-        const float2 f = __fadd2_rn(sum[0], sum[1]);
-        l += f.x + f.y;
+        for (int q = 0; q < 4; ++q) tmem_st16(ts + 16 * q, &p[16 * q]);
+        l += f;
         tmem_wait_st();
+      }
+      // Row tile 0's P is handed over together with the loads that its products
+      // need, V of this tile and K of the next: the waits are these warps' to
+      // spend (a wait takes the issuer 100 cycles between products, with the
+      // data there)
+      if (NT == 2 && warp == 5) {
+        ok = warp_wait(kv_full(ring.stage), ring.phase, wc);
+        ring.step(L::STAGES);
+        if (ok && j + 1 < n_iter) {
+          ok = warp_wait(kv_full(ring.stage), ring.phase, wc);
+          ring.step(L::STAGES);
+        } else if (ok && last_valid < kTileN) {  // its rows past the last key are cleared first
+          ok = warp_wait(v_fixed, 0, wc);
+        }
+        if (!ok) break;
       }
       tc_fence_before();
       __syncwarp();
