@@ -153,16 +153,25 @@ streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* tab
   return st != STREAMKL_OK ? st : check_rows("v_cache", vc, num_pages, HK, page_size, d, dtype, true);
 }
 
-// Key split of the attention over the cache: with few query tiles against
-// long sequences the keys are cut into `splits` ranges of split_tiles 128-key
-// tiles (counted from a sequence's start, so a short one uses fewer ranges).
+// How the attention over the cache is cut into CTAs. Few rows (decode) go to
+// the persistent kernel, which deals the key tiles out evenly by itself. With
+// more, the keys of few query tiles against long sequences are cut into
+// `splits` ranges of split_tiles 128-key tiles (counted from a sequence's
+// start, so a short one uses fewer ranges).
 struct AttnPlan {
+  int decode_ctas;  // 0: not the persistent kernel
   int row_tiles, q_tiles, splits, split_tiles;
 };
 
 AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, int requested) {
-  AttnPlan p;
+  AttnPlan p{};
   const long long rows = static_cast<long long>(max_q) * (HQ / HK);
+  if (requested == 0 && rows <= skl::kDecodeRows) {
+    const long long most = static_cast<long long>(B) * HK * std::max(1, (max_kv + 127) / 128);
+    p.decode_ctas = static_cast<int>(std::min<long long>(most, 2LL * num_sms()));
+    p.split_tiles = 1;
+    return p;
+  }
   p.row_tiles = rows > 128 ? 2 : 1;
   p.q_tiles = static_cast<int>((rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles));
   const int tiles = std::max(1, (max_kv + 127) / 128);
@@ -191,10 +200,14 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   return p;
 }
 
-size_t attn_part_bytes(int splits, int T, int HQ, int d) {
-  if (splits <= 1) return 0;
-  const size_t rows = static_cast<size_t>(splits) * T * HQ;
-  return (rows * (d + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+// Rows of the partial results.
+size_t attn_part_rows(const AttnPlan& p, int T, int HQ) {
+  if (p.decode_ctas > 0) return static_cast<size_t>(2) * p.decode_ctas * skl::kDecodeRows;
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * T * HQ : 0;
+}
+
+size_t attn_part_bytes(const AttnPlan& p, int T, int HQ, int d) {
+  return (attn_part_rows(p, T, HQ) * (d + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
 // 4-D map {d, page size, HK, pages} of a cache, 64-column boxes of one page's
@@ -321,14 +334,14 @@ streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* st
 }
 
 int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len) {
-  if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK) return 0;
+  if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK) return -1;
   return attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, 0).splits;
 }
 
 size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
                                           int num_splits) {
   if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK || num_splits < 0) return 0;
-  return attn_part_bytes(attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits).splits, T, HQ, d);
+  return attn_part_bytes(attn_plan(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits), T, HQ, d);
 }
 
 streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* stream) {
@@ -350,7 +363,7 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
   if (!u.dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
   const AttnPlan p = attn_plan(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
   if (p.splits > 65535) return fail(STREAMKL_ERR_UNSUPPORTED, "%d key splits (at most 65535)", p.splits);
-  const size_t need = attn_part_bytes(p.splits, u.T, u.HQ, u.d);
+  const size_t need = attn_part_bytes(p, u.T, u.HQ, u.d);
   if (need && (!u.workspace || u.ws_bytes < need))
     return fail(STREAMKL_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", u.workspace ? u.ws_bytes : 0, need);
   if (need && !aligned16(u.workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
@@ -389,10 +402,11 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
   a.splits = p.splits;
   a.split_tiles = p.split_tiles;
   a.part_o = static_cast<float*>(u.workspace);
-  a.part_lse = a.part_o ? a.part_o + static_cast<size_t>(p.splits) * u.T * u.HQ * u.d : nullptr;
+  a.part_lse = a.part_o ? a.part_o + attn_part_rows(p, u.T, u.HQ) * u.d : nullptr;
   a.dev_status = u.dev_status;
   a.timeout_ns = wait_timeout_ns();
-  cudaError_t e = skl::launch_paged_attn(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = p.decode_ctas > 0 ? skl::launch_paged_decode(a, p.decode_ctas, static_cast<cudaStream_t>(stream))
+                                    : skl::launch_paged_attn(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "paged attention launch");
 }
 

@@ -100,6 +100,12 @@ int rope_bwd_blocks(int B, int NQ, int HQ, int NK, int HK, int d, int sms);
 cudaError_t launch_rope_fwd(RopeArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, int sms, float* dw_q, float* dw_k, cudaStream_t stream);
 cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream);
+// At most kDecodeRows rows (token, head of the group) per sequence and key
+// head: `ctas` persistent CTAs share the key tiles evenly, at least split_tiles
+// each; part_o [2 ctas][kDecodeRows][d] and part_lse hold the parts of items
+// that they share.
+constexpr int kDecodeRows = 32;
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 
 }  // namespace skl

@@ -351,7 +351,8 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
 
 
 def streamkl_paged_attn_splits(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) -> int:
-    """Key splits of ``streamkl_paged_attn`` for these sizes."""
+    """Key splits that ``streamkl_paged_attn`` takes for these sizes (0: its
+    kernel for few rows, which shares the keys evenly over the GPU)."""
     return int(load().streamkl_paged_attn_splits(B, T, HQ, HK, d, max_seqlen_q, max_kv_len))
 
 

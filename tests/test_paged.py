@@ -317,6 +317,31 @@ def test_long_sequences_that_wait_for_memory(B, n, L, HQ, HK, page, splits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,HQ,HK,d,page,most,n", [(300, 6, 3, 64, 16, 300, 1), (700, 2, 2, 64, 32, 40, 1),
+                                                   (129, 8, 1, 128, 16, 700, 3), (5, 32, 8, 64, 64, 3000, 8)])
+def test_many_ragged_sequences_of_few_rows(B, HQ, HK, d, page, most, n):
+    """Items of zero, one and many key tiles side by side, more sequences than
+    a block has threads, stretches of the persistent CTAs that begin and end
+    anywhere in them."""
+    dt = torch.bfloat16
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, most + 1, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.1] = 0
+    lens[torch.rand(B, generator=g) < 0.1] = 128
+    new = torch.randint(0, n + 1, (B,), generator=g).tolist()
+    new[0] = n
+    lens = lens.tolist()
+    c = Cache(lens, HK, d, page, dt)
+    q = torch.randn(sum(new), HQ, d, generator=g).to(dt).cuda()
+    st = binding.new_status()
+    assert skl.streamkl_paged_attn_splits(B, sum(new), HQ, HK, d, n, most) == 0
+    o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu(new), max_seqlen_q=n,
+                                     max_kv_len=max(lens), dev_status=st)
+    binding.raise_on_device_status(st)
+    _check_attn(o, lse, q, c, new, lens, d ** -0.5, True, dt)
+
+
+@pytest.mark.gpu
 def test_single_tokens_without_offsets():
     lens = [5, 300, 64]
     c = Cache(lens, 2, 128, 16, torch.bfloat16)
@@ -615,16 +640,20 @@ def test_attention_c_call_refuses(lib, over, status):
 
 
 def test_attention_splits_on_the_host(lib):
-    assert skl.streamkl_paged_attn_splits(1, 1, 32, 8, 128, 1, 4096) > 1      # few tiles, long keys
-    assert skl.streamkl_paged_attn_splits(64, 64 * 512, 32, 8, 128, 512, 4096) == 1
-    assert skl.streamkl_paged_attn_splits(1, 1, 32, 8, 128, 1, 100) == 1
-    assert skl.streamkl_paged_attn_splits(1, 1, 32, 5, 128, 1, 100) == 0
-    for args in ((1, 1, 32, 8, 128, 1, 4096), (3, 700, 8, 8, 64, 512, 131072)):
-        s = skl.streamkl_paged_attn_splits(*args)
+    splits, size = skl.streamkl_paged_attn_splits, skl.streamkl_paged_attn_workspace_size
+    assert splits(1, 1, 32, 8, 128, 1, 4096) == 0                 # few rows: the persistent kernel
+    assert splits(1, 8, 32, 8, 128, 8, 4096) == 0 and splits(1, 9, 32, 8, 128, 9, 4096) > 1
+    assert splits(64, 64 * 512, 32, 8, 128, 512, 4096) == 1
+    assert splits(1, 64, 32, 8, 128, 64, 100) == 1
+    assert splits(1, 1, 32, 5, 128, 1, 100) == -1
+    for args in ((1, 40, 32, 8, 128, 40, 4096), (3, 700, 8, 8, 64, 512, 131072)):
+        s = splits(*args)
         need = s * args[1] * args[2] * (args[4] + 1) * 4 if s > 1 else 0
-        got = skl.streamkl_paged_attn_workspace_size(*args)
-        assert need <= got < need + 256
-    assert skl.streamkl_paged_attn_workspace_size(1, 1, 32, 8, 128, 1, 4096, 1) == 0
+        assert need <= size(*args) < need + 256
+    assert size(1, 1, 32, 8, 128, 1, 4096, 1) == 0
+    # two parts of 32 rows a CTA; no more CTAs than key tiles
+    assert size(1, 1, 4, 1, 64, 1, 256) == 2 * 2 * 32 * 65 * 4
+    assert size(64, 64, 32, 8, 128, 1, 16384) == size(1, 1, 1, 1, 128, 1, 1 << 20)
 
 
 @pytest.mark.gpu
