@@ -169,7 +169,7 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   if (requested == 0 && rows <= skl::kDecodeRows) {
     const long long most = static_cast<long long>(B) * HK * std::max(1, (max_kv + 127) / 128);
     p.decode_ctas = static_cast<int>(std::min<long long>(most, 2LL * num_sms()));
-    p.split_tiles = 1;
+    p.split_tiles = 2;  // (one tile each: 21.3 us against 19.6 at one sequence of 4,096 keys)
     return p;
   }
   p.row_tiles = rows > 128 ? 2 : 1;

@@ -48,14 +48,20 @@ struct AttnLayout {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = NT * TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
-  // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], drain
-  static constexpr int NBAR = 2 + 2 * STAGES + 6 + 1;
+  // P in columns of its own, where TMEM has room for them
+  static constexpr bool OWN_P = D == 64 || NT == 1;
+  // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2],
+  // s_read[2], p_read[2], drain
+  static constexpr int NBAR = 2 + 2 * STAGES + 10 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int ALLOC = BYTES;  // (the base is declared 1024-byte aligned)
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int THREADS = 128 + 128 * NT;
-  static constexpr int COL_O = 256;
+  static constexpr int col_s(int t) { return 128 * t; }
+  static constexpr int col_p(int t) { return OWN_P ? 128 * NT + 64 * t : 128 * t; }
+  static constexpr int col_o(int t) { return (OWN_P ? 192 : 128) * NT + D * t; }
+  static_assert(col_o(NT - 1) + D <= 512, "TMEM columns");
 };
 
 // A place in the ring of K and V stages and the parity of its turn.
@@ -156,8 +162,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   auto s_full = [&](int k) { return bar0 + 8u * (2 + 2 * L::STAGES + k); };
   auto p_full = [&](int k) { return bar0 + 8u * (4 + 2 * L::STAGES + k); };
   auto o_full = [&](int k) { return bar0 + 8u * (6 + 2 * L::STAGES + k); };
-  const uint32_t drain = bar0 + 8u * (8 + 2 * L::STAGES);
-  static_assert(2 + 2 * L::STAGES + 6 + 1 == L::NBAR, "barrier region holds every barrier");
+  auto s_read = [&](int k) { return bar0 + 8u * (8 + 2 * L::STAGES + k); };
+  auto p_read = [&](int k) { return bar0 + 8u * (10 + 2 * L::STAGES + k); };
+  const uint32_t drain = bar0 + 8u * (12 + 2 * L::STAGES);
+  static_assert(13 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
   volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
@@ -175,12 +183,14 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       mbar_init(v_fixed, 1);
       for (int s = 0; s < L::STAGES; ++s) {
         mbar_init(kv_full(s), 1);
-        mbar_init(kv_empty(s), NT == 2 ? nt : 1);
+        mbar_init(kv_empty(s), nt);
       }
       for (int k = 0; k < 2; ++k) {
         mbar_init(s_full(k), 1);
         mbar_init(p_full(k), 4);
         mbar_init(o_full(k), 1);
+        mbar_init(s_read(k), 4);
+        mbar_init(p_read(k), 1);
       }
       mbar_init(drain, 1);
     }
@@ -208,9 +218,9 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   const int last_valid = min(kTileN, w.klim - (w.t0 + w.n_iter - 1) * kTileN);
 
   // Place of key tile j's K and V among the loads, in the order in which the
-  // MMAs use them. NT = 2: K0 V0 K1 V1 ..; NT = 1: K0 K1 V0 K2 V1 ..
-  auto idx_k = [&](int j) { return NT == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
-  auto idx_v = [&](int j) { return NT == 2 ? 2 * j + 1 : (j + 1 < w.n_iter ? 2 * j + 2 : 2 * j + 1); };
+  // MMAs use them: K0 V0 K1 V1 .., with P in columns of its own K0 K1 V0 K2 V1 ..
+  auto idx_k = [&](int j) { return !L::OWN_P ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+  auto idx_v = [&](int j) { return !L::OWN_P ? 2 * j + 1 : (j + 1 < w.n_iter ? 2 * j + 2 : 2 * j + 1); };
 
   if (warp < 4) {
   // NT = 2: 128 threads with 88 registers and 256 with 208 make up the launch's
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       return true;
     };
     int pg = page_of(0), pg_next = page_of(1);
-    if (NT == 2) {
+    if (!L::OWN_P) {
       for (int j = 0; ok && j < n_iter; ++j) {
         ok = load(&tm_k, j, pg) && load(&tm_v, j, pg);
         pg = pg_next;
@@ -328,46 +338,60 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && landed();
       uint32_t k_at = next();
       if (ok) {
-        mma_s(q_lo, k_lo + k_at, 0);
+        mma_s(q_lo, k_lo + k_at, L::col_s(0));
         mma_commit(s_full(0));
         if (nt == 2) {
-          mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, 128);
+          mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
           mma_commit(s_full(1));
         }
       }
 #pragma unroll 1
       for (int j = 0; ok && j < n_iter; ++j) {
         const bool more = j + 1 < n_iter;
-        if (NT == 2) {
+        if (!L::OWN_P) {
           // P of row tile 0 comes with V of this tile and K of the next
           const uint32_t v_at = next();
           if (more) k_at = next();
           if (!(ok = wait_bounded(p_full(0), j & 1, wc))) break;
           tc_fence_after();
-          mma_o(v_lo + v_at, 0, L::COL_O, j > 0);
-          if (more) mma_s(q_lo, k_lo + k_at, 0);
+          mma_o(v_lo + v_at, L::col_p(0), L::col_o(0), j > 0);
+          if (more) mma_s(q_lo, k_lo + k_at, L::col_s(0));
           mma_commit(more ? s_full(0) : o_full(0));
           if (nt == 2) {
             if (!(ok = wait_bounded(p_full(1), j & 1, wc))) break;
             tc_fence_after();
-            mma_o(v_lo + v_at, 128, L::COL_O + D, j > 0);
-            if (more) mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, 128);
+            mma_o(v_lo + v_at, L::col_p(1), L::col_o(1), j > 0);
+            if (more) mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
             mma_commit(more ? s_full(1) : o_full(1));
           }
         } else {
           if (more) {
             if (!(ok = landed())) break;
-            mma_s(q_lo, k_lo + next(), ((j + 1) & 1) * 128);
-            mma_commit(s_full((j + 1) & 1));
+            k_at = next();
+            if (!(ok = wait_bounded(s_read(0), j & 1, wc))) break;
+            tc_fence_after();
+            mma_s(q_lo, k_lo + k_at, L::col_s(0));
+            mma_commit(s_full(0));
+            if (nt == 2) {
+              if (!(ok = wait_bounded(s_read(1), j & 1, wc))) break;
+              tc_fence_after();
+              mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
+              mma_commit(s_full(1));
+            }
           }
           // the last tile's V has its rows past the last key cleared first
-          if (!(ok = landed() && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc)) &&
-                     wait_bounded(p_full(j & 1), (j >> 1) & 1, wc)))
-            break;
+          if (!(ok = landed() && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc)))) break;
+          const uint32_t v_at = next();
+          if (!(ok = wait_bounded(p_full(0), j & 1, wc))) break;
           tc_fence_after();
-          mma_o(v_lo + next(), (j & 1) * 128, L::COL_O, j > 0);
-          // (the release of V also tells a rescale that its product is done)
-          mma_commit(more ? kv_empty(idx_v(j) % L::STAGES) : o_full(0));
+          mma_o(v_lo + v_at, L::col_p(0), L::col_o(0), j > 0);
+          mma_commit(more ? p_read(0) : o_full(0));
+          if (nt == 2) {
+            if (!(ok = wait_bounded(p_full(1), j & 1, wc))) break;
+            tc_fence_after();
+            mma_o(v_lo + v_at, L::col_p(1), L::col_o(1), j > 0);
+            mma_commit(more ? p_read(1) : o_full(1));
+          }
         }
       }
       mma_commit(drain);
@@ -403,17 +427,16 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     const int lim = !live ? 0 : a.causal ? min(w.len, w.len - w.n + tok + 1) : w.len;
     const bool warp_live = w.row0 + t * kTileM + (warp & 3) * 32 < w.rows;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t to = tmem + L::COL_O + t * D + lanes;
+    const uint32_t to = tmem + L::col_o(t) + lanes;
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
     RingPos ring{1, 0};  // V of the first tile
     for (int j = 0; t < nt && j < n_iter; ++j) {
-      const int slot = NT == 2 ? t : (j & 1);
-      if (!(ok = warp_wait(s_full(slot), NT == 2 ? (j & 1) : ((j >> 1) & 1), wc))) break;
+      if (!(ok = warp_wait(s_full(t), j & 1, wc))) break;
       tc_fence_after();
       if (warp_live) {
-        const uint32_t ts = tmem + slot * 128 + lanes;
-        if (!(ok = check_tmem(ck, ts, 32, 128, __LINE__))) break;
+        const uint32_t ts = tmem + L::col_s(t) + lanes, tp = tmem + L::col_p(t) + lanes;
+        if (!(ok = check_tmem(ck, ts, 32, 128, __LINE__) && check_tmem(ck, tp, 32, 64, __LINE__))) break;
         float s[128];
         const int seen = lim - (w.t0 + j) * kTileN;  // of this tile's keys
         auto load_s = [&]() {
@@ -441,14 +464,9 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           const float2 f = __fadd2_rn(sum[0], sum[1]);
           return f.x + f.y;
         };
-        load_s();
-        float f = terms();
-        // Terms against the reference as it is, while their sum stays within
-        // 2^8; else (and in a row's first tile) the maximum is taken and moves
-        // the reference if it exceeds it by more than 2^8
-        const bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
-        if (__any_sync(0xFFFFFFFFu, again)) {
-          load_s();
+        // the maximum of the tile moves the reference if it exceeds it by more
+        // than 2^8; by how much O and the sum scale then
+        auto move_ref = [&](bool may) {
           float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int k = 4; k < 124; k += 8) {
@@ -456,45 +474,69 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
-          const bool move = again && (top > ref + kTau || (ref == -INFINITY && top > -INFINITY));
+          const bool move = may && (top > ref + kTau || (ref == -INFINITY && top > -INFINITY));
           const float alpha = move ? ex2(ref - top) : 1.f;
           if (move) {
             ref = top;
             l *= alpha;
           }
-          if (j > 0) {
-            // O holds the tiles before this one: with two row tiles their
-            // products ended before this S; with one, wait for the last,
-            // which frees its V stage
-            if (NT == 1) {
-              const int i = idx_v(j - 1);
-              if (!(ok = warp_wait(kv_empty(i % L::STAGES), (i / L::STAGES) & 1, wc))) break;
-            }
-            tc_fence_after();
+          return alpha;
+        };
+        auto scale_o = [&](float alpha) {  // (all of its products so far have ended)
 #pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              float o[16];
-              tmem_ld16(to + 16 * q, o);
-              tmem_wait_ld();
-              uint32_t r[16];
+          for (int q = 0; q < D / 16; ++q) {
+            float o[16];
+            tmem_ld16(to + 16 * q, o);
+            tmem_wait_ld();
+            uint32_t r[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * alpha);
-              tmem_st16(to + 16 * q, r);
-            }
-            tmem_wait_st();
+            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * alpha);
+            tmem_st16(to + 16 * q, r);
           }
+        };
+        float f;
+        load_s();
+        if (L::OWN_P) {
+          // S is in registers: the next tile's may come. P's columns and O are
+          // touched once the product of the tile before has ended
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read(t));
+          const float alpha = move_ref(true);
           f = terms();
+          if (j > 0) {
+            if (!(ok = warp_wait(p_read(t), (j - 1) & 1, wc))) break;
+            tc_fence_after();
+            if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) scale_o(alpha);
+          }
+        } else {
+          // Terms against the reference as it is, while their sum stays within
+          // 2^8; else (and in a row's first tile) the maximum is taken. The
+          // products of the tiles before ended before this S
+          f = terms();
+          const bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
+          if (__any_sync(0xFFFFFFFFu, again)) {
+            load_s();
+            const float alpha = move_ref(again);
+            if (j > 0) scale_o(alpha);
+            f = terms();
+          }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_st16(ts + 16 * q, &p[16 * q]);
+        for (int q = 0; q < 4; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
         l += f;
         tmem_wait_st();
+      } else if (L::OWN_P) {
+        // a warp without rows keeps step: it must not arrive for this tile's P
+        // while the others still owe the last one's
+        if (lane == 0) mbar_arrive(s_read(t));
+        if (j > 0 && !(ok = warp_wait(p_read(t), (j - 1) & 1, wc))) break;
       }
       // Row tile 0's P is handed over together with the loads that its products
       // need, V of this tile and K of the next: the waits are these warps' to
       // spend (a wait takes the issuer 100 cycles between products, with the
       // data there)
-      if (NT == 2 && warp == 5) {
+      if (!L::OWN_P && warp == 5) {
         ok = warp_wait(kv_full(ring.stage), ring.phase, wc);
         ring.step(L::STAGES);
         if (ok && j + 1 < n_iter) {
@@ -508,11 +550,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(p_full(slot));
-        // S of this tile came from K's stage and, with two row tiles, after
-        // the product of the V before it: both are free
+        mbar_arrive(p_full(t));
+        // S of this tile came from K's stage, the product of the V before it
+        // has ended: both are free
         if ((warp & 3) == 0) {
-          if (NT == 2 && j > 0) mbar_arrive(kv_empty(idx_v(j - 1) % L::STAGES));
+          if (j > 0) mbar_arrive(kv_empty(idx_v(j - 1) % L::STAGES));
           mbar_arrive(kv_empty(idx_k(j) % L::STAGES));
         }
       }
