@@ -51,8 +51,8 @@ struct AttnLayout {
   // P in columns of its own, where TMEM has room for them
   static constexpr bool OWN_P = D == 64 || NT == 1;
   // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2],
-  // s_read[2], p_read[2], drain
-  static constexpr int NBAR = 2 + 2 * STAGES + 10 + 1;
+  // s_read, p_read, drain
+  static constexpr int NBAR = 2 + 2 * STAGES + 9;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int ALLOC = BYTES;  // (the base is declared 1024-byte aligned)
@@ -162,10 +162,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   auto s_full = [&](int k) { return bar0 + 8u * (2 + 2 * L::STAGES + k); };
   auto p_full = [&](int k) { return bar0 + 8u * (4 + 2 * L::STAGES + k); };
   auto o_full = [&](int k) { return bar0 + 8u * (6 + 2 * L::STAGES + k); };
-  auto s_read = [&](int k) { return bar0 + 8u * (8 + 2 * L::STAGES + k); };
-  auto p_read = [&](int k) { return bar0 + 8u * (10 + 2 * L::STAGES + k); };
-  const uint32_t drain = bar0 + 8u * (12 + 2 * L::STAGES);
-  static_assert(13 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
+  const uint32_t s_read = bar0 + 8u * (8 + 2 * L::STAGES), p_read = s_read + 8, drain = s_read + 16;
+  static_assert(11 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
   volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
@@ -187,11 +185,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       }
       for (int k = 0; k < 2; ++k) {
         mbar_init(s_full(k), 1);
-        mbar_init(p_full(k), 4);
+        mbar_init(p_full(k), L::OWN_P ? 4 * nt : 4);
         mbar_init(o_full(k), 1);
-        mbar_init(s_read(k), 4);
-        mbar_init(p_read(k), 1);
       }
+      mbar_init(s_read, 4 * nt);
+      mbar_init(p_read, 1);
       mbar_init(drain, 1);
     }
     // a failure recorded earlier, or a failed layout check, skips the work
@@ -337,14 +335,13 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       };
       bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && landed();
       uint32_t k_at = next();
-      if (ok) {
+      auto both_s = [&]() {
         mma_s(q_lo, k_lo + k_at, L::col_s(0));
-        mma_commit(s_full(0));
-        if (nt == 2) {
-          mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
-          mma_commit(s_full(1));
-        }
-      }
+        if (!L::OWN_P && nt == 2) mma_commit(s_full(0));
+        if (nt == 2) mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
+        mma_commit(s_full(L::OWN_P ? 0 : nt - 1));
+      };
+      if (ok) both_s();
 #pragma unroll 1
       for (int j = 0; ok && j < n_iter; ++j) {
         const bool more = j + 1 < n_iter;
@@ -365,33 +362,19 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             mma_commit(more ? s_full(1) : o_full(1));
           }
         } else {
+          // S comes back with K of the next tile, P with V of this one
           if (more) {
-            if (!(ok = landed())) break;
             k_at = next();
-            if (!(ok = wait_bounded(s_read(0), j & 1, wc))) break;
+            if (!(ok = wait_bounded(s_read, j & 1, wc))) break;
             tc_fence_after();
-            mma_s(q_lo, k_lo + k_at, L::col_s(0));
-            mma_commit(s_full(0));
-            if (nt == 2) {
-              if (!(ok = wait_bounded(s_read(1), j & 1, wc))) break;
-              tc_fence_after();
-              mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
-              mma_commit(s_full(1));
-            }
+            both_s();
           }
-          // the last tile's V has its rows past the last key cleared first
-          if (!(ok = landed() && (more || last_valid == kTileN || wait_bounded(v_fixed, 0, wc)))) break;
           const uint32_t v_at = next();
           if (!(ok = wait_bounded(p_full(0), j & 1, wc))) break;
           tc_fence_after();
           mma_o(v_lo + v_at, L::col_p(0), L::col_o(0), j > 0);
-          mma_commit(more ? p_read(0) : o_full(0));
-          if (nt == 2) {
-            if (!(ok = wait_bounded(p_full(1), j & 1, wc))) break;
-            tc_fence_after();
-            mma_o(v_lo + v_at, L::col_p(1), L::col_o(1), j > 0);
-            mma_commit(more ? p_read(1) : o_full(1));
-          }
+          if (nt == 2) mma_o(v_lo + v_at, L::col_p(1), L::col_o(1), j > 0);
+          mma_commit(more ? p_read : o_full(0));
         }
       }
       mma_commit(drain);
@@ -430,9 +413,19 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     const uint32_t to = tmem + L::col_o(t) + lanes;
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
-    RingPos ring{1, 0};  // V of the first tile
+    auto landed_k = [&](int j) {
+      const int i = idx_k(j);
+      return warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc);
+    };
+    auto hand_back_s = [&](int j) {  // S has been read; K of the next tile comes with it
+      const bool got = warp != 6 || j + 1 == n_iter || landed_k(j + 1);
+      tc_fence_before();
+      __syncwarp();
+      if (got && lane == 0) mbar_arrive(s_read);
+      return got;
+    };
     for (int j = 0; t < nt && j < n_iter; ++j) {
-      if (!(ok = warp_wait(s_full(t), j & 1, wc))) break;
+      if (!(ok = warp_wait(s_full(L::OWN_P ? 0 : t), j & 1, wc))) break;
       tc_fence_after();
       if (warp_live) {
         const uint32_t ts = tmem + L::col_s(t) + lanes, tp = tmem + L::col_p(t) + lanes;
@@ -499,13 +492,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         if (L::OWN_P) {
           // S is in registers: the next tile's may come. P's columns and O are
           // touched once the product of the tile before has ended
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_read(t));
+          if (!(ok = hand_back_s(j))) break;
           const float alpha = move_ref(true);
           f = terms();
           if (j > 0) {
-            if (!(ok = warp_wait(p_read(t), (j - 1) & 1, wc))) break;
+            if (!(ok = warp_wait(p_read, (j - 1) & 1, wc))) break;
             tc_fence_after();
             if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) scale_o(alpha);
           }
@@ -529,28 +520,24 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       } else if (L::OWN_P) {
         // a warp without rows keeps step: it must not arrive for this tile's P
         // while the others still owe the last one's
-        if (lane == 0) mbar_arrive(s_read(t));
-        if (j > 0 && !(ok = warp_wait(p_read(t), (j - 1) & 1, wc))) break;
+        if (!(ok = hand_back_s(j) && (j == 0 || warp_wait(p_read, (j - 1) & 1, wc)))) break;
       }
-      // Row tile 0's P is handed over together with the loads that its products
-      // need, V of this tile and K of the next: the waits are these warps' to
-      // spend (a wait takes the issuer 100 cycles between products, with the
+      // P is handed over together with the loads that its products need, V of
+      // this tile and (if S was not) K of the next: the waits are these warps'
+      // to spend (a wait takes the issuer 100 cycles between products, with the
       // data there)
-      if (!L::OWN_P && warp == 5) {
-        ok = warp_wait(kv_full(ring.stage), ring.phase, wc);
-        ring.step(L::STAGES);
-        if (ok && j + 1 < n_iter) {
-          ok = warp_wait(kv_full(ring.stage), ring.phase, wc);
-          ring.step(L::STAGES);
-        } else if (ok && last_valid < kTileN) {  // its rows past the last key are cleared first
-          ok = warp_wait(v_fixed, 0, wc);
-        }
+      if (warp == 5) {
+        const int i = idx_v(j);
+        ok = warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc);
+        if (ok && !L::OWN_P && j + 1 < n_iter) ok = landed_k(j + 1);
+        // (the last tile's rows past the last key are cleared first)
+        if (ok && j + 1 == n_iter && last_valid < kTileN) ok = warp_wait(v_fixed, 0, wc);
         if (!ok) break;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(p_full(t));
+        mbar_arrive(p_full(L::OWN_P ? 0 : t));
         // S of this tile came from K's stage, the product of the V before it
         // has ended: both are free
         if ((warp & 3) == 0) {
@@ -560,7 +547,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       }
     }
     // ------------------------------------------------------------ output
-    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(t), 0, wc) && warp_live) {
+    if (t < nt && n_iter > 0 && ok && warp_wait(o_full(L::OWN_P ? 0 : t), 0, wc) && warp_live) {
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (NaN stays NaN)
       const bool none = l == 0.f;
