@@ -33,6 +33,10 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
+// Copies in flight per warp of the backward, repeats of a head (64 KB of shared
+// memory a block, two blocks per SM).
+template <int TYPE>
+constexpr int kBwdStages = TYPE == kTypeF32 ? 2 : 4;
 
 // 8 consecutive elements of a row: raw, as loaded with 16-byte loads.
 template <int TYPE>
@@ -180,33 +184,75 @@ __device__ __forceinline__ float sum_sq(const float (&a)[8], const float (&b)[8]
   return t + u;
 }
 
-// A warp item of a side: batch, this lane's token and the head range.
-struct Item {
-  int b, n, h0, h1;
-  bool ok;  // a token of the batch, its position inside the tables
-  int pos;
-};
-__device__ __forceinline__ Item decode_item(const RopeArgs& a, const RopeSide& s, long long item,
-                                            int tokens, int grp) {
-  Item t;
-  const int tile = static_cast<int>(item / s.hchunks);
-  const int hch = static_cast<int>(item - static_cast<long long>(tile) * s.hchunks);
-  t.b = tile / s.tiles;
-  t.n = (tile - t.b * s.tiles) * tokens + grp;
-  t.h0 = hch * a.hc;
-  t.h1 = min(s.H, t.h0 + a.hc);
-  t.ok = t.n < s.N;
-  t.pos = 0;
-  if (t.ok) {
-    t.pos = s.pos != nullptr ? __ldg(s.pos + t.b * s.pos_sb + t.n) : s.pos0 + t.n;
-    if (t.pos < 0 || t.pos >= a.table_len) {  // reported, its rows left unwritten
-      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-      t.ok = false;
-    }
-  }
-  return t;
+// 16 bytes, global to shared, in this thread's current copy group.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's N newest copy groups have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A lane's chunk in shared memory: 16-byte pieces 512 bytes (32 lanes) apart.
+template <int TYPE>
+__device__ __forceinline__ void copy8(uint32_t dst, const void* p, long long elem) {
+  const char* src = static_cast<const char*>(p) + elem * ElemSize<TYPE>::value;
+#pragma unroll
+  for (int i = 0; i < ElemSize<TYPE>::value / 2; ++i) copy16(dst + 512 * i, src + 16 * i);
+}
+template <int TYPE>
+__device__ __forceinline__ void read8(uint32_t src, float (&f)[8]) {
+  Raw8<TYPE> r;
+#pragma unroll
+  for (int i = 0; i < ElemSize<TYPE>::value / 2; ++i) ld_shared_v4(src + 512 * i, r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w);
+  unpack8<TYPE>(r, f);
+}
+template <int TYPE>
+constexpr int kChunkBytes = 512 * (ElemSize<TYPE>::value / 2);  // of a warp
+
+// A warp's items of a side, from `item` on in strides of the grid's warps: a
+// batch's token tile and a range of heads.
+struct Item {
+  int b, n, h0, h1;
+  bool there;  // this lane's token exists
+};
+__device__ __forceinline__ Item decode_item(const RopeArgs& a, const RopeSide& s, uint32_t item, int tokens,
+                                            int grp) {
+  Item t;
+  const uint32_t tile = item / static_cast<uint32_t>(s.hchunks);
+  t.b = static_cast<int>(tile / static_cast<uint32_t>(s.tiles));
+  t.n = static_cast<int>(tile - static_cast<uint32_t>(t.b) * s.tiles) * tokens + grp;
+  t.h0 = static_cast<int>(item - tile * s.hchunks) * a.hc;
+  t.h1 = min(s.H, t.h0 + a.hc);
+  t.there = item < s.items && t.n < s.N;
+  return t;
+}
+__device__ __forceinline__ int position(const RopeSide& s, const Item& t) {
+  return !t.there ? 0 : s.pos != nullptr ? __ldg(s.pos + t.b * s.pos_sb + t.n) : s.pos0 + t.n;
+}
+
+// Angles one item early, positions two.
+template <int D, bool INTER>
+struct Angles {
+  float c[8], s[8];
+  bool ok;    // the token exists, its position lies inside the tables
+};
+template <int D, bool INTER>
+__device__ __forceinline__ void fetch_angles(const RopeArgs& a, const Item& t, int pos, const LaneChunks& lc,
+                                             Angles<D, INTER>& g) {
+  g.ok = t.there;
+  if (g.ok && (pos < 0 || pos >= a.table_len)) {  // reported, its rows left unwritten
+    atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    g.ok = false;
+  }
+  if (lc.turned && g.ok) load_angles<INTER>(a.cos, a.sin, pos, a.rot, lc, g.c, g.s);
+}
+
+// Forward: one item per warp, four heads' loads in flight at a time. (Copies
+// through shared memory as in the backward gain nothing here: 238 us against
+// 239 at 65,521 tokens x 40 heads.)
 template <int TYPE, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2)
     streamkl_rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
@@ -214,15 +260,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   constexpr int TOKENS = 32 / LPR;     // tokens of a warp
   constexpr int UNROLL = 4;            // heads whose loads are in flight together
   const int lane = threadIdx.x & 31, grp = lane / LPR, l = lane % LPR;
-  long long item = static_cast<long long>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+  uint32_t item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
   const int k = item >= a.side[0].items;
-  if (k) item -= a.side[0].items;
+  if (k) item -= static_cast<uint32_t>(a.side[0].items);
   const RopeSide& s = a.side[k];
   if (item >= s.items) return;
   const LaneChunks lc = lane_chunks(l, a.rot);
   const Item t = decode_item(a, s, item, TOKENS, grp);
-  float c[8], sn[8];
-  if (lc.turned && t.ok) load_angles<INTER>(a.cos, a.sin, t.pos, a.rot, lc, c, sn);
+  Angles<D, INTER> g;
+  fetch_angles(a, t, position(s, t), lc, g);
   float w0[8], w1[8];
   const bool norm = s.w != nullptr;
   if (norm) {
@@ -235,7 +281,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     Raw8<TYPE> r0[UNROLL], r1[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
-      if (t.ok && h + u < t.h1) {
+      if (g.ok && h + u < t.h1) {
         r0[u] = load8<TYPE>(s.x, x0 + (h + u) * s.xs.sh + 8 * lc.c0);
         r1[u] = load8<TYPE>(s.x, x0 + (h + u) * s.xs.sh + 8 * lc.c1);
       } else {
@@ -255,8 +301,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
           f1[e] *= r * w1[e];
         }
       }
-      if (lc.turned) turn<INTER, false>(f0, f1, c, sn);
-      if (!t.ok) continue;
+      if (lc.turned) turn<INTER, false>(f0, f1, g.c, g.s);
+      if (!g.ok) continue;
       const Raw8<TYPE> o0 = pack8<TYPE>(f0), o1 = pack8<TYPE>(f1);
       for (int q = 0; q < s.rep; ++q) {
         const long long y = y0 + (static_cast<long long>(h + u) * s.rep + q) * s.ys.sh;
@@ -267,7 +313,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   }
 }
 
-// Persistent grid: each warp takes items with a fixed stride and keeps its
+// Backward, a persistent grid: each warp takes items with a fixed stride and keeps its
 // lanes' part of dw in registers, so the partials are one row per block and
 // their order of summation is the same in every run.
 template <int TYPE, int D, bool INTER>
@@ -275,99 +321,141 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     streamkl_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 16;
   constexpr int TOKENS = 32 / LPR;
-  constexpr int UNROLL = 2;
+  constexpr int STAGES = kBwdStages<TYPE>;
+  constexpr int SLOT = 4 * kChunkBytes<TYPE>;  // one repeat of a head: two chunks of dy, two of x with the first
+  extern __shared__ __align__(16) uint8_t stage_mem[];
   __shared__ float red[kRopeWarps][D];
+  __shared__ float ws[D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPR, l = lane % LPR;
+  const uint32_t mem = smem_u32(stage_mem) + warp * STAGES * SLOT + lane * 16;
   const LaneChunks lc = lane_chunks(l, a.rot);
+  const uint32_t stride = gridDim.x * kRopeWarps;
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const RopeSide& s = a.side[k];
     if (s.x == nullptr) continue;
     const bool norm = s.w != nullptr;
-    float w0[8], w1[8], dw0[8], dw1[8];
-    if (norm) {
-      load_f8(s.w + 8 * lc.c0, w0);
-      load_f8(s.w + 8 * lc.c1, w1);
-    }
+    if (norm && threadIdx.x < D) ws[threadIdx.x] = __ldg(s.w + threadIdx.x);
+    __syncthreads();
+    float dw0[8], dw1[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw0[e] = dw1[e] = 0.f;
-    for (long long item = static_cast<long long>(blockIdx.x) * kRopeWarps + warp; item < s.items;
-         item += static_cast<long long>(gridDim.x) * kRopeWarps) {
-      const Item t = decode_item(a, s, item, TOKENS, grp);
-      float c[8], sn[8];
-      if (lc.turned && t.ok) load_angles<INTER>(a.cos, a.sin, t.pos, a.rot, lc, c, sn);
-      const long long x0 = t.b * s.xs.sb + t.n * s.xs.sn;
-      const long long y0 = t.b * s.ys.sb + t.n * s.ys.sn;
-      const long long d0 = t.b * s.dxs.sb + t.n * s.dxs.sn;
-      for (int h = t.h0; h < t.h1; h += UNROLL) {
-        Raw8<TYPE> x0r[UNROLL], x1r[UNROLL], g0r[UNROLL], g1r[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          const bool on = t.ok && h + u < t.h1;
-          if (on && norm) {
-            x0r[u] = load8<TYPE>(s.x, x0 + (h + u) * s.xs.sh + 8 * lc.c0);
-            x1r[u] = load8<TYPE>(s.x, x0 + (h + u) * s.xs.sh + 8 * lc.c1);
-          } else {
-            x0r[u] = x1r[u] = Raw8<TYPE>{};
+    uint32_t item = blockIdx.x * kRopeWarps + warp;
+    if (k == 1) item = (item + stride - static_cast<uint32_t>(a.side[0].items % stride)) % stride;
+    if (item < s.items) {
+      // copies: the repeat that comes next
+      uint32_t p_item = item;
+      Item p = decode_item(a, s, p_item, TOKENS, grp);
+      int p_h = p.h0, p_q = 0, p_slot = 0;
+      long long p_x, p_y;
+      auto start = [&]() {
+        p_x = p.b * s.xs.sb + p.n * s.xs.sn + p.h0 * s.xs.sh;
+        p_y = p.b * s.ys.sb + p.n * s.ys.sn + static_cast<long long>(p.h0) * s.rep * s.ys.sh;
+      };
+      start();
+      auto issue = [&]() {
+        if (p_item < s.items) {
+          if (p.there) {
+            const uint32_t dst = mem + p_slot * SLOT;
+            copy8<TYPE>(dst, s.y_in, p_y + 8 * lc.c0);
+            copy8<TYPE>(dst + kChunkBytes<TYPE>, s.y_in, p_y + 8 * lc.c1);
+            if (norm && p_q == 0) {
+              copy8<TYPE>(dst + 2 * kChunkBytes<TYPE>, s.x, p_x + 8 * lc.c0);
+              copy8<TYPE>(dst + 3 * kChunkBytes<TYPE>, s.x, p_x + 8 * lc.c1);
+            }
           }
-          if (on) {
-            const long long y = y0 + static_cast<long long>(h + u) * s.rep * s.ys.sh;
-            g0r[u] = load8<TYPE>(s.y_in, y + 8 * lc.c0);
-            g1r[u] = load8<TYPE>(s.y_in, y + 8 * lc.c1);
-          } else {
-            g0r[u] = g1r[u] = Raw8<TYPE>{};
+          p_y += s.ys.sh;
+          if (++p_q == s.rep) {
+            p_q = 0;
+            p_x += s.xs.sh;
+            if (++p_h == p.h1) {
+              p_item += stride;
+              p = decode_item(a, s, p_item, TOKENS, grp);
+              p_h = p.h0;
+              start();
+            }
           }
         }
+        p_slot = p_slot + 1 == STAGES ? 0 : p_slot + 1;
+        copies_commit();
+      };
+      Item t = decode_item(a, s, item, TOKENS, grp), t1 = decode_item(a, s, item + stride, TOKENS, grp);
+      const int pos0 = position(s, t);
+      int pos1 = position(s, t1);
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          if (h + u >= t.h1) break;
-          float g0[8], g1[8];
-          unpack8<TYPE>(g0r[u], g0);
-          unpack8<TYPE>(g1r[u], g1);
+      for (int i = 0; i < STAGES - 1; ++i) issue();
+      Angles<D, INTER> now, next;
+      fetch_angles(a, t, pos0, lc, now);
+      int slot = 0;
+      for (; item < s.items; item += stride) {
+        fetch_angles(a, t1, pos1, lc, next);
+        const Item t2 = decode_item(a, s, item + 2 * stride, TOKENS, grp);
+        pos1 = position(s, t2);
+        long long dx = t.b * s.dxs.sb + t.n * s.dxs.sn + t.h0 * s.dxs.sh;
+        for (int h = t.h0; h < t.h1; ++h, dx += s.dxs.sh) {
+          copies_wait<STAGES - 2>();
+          float g0[8], g1[8], f0[8], f1[8];
+          read8<TYPE>(mem + slot * SLOT, g0);
+          read8<TYPE>(mem + slot * SLOT + kChunkBytes<TYPE>, g1);
+          if (norm) {
+            read8<TYPE>(mem + slot * SLOT + 2 * kChunkBytes<TYPE>, f0);
+            read8<TYPE>(mem + slot * SLOT + 3 * kChunkBytes<TYPE>, f1);
+          }
+          slot = slot + 1 == STAGES ? 0 : slot + 1;
+          issue();
           for (int q = 1; q < s.rep; ++q) {
-            if (!t.ok) break;
-            const long long y = y0 + (static_cast<long long>(h + u) * s.rep + q) * s.ys.sh;
+            copies_wait<STAGES - 2>();
             float e0[8], e1[8];
-            unpack8<TYPE>(load8<TYPE>(s.y_in, y + 8 * lc.c0), e0);
-            unpack8<TYPE>(load8<TYPE>(s.y_in, y + 8 * lc.c1), e1);
+            read8<TYPE>(mem + slot * SLOT, e0);
+            read8<TYPE>(mem + slot * SLOT + kChunkBytes<TYPE>, e1);
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            issue();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               g0[e] += e0[e];
               g1[e] += e1[e];
             }
           }
-          if (lc.turned) turn<INTER, true>(g0, g1, c, sn);
+          if (lc.turned) turn<INTER, true>(g0, g1, now.c, now.s);
           if (norm) {
-            float f0[8], f1[8];
-            unpack8<TYPE>(x0r[u], f0);
-            unpack8<TYPE>(x1r[u], f1);
-            float dot = 0.f, dot1 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              dot = fmaf(g0[e] * w0[e], f0[e], dot);
-              dot1 = fmaf(g1[e] * w1[e], f1[e], dot1);
-            }
             const float r = rsqrtf(row_sum<LPR>(sum_sq(f0, f1)) * (1.f / D) + a.eps);
-            const float m = row_sum<LPR>(dot + dot1) * (1.f / D) * r * r;
-            if (t.ok) {  // (a row that is absent has r = rsqrt(eps), infinite at eps = 0)
+            if (now.ok) {  // (a row that is absent holds anything)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 dw0[e] = fmaf(g0[e] * r, f0[e], dw0[e]);
                 dw1[e] = fmaf(g1[e] * r, f1[e], dw1[e]);
               }
             }
+            float w0[8], w1[8];
+            *reinterpret_cast<float4*>(&w0[0]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c0]);
+            *reinterpret_cast<float4*>(&w0[4]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c0 + 4]);
+            *reinterpret_cast<float4*>(&w1[0]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c1]);
+            *reinterpret_cast<float4*>(&w1[4]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c1 + 4]);
+            float dot = 0.f, dot1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              g0[e] = r * (g0[e] * w0[e] - f0[e] * m);
-              g1[e] = r * (g1[e] * w1[e] - f1[e] * m);
+              g0[e] *= w0[e];
+              g1[e] *= w1[e];
+              dot = fmaf(g0[e], f0[e], dot);
+              dot1 = fmaf(g1[e], f1[e], dot1);
+            }
+            const float m = row_sum<LPR>(dot + dot1) * (1.f / D) * r * r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              g0[e] = r * (g0[e] - f0[e] * m);
+              g1[e] = r * (g1[e] - f1[e] * m);
             }
           }
-          if (t.ok) {
-            store8<TYPE>(s.dx, d0 + (h + u) * s.dxs.sh + 8 * lc.c0, pack8<TYPE>(g0));
-            store8<TYPE>(s.dx, d0 + (h + u) * s.dxs.sh + 8 * lc.c1, pack8<TYPE>(g1));
+          if (now.ok) {
+            store8<TYPE>(s.dx, dx + 8 * lc.c0, pack8<TYPE>(g0));
+            store8<TYPE>(s.dx, dx + 8 * lc.c1, pack8<TYPE>(g1));
           }
         }
+        t = t1;
+        t1 = t2;
+        now = next;
       }
+      copies_wait<0>();
     }
     if (!norm) continue;  // (uniform in the grid)
 #pragma unroll
@@ -391,6 +479,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     }
     __syncthreads();
   }
+  grid_launch_dependents();  // the sum of the partials may be launched
 }
 
 // Sum the partials [2][blocks][D] over the blocks; a block takes 32 columns
@@ -398,6 +487,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 __global__ void __launch_bounds__(1024)
     streamkl_rope_dw_kernel(const float* __restrict__ part, int blocks, int D, float* dw_q, float* dw_k) {
   __shared__ float red[32][33];
+  grid_dependency_wait();  // launched while the backward ends
   float* out = blockIdx.y ? dw_k : dw_q;
   if (out == nullptr) return;
   const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
@@ -522,7 +612,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 // often, from L2).
 int head_chunk(long long tiles, int heads, int sms) {
   int hc = 16;
-  while (hc > 1 && tiles * ((heads + hc - 1) / hc) < 8LL * 2 * sms) hc >>= 1;
+  while (hc > 1 && tiles * ((heads + hc - 1) / hc) < 32LL * sms) hc >>= 1;
   return std::min(hc, heads);
 }
 
@@ -556,10 +646,11 @@ cudaError_t rope_fwd_t(const RopeArgs& a, unsigned blocks, cudaStream_t stream) 
 
 template <int TYPE, int D>
 cudaError_t rope_bwd_t(const RopeArgs& a, unsigned blocks, cudaStream_t stream) {
-  if (a.interleaved)
-    streamkl_rope_bwd_kernel<TYPE, D, true><<<blocks, kRopeThreads, 0, stream>>>(a);
-  else
-    streamkl_rope_bwd_kernel<TYPE, D, false><<<blocks, kRopeThreads, 0, stream>>>(a);
+  constexpr int bytes = kRopeWarps * kBwdStages<TYPE> * 4 * kChunkBytes<TYPE>;
+  auto kern = a.interleaved ? streamkl_rope_bwd_kernel<TYPE, D, true> : streamkl_rope_bwd_kernel<TYPE, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, kRopeThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -579,7 +670,7 @@ int rope_bwd_blocks(int B, int NQ, int HQ, int NK, int HK, int d, int sms) {
   const int hc = rope_head_chunk(B, NQ, HQ, NK, HK, d, sms);
   const long long iq = static_cast<long long>(B) * ((NQ + tokens - 1) / tokens) * ((HQ + hc - 1) / hc);
   const long long ik = static_cast<long long>(B) * ((NK + tokens - 1) / tokens) * ((HK + hc - 1) / hc);
-  const long long want = (std::max(iq, ik) + kRopeWarps - 1) / kRopeWarps;
+  const long long want = (iq + ik + kRopeWarps - 1) / kRopeWarps;
   return static_cast<int>(std::max(1LL, std::min<long long>(want, 2LL * sms)));
 }
 
@@ -613,8 +704,17 @@ cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, int sms, float* dw_q, float
         : a.type == kTypeF16 ? rope_bwd_t<kTypeF16, 64>(a, n, stream)
                              : rope_bwd_t<kTypeF32, 64>(a, n, stream);
   if (e != cudaSuccess || (dw_q == nullptr && dw_k == nullptr)) return e;
-  streamkl_rope_dw_kernel<<<dim3(a.d / 32, 2), 1024, 0, stream>>>(a.part, blocks, a.d, dw_q, dw_k);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.d / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const float* part = a.part;
+  return cudaLaunchKernelEx(&cfg, streamkl_rope_dw_kernel, part, blocks, a.d, dw_q, dw_k);
 }
 
 cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream) {
