@@ -20,7 +20,7 @@ static_assert(STREAMKL_BF16 == skl::kTypeBf16 && STREAMKL_FP16 == skl::kTypeF16 
                   STREAMKL_FP32 == skl::kTypeF32,
               "element types of the header and the kernels agree");
 
-constexpr long long kMaxRows = 1LL << 31;  // rows (tokens x heads) of one tensor
+constexpr long long kMaxRows = 1LL << 30;  // rows (tokens x heads) of one tensor
 
 size_t elem_size(int dtype) { return dtype == STREAMKL_FP32 ? 4 : 2; }
 
@@ -87,7 +87,7 @@ streamkl_status rope_common(skl::RopeArgs* a, streamkl_rope_args* u, bool backwa
   if (!k) u->NK = u->HK = 0;
   if (static_cast<long long>(u->NQ) * u->HQ > kMaxRows / u->B ||
       static_cast<long long>(u->NK) * u->HK > kMaxRows / u->B / u->k_repeat)
-    return fail(STREAMKL_ERR_UNSUPPORTED, "rows x heads above 2^31");
+    return fail(STREAMKL_ERR_UNSUPPORTED, "tokens x heads above 2^30");
   if (q && k && !u->q_positions && u->NQ > u->NK)
     return fail(STREAMKL_ERR_INVALID_ARG, "more queries than keys (%d > %d) need q_positions", u->NQ, u->NK);
   if (!u->dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
@@ -145,8 +145,7 @@ streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* tab
   if (static_cast<long long>(max_pages) * page_size > (1LL << 30))
     return fail(STREAMKL_ERR_UNSUPPORTED, "sequence length above 2^30");
   if (!table || !kv_lens) return fail(STREAMKL_ERR_INVALID_ARG, "block_table and kv_lens must be non-NULL");
-  if (table_stride < max_pages && B > 1)
-    return fail(STREAMKL_ERR_INVALID_ARG, "block_table rows overlap (stride %lld, %d pages)", table_stride, max_pages);
+  if (table_stride < 0) return fail(STREAMKL_ERR_INVALID_ARG, "block_table stride %lld", table_stride);
   if (!cu_seqlens && T != B)
     return fail(STREAMKL_ERR_INVALID_ARG, "without cu_seqlens each sequence has one token (T=%d B=%d)", T, B);
   streamkl_status st = check_rows("k_cache", kc, num_pages, HK, page_size, d, dtype, true);
@@ -291,7 +290,10 @@ streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* st
   streamkl_status st = check_cache(&u.k_cache, &u.v_cache, u.block_table, u.table_stride, u.kv_lens, u.cu_seqlens,
                                    u.dtype, u.B, u.T, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
   if (st != STREAMKL_OK) return st;
-  if (static_cast<long long>(u.T) * u.HK > kMaxRows) return fail(STREAMKL_ERR_UNSUPPORTED, "rows x heads above 2^31");
+  if (u.table_stride < u.max_pages && u.B > 1)  // (to read them the sequences may share a row)
+    return fail(STREAMKL_ERR_INVALID_ARG, "block_table rows overlap (stride %lld, %d pages)", u.table_stride,
+                u.max_pages);
+  if (static_cast<long long>(u.T) * u.HK > kMaxRows) return fail(STREAMKL_ERR_UNSUPPORTED, "tokens x heads above 2^30");
   if ((st = check_rows("k", &u.k, 0, u.T, u.HK, u.d, u.dtype, false)) != STREAMKL_OK) return st;
   if ((st = check_rows("v", &u.v, 0, u.T, u.HK, u.d, u.dtype, false)) != STREAMKL_OK) return st;
   if ((u.cos == nullptr) != (u.sin == nullptr))
@@ -401,6 +403,10 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   a.split_tiles = p.split_tiles;
+  // more than one CTA per SM one after the other: long ones first, so that the
+  // last to start are short (four ragged chunks of up to 2,048 rows over 16,384
+  // keys, d = 64: 250 us against 258)
+  a.by_length = u.B > 1 && u.B <= 32 && static_cast<long long>(p.q_tiles) * u.B * u.HK > num_sms();
   a.part_o = static_cast<float*>(u.workspace);
   a.part_lse = a.part_o ? a.part_o + attn_part_rows(p, u.T, u.HQ) * u.d : nullptr;
   a.dev_status = u.dev_status;

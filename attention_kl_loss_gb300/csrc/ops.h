@@ -88,6 +88,7 @@ struct PagedAttnArgs {
   int q_tiles;               // query tiles of a (sequence, key head)
   int row_tiles;             // 128-row tiles of a CTA (1 or 2)
   int splits, split_tiles;   // key splits and key tiles of one
+  int by_length;             // the longest sequences' CTAs first (at most 32 sequences)
   float* part_o;             // [splits][T][HQ][d]; null without splits
   float* part_lse;           // [splits][T][HQ], log2 units
   int* dev_status;

@@ -9,35 +9,44 @@
 //
 // One pass over the key tiles (128 keys) with the running reference and sum
 // of the softmax, S = Q K^T and O += P V as tcgen05 MMAs:
-//   S (fp32, TMEM) -> registers -> P = 2^(c s - ref) in the inputs' type,
-//   written over S's columns, from where it is the PV product's A operand.
+//   S (fp32, TMEM) -> registers -> P = 2^(c s - ref) in the inputs' type (TMEM,
+//   the PV product's A operand).
 // P has 8 (bf16) or 11 (fp16) bits: its rounding is the size of the output's
 // own. ref, the sum (of unrounded terms) and O are fp32. The reference moves
-// only when a tile's maximum exceeds it by more than 2^8, so O is seldom
-// rescaled; the results do not depend on it.
+// only when terms would exceed 2^8 of it, so O is seldom rescaled; the results
+// do not depend on it.
 //
 // CTA: warp 0 loads (each lane one page's box of a tile; pages are found
 // through the block table), warp 1 issues MMAs, warps 4.. are one softmax
-// warpgroup per row tile, thread = row.
-// Two row tiles (NT = 2) share each K and V tile and the tensor pipe works on
-// one while the other's softmax runs. With at most 128 rows (NT = 1) the keys
-// are what costs; S is then double-buffered. Few rows against many keys are
-// split over the keys; a combine kernel joins the splits by their lse.
+// warpgroup per row tile, thread = row. Two row tiles (NT = 2) share each K and
+// V tile. At d = 128 their O fill half of TMEM and P has to take S's place:
+// the tiles alternate, the tensor pipe works on one while the other's softmax
+// runs. At d = 64, or with one row tile, P has columns of its own and the next
+// S is made while this one's terms are.
+//
+// Bound by the tensor pipe at d = 128: 512 rows x 32 heads against 131,072 keys
+// take 0.72 ms, 1.53 PFLOP/s. The 16 products of 128 x 128 x 128 per pair of
+// tiles take 2,048 cycles if nothing holds them up, a turn takes 2,900; tried
+// and not faster: two softmax warpgroups per row tile (936 us), an issuing
+// thread per row tile (765 us), L2 prefetches (738 us). At d = 64 a product has
+// half the work and takes the same time (82 cycles for 128 x 64 x 16), so the
+// rate halves.
+//
+// With few query tiles the keys are split over CTAs and a combine kernel joins
+// the splits by their lse.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "ops.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace skl {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTau = 8.0f;  // log2 units
-constexpr float kSumMax = 256.0f;  // 2^kTau
-constexpr int kTileM = 128, kTileN = 128;
+constexpr int kTileM = 128;  // rows per tile
 
 template <int D, int NT>
 struct AttnLayout {
@@ -55,25 +64,12 @@ struct AttnLayout {
   static constexpr int NBAR = 2 + 2 * STAGES + 9;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
-  static constexpr int ALLOC = BYTES;  // (the base is declared 1024-byte aligned)
-  static_assert(ALLOC <= 232448, "shared memory budget");
+  static_assert(BYTES <= 232448, "shared memory budget");
   static constexpr int THREADS = 128 + 128 * NT;
   static constexpr int col_s(int t) { return 128 * t; }
   static constexpr int col_p(int t) { return OWN_P ? 128 * NT + 64 * t : 128 * t; }
   static constexpr int col_o(int t) { return (OWN_P ? 192 : 128) * NT + D * t; }
   static_assert(col_o(NT - 1) + D <= 512, "TMEM columns");
-};
-
-// A place in the ring of K and V stages and the parity of its turn.
-struct RingPos {
-  int stage;
-  uint32_t phase;
-  __device__ __forceinline__ void step(int stages) {
-    if (++stage == stages) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
 };
 
 // What a CTA works on: one sequence's rows of one key head, a range of keys.
@@ -108,15 +104,10 @@ __device__ __forceinline__ Work find_work(const PagedAttnArgs& a, int b, int G, 
   return w;
 }
 
-template <int TYPE>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-}
-
-// A bounded wait of a whole warp: false for all lanes where any gave up, so
-// that the warp stays together for its .aligned instructions.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
-  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, wc));
+// Lane `from`'s pointer.
+template <typename T>
+__device__ __forceinline__ T* shfl_ptr(T* p, int from) {
+  return reinterpret_cast<T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(p), from));
 }
 
 // One row of the output: finished (o, lse) or a split's partial.
@@ -143,7 +134,18 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   const uint32_t sb = smem_u32(gb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.HQ / a.HK;
-  const int b = static_cast<int>(blockIdx.z) / a.HK, hk = static_cast<int>(blockIdx.z) - b * a.HK;
+  int b = static_cast<int>(blockIdx.z) / a.HK;
+  const int hk = static_cast<int>(blockIdx.z) - b * a.HK;
+  if (a.by_length) {  // (at most 32 sequences) the b-th longest
+    const int len = lane < a.B ? __ldg(a.kv_lens + lane) : INT_MIN;
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const int other = __shfl_sync(0xFFFFFFFFu, len, i);
+      rank += other > len || (other == len && i < lane);
+    }
+    b = __ffs(__ballot_sync(0xFFFFFFFFu, rank == b)) - 1;
+  }
   const Work w = find_work(a, b, G, kTileM * NT);
   if (!w.ok && threadIdx.x == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
   if (w.row0 >= w.rows) return;
@@ -391,15 +393,23 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     const int tok = live ? row / G : 0;
     const int token = w.tok0 + tok, head = hk * G + (live ? row - tok * G : 0);
     if (n_iter > 0) {
-      // this row of Q, 128-byte swizzled as TMA would place it; rows that are
-      // not there are zero
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + token * a.q_sn + head * a.q_sh);
-      const uint32_t dst = sb + L::OFF_Q + t * L::TILE + r_tile * 128;
+      // this warp's rows of Q, D / 8 lanes a row, 128-byte swizzled as TMA would
+      // place them; rows that are not there are zero
+      constexpr int LPR = D / 8, RPI = 32 / LPR;
+      const int cq = lane % LPR;
+      const uint16_t* mine = live ? static_cast<const uint16_t*>(a.q) + token * a.q_sn + head * a.q_sh : nullptr;
+      uint4 v[LPR];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = __ldg(src + c);
-        st_shared_v4(dst + (c >> 3) * L::BOX + (((c & 7) ^ (r_tile & 7)) << 4), v.x, v.y, v.z, v.w);
+      for (int i = 0; i < LPR; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (row_q != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(row_q) + cq);
+      }
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        const int r = (warp & 3) * 32 + i * RPI + lane / LPR;
+        st_shared_v4(sb + L::OFF_Q + t * L::TILE + (cq >> 3) * L::BOX + r * 128 + (((cq & 7) ^ (r & 7)) << 4), v[i].x,
+                     v[i].y, v[i].z, v[i].w);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -553,6 +563,26 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       const bool none = l == 0.f;
       const long long e = static_cast<long long>(token) * a.HQ + head;
       const long long plane = static_cast<long long>(blockIdx.y) * a.T * a.HQ;
+      // The rows go out through shared memory (this warp's part of Q's tile,
+      // which no product reads any more), 128 bytes of each at a time, so that
+      // eight lanes write a row's line together
+      const uint32_t stage = sb + L::OFF_Q + t * L::TILE + (warp & 3) * 32 * 128;
+      const bool parts = a.splits > 1;
+      uint8_t* mine = !live  ? nullptr
+                      : parts ? reinterpret_cast<uint8_t*>(a.part_o + (plane + e) * D)
+                              : reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
+      auto write_out = [&](int byte) {  // 128 bytes of each row from this one on
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int r = i + (lane >> 3);
+          uint8_t* row_out = shfl_ptr(mine, r);
+          uint4 v;
+          ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+          if (row_out != nullptr) *reinterpret_cast<uint4*>(row_out + byte + (lane & 7) * 16) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
@@ -560,18 +590,19 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = none ? 0.f : o[k] * inv;
-        if (live) {
-          if (a.splits > 1) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (plane + e) * D + 32 * q);
+        if (parts) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + 32 * q);
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(stage + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]),
+                         __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+          write_out(128 * q);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_uint4(pack2<TYPE>(o[8 * k], o[8 * k + 1]), pack2<TYPE>(o[8 * k + 2], o[8 * k + 3]),
-                                  pack2<TYPE>(o[8 * k + 4], o[8 * k + 5]), pack2<TYPE>(o[8 * k + 6], o[8 * k + 7]));
-          }
+          for (int k = 0; k < 4; ++k)
+            st_shared_v4(stage + lane * 128 + (((4 * (q & 1) + k) ^ (lane & 7)) << 4), pack2<TYPE>(o[8 * k], o[8 * k + 1]),
+                         pack2<TYPE>(o[8 * k + 2], o[8 * k + 3]), pack2<TYPE>(o[8 * k + 4], o[8 * k + 5]),
+                         pack2<TYPE>(o[8 * k + 6], o[8 * k + 7]));
+          if (q & 1) write_out(64 * (q - 1));
         }
       }
       if (live) {
@@ -656,11 +687,11 @@ cudaError_t attn_t(const PagedAttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
-  kern<<<dim3(a.q_tiles, a.splits, a.B * a.HK), L::THREADS, L::ALLOC, stream>>>(*a.tm_k, *a.tm_v, a);
+  kern<<<dim3(a.q_tiles, a.splits, a.B * a.HK), L::THREADS, L::BYTES, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   const long long rows = static_cast<long long>(a.T) * a.HQ;

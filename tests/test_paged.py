@@ -353,6 +353,18 @@ def test_single_tokens_without_offsets():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 40])
+def test_sequences_may_share_one_row_of_pages(n):
+    """Several continuations of one prefix: a broadcast row of the block table."""
+    c = Cache([333], 2, 64, 16, torch.bfloat16)
+    q = torch.randn(3 * n, 4, 64, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    lens = torch.full((3,), 333, dtype=torch.int32, device="cuda")
+    a = skl.streamkl_paged_attn(q, c.k, c.v, c.table.expand(3, -1), lens, cu_seqlens=_cu([n] * 3), max_seqlen_q=n)
+    b = skl.streamkl_paged_attn(q, c.k, c.v, c.table.repeat(3, 1), lens, cu_seqlens=_cu([n] * 3), max_seqlen_q=n)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
 def test_nan_in_one_sequence_stays_there():
     lens = [200, 200]
     c = Cache(lens, 1, 64, 16, torch.bfloat16)
@@ -413,7 +425,8 @@ def test_attention_reports_what_does_not_fit(what):
 
 
 @pytest.mark.gpu
-def test_cache_lives_through_prefill_and_captured_decode_steps():
+@pytest.mark.parametrize("splits", [0, 2])
+def test_cache_lives_through_prefill_and_captured_decode_steps(splits):
     """A chunk of new tokens, then single tokens: norm + rotation of the
     queries, append, attention. The decode step is captured once and replayed,
     lengths advancing on the device; each step equals the eager calls bit for
@@ -444,10 +457,10 @@ def test_cache_lives_through_prefill_and_captured_decode_steps():
         skl.streamkl_paged_append(k, v, *caches, table, lens, cu_seqlens=cu_seqlens, cos=cos, sin=sin, k_weight=wk,
                                   eps=eps, dev_status=st)
         return skl.streamkl_paged_attn(q, *caches, table, lens, cu_seqlens=cu_seqlens, max_seqlen_q=n,
-                                       num_splits=2, out=out, workspace=ws, dev_status=st)
+                                       num_splits=splits, out=out, workspace=ws, dev_status=st)
 
     pos = torch.cat([torch.arange(n) for n in start]).to(torch.int32).to(dev)
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device=dev)
 
     def prefill(caches):
         lens = torch.tensor(start, dtype=torch.int32, device=dev)
@@ -509,6 +522,36 @@ def test_on_another_stream_and_the_same_in_every_run():
     for _ in range(3):
         b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 40])
+def test_two_captured_calls_at_once(n):
+    """Two graphs with a workspace each, replayed on two streams side by side."""
+    lens = [900, 3000]
+    c = Cache(lens, 2, 128, 32, torch.bfloat16)
+    st = binding.new_status()
+    graphs = []
+    for seed in (0, 1):
+        q = torch.randn(2 * n, 8, 128, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+        kw = dict(cu_seqlens=_cu([n, n]), max_seqlen_q=n, max_kv_len=3000, dev_status=st)
+        ref = [t.clone() for t in skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)]
+        kw["out"] = (torch.empty_like(ref[0]), torch.empty_like(ref[1]))
+        kw["workspace"] = torch.empty(skl.streamkl_paged_attn_workspace_size(2, 2 * n, 8, 2, 128, n, 3000),
+                                      dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)
+        graphs.append((graph, torch.cuda.Stream(), kw, ref, q))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream, *_ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    binding.raise_on_device_status(st)
+    for _, _, kw, ref, _ in graphs:
+        assert all(torch.equal(x, y) for x, y in zip(kw["out"], ref))
 
 
 @pytest.mark.gpu
@@ -584,7 +627,7 @@ def _raw(cls, over, **base):
 CACHE_REFUSED = [
     (dict(struct_size=8), 1), (dict(dtype=2), 2), (dict(d=80), 2), (dict(B=0), 1), (dict(T=0), 1), (dict(HK=0), 1),
     (dict(num_pages=0), 1), (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=2048), 2),
-    (dict(max_pages=1 << 27), 2), (dict(table_stride=3), 1), (dict(block_table=None), 1), (dict(kv_lens=None), 1),
+    (dict(max_pages=1 << 27), 2), (dict(table_stride=-1), 1), (dict(block_table=None), 1), (dict(kv_lens=None), 1),
     (dict(cu_seqlens=None), 1), (dict(k_cache__data=None), 1), (dict(v_cache__data=4100), 1),
     (dict(k_cache__stride=(2048, 1024, 60)), 1), (dict(k_cache__stride=(2048, 1024, 0)), 1),
     (dict(v_cache__stride=(0, 1024, 64)), 1), (dict(dev_status=None), 1),
@@ -592,7 +635,8 @@ CACHE_REFUSED = [
 
 
 @pytest.mark.parametrize("over,status", CACHE_REFUSED + [
-    (dict(k__data=4104), 1), (dict(v__data=None), 1), (dict(k__stride=(0, -128, 64)), 1), (dict(cos=None), 1),
+    (dict(table_stride=3), 1), (dict(k__data=4104), 1), (dict(v__data=None), 1), (dict(k__stride=(0, -128, 64)), 1),
+    (dict(cos=None), 1),
     (dict(rot=8), 2), (dict(rot=72), 2), (dict(table_len=0), 1), (dict(eps=-1.0), 1),
     (dict(eps=-1.0, cos=None, sin=None), 1), (dict(interleaved=2), 1), (dict(T=1 << 30, HK=4), 2),
     (dict(k_weight=4104), 1),
