@@ -606,13 +606,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   }
 }
 
-// Head chunks: up to 16 heads a warp (238 us against 255 with 8 and 299 with 4
-// at 65,521 tokens x 40 heads: the angles are loaded less often), fewer when
-// there are too few warps to fill the GPU (the angles are then loaded more
-// often, from L2).
-int head_chunk(long long tiles, int heads, int sms) {
+// Head chunks: up to 16 heads a warp (the forward at 65,521 tokens x 40 heads
+// takes 238 us, 255 with 8 and 299 with 4: the angles are loaded less often),
+// fewer when there are not `per_sm` warps' items an SM to fill the GPU with.
+int head_chunk(long long tiles, int heads, int per_sm, int sms) {
   int hc = 16;
-  while (hc > 1 && tiles * ((heads + hc - 1) / hc) < 32LL * sms) hc >>= 1;
+  while (hc > 1 && tiles * ((heads + hc - 1) / hc) < static_cast<long long>(per_sm) * sms) hc >>= 1;
   return std::min(hc, heads);
 }
 
@@ -632,7 +631,7 @@ long long side_items(RopeSide& s, int B, int d, int hc) {
 int rope_head_chunk(int B, int NQ, int HQ, int NK, int HK, int d, int sms) {
   const int tokens = 32 / (d / 16);
   const long long tiles = static_cast<long long>(B) * ((std::max(NQ, NK) + tokens - 1) / tokens);
-  return head_chunk(tiles, HQ + HK, sms);
+  return head_chunk(tiles, HQ + HK, 32, sms);  // (16: the backward at 8,192 tokens x 32 heads 56 us, with 32 54)
 }
 
 template <int TYPE, int D>
@@ -720,7 +719,7 @@ cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, int sms, float* dw_q, float
 cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream) {
   const int tokens = 32 / (a.d / 16);
   const long long tiles = (a.T + tokens - 1) / tokens;
-  a.hc = head_chunk(tiles, 2 * a.H, sms);
+  a.hc = head_chunk(tiles, 2 * a.H, 16, sms);  // (32: 10,000 tokens x 8 heads 24.6 us, with 16 22.5)
   a.hc = std::min(a.hc, a.H);
   a.hchunks = (a.H + a.hc - 1) / a.hc;
   const long long items = tiles * 2 * a.hchunks;

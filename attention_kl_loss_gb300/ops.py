@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from .binding import _check, load, new_status
+from .binding import StreamKLError, _check, load, new_status
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 # the current stream's handle without making a Stream object (2 us of a call
@@ -420,12 +420,21 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     if total == 0 or HQ == 0:
         return o, lse
     lib = load()
-    need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
-    ws = _workspace(need, dev, workspace)
+    if workspace is None:
+        need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     args = _ATTN.pack(_ATTN.size, q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(),
-                      ws.data_ptr() if need else 0, need, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q,
+                      workspace.data_ptr(), workspace.nbytes, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q,
                       max_kv, bool(causal), num_splits, 1.0 / math.sqrt(d) if scale is None else scale)
     st = lib.streamkl_paged_attn(args, _stream(stream, index))
     if st:
-        _check(st, "streamkl_paged_attn")
+        try:
+            _check(st, "streamkl_paged_attn")
+        except StreamKLError as error:
+            need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+            if workspace.nbytes < need:
+                raise ValueError(f"workspace too small: need {need} bytes") from error
+            raise
     return o, lse
