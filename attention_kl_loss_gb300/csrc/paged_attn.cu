@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
   ck.tmem = tmem;
   ck.tmem_cols = 512;
   const WaitCtx wc{abort_flag, a.dev_status, a.timeout_ns};
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
     // descriptors are a constant high word and a running low word, the loads
     // are consumed in the order of their ring, and the stages are released by
     // the softmax warps (a commit for each would hold the issuer up).
-    if (lane == 0 && n_iter > 0) {
+    if (n_iter > 0 && elect_one()) {
       constexpr uint32_t id_s = TYPE == kTypeBf16 ? idesc_bf16(kTileM, kTileN, 0, 0) : idesc_f16(kTileM, kTileN, 0, 0);
       constexpr uint32_t id_o = TYPE == kTypeBf16 ? idesc_bf16(kTileM, D, 0, 1) : idesc_f16(kTileM, D, 0, 1);
       const uint64_t q0 = smem_desc_sw128(sb + L::OFF_Q, 16, 1024);

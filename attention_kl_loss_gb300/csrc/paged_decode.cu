@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
   st.b = start->b;
   st.hk = start->hk;
   st.tile = start->tile;
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t id_s = TYPE == kTypeBf16 ? idesc_bf16(128, kTileN, 0, 0) : idesc_f16(128, kTileN, 0, 0);
       constexpr uint32_t id_o = TYPE == kTypeBf16 ? idesc_bf16(128, D, 0, 1) : idesc_f16(128, D, 0, 1);
       const uint64_t q0 = smem_desc_sw128(sb + L::OFF_Q, 16, 1024);
