@@ -24,13 +24,13 @@
 // runs. At d = 64, or with one row tile, P has columns of its own and the next
 // S is made while this one's terms are.
 //
-// Bound by the tensor pipe at d = 128: 512 rows x 32 heads against 131,072 keys
-// take 0.72 ms, 1.53 PFLOP/s. The 16 products of 128 x 128 x 128 per pair of
-// tiles take 2,048 cycles if nothing holds them up, a turn takes 2,900; tried
-// and not faster: two softmax warpgroups per row tile (936 us), an issuing
-// thread per row tile (765 us), L2 prefetches (738 us). At d = 64 a product has
-// half the work and takes the same time (82 cycles for 128 x 64 x 16), so the
-// rate halves.
+// At d = 128 512 rows x 32 heads against 131,072 keys take 0.71 ms, 1.55 PFLOP/s:
+// 2,900 cycles a turn (a key tile for both row tiles), of which the 32 products
+// take 2,048 back to back, as the 256 KB of operands and loads at 128 bytes a
+// cycle do; a row tile's own chain, S, terms (1,330), P, PV, is what is left.
+// Tried and not faster: two softmax warpgroups per row tile (936 us), an issuing
+// thread per row tile (765 us), L2 prefetches (738 us). At d = 64 the terms are
+// half of a turn: 2,700 cycles, the exponentials alone 1,024, the products 1,050.
 //
 // With few query tiles the keys are split over CTAs and a combine kernel joins
 // the splits by their lse.
@@ -300,10 +300,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    // One thread issues every product, so its own instructions count: the
-    // descriptors are a constant high word and a running low word, the loads
-    // are consumed in the order of their ring, and the stages are released by
-    // the softmax warps (a commit for each would hold the issuer up).
+    // One thread issues every product, so its own instructions count: it waits
+    // for P and S only (with them come the loads), the stages are released by
+    // the softmax warps, and its branch is taken under elect.sync (729 -> 710 us
+    // at the 131,072 keys above).
     if (n_iter > 0 && elect_one()) {
       constexpr uint32_t id_s = TYPE == kTypeBf16 ? idesc_bf16(kTileM, kTileN, 0, 0) : idesc_f16(kTileM, kTileN, 0, 0);
       constexpr uint32_t id_o = TYPE == kTypeBf16 ? idesc_bf16(kTileM, D, 0, 1) : idesc_f16(kTileM, D, 0, 1);
