@@ -32,19 +32,17 @@ _APPEND = struct.Struct("N" + 4 * _ROWS + "PqPPPPPP11if")
 _ATTN = struct.Struct("N" + 4 * _ROWS + "PqPPPPNP13if")
 
 
-def _on_device(call, device, kwargs):
-    """Run ``call`` with ``device`` current: launches and tensor maps go to
-    the current device."""
-    with torch.cuda.device(device):
-        return call(**kwargs)
-
-
-def _stream(stream, index):
+def _elsewhere(call, device, stream, kwargs):
+    """Run ``call`` with ``device`` current (launches and tensor maps go to the
+    current device) and ``stream``, if given, the current stream: what the call
+    allocates then belongs to the stream that its kernels run on."""
     if stream is None:
-        return _raw_stream(index)
-    if stream.device.index != index:
-        raise ValueError(f"stream of {stream.device} for tensors on cuda:{index}")
-    return stream.cuda_stream
+        with torch.cuda.device(device):
+            return call(**kwargs)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    with torch.cuda.stream(stream):  # (and its device)
+        return call(**kwargs)
 
 
 # The checks below are on the way of every call, some of which take 3 us on the
@@ -210,11 +208,10 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
-    if index >= 0 and index != torch.cuda.current_device():
-        return _on_device(streamkl_qk_norm_rope_fwd, x.device, dict(
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_qk_norm_rope_fwd, x.device, stream, dict(
             q=q, k=k, cos=cos, sin=sin, positions=positions, k_positions=k_positions, q_weight=q_weight,
-            k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out, dev_status=dev_status,
-            stream=stream))
+            k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out, dev_status=dev_status))
     yq = yk = None
     B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = 0
     iq = ik = oq = ok = _NONE
@@ -233,7 +230,7 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
         return yq, yk
     args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *_NONE, *_NONE, cos_at, sin_at, pq, sq, pk, sk, wq, wk, 0, 0, 0, 0,
                       status, _DTYPES[x.dtype], B, NQ, NK, HQ, HK, d, rot, length, bool(interleaved), k_repeat, eps)
-    st = load().streamkl_qk_norm_rope_fwd(args, _stream(stream, index))
+    st = load().streamkl_qk_norm_rope_fwd(args, _raw_stream(index))
     if st:
         _check(st, "streamkl_qk_norm_rope_fwd")
     return yq, yk
@@ -254,11 +251,11 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
-    if index >= 0 and index != torch.cuda.current_device():
-        return _on_device(streamkl_qk_norm_rope_bwd, x.device, dict(
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_qk_norm_rope_bwd, x.device, stream, dict(
             q=q, k=k, dq_out=dq_out, dk_out=dk_out, cos=cos, sin=sin, positions=positions, k_positions=k_positions,
             q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved, k_repeat=k_repeat, out=out,
-            workspace=workspace, dev_status=dev_status, stream=stream))
+            workspace=workspace, dev_status=dev_status))
     dev = x.device
     dq = dk = dwq = dwk = None
     B = NQ = NK = HQ = HK = pq = pk = sq = sk = wq = wk = dwq_at = dwk_at = 0
@@ -293,7 +290,7 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *gq, *gk, cos_at, sin_at, pq, sq, pk, sk, wq, wk, dwq_at, dwk_at,
                       ws.data_ptr() if need else 0, need, status, _DTYPES[x.dtype], B, NQ, NK, HQ, HK, d, rot, length,
                       bool(interleaved), k_repeat, eps)
-    st = lib.streamkl_qk_norm_rope_bwd(args, _stream(stream, index))
+    st = lib.streamkl_qk_norm_rope_bwd(args, _raw_stream(index))
     if st:
         _check(st, "streamkl_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
@@ -339,11 +336,11 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     ``streamkl_qk_norm_rope_fwd``, None to leave out the rotation or the norm.
     Writes the caches in place and returns them."""
     index, dtype = k_cache.get_device(), k_cache.dtype
-    if index >= 0 and index != torch.cuda.current_device():
-        return _on_device(streamkl_paged_append, k_cache.device, dict(
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_append, k_cache.device, stream, dict(
             k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens,
             cu_seqlens=cu_seqlens, cos=cos, sin=sin, k_weight=k_weight, eps=eps, interleaved=interleaved,
-            dev_status=dev_status, stream=stream))
+            dev_status=dev_status))
     k0, k1, _ = _rows("k", k, 3, dtype, index)
     v0, v1, _ = _rows("v", v, 3, dtype, index)
     total, HK, d = shape = k.shape
@@ -359,7 +356,7 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
         return k_cache, v_cache
     args = _APPEND.pack(_APPEND.size, k.data_ptr(), 0, k0, k1, v.data_ptr(), 0, v0, v1, *cache, cos_at, sin_at, w, status,
                         _DTYPES[dtype], B, total, HK, d, *pages, rot, length, bool(interleaved), eps)
-    st = load().streamkl_paged_append(args, _stream(stream, index))
+    st = load().streamkl_paged_append(args, _raw_stream(index))
     if st:
         _check(st, "streamkl_paged_append")
     return k_cache, v_cache
@@ -390,11 +387,11 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     block_table); close ones give a better grid. Rows that see no key get
     zeros and -inf; rows behind the last sequence stay as they were."""
     index, dtype = k_cache.get_device(), k_cache.dtype
-    if index >= 0 and index != torch.cuda.current_device():
-        return _on_device(streamkl_paged_attn, k_cache.device, dict(
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_attn, k_cache.device, stream, dict(
             q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
             max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, causal=causal, num_splits=num_splits,
-            out=out, workspace=workspace, dev_status=dev_status, stream=stream))
+            out=out, workspace=workspace, dev_status=dev_status))
     q0, q1, _ = _rows("q", q, 3, dtype, index)
     total, HQ, d = shape = q.shape
     HK, dim, pages, B, offsets, cache = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total, dtype, index)
@@ -428,7 +425,7 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     args = _ATTN.pack(_ATTN.size, q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(),
                       workspace.data_ptr(), workspace.nbytes, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q,
                       max_kv, bool(causal), num_splits, 1.0 / math.sqrt(d) if scale is None else scale)
-    st = lib.streamkl_paged_attn(args, _stream(stream, index))
+    st = lib.streamkl_paged_attn(args, _raw_stream(index))
     if st:
         try:
             _check(st, "streamkl_paged_attn")

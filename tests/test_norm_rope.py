@@ -259,6 +259,13 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (*out, *back, *dws)))
     binding.raise_on_device_status(st)
+    # everything made by the calls, while the current stream is held up
+    del kw["dev_status"]
+    torch.cuda._sleep(20_000_000)
+    ys = skl.streamkl_qk_norm_rope_fwd(q, k, cos, sin, stream=side, **kw)
+    grads = skl.streamkl_qk_norm_rope_bwd(q, k, *ys, cos, sin, stream=side, **kw)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*ys, *grads), (*out, *back, *dws)))
 
 
 @pytest.mark.gpu

@@ -519,6 +519,18 @@ def test_on_another_stream_and_the_same_in_every_run():
                                 workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), **kw)
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+    # status, workspace and outputs made by the call, while the current stream
+    # is held up: they belong to the stream given
+    torch.cuda._sleep(20_000_000)
+    b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, stream=side, **kw)
+    del kw["num_splits"]
+    one = skl.streamkl_paged_attn(q[:2], c.k, c.v, c.table, c.lens, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    torch.cuda.synchronize()
+    two = skl.streamkl_paged_attn(q[:2], c.k, c.v, c.table, c.lens)
+    assert all(torch.equal(x, y) for x, y in zip(one, two))
+    kw["num_splits"] = 3
     for _ in range(3):
         b = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, **kw)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
