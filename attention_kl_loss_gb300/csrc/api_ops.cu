@@ -38,8 +38,8 @@ bool take_args(A* to, const A* from) {
 
 // Rows of d contiguous elements in dimensions of the sizes given (0: not
 // used). The stride of a dimension of size 1 says nothing and becomes d.
-// `own_rows`: the rows must be apart (outputs, caches); inputs may repeat rows
-// (stride 0).
+// `own_rows`: the rows must be apart (outputs, caches), so each stride spans all
+// that the smaller ones reach; inputs may repeat rows (stride 0).
 streamkl_status check_rows(const char* name, streamkl_rows* r, int s0, int s1, int s2, int d, int dtype,
                            bool own_rows) {
   if (!r->data) return fail(STREAMKL_ERR_INVALID_ARG, "%s is NULL", name);
@@ -51,6 +51,18 @@ streamkl_status check_rows(const char* name, streamkl_rows* r, int s0, int s1, i
     if (s < 0 || s * static_cast<long long>(elem_size(dtype)) % 16)
       return fail(STREAMKL_ERR_INVALID_ARG, "%s: stride %lld is not a multiple of 16 bytes", name, s);
     if (own_rows && s < d) return fail(STREAMKL_ERR_INVALID_ARG, "%s: stride %lld below one row of %d", name, s, d);
+  }
+  if (own_rows) {
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return r->stride[x] < r->stride[y]; });
+    double reach = d;  // (elements; in a double, since a stride can be anything)
+    for (int i : order) {
+      if (sizes[i] <= 1) continue;
+      if (static_cast<double>(r->stride[i]) < reach)
+        return fail(STREAMKL_ERR_INVALID_ARG, "%s: its rows overlap (stride %lld, %.0f elements within)", name,
+                    r->stride[i], reach);
+      reach += static_cast<double>(r->stride[i]) * (sizes[i] - 1);
+    }
   }
   return STREAMKL_OK;
 }
@@ -287,13 +299,13 @@ streamkl_status streamkl_qk_norm_rope_bwd(const streamkl_rope_args* args, void* 
 streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* stream) {
   streamkl_append_args u;
   if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  if (static_cast<long long>(u.T) * u.HK > kMaxRows) return fail(STREAMKL_ERR_UNSUPPORTED, "tokens x heads above 2^30");
   streamkl_status st = check_cache(&u.k_cache, &u.v_cache, u.block_table, u.table_stride, u.kv_lens, u.cu_seqlens,
                                    u.dtype, u.B, u.T, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
   if (st != STREAMKL_OK) return st;
   if (u.table_stride < u.max_pages && u.B > 1)  // (to read them the sequences may share a row)
     return fail(STREAMKL_ERR_INVALID_ARG, "block_table rows overlap (stride %lld, %d pages)", u.table_stride,
                 u.max_pages);
-  if (static_cast<long long>(u.T) * u.HK > kMaxRows) return fail(STREAMKL_ERR_UNSUPPORTED, "tokens x heads above 2^30");
   if ((st = check_rows("k", &u.k, 0, u.T, u.HK, u.d, u.dtype, false)) != STREAMKL_OK) return st;
   if ((st = check_rows("v", &u.v, 0, u.T, u.HK, u.d, u.dtype, false)) != STREAMKL_OK) return st;
   if ((u.cos == nullptr) != (u.sin == nullptr))

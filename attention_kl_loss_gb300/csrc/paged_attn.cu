@@ -633,9 +633,10 @@ __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __gri
   const int lane = threadIdx.x & 31;
   const long long e = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const long long rows = static_cast<long long>(a.T) * a.HQ;
-  const int end = a.cu != nullptr ? __ldg(a.cu + a.B) : a.B;  // tokens behind the last sequence stay
+  // tokens in front of the first sequence and behind the last one stay
+  const int begin = a.cu != nullptr ? __ldg(a.cu) : 0, end = a.cu != nullptr ? __ldg(a.cu + a.B) : a.B;
   const int token = static_cast<int>(e / a.HQ), head = static_cast<int>(e - static_cast<long long>(token) * a.HQ);
-  if (e >= rows || token >= end) return;
+  if (e >= rows || token < begin || token >= end) return;
   float top = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + e]);
 #pragma unroll

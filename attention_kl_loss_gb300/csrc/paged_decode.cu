@@ -563,6 +563,8 @@ __global__ void __launch_bounds__(kThreads)
       a, gridDim.x, scratch, &where, &total, [&](int per_cta) { return (c0 + 1LL) * per_cta; },
       [](int, const Seq&) {});
   __syncthreads();
+  grid_dependency_wait();  // launched while the decode kernel ends; every block waits for its end, since
+                           // what comes after this kernel counts on both
   const long long cut = (c0 + 1LL) * chunk;  // the first tile of the next stretch
   // nothing after it, or an item that starts there, or before this stretch
   if (cut >= total || where.tile == 0 || where.tile > chunk) return;
@@ -571,7 +573,6 @@ __global__ void __launch_bounds__(kThreads)
   const int inside = where.tile < chunk ? 1 : 0;  // the item starts inside this stretch: its last part
   const int parts = 1 + (s.tiles - where.tile + chunk - 1) / chunk;
   auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? inside : 0); };
-  grid_dependency_wait();  // launched while the decode kernel ends
   const int G = a.HQ / a.HK, lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < s.n * G; r += kThreads / 32) {
     float top = -INFINITY;

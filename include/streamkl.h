@@ -371,7 +371,8 @@ typedef struct {
  * Backward: q_out, k_out are the gradients of the outputs (those of a key
  * head's repeats are summed), dq, dk and dq_weight, dk_weight are written.
  * workspace: ws_bytes >= streamkl_qk_norm_rope_bwd_workspace_size(...) (sizes
- * of an absent side 0; may be NULL without weights); no initialisation. The
+ * of an absent side 0; may be NULL without weights); no initialisation; calls
+ * that may overlap need one each. The
  * weight gradients are summed in a fixed order: the same in every run. Rows
  * that the forward does not write get no gradient and add none.
  */
@@ -405,7 +406,7 @@ streamkl_status streamkl_qk_norm_rope_bwd(const streamkl_rope_args* args, void* 
  * Append new keys and values to a paged cache, the keys normed (k_weight) and
  * rotated (cos, sin) on the way as above; NULL leaves either out.
  *   k, v [T, HK, d]: the new tokens of B sequences packed one after the other;
- *   those from cu_seqlens[B] on are padding and ignored. Position p of
+ *   those from cu_seqlens[B] on (or before cu_seqlens[0]) are padding and ignored. Position p of
  *   sequence b lies in slot p % page_size of page block_table[b][p / page_size]
  *   of k_cache, v_cache [num_pages, HK, page_size, d]. Only the new tokens'
  *   slots are written. Two tokens of one call must not share a slot (one of
@@ -441,7 +442,7 @@ streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* st
  *   out [T, HQ, d] and lse [T, HQ] (fp32, contiguous, the log of the softmax's
  *   sum, as streamkl_fwd's). A row that sees no key (length 0, or causal with
  *   more new tokens than keys) gets zeros and -inf. Rows behind the last
- *   sequence are left as they were.
+ *   sequence, or in front of the first, are left as they were.
  * workspace: ws_bytes >= streamkl_paged_attn_workspace_size(...) of the same
  * sizes and num_splits (may be NULL when that is 0); contents need no
  * initialisation; calls that may overlap need one each.

@@ -379,6 +379,7 @@ REFUSED = [
     (dict(k__data=8193), 1), (dict(q_out__data=None), 1), (dict(k_out__data=4100), 1),
     (dict(q__stride=(512, 128, 60)), 1), (dict(k_out__stride=(512, -128, 64)), 1), (dict(q_weight=4100), 1),
     (dict(q_out__stride=(512, 128, 0)), 1), (dict(k_out__stride=(0, 128, 64)), 1),
+    (dict(q_out__stride=(512, 64, 64)), 1), (dict(q_out__stride=(64, 256, 64)), 1),  # rows overlap
 ]
 
 
@@ -394,7 +395,7 @@ def test_c_call_refuses(lib, over, status):
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(dq__data=None), 1), (dict(dk__stride=(512, 0, 64)), 1), (dict(q_weight=4096), 1),
+    (dict(dq__data=None), 1), (dict(dk__stride=(512, 0, 64)), 1), (dict(dq__stride=(384, 128, 64)), 1), (dict(q_weight=4096), 1),
     (dict(q_weight=4096, dq_weight=4096), 1), (dict(k_weight=4096, dk_weight=4096, workspace=4100, ws_bytes=1 << 20), 1),
     (dict(k_weight=4096, dk_weight=4096, workspace=4096, ws_bytes=16), 1),
 ])

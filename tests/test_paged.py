@@ -365,6 +365,42 @@ def test_sequences_may_share_one_row_of_pages(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,splits", [(1, 0), (40, 1), (40, 3)])
+def test_rows_in_front_of_the_first_sequence_stay(n, splits):
+    c = Cache([500, 300], 2, 64, 16, torch.bfloat16, seed=n)
+    q = torch.randn(2 * n + 5, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    o, lse = torch.full_like(q, 3.0), torch.full((2 * n + 5, 4), 3.0, device="cuda")
+    st = binding.new_status()
+    cu = torch.tensor([3, 3 + n, 3 + 2 * n], dtype=torch.int32, device="cuda")
+    skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=cu, max_seqlen_q=n, max_kv_len=500,
+                            num_splits=splits, out=(o, lse), dev_status=st)
+    binding.raise_on_device_status(st)
+    for rows in (slice(0, 3), slice(3 + 2 * n, None)):
+        assert torch.all(o[rows] == 3) and torch.all(lse[rows] == 3)
+    at = slice(3, 3 + 2 * n)
+    _check_attn(o[at], lse[at], q[at], c, [n, n], [500, 300], 64 ** -0.5, True, torch.bfloat16)
+
+
+@pytest.mark.gpu
+def test_single_tokens_whose_items_are_whole_follow_one_another():
+    """Two tiles a sequence, none cut: each call's output is the next one's queries."""
+    B, d = 152, 64
+    c = Cache([256] * B, 1, d, 16, torch.bfloat16)
+    q0 = torch.randn(B, 1, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+
+    def chain(wait):
+        q = q0
+        for _ in range(20):
+            o, _ = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, max_kv_len=256)
+            q = o * 16
+            if wait:
+                torch.cuda.synchronize()
+        return q
+
+    assert torch.equal(chain(True), chain(False))
+
+
+@pytest.mark.gpu
 def test_nan_in_one_sequence_stays_there():
     lens = [200, 200]
     c = Cache(lens, 1, 64, 16, torch.bfloat16)
@@ -643,6 +679,7 @@ CACHE_REFUSED = [
     (dict(cu_seqlens=None), 1), (dict(k_cache__data=None), 1), (dict(v_cache__data=4100), 1),
     (dict(k_cache__stride=(2048, 1024, 60)), 1), (dict(k_cache__stride=(2048, 1024, 0)), 1),
     (dict(v_cache__stride=(0, 1024, 64)), 1), (dict(dev_status=None), 1),
+    (dict(k_cache__stride=(1024, 1024, 64)), 1), (dict(v_cache__stride=(2048, 1016, 64)), 1),  # pages, heads overlap
 ]
 
 
@@ -686,6 +723,7 @@ def test_append_python_call_refuses():
     (dict(max_kv_len=65), 1), (dict(q__data=4104), 1), (dict(out__data=None), 1), (dict(out__data=4104), 1),
     (dict(lse=None), 1), (dict(causal=2), 1), (dict(num_splits=-1), 1), (dict(scale=0.0), 1),
     (dict(scale=float("inf")), 1), (dict(q__stride=(0, 256, 60)), 1), (dict(out__stride=(0, 256, 0)), 1),
+    (dict(out__stride=(0, 128, 64)), 1), (dict(out__stride=(0, 64, 312)), 1),
     (dict(B=40000, T=40000, cu_seqlens=None, max_seqlen_q=1), 2),
     (dict(num_splits=2, max_pages=40, table_stride=40, max_kv_len=640), 1),
     (dict(num_splits=2, max_pages=40, table_stride=40, max_kv_len=640, workspace=4100, ws_bytes=1 << 20), 1),
