@@ -9,8 +9,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
+import importlib.machinery
+import importlib.util
 import math
 import os
+import types
 from typing import Optional
 
 import torch
@@ -101,8 +105,23 @@ def _load_variant(debug: bool) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    lib.native = _native_calls(path)
     _libs[debug] = lib
     return lib
+
+
+def _native_calls(path: str):
+    """The native way to the operators' entries of this library (``ops`` takes
+    it first), None where it was built under another version of PyTorch."""
+    so = _build.marshal_path()
+    if not os.path.exists(so):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", so)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", so, loader=loader))
+    loader.exec_module(module)
+    entries = module.entries(path)
+    return types.SimpleNamespace(**{name: functools.partial(getattr(module, name), entries)
+                                    for name in ("rope_fwd", "rope_bwd", "append", "attn")})
 
 
 def load(debug: Optional[bool] = None) -> ctypes.CDLL:

@@ -8,14 +8,20 @@ sources with STREAMKL_DEVICE_CHECKS defined: the kernels then check the
 operands of every TMA copy, TMEM access and mbarrier against their layout
 and report a failed check as STREAMKL_ERR_DEVICE_CHECK in the caller's
 status word instead of issuing the access.
+
+``build()`` also makes ``_lib/_marshal_<torch version>.so``, the Python module
+that takes tensors to the operators' C entries (``csrc/marshal.cpp``). It is
+tied to the version of PyTorch that it was built with, the library is not.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -40,6 +46,22 @@ def nvcc() -> str:
 
 def lib_path(debug: bool = False) -> str:
     return os.path.join(OUT_DIR, DEBUG_LIB_NAME if debug else LIB_NAME)
+
+
+def marshal_path() -> str:
+    import torch
+    return os.path.join(OUT_DIR, f"_marshal_{re.sub('[^0-9A-Za-z]', '_', torch.__version__)}.so")
+
+
+def _marshal_cmd() -> list:
+    import torch
+    inc, lib = (os.path.join(os.path.dirname(torch.__file__), d) for d in ("include", "lib"))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [os.path.join(ROOT, "include"), inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            *(f"-I{d}" for d in dirs), os.path.join(CSRC, "marshal.cpp"), "-o", marshal_path(), f"-L{lib}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _stale(target: str, deps) -> bool:
@@ -70,6 +92,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    if not debug and (force or _stale(marshal_path(), [os.path.join(CSRC, "marshal.cpp"), headers[-1]])):
+        jobs.append(_marshal_cmd())
+
     def run(cmd):
         p = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, p
@@ -79,7 +104,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
             if verbose or ptxas_info or p.returncode != 0:
                 sys.stderr.write(p.stdout + p.stderr)
             if p.returncode != 0:
-                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+                raise RuntimeError(f"compiling failed: {' '.join(cmd)}")
     lib = lib_path(debug)
     if force or _stale(lib, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", lib, *objs]

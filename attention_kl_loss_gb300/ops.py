@@ -7,6 +7,10 @@ gradients back. ``streamkl_paged_append`` puts a trained student's new keys
 and values into a paged cache, ``streamkl_paged_attn`` is the attention of new
 tokens (one, or a chunk) over it. As in ``binding``: argument marshalling only,
 PyTorch provides device memory and the current stream.
+
+Each call tries ``csrc/marshal.cpp`` first, which takes ordinary arguments in a
+third of the time and returns None for any others; these, and all refusals, are
+dealt with here.
 """
 from __future__ import annotations
 
@@ -205,6 +209,11 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
     k_positions is given); without them key n stands at position n and the
     queries at the last N positions of the keys. Weights: fp32 [d], None for
     rotation without norm."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.rope_fwd(q, k, cos, sin, positions, k_positions, q_weight, k_weight, eps, interleaved, k_repeat,
+                               dev_status)
+        if done is not None:
+            return done
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
@@ -248,6 +257,11 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     the shapes of q, k (``out`` = (dq, dk) may be slices of one buffer); the
     gradients of a key head's repeats are summed; weight gradients are fp32
     [d], None where there is no weight."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.rope_bwd(q, k, dq_out, dk_out, cos, sin, positions, k_positions, q_weight, k_weight, eps, interleaved,
+                               k_repeat, workspace, dev_status)
+        if done is not None:
+            return done
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
@@ -335,6 +349,10 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     bf16 or fp16, any strides with d contiguous. cos, sin, k_weight as in
     ``streamkl_qk_norm_rope_fwd``, None to leave out the rotation or the norm.
     Writes the caches in place and returns them."""
+    if stream is None and (native := load().native) is not None:
+        if native.append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, cos, sin, k_weight, eps, interleaved,
+                         dev_status):
+            return k_cache, v_cache
     index, dtype = k_cache.get_device(), k_cache.dtype
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_append, k_cache.device, stream, dict(
@@ -386,6 +404,11 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     the sequences' new tokens and lengths (default: every token, every page of
     block_table); close ones give a better grid. Rows that see no key get
     zeros and -inf; rows behind the last sequence stay as they were."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
+                           num_splits, workspace, dev_status)
+        if done is not None:
+            return done
     index, dtype = k_cache.get_device(), k_cache.dtype
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_attn, k_cache.device, stream, dict(

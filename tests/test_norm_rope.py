@@ -269,6 +269,49 @@ def test_captured_and_on_another_stream():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+def test_the_native_way_and_the_one_in_python_do_the_same(packed, monkeypatch):
+    g = torch.Generator().manual_seed(9)
+    lead = (37,) if packed else (2, 37)
+    qkv = torch.randn(*lead, 10, 64, generator=g).half().cuda()
+    q, k = qkv[..., :6, :], qkv[..., 6:8, :]
+    cos, sin = _tables(64, 32, "cuda")
+    w = [torch.randn(64, generator=g).cuda() for _ in range(2)]
+    pos = torch.randint(0, 64, (37,), generator=g, dtype=torch.int32).cuda()
+    both = pos if packed else torch.stack([pos, pos.flip(0)])
+    native, st = binding.load().native, binding.new_status()
+    space = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    got = []
+    for way in (native, None):
+        monkeypatch.setattr(binding.load(), "native", way)
+        for kw in (dict(positions=pos, dev_status=st), dict(positions=both, q_weight=w[0], k_weight=w[1], k_repeat=3),
+                   dict(positions=pos, k_positions=both, interleaved=True, q_weight=w[0]),
+                   dict(positions=pos, k_repeat=np.int64(2), eps=0)):
+            for a, b in ((q, k), (q, None), (None, k)):
+                ya, yb = skl.streamkl_qk_norm_rope_fwd(a, b, cos, sin, **kw)
+                back = dict(kw, workspace=space) if kw.get("interleaved") else kw
+                got += [ya, yb, *skl.streamkl_qk_norm_rope_bwd(a, b, ya, yb, cos, sin, **back)]
+    binding.raise_on_device_status(st)
+    half = len(got) // 2
+    for a, b in zip(got[:half], got[half:]):
+        assert (a is None) == (b is None)
+        if a is not None:
+            assert a.dtype == b.dtype and a.stride() == b.stride() and torch.equal(a, b)
+
+    def fwd(**at):
+        a = dict(dict(q=q, k=k, cos=cos, pos=pos, w=w[0], eps=1e-6, inter=False, repeat=1), **at)
+        return native.rope_fwd(a["q"], a["k"], a["cos"], sin, a["pos"], None, a["w"], w[1], a["eps"], a["inter"], a["repeat"],
+                               st)
+
+    assert fwd() is not None
+    for bad in (dict(q=q.cpu()), dict(q=q.float()), dict(q=q[..., :32]), dict(q=q[..., :30, :, :]), dict(q=q[None]),
+                dict(k=k[..., 1:, :, :]), dict(cos=cos[1:]), dict(cos=cos.double()), dict(pos=pos.long()), dict(pos=pos[1:]),
+                dict(w=w[0][1:]), dict(w=w[0].half()), dict(eps=-1.0), dict(eps=1e300), dict(inter=1), dict(repeat=0),
+                dict(repeat=1 << 40), dict(q=torch.nn.Parameter(q[..., 1:]))):
+        assert fwd(**bad) is None, bad
+
+
+@pytest.mark.gpu
 def test_training_step_from_projection_to_its_gradients():
     """Projection -> norm + rotation -> KL -> its gradients -> back: as a
     training step uses them together, grouped heads repeated for the KL,

@@ -603,6 +603,44 @@ def test_two_captured_calls_at_once(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,layout", [(1, "heads"), (40, "slots")])
+def test_the_native_way_and_the_one_in_python_do_the_same(n, layout, monkeypatch):
+    lens = [500, 300]
+    g = torch.Generator().manual_seed(n)
+    kv = torch.randn(2 * n, 2, 3, 64, generator=g).bfloat16().cuda()[:, :, :2]
+    q = torch.randn(2 * n, 4, 64, generator=g).bfloat16().cuda()
+    cos, sin = _tables(600, 32, "cuda")
+    w = torch.randn(64, generator=g).cuda()
+    native, st = binding.load().native, binding.new_status()
+    cu = _cu([n, n])
+    got = []
+    for way in (native, None):
+        monkeypatch.setattr(binding.load(), "native", way)
+        c = Cache(lens, 2, 64, 16, torch.bfloat16, layout=layout)
+        for offsets in [cu] + ([None] if n == 1 else []):
+            for extra in (dict(), dict(cos=cos, sin=sin, k_weight=w, dev_status=st, interleaved=True)):
+                skl.streamkl_paged_append(kv[:, 0], kv[:, 1], c.k, c.v, c.table, c.lens, cu_seqlens=offsets, **extra)
+                got += [c.k.clone(), c.v.clone()]
+            space = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+            for extra in (dict(), dict(max_seqlen_q=n, max_kv_len=500, scale=0.2, causal=False, workspace=space,
+                                       dev_status=st), dict(scale=np.float64(0.2), num_splits=2)):
+                got += skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=offsets, **extra)
+    binding.raise_on_device_status(st)
+    half = len(got) // 2
+    assert all(torch.equal(torch.nan_to_num(a.float(), 7.0), torch.nan_to_num(b.float(), 7.0))
+               for a, b in zip(got[:half], got[half:]))
+    # it is the native way that takes ordinary calls, and it leaves the others alone
+    assert native.attn(q, c.k, c.v, c.table, c.lens, cu, n, 500, 0.2, True, 0, None, st) is not None
+    assert native.append(kv[:, 0], kv[:, 1], c.k, c.v, c.table, c.lens, cu, None, None, None, 1e-6, False, st) is True
+    for bad in (dict(q=q.float()), dict(lens=c.lens.long()), dict(lens=c.lens[:1]), dict(q=q[:, :3]), dict(q=q.cpu()),
+                dict(q=None), dict(table=c.table[0]), dict(cu=cu[:2]), dict(max_q=3 * n), dict(max_kv=1 << 20),
+                dict(max_kv=1 << 40), dict(scale=0.0), dict(scale=1e300), dict(splits=-1), dict(space=space[:16])):
+        a = dict(dict(q=q, lens=c.lens, table=c.table, cu=cu, max_q=n, max_kv=500, scale=0.2, splits=2, space=None), **bad)
+        assert native.attn(a["q"], c.k, c.v, a["table"], a["lens"], a["cu"], a["max_q"], a["max_kv"], a["scale"], True,
+                           a["splits"], a["space"], st) is None, bad
+
+
+@pytest.mark.gpu
 def test_debug_build_finds_nothing_and_gives_the_same():
     """Every TMA copy, TMEM access and barrier range-checked: no check fails
     and the results are the release build's."""
@@ -731,6 +769,13 @@ def test_append_python_call_refuses():
 def test_attention_c_call_refuses(lib, over, status):
     a = _raw(AttnArgs, over, HQ=4, max_seqlen_q=4, max_kv_len=64, scale=0.1, causal=1, num_splits=1, lse=4096)
     assert lib.streamkl_paged_attn(a, None) == status and lib.streamkl_last_error()
+
+
+def test_native_calls_leave_what_they_do_not_know(lib):
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    for call in (lib.native.rope_fwd, lib.native.rope_bwd, lib.native.append, lib.native.attn):
+        assert call() is None and call(None) is None and call(*[x] * 12) is None
+        assert all(call(*[a] * n) is None for n in (12, 13, 15) for a in (x, None, 1, "text"))
 
 
 def test_attention_splits_on_the_host(lib):
