@@ -23,6 +23,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -647,8 +648,17 @@ template <int TYPE, int D>
 cudaError_t rope_bwd_t(const RopeArgs& a, unsigned blocks, cudaStream_t stream) {
   constexpr int bytes = kRopeWarps * kBwdStages<TYPE> * 4 * kChunkBytes<TYPE>;
   auto kern = a.interleaved ? streamkl_rope_bwd_kernel<TYPE, D, true> : streamkl_rope_bwd_kernel<TYPE, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // the shared-memory attribute, once per device
+  static std::atomic<unsigned long long> done[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done[a.interleaved].load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    done[a.interleaved].fetch_or(bit);
+  }
   kern<<<blocks, kRopeThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
