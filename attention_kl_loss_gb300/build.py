@@ -61,7 +61,7 @@ def _marshal_cmd() -> list:
             sysconfig.get_paths()["include"], cuda]
     return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             *(f"-I{d}" for d in dirs), os.path.join(CSRC, "marshal.cpp"), "-o", marshal_path(), f"-L{lib}",
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def _stale(target: str, deps) -> bool:
