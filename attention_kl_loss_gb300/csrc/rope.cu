@@ -325,19 +325,25 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   constexpr int STAGES = kBwdStages<TYPE>;
   constexpr int SLOT = 4 * kChunkBytes<TYPE>;  // one repeat of a head: two chunks of dy, two of x with the first
   extern __shared__ __align__(16) uint8_t stage_mem[];
-  __shared__ float red[kRopeWarps][D];
-  __shared__ float ws[D];
+  __shared__ float red[2][kRopeWarps][D];
+  __shared__ float weights[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPR, l = lane % LPR;
   const uint32_t mem = smem_u32(stage_mem) + warp * STAGES * SLOT + lane * 16;
   const LaneChunks lc = lane_chunks(l, a.rot);
   const uint32_t stride = gridDim.x * kRopeWarps;
+  if (threadIdx.x < 2 * D) {
+    const float* w = a.side[threadIdx.x / D].w;
+    if (w != nullptr) weights[threadIdx.x / D][threadIdx.x % D] = __ldg(w + threadIdx.x % D);
+  }
+  __syncthreads();
+  // (no barrier from one side to the other: a warp that has no row of the first
+  // goes on to the second)
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const RopeSide& s = a.side[k];
     if (s.x == nullptr) continue;
     const bool norm = s.w != nullptr;
-    if (norm && threadIdx.x < D) ws[threadIdx.x] = __ldg(s.w + threadIdx.x);
-    __syncthreads();
+    const float* ws = weights[k];
     float dw0[8], dw1[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw0[e] = dw1[e] = 0.f;
@@ -467,18 +473,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         dw1[e] += __shfl_xor_sync(0xFFFFFFFFu, dw1[e], m);
       }
       if (grp == 0) {
-        red[warp][8 * lc.c0 + e] = dw0[e];
-        red[warp][8 * lc.c1 + e] = dw1[e];
+        red[k][warp][8 * lc.c0 + e] = dw0[e];
+        red[k][warp][8 * lc.c1 + e] = dw1[e];
       }
     }
-    __syncthreads();
-    if (threadIdx.x < D) {
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * D) {
+    const int k = threadIdx.x / D, c = threadIdx.x % D;
+    if (a.side[k].x != nullptr && a.side[k].w != nullptr) {
       float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRopeWarps; ++i) t += red[i][threadIdx.x];
-      a.part[(static_cast<long long>(k) * gridDim.x + blockIdx.x) * D + threadIdx.x] = t;
+      for (int i = 0; i < kRopeWarps; ++i) t += red[k][i][c];
+      a.part[(static_cast<long long>(k) * gridDim.x + blockIdx.x) * D + c] = t;
     }
-    __syncthreads();
   }
   grid_launch_dependents();  // the sum of the partials may be launched
 }
