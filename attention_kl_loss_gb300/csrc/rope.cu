@@ -615,12 +615,19 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   }
 }
 
-// Head chunks: up to 16 heads a warp (the forward at 65,521 tokens x 40 heads
-// takes 238 us, 255 with 8 and 299 with 4: the angles are loaded less often),
-// fewer when there are not `per_sm` warps' items an SM to fill the GPU with.
-int head_chunk(long long tiles, int heads, int per_sm, int sms) {
-  int hc = 16;
-  while (hc > 1 && tiles * ((heads + hc - 1) / hc) < static_cast<long long>(per_sm) * sms) hc >>= 1;
+// Heads per item. Where the warps that are resident together (two blocks an SM)
+// can have one item each, as few heads as leave it at that (forward, 2,048 tokens
+// x 20 heads 7.0 -> 5.5 us, 8,000 x 8 of 64 7.5 -> 4.3, append of 10,000 tokens x 8
+// of 64 12.0 -> 9.8, against items of which a warp gets two or three). Else up to
+// 16 (the forward at 65,521 tokens x 40 heads takes 238 us, 255 with 8 and 299
+// with 4: the angles are loaded less often), fewer when there are not `per_sm`
+// items an SM to even out the last round.
+template <typename F>
+int head_chunk(F&& items, long long tiles, int heads, int per_sm, int sms) {
+  int hc = 1;
+  for (; hc <= 16; ++hc)
+    if (items(hc) <= 2LL * kRopeWarps * sms) return hc;
+  for (hc = 16; hc > 1 && tiles * ((heads + hc - 1) / hc) < static_cast<long long>(per_sm) * sms;) hc >>= 1;
   return std::min(hc, heads);
 }
 
@@ -639,8 +646,11 @@ long long side_items(RopeSide& s, int B, int d, int hc) {
 
 int rope_head_chunk(int B, int NQ, int HQ, int NK, int HK, int d, int sms) {
   const int tokens = 32 / (d / 16);
-  const long long tiles = static_cast<long long>(B) * ((std::max(NQ, NK) + tokens - 1) / tokens);
-  return head_chunk(tiles, HQ + HK, 32, sms);  // (16: the backward at 8,192 tokens x 32 heads 56 us, with 32 54)
+  const long long tq = static_cast<long long>(B) * ((NQ + tokens - 1) / tokens);
+  const long long tk = static_cast<long long>(B) * ((NK + tokens - 1) / tokens);
+  auto items = [&](int hc) { return tq * ((HQ + hc - 1) / hc) + tk * ((HK + hc - 1) / hc); };
+  // (16: the backward at 8,192 tokens x 32 heads 56 us, with 32 54)
+  return head_chunk(items, std::max(tq, tk), HQ + HK, 32, sms);
 }
 
 template <int TYPE, int D>
@@ -737,7 +747,8 @@ cudaError_t launch_rope_bwd(RopeArgs& a, int blocks, int sms, float* dw_q, float
 cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream) {
   const int tokens = 32 / (a.d / 16);
   const long long tiles = (a.T + tokens - 1) / tokens;
-  a.hc = head_chunk(tiles, 2 * a.H, 16, sms);  // (32: 10,000 tokens x 8 heads 24.6 us, with 16 22.5)
+  auto items_of = [&](int hc) { return 2 * tiles * ((a.H + hc - 1) / hc); };
+  a.hc = head_chunk(items_of, tiles, 2 * a.H, 16, sms);  // (32: 10,000 tokens x 8 heads 24.6 us, with 16 22.5)
   a.hc = std::min(a.hc, a.H);
   a.hchunks = (a.H + a.hc - 1) / a.hc;
   const long long items = tiles * 2 * a.hchunks;
