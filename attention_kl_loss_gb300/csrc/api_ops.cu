@@ -165,12 +165,14 @@ streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* tab
 }
 
 // How the attention over the cache is cut into CTAs. Few rows (decode) go to
-// the persistent kernel, which deals the key tiles out evenly by itself. With
+// the persistent kernel, which deals the key tiles out evenly by itself, or a
+// short (sequence, key head) to each CTA. With
 // more, the keys of few query tiles against long sequences are cut into
 // `splits` ranges of split_tiles 128-key tiles (counted from a sequence's
 // start, so a short one uses fewer ranges).
 struct AttnPlan {
   int decode_ctas;  // 0: not the persistent kernel
+  bool whole;       // there: each CTA takes one whole (sequence, key head)
   int row_tiles, q_tiles, splits, split_tiles;
 };
 
@@ -178,9 +180,16 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   AttnPlan p{};
   const long long rows = static_cast<long long>(max_q) * (HQ / HK);
   if (requested == 0 && rows <= skl::kDecodeRows) {
-    const long long most = static_cast<long long>(B) * HK * std::max(1, (max_kv + 127) / 128);
-    p.decode_ctas = static_cast<int>(std::min<long long>(most, 2LL * num_sms()));
+    const long long ctas = 2LL * num_sms(), items = static_cast<long long>(B) * HK;
+    const long long tiles = std::max(1, (max_kv + 127) / 128), all = items * tiles;
+    // a whole item each, without a search and without parts to join, where that is
+    // four tiles or one more than an equal share (8 key heads of 128, one sequence
+    // of 128 keys 10.1 -> 6.5 us, of 256 9.4 -> 8.1, of 512 level, of 768 10.9 -> 13.8
+    // the other way; 32 of 1,024, 8 tiles for 7, 23.0 -> 21.8, of 2,048, 16 for 14,
+    // 33.5 -> 36.4 the other way)
     p.split_tiles = 2;  // (one tile each: 21.3 us against 19.6 at one sequence of 4,096 keys)
+    p.whole = items <= ctas && tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
+    p.decode_ctas = static_cast<int>(p.whole ? items : std::min(all, ctas));
     return p;
   }
   p.row_tiles = rows > 128 ? 2 : 1;
@@ -213,6 +222,7 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
 
 // Rows of the partial results.
 size_t attn_part_rows(const AttnPlan& p, int T, int HQ) {
+  if (p.whole) return 0;
   if (p.decode_ctas > 0) return static_cast<size_t>(2) * p.decode_ctas * skl::kDecodeRows;
   return p.splits > 1 ? static_cast<size_t>(p.splits) * T * HQ : 0;
 }
@@ -415,6 +425,7 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   a.split_tiles = p.split_tiles;
+  a.whole = p.whole;
   // more than one CTA per SM one after the other: long ones first, so that the
   // last to start are short (four ragged chunks of up to 2,048 rows over 16,384
   // keys, d = 64: 250 us against 258)

@@ -6,7 +6,8 @@
 //     (sequence, key head) items, in order, are one line of W tiles; each CTA
 //     takes an equal stretch of it, whatever the sequences' lengths. A stretch
 //     cuts at most its first and its last item; a combine kernel joins those
-//     parts by their lse, whole items are written directly.
+//     parts by their lse, whole items are written directly. Short sequences on
+//     few heads: each CTA takes one whole item, and there is nothing to join.
 //   - A CTA's loads run on through its items: Q of the next item is fetched by
 //     a warp of its own while the current one is worked on, and the ring of K
 //     and V stages never empties between items. Two CTAs per SM cover each
@@ -226,30 +227,42 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_alloc(smem_u32(tmem_slot), 256);
     tmem_relinquish();
   }
-  // this CTA's stretch of the line of tiles
-  long long total;
-  const int chunk = locate(
-      a, gridDim.x, scratch, start, &total, [&](int per_cta) { return static_cast<long long>(blockIdx.x) * per_cta; },
-      [&](int b, const Seq& s) {
-        if (blockIdx.x == 0 && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-        if (s.n == 0 || s.tiles > 0 || b % gridDim.x != blockIdx.x) return;
-        for (int r = 0; r < s.n * a.HQ; ++r) {  // a sequence without a key
-          const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
-          for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-          a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
-        }
-      });
+  // a sequence's numbers; its rows, where it has no key
+  auto visit = [&](int b, const Seq& s, bool report, bool mine) {
+    if (report && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    if (s.n == 0 || s.tiles > 0 || !mine) return;
+    for (int r = 0; r < s.n * a.HQ; ++r) {
+      const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
+      for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+      a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
+    }
+  };
   Stretch st;
-  st.left = static_cast<int>(
-      max(0LL, min(total - static_cast<long long>(blockIdx.x) * chunk, static_cast<long long>(chunk))));
+  if (a.whole) {  // one item
+    st.b = static_cast<int>(blockIdx.x) / a.HK;
+    st.hk = static_cast<int>(blockIdx.x) - st.b * a.HK;
+    st.tile = 0;
+    const Seq s = load_seq(a, st.b);
+    st.left = s.tiles;
+    if (threadIdx.x == 0) visit(st.b, s, st.hk == 0, st.hk == 0);
+  } else {  // this CTA's stretch of the line of tiles
+    long long total;
+    const int chunk = locate(
+        a, gridDim.x, scratch, start, &total, [&](int per_cta) { return static_cast<long long>(blockIdx.x) * per_cta; },
+        [&](int b, const Seq& s) { visit(b, s, blockIdx.x == 0, b % gridDim.x == blockIdx.x); });
+    st.left = static_cast<int>(
+        max(0LL, min(total - static_cast<long long>(blockIdx.x) * chunk, static_cast<long long>(chunk))));
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
-  st.b = start->b;
-  st.hk = start->hk;
-  st.tile = start->tile;
+  if (!a.whole) {
+    st.b = start->b;
+    st.hk = start->hk;
+    st.tile = start->tile;
+  }
   if (*skip_flag) st.left = 0;
   __syncthreads();  // (the items are written there from here on)
   ck.tmem = tmem;
@@ -639,7 +652,7 @@ cudaError_t decode_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   }
   kern<<<ctas, kThreads, L::BYTES, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);

@@ -472,7 +472,8 @@ typedef struct {
 
 /* Key splits that num_splits = 0 takes for these sizes; 0: few rows (at most 32
  * (token, head of a group) rows per sequence and key head), where persistent
- * CTAs share all key tiles evenly instead; -1 on invalid sizes. */
+ * CTAs share all key tiles evenly instead, or take short sequences whole; -1 on
+ * invalid sizes. */
 int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len);
 size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
                                           int num_splits);

@@ -382,9 +382,31 @@ def test_rows_in_front_of_the_first_sequence_stay(n, splits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,HQ,HK,d,n,most", [(1, 8, 8, 64, 1, 130), (5, 12, 3, 128, 2, 300), (38, 32, 8, 64, 1, 512),
+                                              (40, 8, 8, 64, 1, 512), (9, 2, 2, 128, 16, 512)])
+def test_short_sequences_of_few_rows(B, HQ, HK, d, n, most):
+    """Up to and past 2 x 152 (sequence, key head) pairs; sequences without keys or new tokens among them."""
+    r = np.random.default_rng(B + d)
+    lens = [most] + [int(x) for x in r.integers(0, most + 1, B - 1)]
+    new = [n] + [int(x) for x in r.integers(0, n + 1, B - 1)]
+    if B > 3:
+        lens[1], new[1], new[2] = 0, n, 0
+    c = Cache(lens, HK, d, 16, torch.bfloat16, seed=B)
+    q = torch.randn(sum(new) + 1, HQ, d, generator=torch.Generator().manual_seed(B)).bfloat16().cuda()
+    for causal in (True, False):
+        o, lse = torch.full_like(q, 3.0), torch.full((sum(new) + 1, HQ), 3.0, device="cuda")
+        st = binding.new_status()
+        skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu(new), max_seqlen_q=n, max_kv_len=most,
+                                causal=causal, out=(o, lse), dev_status=st)
+        binding.raise_on_device_status(st)
+        assert torch.all(o[-1] == 3) and torch.all(lse[-1] == 3)
+        _check_attn(o[:-1], lse[:-1], q[:-1], c, new, lens, d ** -0.5, causal, torch.bfloat16)
+
+
+@pytest.mark.gpu
 def test_single_tokens_whose_items_are_whole_follow_one_another():
     """Two tiles a sequence, none cut: each call's output is the next one's queries."""
-    B, d = 152, 64
+    B, d = 305, 64  # more than 2 x 152, so that the kernel that joins parts is launched
     c = Cache([256] * B, 1, d, 16, torch.bfloat16)
     q0 = torch.randn(B, 1, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
 
@@ -791,7 +813,9 @@ def test_attention_splits_on_the_host(lib):
         assert need <= size(*args) < need + 256
     assert size(1, 1, 32, 8, 128, 1, 4096, 1) == 0
     # two parts of 32 rows a CTA; no more CTAs than key tiles
-    assert size(1, 1, 4, 1, 64, 1, 256) == 2 * 2 * 32 * 65 * 4
+    assert size(1, 1, 4, 1, 64, 1, 1024) == 2 * 8 * 32 * 65 * 4
+    assert size(1, 1, 4, 1, 64, 1, 512) == 0 and size(38, 38, 8, 8, 64, 1, 512) == 0  # each CTA takes a whole one
+    assert size(39, 39, 8, 8, 64, 1, 512) == 2 * 304 * 32 * 65 * 4                    # (more than 2 x 152 of them)
     assert size(64, 64, 32, 8, 128, 1, 16384) == size(1, 1, 1, 1, 128, 1, 1 << 20)
 
 
