@@ -172,7 +172,7 @@ streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* tab
 // start, so a short one uses fewer ranges).
 struct AttnPlan {
   int decode_ctas;  // 0: not the persistent kernel
-  bool whole;       // there: each CTA takes one whole (sequence, key head)
+  bool whole;       // there: each CTA takes whole (sequence, key head) pairs
   int row_tiles, q_tiles, splits, split_tiles;
 };
 
@@ -182,14 +182,14 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   if (requested == 0 && rows <= skl::kDecodeRows) {
     const long long ctas = 2LL * num_sms(), items = static_cast<long long>(B) * HK;
     const long long tiles = std::max(1, (max_kv + 127) / 128), all = items * tiles;
-    // a whole item each, without a search and without parts to join, where that is
-    // four tiles or one more than an equal share (8 key heads of 128, one sequence
-    // of 128 keys 10.1 -> 6.5 us, of 256 9.4 -> 8.1, of 512 level, of 768 10.9 -> 13.8
-    // the other way; 32 of 1,024, 8 tiles for 7, 23.0 -> 21.8, of 2,048, 16 for 14,
-    // 33.5 -> 36.4 the other way)
+    // Whole items, without a search and without parts to join, where the longest
+    // row of them is four tiles or one more than an equal share (8 key heads of
+    // 128, one sequence of 128 keys 10.1 -> 6.7 us, of 512 level, of 768 10.9 -> 14.3
+    // the other way; 64 sequences of up to 256 keys, two a CTA, 19.1 -> 16.7, 100 of
+    // up to 512 34.8 -> 32.3, of 1,024 50.8 -> 52.5 the other way)
     p.split_tiles = 2;  // (one tile each: 21.3 us against 19.6 at one sequence of 4,096 keys)
-    p.whole = items <= ctas && tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
-    p.decode_ctas = static_cast<int>(p.whole ? items : std::min(all, ctas));
+    p.whole = (items + ctas - 1) / ctas * tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
+    p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
     return p;
   }
   p.row_tiles = rows > 128 ? 2 : 1;

@@ -89,7 +89,7 @@ struct PagedAttnArgs {
   int row_tiles;             // 128-row tiles of a CTA (1 or 2)
   int splits, split_tiles;   // key splits and key tiles of one
   int by_length;             // the longest sequences' CTAs first (at most 32 sequences)
-  int whole;                 // few rows: each CTA takes one whole (sequence, key head), no parts
+  int whole;                 // few rows: each CTA takes whole (sequence, key head) pairs, no parts
   float* part_o;             // [splits][T][HQ][d]; null without splits
   float* part_lse;           // [splits][T][HQ], log2 units
   int* dev_status;

@@ -6,8 +6,8 @@
 //     (sequence, key head) items, in order, are one line of W tiles; each CTA
 //     takes an equal stretch of it, whatever the sequences' lengths. A stretch
 //     cuts at most its first and its last item; a combine kernel joins those
-//     parts by their lse, whole items are written directly. Short sequences on
-//     few heads: each CTA takes one whole item, and there is nothing to join.
+//     parts by their lse, whole items are written directly. Where sequences are
+//     short each CTA takes whole items instead, and there is nothing to join.
 //   - A CTA's loads run on through its items: Q of the next item is fetched by
 //     a warp of its own while the current one is worked on, and the ring of K
 //     and V stages never empties between items. Two CTAs per SM cover each
@@ -63,10 +63,12 @@ struct Segment {
   int slot;  // partial slot, or -1: the whole item
 };
 
-// A CTA's stretch of the line of tiles, from its next tile on.
+// A CTA's stretch of the line of tiles, from its next tile on; with whole items,
+// its next one of them.
 struct Stretch {
   int b, hk, tile;
   int left;  // tiles
+  int item;
 };
 
 struct Seq {
@@ -143,6 +145,17 @@ __device__ __forceinline__ int locate(const PagedAttnArgs& a, int ctas, long lon
 // The next part of a CTA's stretch; false at its end.
 __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Stretch& st, Segment& sg, bool first) {
   if (st.left <= 0) return false;
+  if (a.whole) {
+    for (; st.item < a.B * a.HK; st.item += gridDim.x) {
+      const int b = st.item / a.HK;
+      const Seq s = load_seq(a, b);
+      if (s.tiles == 0) continue;
+      sg = {b, st.item - b * a.HK, 0, s.tiles, s.tok0, s.n, s.len, -1};
+      st.item += gridDim.x;
+      return true;
+    }
+    return false;
+  }
   Seq s = load_seq(a, st.b);
   while (s.tiles == 0) {  // (b < B: tiles are left)
     ++st.b;
@@ -239,13 +252,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   Stretch st;
-  if (a.whole) {  // one item
-    st.b = static_cast<int>(blockIdx.x) / a.HK;
-    st.hk = static_cast<int>(blockIdx.x) - st.b * a.HK;
-    st.tile = 0;
-    const Seq s = load_seq(a, st.b);
-    st.left = s.tiles;
-    if (threadIdx.x == 0) visit(st.b, s, st.hk == 0, st.hk == 0);
+  if (a.whole) {  // every gridDim-th item
+    st.item = static_cast<int>(blockIdx.x);
+    st.left = 1;
+    for (int i = st.item + static_cast<int>(threadIdx.x) * gridDim.x; i < a.B * a.HK; i += kThreads * gridDim.x)
+      if (i % a.HK == 0) visit(i / a.HK, load_seq(a, i / a.HK), true, true);
   } else {  // this CTA's stretch of the line of tiles
     long long total;
     const int chunk = locate(

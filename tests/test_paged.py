@@ -383,7 +383,8 @@ def test_rows_in_front_of_the_first_sequence_stay(n, splits):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,HQ,HK,d,n,most", [(1, 8, 8, 64, 1, 130), (5, 12, 3, 128, 2, 300), (38, 32, 8, 64, 1, 512),
-                                              (40, 8, 8, 64, 1, 512), (9, 2, 2, 128, 16, 512)])
+                                              (40, 8, 8, 64, 1, 512), (9, 2, 2, 128, 16, 512),
+                                              (64, 8, 8, 64, 1, 250), (100, 16, 8, 128, 1, 200), (700, 2, 1, 64, 3, 100)])
 def test_short_sequences_of_few_rows(B, HQ, HK, d, n, most):
     """Up to and past 2 x 152 (sequence, key head) pairs; sequences without keys or new tokens among them."""
     r = np.random.default_rng(B + d)
@@ -406,14 +407,15 @@ def test_short_sequences_of_few_rows(B, HQ, HK, d, n, most):
 @pytest.mark.gpu
 def test_single_tokens_whose_items_are_whole_follow_one_another():
     """Two tiles a sequence, none cut: each call's output is the next one's queries."""
-    B, d = 305, 64  # more than 2 x 152, so that the kernel that joins parts is launched
+    B, d = 152, 64
     c = Cache([256] * B, 1, d, 16, torch.bfloat16)
+    table = torch.nn.functional.pad(c.table, (0, 60))  # (room for 1,024 keys, so that the joining kernel is launched)
     q0 = torch.randn(B, 1, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
 
     def chain(wait):
         q = q0
         for _ in range(20):
-            o, _ = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, max_kv_len=256)
+            o, _ = skl.streamkl_paged_attn(q, c.k, c.v, table, c.lens, max_kv_len=1024)
             q = o * 16
             if wait:
                 torch.cuda.synchronize()
@@ -814,7 +816,7 @@ def test_attention_splits_on_the_host(lib):
     assert size(1, 1, 32, 8, 128, 1, 4096, 1) == 0
     # two parts of 32 rows a CTA; no more CTAs than key tiles
     assert size(1, 1, 4, 1, 64, 1, 1024) == 2 * 8 * 32 * 65 * 4
-    assert size(1, 1, 4, 1, 64, 1, 512) == 0 and size(38, 38, 8, 8, 64, 1, 512) == 0  # each CTA takes a whole one
+    assert size(1, 1, 4, 1, 64, 1, 512) == 0 and size(64, 64, 8, 8, 64, 1, 250) == 0  # CTAs take whole ones
     assert size(39, 39, 8, 8, 64, 1, 512) == 2 * 304 * 32 * 65 * 4                    # (more than 2 x 152 of them)
     assert size(64, 64, 32, 8, 128, 1, 16384) == size(1, 1, 1, 1, 128, 1, 1 << 20)
 
