@@ -16,10 +16,10 @@
 // only when terms would exceed 2^8 of it, so O is seldom rescaled; the results
 // do not depend on it.
 //
-// CTA: warp 0 loads (each lane one page's box of a tile; pages are found
-// through the block table), warp 1 issues MMAs, warps 4.. are one softmax
-// warpgroup per row tile, thread = row. Two row tiles (NT = 2) share each K and
-// V tile. At d = 128 their O fill half of TMEM and P has to take S's place:
+// CTA: warp 0 loads (at d = 128 K, and warp 2 V; each lane one page's box of a
+// tile; pages are found through the block table), warp 1 issues MMAs, warps 4..
+// are one softmax warpgroup per row tile, thread = row. Two row tiles (NT = 2)
+// share each K and V tile. At d = 128 their O fill half of TMEM and P has to take S's place:
 // the tiles alternate, the tensor pipe works on one while the other's softmax
 // runs. At d = 64, or with one row tile, P has columns of its own and the next
 // S is made while this one's terms are.
@@ -59,6 +59,11 @@ struct AttnLayout {
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
   // P in columns of its own, where TMEM has room for them
   static constexpr bool OWN_P = D == 64 || NT == 1;
+  // Warps that load. Each box is an instruction of its own: with 16-slot pages one
+  // warp takes longer over K and V of 128 columns than the rest takes (16 tokens x
+  // 4 heads over 4,096 keys in one CTA a key head 56 us, 39 with one warp for each;
+  // 64 tokens 61 and 56; at d = 64 50.1 and 51.6, a warp's share of the issue slots)
+  static constexpr int LOADERS = D == 128 ? 2 : 1;
   // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2],
   // s_read, p_read, drain
   static constexpr int NBAR = 2 + 2 * STAGES + 9;
@@ -226,12 +231,13 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   // NT = 2: 128 threads with 88 registers and 256 with 208 make up the launch's
   // 384 x 168; a softmax thread holds a row of S (128)
   if (NT == 2) regs_dec<88>();
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
+  if (warp == 0 || (L::LOADERS == 2 && warp == 2)) {
+    // ------------------------------------------------- loads, of K, V or both
     const int page = 1 << a.page_shift;
     const int box_rows = min(page, kTileN);
     const int* table = a.table + static_cast<long long>(b) * a.table_sb;
-    int issued = 0;
+    const bool has_v = L::LOADERS == 1 || warp == 2;
+    int loads = 0;  // issued
     bool ok = true;
     // the page this lane loads of tile j; a number that is none is reported
     // and page 0 read in its place
@@ -245,9 +251,12 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       }
       return p;
     };
-    auto load = [&](const CUtensorMap* map, int j, int pg) {
-      const int s = issued % L::STAGES;
-      if (!warp_wait(kv_empty(s), ((issued / L::STAGES) & 1) ^ 1, wc)) return false;
+    auto load = [&](const CUtensorMap* map, int i, int j, int pg) {
+      // The stage's barrier cannot be two phases behind what is waited for: loads
+      // are used in their order, so when this warp's one before this had its
+      // stage, all that lie a ring and more back from there had been used
+      const int s = i % L::STAGES;
+      if (!warp_wait(kv_empty(s), ((i / L::STAGES) & 1) ^ 1, wc)) return false;
       const int key0 = (w.t0 + j) * kTileN;
       const int pages = (min(kTileN, w.klim - key0) + box_rows - 1) / box_rows;
       const uint32_t dst = sb + L::OFF_KV + s * L::TILE + lane * box_rows * 128;
@@ -261,29 +270,30 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
                         a.HK, __LINE__))
             tma_load_4d(dst + kb * L::BOX, map, kv_full(s), kb * 64, slot, hk, pg);
       }
-      ++issued;
+      ++loads;
       return true;
     };
     int pg = page_of(0), pg_next = page_of(1);
-    if (!L::OWN_P) {
+    if (L::LOADERS == 1) {
+      static_assert(L::LOADERS == 2 || L::OWN_P, "K0 K1 V0 K2 V1 ..");
+      if (n_iter > 0) ok = load(&tm_k, 0, 0, pg);
       for (int j = 0; ok && j < n_iter; ++j) {
-        ok = load(&tm_k, j, pg) && load(&tm_v, j, pg);
+        if (j + 1 < n_iter) ok = load(&tm_k, idx_k(j + 1), j + 1, pg_next);
+        if (ok) ok = load(&tm_v, idx_v(j), j, pg);
         pg = pg_next;
         pg_next = page_of(j + 2);
       }
     } else {
-      if (n_iter > 0) ok = load(&tm_k, 0, pg);
       for (int j = 0; ok && j < n_iter; ++j) {
-        if (j + 1 < n_iter) ok = load(&tm_k, j + 1, pg_next);
-        if (ok) ok = load(&tm_v, j, pg);
+        ok = has_v ? load(&tm_v, idx_v(j), j, pg) : load(&tm_k, idx_k(j), j, pg);
         pg = pg_next;
         pg_next = page_of(j + 2);
       }
     }
-    // the last load is the last tile's V: clear its rows past the last key
-    // (the slots there hold anything, and 0 x NaN is NaN)
-    if (ok && n_iter > 0 && last_valid < kTileN) {
-      const int i = issued - 1;
+    // the last tile's V: clear its rows past the last key (the slots there hold
+    // anything, and 0 x NaN is NaN)
+    if (has_v && ok && n_iter > 0 && last_valid < kTileN) {
+      const int i = idx_v(n_iter - 1);
       if (warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc)) {
         uint8_t* v = gb + L::OFF_KV + (i % L::STAGES) * L::TILE;
         for (int e = last_valid * 8 + lane; e < kTileN * 8; e += 32)  // 16 bytes each
@@ -295,9 +305,12 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         if (lane == 0) mbar_arrive(v_fixed);
       }
     }
-    // let every copy land before the CTA can exit
-    for (int i = max(0, issued - L::STAGES); i < issued; ++i)
-      wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
+    // let every copy land before the CTA can exit: this warp's last in the ring
+    // (a stage that was used again, its copy had landed)
+    for (int j = max(0, loads - (L::STAGES + L::LOADERS - 1) / L::LOADERS); j < loads; ++j) {
+      const int i = L::LOADERS == 1 ? j : has_v ? idx_v(j) : idx_k(j);
+      if (!ok || i >= 2 * n_iter - L::STAGES) wait_drain(kv_full(i % L::STAGES), (i / L::STAGES) & 1, a.timeout_ns);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
     // One thread issues every product, so its own instructions count: it waits
