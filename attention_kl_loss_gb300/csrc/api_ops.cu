@@ -197,21 +197,21 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   const int tiles = std::max(1, (max_kv + 127) / 128);
   int s = requested;
   if (s <= 0) {
-    // A tile's time, a CTA's own, and the joining of partials; of several
-    // sequences, which are seldom all of the largest size, 3/4 of the CTAs have
-    // work. The constants are those that come nearest to the best split of 37
-    // shapes (1 to 100 sequences, 16 to 2,048 new tokens, 300 to 131,072 keys): 2 %
-    // from it, 30 % at worst (two chunks of up to 700 rows over up to 9,000 keys, 84
-    // us in three splits and 65 in two; five of 400 over 3,000 43 us whole, 26 in
-    // three).
+    // A tile's time, a CTA's own, and the joining of partials. One sequence's CTAs
+    // come in whole waves; of several sequences, which are seldom all of the largest
+    // size, 3/4 of the CTAs have work and one follows another as it ends. The
+    // constants are those that come nearest to the best split of 48 shapes (1 to
+    // 100 sequences, 16 to 2,048 new tokens, 300 to 131,072 keys): 1.4 % from it, 22 %
+    // at worst (five chunks of up to 400 rows over up to 3,000 keys: 43 us whole, 31
+    // in two splits, 26 in three).
     const int sms = num_sms();
     const double ctas = static_cast<double>(p.q_tiles) * B * HK * (B > 1 ? 0.75 : 1.0);
-    const double tile_us = d == 128 ? 1.7 : 1.1, cta_us = 2.0, join_us = 6.0;
+    const double tile_us = d == 128 ? 1.5 : 1.1, cta_us = 5.0, join_us = 5.0, whole = B > 1 ? 0.1 : 1.0;
     const double part_us = static_cast<double>(T) * HQ * (d + 1) * 8.0 / 6.0e12 * 1e6;
     auto cost = [&](int n) {
       const int per = (tiles + n - 1) / n;
       const double waves = ctas * ((tiles + per - 1) / per) / sms;
-      const double turns = std::max(1.0, 0.15 * std::ceil(waves - 1e-9) + 0.85 * waves);
+      const double turns = std::max(1.0, whole * std::ceil(waves - 1e-9) + (1.0 - whole) * waves);
       return turns * (per * tile_us + cta_us) + (n > 1 ? join_us + n * part_us : 0.0);
     };
     s = 1;
