@@ -650,37 +650,39 @@ __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __gri
   const int begin = a.cu != nullptr ? __ldg(a.cu) : 0, end = a.cu != nullptr ? __ldg(a.cu + a.B) : a.B;
   const int token = static_cast<int>(e / a.HQ), head = static_cast<int>(e - static_cast<long long>(token) * a.HQ);
   if (e >= rows || token < begin || token >= end) return;
+  // splits whose loads are in flight, the first ones beside the lse's (16 tokens x
+  // 4 heads over 4,096 keys in 16 splits, both kernels: 12.5 us, 15.3 after the lse)
+  constexpr int RUN = 8;
+  float p[RUN][V];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      if (s0 + i >= a.splits) break;
+      const float* src = a.part_o + ((s0 + i) * rows + e) * D + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(src);
+      else
+        *reinterpret_cast<float2*>(p[i]) = *reinterpret_cast<const float2*>(src);
+    }
+  };
+  fetch(0);
   float top = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + e]);
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
   const float t0 = top == -INFINITY ? 0.f : top;
   float total = 0.f, o[V] = {};
-  for (int s0 = 0; s0 < a.splits; s0 += 32) {
-    const float mine = s0 + lane < a.splits ? ex2(a.part_lse[(s0 + lane) * rows + e] - t0) : 0.f;
-    const int end_s = min(32, a.splits - s0);
-    for (int s1 = 0; s1 < end_s; s1 += 8) {  // 8 splits' loads in flight
-      float w[8], p[8][V];
+  for (int s0 = 0; s0 < a.splits; s0 += RUN) {
+    if (s0 > 0) fetch(s0);
+    const float mine = lane < RUN && s0 + lane < a.splits ? ex2(a.part_lse[(s0 + lane) * rows + e] - t0) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] = __shfl_sync(0xFFFFFFFFu, mine, s1 + i);  // 0 past the last split
-        if (w[i] != 0.f) {  // (the partial of an empty range is not written)
-          const float* src = a.part_o + ((s0 + s1 + i) * rows + e) * D + lane * V;
-          if constexpr (V == 4)
-            *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(src);
-          else
-            *reinterpret_cast<float2*>(p[i]) = *reinterpret_cast<const float2*>(src);
-        } else {
+    for (int i = 0; i < RUN; ++i) {
+      if (s0 + i >= a.splits) break;
+      const float w = __shfl_sync(0xFFFFFFFFu, mine, i);
+      total += w;
 #pragma unroll
-          for (int k = 0; k < V; ++k) p[i][k] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        total += w[i];
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = fmaf(w[i], p[i][k], o[k]);
-      }
+      for (int k = 0; k < V; ++k)  // (the partial of an empty range is not written)
+        if (w != 0.f) o[k] = fmaf(w, p[i][k], o[k]);
     }
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
