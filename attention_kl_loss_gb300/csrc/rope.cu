@@ -527,7 +527,23 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   const bool is_v = part >= a.hchunks;
   const int h0 = (is_v ? part - a.hchunks : part) * a.hc, h1 = min(a.H, h0 + a.hc);
   const int t = tile * TOKENS + grp;
-  bool ok = t < a.T;
+  const bool there = t < a.T;
+  const void* src = is_v ? a.v : a.k;
+  const RowStrides& st = is_v ? a.vs : a.ks;
+  const LaneChunks lc = lane_chunks(l, a.rot);
+  Raw8<TYPE> r0[UNROLL], r1[UNROLL];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+      if (there && h + u < h1) {
+        r0[u] = load8<TYPE>(src, t * st.sn + (h + u) * st.sh + 8 * lc.c0);
+        r1[u] = load8<TYPE>(src, t * st.sn + (h + u) * st.sh + 8 * lc.c1);
+      } else {
+        r0[u] = r1[u] = Raw8<TYPE>{};
+      }
+  };
+  fetch(h0);  // beside the search for its place, a chain of loads
+  bool ok = there;
   int pos = 0;
   long long place = 0, head = 0;  // element of head 0's slot, head stride
   if (ok) {
@@ -564,7 +580,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
       head = is_v ? a.vc_sh : a.kc_sh;
     }
   }
-  const LaneChunks lc = lane_chunks(l, a.rot);
   const bool norm = !is_v && a.w != nullptr;
   const bool turned = !is_v && lc.turned && a.cos != nullptr;
   float c[8], sn[8], w0[8], w1[8];
@@ -573,19 +588,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     load_f8(a.w + 8 * lc.c0, w0);
     load_f8(a.w + 8 * lc.c1, w1);
   }
-  const void* src = is_v ? a.v : a.k;
-  const RowStrides& st = is_v ? a.vs : a.ks;
   void* dst = is_v ? a.vc : a.kc;
   for (int h = h0; h < h1; h += UNROLL) {
-    Raw8<TYPE> r0[UNROLL], r1[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (ok && h + u < h1) {
-        r0[u] = load8<TYPE>(src, t * st.sn + (h + u) * st.sh + 8 * lc.c0);
-        r1[u] = load8<TYPE>(src, t * st.sn + (h + u) * st.sh + 8 * lc.c1);
-      } else {
-        r0[u] = r1[u] = Raw8<TYPE>{};
-      }
+    if (h > h0) fetch(h);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       if (h + u >= h1) break;
