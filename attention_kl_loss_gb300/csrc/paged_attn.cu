@@ -639,7 +639,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
 
 // Join the splits of a row (token, head), one warp a row: with weights
 // 2^(lse_s - lse), o = sum_s w_s o_s.
-template <int TYPE, int D>
+// RUN: splits whose loads are in flight, the first ones beside the lse's (16
+// tokens x 4 heads over 4,096 keys in 16 splits, both kernels: 12.5 us, 15.3 after
+// the lse); few where there are few, for more warps (512 tokens x 32 heads in two
+// splits, both kernels: 112.5 us, 114.2 with 8).
+template <int TYPE, int D, int RUN>
 __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
   grid_dependency_wait();  // launched while the attention kernel ends
@@ -650,9 +654,6 @@ __global__ void __launch_bounds__(256) streamkl_paged_combine_kernel(const __gri
   const int begin = a.cu != nullptr ? __ldg(a.cu) : 0, end = a.cu != nullptr ? __ldg(a.cu + a.B) : a.B;
   const int token = static_cast<int>(e / a.HQ), head = static_cast<int>(e - static_cast<long long>(token) * a.HQ);
   if (e >= rows || token < begin || token >= end) return;
-  // splits whose loads are in flight, the first ones beside the lse's (16 tokens x
-  // 4 heads over 4,096 keys in 16 splits, both kernels: 12.5 us, 15.3 after the lse)
-  constexpr int RUN = 8;
   float p[RUN][V];
   auto fetch = [&](int s0) {
 #pragma unroll
@@ -720,7 +721,10 @@ cudaError_t attn_t(const PagedAttnArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, streamkl_paged_combine_kernel<TYPE, D>, a);
+  auto combine = a.splits <= 2   ? streamkl_paged_combine_kernel<TYPE, D, 2>
+                 : a.splits <= 4 ? streamkl_paged_combine_kernel<TYPE, D, 4>
+                                 : streamkl_paged_combine_kernel<TYPE, D, 8>;
+  return cudaLaunchKernelEx(&cfg, combine, a);
 }
 
 template <int TYPE, int D>

@@ -16,8 +16,8 @@
 //   - Only 32 rows of Q are kept (4 KB per 64 columns): the MMA reads 128 rows,
 //     the ones past the 32nd from whatever lies behind, and its result rows
 //     past the 32nd are never looked at.
-// 64 sequences of 4,096 to 16,384 keys, 32 heads over 8 key heads of 128: 0.38 ms
-// for 2.6 GB, 6.9 TB/s (one CTA per (sequence, key head) and key split: 0.54 ms).
+// 64 sequences of 4,096 to 16,384 keys, 32 heads over 8 key heads of 128: 0.39 ms
+// for 2.6 GB, 6.7 TB/s (one CTA per (sequence, key head) and key split: 0.54 ms).
 // CTA: warp 0 softmax and output (thread = row, TMEM lanes 0..31), warp 1 loads
 // of K and V, warp 2 MMAs, warp 3 Q and the items' numbers.
 #include <algorithm>
