@@ -15,6 +15,7 @@ import importlib.util
 import math
 import os
 import types
+import warnings
 from typing import Optional
 
 import torch
@@ -112,13 +113,17 @@ def _load_variant(debug: bool) -> ctypes.CDLL:
 
 def _native_calls(path: str):
     """The native way to the operators' entries of this library (``ops`` takes
-    it first), None where it was built under another version of PyTorch."""
+    it first), None where the tree was built under another PyTorch."""
     so = _build.marshal_path()
     if not os.path.exists(so):
         return None
     loader = importlib.machinery.ExtensionFileLoader("_marshal", so)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", so, loader=loader))
-    loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", so, loader=loader))
+        loader.exec_module(module)
+    except ImportError as error:
+        warnings.warn(f"{so} does not fit this PyTorch ({error}): calls around the KL take longer on the host")
+        return None
     entries = module.entries(path)
     return types.SimpleNamespace(**{name: functools.partial(getattr(module, name), entries)
                                     for name in ("rope_fwd", "rope_bwd", "append", "attn")})

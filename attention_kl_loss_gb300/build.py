@@ -92,7 +92,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    if not debug and (force or _stale(marshal_path(), [os.path.join(CSRC, "marshal.cpp"), headers[-1]])):
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        sys.stderr.write("no Python.h: calls around the KL will go through ctypes\n")
+    elif not debug and (force or _stale(marshal_path(), [os.path.join(CSRC, "marshal.cpp"), headers[-1]])):
         jobs.append(_marshal_cmd())
 
     def run(cmd):

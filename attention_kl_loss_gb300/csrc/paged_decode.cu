@@ -228,8 +228,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(o_full, 1);
       mbar_init(drain, 1);
     }
-    // a failure recorded earlier, or a failed layout check, skips the work
-    *skip_flag = !lay_ok || *reinterpret_cast<volatile int*>(a.dev_status) != 0;
+    // a failure recorded earlier, or a failed layout check, skips the work; not a
+    // bad number of some sequence, which may come from this very call
+    const int before = *reinterpret_cast<volatile int*>(a.dev_status);
+    *skip_flag = !lay_ok || (before != 0 && before != kStatusInvalidArg);
     fence_mbar_init();
   }
   if (warp == 1 && lane == 0) {

@@ -36,6 +36,13 @@ _APPEND = struct.Struct("N" + 4 * _ROWS + "PqPPPPPP11if")
 _ATTN = struct.Struct("N" + 4 * _ROWS + "PqPPPPNP13if")
 
 
+def _pack(fields, *values):
+    try:
+        return fields.pack(fields.size, *values)
+    except struct.error as error:
+        raise ValueError(f"an argument is no number or out of range: {error}") from error
+
+
 def _elsewhere(call, device, stream, kwargs):
     """Run ``call`` with ``device`` current (launches and tensor maps go to the
     current device) and ``stream``, if given, the current stream: what the call
@@ -237,7 +244,7 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
     status, _keep = _status(dev_status, index)
     if B * (NQ * HQ + NK * HK) == 0:
         return yq, yk
-    args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *_NONE, *_NONE, cos_at, sin_at, pq, sq, pk, sk, wq, wk, 0, 0, 0, 0,
+    args = _pack(_ROPE, *iq, *ik, *oq, *ok, *_NONE, *_NONE, cos_at, sin_at, pq, sq, pk, sk, wq, wk, 0, 0, 0, 0,
                       status, _DTYPES[x.dtype], B, NQ, NK, HQ, HK, d, rot, length, bool(interleaved), k_repeat, eps)
     st = load().streamkl_qk_norm_rope_fwd(args, _raw_stream(index))
     if st:
@@ -301,7 +308,7 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     lib = load()
     need = lib.streamkl_qk_norm_rope_bwd_workspace_size(B, NQ, NK, HQ, HK, d) if wq or wk else 0
     ws = _workspace(need, dev, workspace)
-    args = _ROPE.pack(_ROPE.size, *iq, *ik, *oq, *ok, *gq, *gk, cos_at, sin_at, pq, sq, pk, sk, wq, wk, dwq_at, dwk_at,
+    args = _pack(_ROPE, *iq, *ik, *oq, *ok, *gq, *gk, cos_at, sin_at, pq, sq, pk, sk, wq, wk, dwq_at, dwk_at,
                       ws.data_ptr() if need else 0, need, status, _DTYPES[x.dtype], B, NQ, NK, HQ, HK, d, rot, length,
                       bool(interleaved), k_repeat, eps)
     st = lib.streamkl_qk_norm_rope_bwd(args, _raw_stream(index))
@@ -372,7 +379,7 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     status, _keep = _status(dev_status, index)
     if total == 0 or HK == 0:
         return k_cache, v_cache
-    args = _APPEND.pack(_APPEND.size, k.data_ptr(), 0, k0, k1, v.data_ptr(), 0, v0, v1, *cache, cos_at, sin_at, w, status,
+    args = _pack(_APPEND, k.data_ptr(), 0, k0, k1, v.data_ptr(), 0, v0, v1, *cache, cos_at, sin_at, w, status,
                         _DTYPES[dtype], B, total, HK, d, *pages, rot, length, bool(interleaved), eps)
     st = load().streamkl_paged_append(args, _raw_stream(index))
     if st:
@@ -445,7 +452,7 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    args = _ATTN.pack(_ATTN.size, q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(),
+    args = _pack(_ATTN, q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(),
                       workspace.data_ptr(), workspace.nbytes, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q,
                       max_kv, bool(causal), num_splits, 1.0 / math.sqrt(d) if scale is None else scale)
     st = lib.streamkl_paged_attn(args, _raw_stream(index))

@@ -449,7 +449,8 @@ streamkl_status streamkl_paged_append(const streamkl_append_args* args, void* st
  * Slots past a sequence's length and page numbers past its last page are
  * never used, whatever they hold. A value of V that is not finite reaches
  * every row whose key tile it lies in. Offsets or lengths out of range or
- * above their bounds, and bad page numbers, are reported in *dev_status.
+ * above their bounds, and bad page numbers, are reported in *dev_status; the
+ * rows of such a sequence mean nothing, those of the others are computed.
  * Results are the same in every run for the same sizes.
  */
 typedef struct {

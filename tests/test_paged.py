@@ -425,6 +425,43 @@ def test_single_tokens_whose_items_are_whole_follow_one_another():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,bound,splits", [(1, 300, 0), (1, 1024, 0), (40, 300, 1), (40, 1024, 3)])
+def test_each_kernel_reports_and_leaves_the_other_sequences_right(n, bound, splits):
+    """Whole sequences, equal shares of the tiles, chunks, chunks with split keys."""
+    lens, HK, d = [300, 190], 2, 64
+    q = torch.randn(2 * n, 4, d, generator=torch.Generator().manual_seed(n)).bfloat16().cuda()
+    for what in ("nothing", "page", "negative page", "length", "negative length", "offsets", "NaN"):
+        c = Cache(lens, HK, d, 16, torch.bfloat16)
+        table = torch.nn.functional.pad(c.table, (0, 60), value=-7)
+        cu = _cu([n, n])
+        if what == "page":
+            table[0, 5] = c.k.shape[0]
+        elif what == "negative page":
+            table[0, 18] = -1
+        elif what == "length":
+            c.lens[0] = bound + 1
+        elif what == "negative length":
+            c.lens[0] = -3
+        elif what == "offsets":
+            cu[0] = -1
+        elif what == "NaN":
+            c.k[c.table[0, 3].long(), 0, 5] = float("nan")
+        st = binding.new_status()
+        o, lse = skl.streamkl_paged_attn(q, c.k, c.v, table, c.lens, cu_seqlens=cu, max_seqlen_q=n, max_kv_len=bound,
+                                         num_splits=splits, dev_status=st)
+        if what in ("nothing", "NaN"):
+            binding.raise_on_device_status(st)
+        else:
+            with pytest.raises(binding.StreamKLError):
+                binding.raise_on_device_status(st)
+        _check_attn(o[n:], lse[n:], q[n:], type("", (), {"rows": c.rows[1:]}), [n], lens[1:], d ** -0.5, True,
+                    torch.bfloat16)
+        if what == "NaN":
+            assert torch.all(torch.isnan(o[:n, :2])) and torch.all(torch.isnan(lse[:n, :2]))
+            assert torch.all(torch.isfinite(o[:n, 2:]))
+
+
+@pytest.mark.gpu
 def test_nan_in_one_sequence_stays_there():
     lens = [200, 200]
     c = Cache(lens, 1, 64, 16, torch.bfloat16)
@@ -778,6 +815,10 @@ def test_append_python_call_refuses():
     ]:
         with pytest.raises(ValueError, match=match):
             call(*args, **kw)
+    with pytest.raises(ValueError, match="out of range"):
+        call(*ok, eps="1")
+    with pytest.raises(binding.StreamKLError):  # (infinite as a float)
+        call(*ok, eps=1e300)
 
 
 @pytest.mark.parametrize("over,status", CACHE_REFUSED + [
