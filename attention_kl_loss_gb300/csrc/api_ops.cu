@@ -187,7 +187,7 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
     // 128, one sequence of 128 keys 10.1 -> 6.7 us, of 512 level, of 768 10.9 -> 14.3
     // the other way; 64 sequences of up to 256 keys, two a CTA, 19.1 -> 16.7, 100 of
     // up to 512 34.8 -> 32.3, of 1,024 50.8 -> 52.5 the other way)
-    p.split_tiles = 2;  // (one tile each: 21.3 us against 19.6 at one sequence of 4,096 keys)
+    p.split_tiles = 2;  // (one tile each is level: one sequence of 4,096 keys 18.7 us against 18.4)
     p.whole = (items + ctas - 1) / ctas * tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
     p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
     return p;
