@@ -24,10 +24,12 @@
 // runs. At d = 64, or with one row tile, P has columns of its own and the next
 // S is made while this one's terms are.
 //
-// At d = 128 512 rows x 32 heads against 131,072 keys take 0.71 ms, 1.55 PFLOP/s:
-// 2,900 cycles a turn (a key tile for both row tiles), of which the 32 products
-// take 2,048 back to back, as the 256 KB of operands and loads at 128 bytes a
-// cycle do; a row tile's own chain, S, terms (1,330), P, PV, is what is left.
+// At d = 128 512 rows x 32 heads against 131,072 keys take 0.68 ms, 1.61 PFLOP/s:
+// about 2,800 cycles a turn (a key tile for both row tiles), of which the 32
+// products take 2,048 back to back, as the 256 KB of operands and loads at 128
+// bytes a cycle do; a row tile's own chain, S, terms, P, PV, is what is left. P is
+// handed over in halves, so that PV starts while half of the terms are made (0.70
+// ms whole).
 // Tried and not faster: two softmax warpgroups per row tile (936 us), an issuing
 // thread per row tile (765 us), L2 prefetches (738 us). At d = 64 the terms are
 // half of a turn: 2,700 cycles, the exponentials alone 1,024, the products 1,050.
@@ -37,6 +39,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "ops.h"
 #include "paged.cuh"
@@ -65,8 +68,8 @@ struct AttnLayout {
   // 64 tokens 61 and 56; at d = 64 50.1 and 51.6, a warp's share of the issue slots)
   static constexpr int LOADERS = D == 128 ? 2 : 1;
   // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2],
-  // s_read, p_read, drain
-  static constexpr int NBAR = 2 + 2 * STAGES + 9;
+  // s_read, p_read, drain, p_half[2], o_half[2]
+  static constexpr int NBAR = 2 + 2 * STAGES + 13;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 232448, "shared memory budget");
@@ -170,7 +173,9 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   auto p_full = [&](int k) { return bar0 + 8u * (4 + 2 * L::STAGES + k); };
   auto o_full = [&](int k) { return bar0 + 8u * (6 + 2 * L::STAGES + k); };
   const uint32_t s_read = bar0 + 8u * (8 + 2 * L::STAGES), p_read = s_read + 8, drain = s_read + 16;
-  static_assert(11 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
+  auto p_half = [&](int k) { return bar0 + 8u * (11 + 2 * L::STAGES + k); };
+  auto o_half = [&](int k) { return bar0 + 8u * (13 + 2 * L::STAGES + k); };
+  static_assert(15 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
   volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
@@ -194,6 +199,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         mbar_init(s_full(k), 1);
         mbar_init(p_full(k), L::OWN_P ? 4 * nt : 4);
         mbar_init(o_full(k), 1);
+        mbar_init(p_half(k), 4);
+        mbar_init(o_half(k), 1);
       }
       mbar_init(s_read, 4 * nt);
       mbar_init(p_read, 1);
@@ -350,6 +357,13 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         for (int i = 0; i < kTileN / 16; ++i)
           mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * i, desc(v + i * (2048 >> 4)), id_o, i > 0 ? 1 : add);
       };
+      auto mma_o_half = [&](int half, uint32_t v, uint32_t col_p, uint32_t col_o, uint32_t add) {  // 64 keys of it
+#pragma unroll
+        for (int i = 0; i < kTileN / 32; ++i) {
+          const int k = half * (kTileN / 32) + i;
+          mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * k, desc(v + k * (2048 >> 4)), id_o, i > 0 ? 1 : add);
+        }
+      };
       bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && landed();
       uint32_t k_at = next();
       auto both_s = [&]() {
@@ -366,18 +380,20 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           // P of row tile 0 comes with V of this tile and K of the next
           const uint32_t v_at = next();
           if (more) k_at = next();
-          if (!(ok = wait_bounded(p_full(0), j & 1, wc))) break;
-          tc_fence_after();
-          mma_o(v_lo + v_at, L::col_p(0), L::col_o(0), j > 0);
-          if (more) mma_s(q_lo, k_lo + k_at, L::col_s(0));
-          mma_commit(more ? s_full(0) : o_full(0));
-          if (nt == 2) {
-            if (!(ok = wait_bounded(p_full(1), j & 1, wc))) break;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t == nt) break;
+            if (!(ok = wait_bounded(p_half(t), j & 1, wc))) break;
             tc_fence_after();
-            mma_o(v_lo + v_at, L::col_p(1), L::col_o(1), j > 0);
-            if (more) mma_s(q_lo + (L::TILE >> 4), k_lo + k_at, L::col_s(1));
-            mma_commit(more ? s_full(1) : o_full(1));
+            mma_o_half(0, v_lo + v_at, L::col_p(t), L::col_o(t), j > 0);
+            mma_commit(o_half(t));
+            if (!(ok = wait_bounded(p_full(t), j & 1, wc))) break;
+            tc_fence_after();
+            mma_o_half(1, v_lo + v_at, L::col_p(t), L::col_o(t), 1);
+            if (more) mma_s(q_lo + t * (L::TILE >> 4), k_lo + k_at, L::col_s(t));
+            mma_commit(more ? s_full(t) : o_full(t));
           }
+          if (!ok) break;
         } else {
           // S comes back with K of the next tile, P with V of this one
           if (more) {
@@ -449,7 +465,21 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       if (got && lane == 0) mbar_arrive(s_read);
       return got;
     };
+    auto landed_v = [&](int j) {
+      const int i = idx_v(j);
+      return warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc) &&
+             // (the last tile's rows past the last key are cleared first)
+             (j + 1 < n_iter || last_valid == kTileN || warp_wait(v_fixed, 0, wc));
+    };
+    auto hand_half = [&](int j) {  // the first half of P, with V
+      const bool got = warp != 5 || landed_v(j);
+      tc_fence_before();
+      __syncwarp();
+      if (got && lane == 0) mbar_arrive(p_half(t));
+      return got;
+    };
     for (int j = 0; t < nt && j < n_iter; ++j) {
+      bool handed = false;  // the first half of P
       if (!(ok = warp_wait(s_full(L::OWN_P ? 0 : t), j & 1, wc))) break;
       tc_fence_after();
       if (warp_live) {
@@ -468,12 +498,12 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           }
         };
         uint32_t p[64];
-        auto terms = [&]() {  // P against ref, in the inputs' type; its fp32 sum
+        auto terms_of = [&](auto first, auto last) {  // P against ref, in the inputs' type; its fp32 sum
           const float r0 = ref == -INFINITY ? 0.f : ref;
           const float2 c2 = make_float2(c, c), nr = make_float2(-r0, -r0);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
+          for (int k = first; k < last; ++k) {
             const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, nr);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
@@ -482,6 +512,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           const float2 f = __fadd2_rn(sum[0], sum[1]);
           return f.x + f.y;
         };
+        using std::integral_constant;
+        auto terms = [&]() { return terms_of(integral_constant<int, 0>{}, integral_constant<int, 64>{}); };
         // the maximum of the tile moves the reference if it exceeds it by more
         // than 2^8; by how much O and the sum scale then
         auto move_ref = [&](bool may) {
@@ -528,18 +560,51 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         } else {
           // Terms against the reference as it is, while their sum stays within
           // 2^8; else (and in a row's first tile) the maximum is taken. The
-          // products of the tiles before ended before this S
-          f = terms();
-          const bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
+          // products of the tiles before ended before this S. The first half's P
+          // is handed over while the second's is made
+          f = terms_of(integral_constant<int, 0>{}, integral_constant<int, 32>{});
+          bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
           if (__any_sync(0xFFFFFFFFu, again)) {
             load_s();
             const float alpha = move_ref(again);
             if (j > 0) scale_o(alpha);
             f = terms();
+            again = false;  // (S of the whole tile was looked at)
+          } else {
+            tmem_st16(tp, &p[0]);
+            tmem_st16(tp + 16, &p[16]);
+            tmem_wait_st();
+            if (!hand_half(j)) {
+              ok = false;
+              break;
+            }
+            handed = true;
+            float f2 = terms_of(integral_constant<int, 32>{}, integral_constant<int, 64>{});
+            again = !(f2 <= kSumMax);
+            if (__any_sync(0xFFFFFFFFu, again)) {  // the second half's maximum; the first is in O by then
+              if (!(ok = warp_wait(o_half(t), j & 1, wc))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int q = 2; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 128; ++k)
+                if (k < 64 || k >= seen) s[k] = -INFINITY;
+              l += f;
+              f = 0.f;
+              const float alpha = move_ref(again);
+              scale_o(alpha);
+              f2 = terms_of(integral_constant<int, 32>{}, integral_constant<int, 64>{});
+            }
+            f += f2;
           }
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
+        if (!handed) {
+          tmem_st16(tp, &p[0]);
+          tmem_st16(tp + 16, &p[16]);
+        }
+        tmem_st16(tp + 32, &p[32]);
+        tmem_st16(tp + 48, &p[48]);
         l += f;
         tmem_wait_st();
       } else if (L::OWN_P) {
@@ -551,12 +616,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       // this tile and (if S was not) K of the next: the waits are these warps'
       // to spend (a wait takes the issuer 100 cycles between products, with the
       // data there)
+      if (!L::OWN_P && !handed) {
+        if (!(ok = hand_half(j))) break;
+      }
       if (warp == 5) {
-        const int i = idx_v(j);
-        ok = warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc);
-        if (ok && !L::OWN_P && j + 1 < n_iter) ok = landed_k(j + 1);
-        // (the last tile's rows past the last key are cleared first)
-        if (ok && j + 1 == n_iter && last_valid < kTileN) ok = warp_wait(v_fixed, 0, wc);
+        ok = L::OWN_P ? landed_v(j) : j + 1 == n_iter || landed_k(j + 1);
         if (!ok) break;
       }
       tc_fence_before();

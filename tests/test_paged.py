@@ -280,6 +280,34 @@ def test_large_logits_move_the_reference(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,n,rise", [(128, 100, 1), (128, 100, -1), (128, 60, 1), (64, 100, 1)])
+def test_logits_that_rise_within_a_tile(d, n, rise, dtype):
+    """Scores of even rows rise (odd ones fall) by about 10 from one run of 64 keys to the next, so that the reference
+    moves in the middle of a tile, for some rows of a warp; the last rows also at the sequence's ragged end."""
+    dt = TYPES[dtype]
+    c = Cache([700], 1, d, 16, dt, fill=False)
+    g = torch.Generator().manual_seed(d + n)
+    u = torch.randn(d, generator=g)
+    u *= d ** 0.5 / u.norm()
+    steps = torch.arange(700) // 64 * rise * 10 / d ** 0.5
+    k = (steps[:, None, None] * u + 0.1 * torch.randn(700, 1, d, generator=g)).to(dt)
+    v = torch.randn(700, 1, d, generator=g).to(dt)
+    c.rows = [(k, v)]
+    at = torch.arange(700)
+    p, s = c.table[0, at.cuda() // 16].long(), (at % 16).cuda()
+    c.k[p, :, s], c.v[p, :, s] = k.cuda(), v.cuda()
+    sign = torch.where(torch.arange(n) % 2 == 0, 1.0, -1.0)[:, None, None]
+    q = (sign * u + 0.1 * torch.randn(n, 2, d, generator=g)).to(dt).cuda()
+    for splits, causal in ((1, True), (2, False)):
+        st = binding.new_status()
+        o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), max_kv_len=700, causal=causal,
+                                         num_splits=splits, dev_status=st)
+        binding.raise_on_device_status(st)
+        _check_attn(o, lse, q, c, [n], [700], d ** -0.5, causal, dt)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,n,L,HQ,HK,page,splits", [(32, 1, 9000, 8, 8, 16, 1), (16, 1, 20000, 16, 4, 32, 0),
                                                      (4, 300, 5000, 8, 4, 128, 0), (2, 40, 30000, 8, 4, 64, 3)])
 def test_long_sequences_that_wait_for_memory(B, n, L, HQ, HK, page, splits):
