@@ -19,17 +19,17 @@
 // CTA: warp 0 loads (at d = 128 K, and warp 2 V; each lane one page's box of a
 // tile; pages are found through the block table), warp 1 issues MMAs, warps 4..
 // are one softmax warpgroup per row tile, thread = row. Two row tiles (NT = 2)
-// share each K and V tile. At d = 128 their O fill half of TMEM and P has to take S's place:
-// the tiles alternate, the tensor pipe works on one while the other's softmax
-// runs. At d = 64, or with one row tile, P has columns of its own and the next
+// share each K and V tile. At d = 128 their O fill half of TMEM and P has to take
+// S's place: the tiles alternate, the tensor pipe works on one while the other's
+// softmax runs. At d = 64, or with one row tile, P has columns of its own and the next
 // S is made while this one's terms are.
 //
-// At d = 128 512 rows x 32 heads against 131,072 keys take 0.68 ms, 1.61 PFLOP/s:
+// At d = 128 512 rows x 32 heads against 131,072 keys take 0.68 ms, 1.62 PFLOP/s:
 // about 2,800 cycles a turn (a key tile for both row tiles), of which the 32
 // products take 2,048 back to back, as the 256 KB of operands and loads at 128
-// bytes a cycle do; a row tile's own chain, S, terms, P, PV, is what is left. P is
-// handed over in halves, so that PV starts while half of the terms are made (0.70
-// ms whole).
+// bytes a cycle do; a row tile's own chain, S, terms, P, PV, is what is left. P of
+// the first 96 keys is handed over before the others' terms are made (685 us with
+// 64, 704 whole).
 // Tried and not faster: two softmax warpgroups per row tile (936 us), an issuing
 // thread per row tile (765 us), L2 prefetches (738 us). At d = 64 the terms are
 // half of a turn: 2,700 cycles, the exponentials alone 1,024, the products 1,050.
@@ -50,6 +50,7 @@ namespace skl {
 namespace {
 
 constexpr int kTileM = 128;  // rows per tile
+constexpr int kFirst = 96;   // keys of a tile whose P is handed over first (d = 128, two row tiles)
 
 template <int D, int NT>
 struct AttnLayout {
@@ -68,7 +69,7 @@ struct AttnLayout {
   // 64 tokens 61 and 56; at d = 64 50.1 and 51.6, a warp's share of the issue slots)
   static constexpr int LOADERS = D == 128 ? 2 : 1;
   // q_full, v_fixed, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2],
-  // s_read, p_read, drain, p_half[2], o_half[2]
+  // s_read, p_read, drain, p_first[2], o_first[2]
   static constexpr int NBAR = 2 + 2 * STAGES + 13;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
@@ -173,8 +174,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
   auto p_full = [&](int k) { return bar0 + 8u * (4 + 2 * L::STAGES + k); };
   auto o_full = [&](int k) { return bar0 + 8u * (6 + 2 * L::STAGES + k); };
   const uint32_t s_read = bar0 + 8u * (8 + 2 * L::STAGES), p_read = s_read + 8, drain = s_read + 16;
-  auto p_half = [&](int k) { return bar0 + 8u * (11 + 2 * L::STAGES + k); };
-  auto o_half = [&](int k) { return bar0 + 8u * (13 + 2 * L::STAGES + k); };
+  auto p_first = [&](int k) { return bar0 + 8u * (11 + 2 * L::STAGES + k); };
+  auto o_first = [&](int k) { return bar0 + 8u * (13 + 2 * L::STAGES + k); };
   static_assert(15 + 2 * L::STAGES == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
@@ -199,8 +200,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         mbar_init(s_full(k), 1);
         mbar_init(p_full(k), L::OWN_P ? 4 * nt : 4);
         mbar_init(o_full(k), 1);
-        mbar_init(p_half(k), 4);
-        mbar_init(o_half(k), 1);
+        mbar_init(p_first(k), 4);
+        mbar_init(o_first(k), 1);
       }
       mbar_init(s_read, 4 * nt);
       mbar_init(p_read, 1);
@@ -357,12 +358,11 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         for (int i = 0; i < kTileN / 16; ++i)
           mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * i, desc(v + i * (2048 >> 4)), id_o, i > 0 ? 1 : add);
       };
-      auto mma_o_half = [&](int half, uint32_t v, uint32_t col_p, uint32_t col_o, uint32_t add) {  // 64 keys of it
+      // of the first keys, or of the others
+      auto mma_o_part = [&](int part, uint32_t v, uint32_t col_p, uint32_t col_o, uint32_t add) {
 #pragma unroll
-        for (int i = 0; i < kTileN / 32; ++i) {
-          const int k = half * (kTileN / 32) + i;
-          mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * k, desc(v + k * (2048 >> 4)), id_o, i > 0 ? 1 : add);
-        }
+        for (int k = part ? kFirst / 16 : 0; k < (part ? kTileN : kFirst) / 16; ++k)
+          mma_bf16_ts(tmem + col_o, tmem + col_p + 8 * k, desc(v + k * (2048 >> 4)), id_o, k > 0 ? 1 : add);
       };
       bool ok = check_tmem(ck, tmem, 128, 512, __LINE__) && wait_bounded(q_full, 0, wc) && landed();
       uint32_t k_at = next();
@@ -383,13 +383,13 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t == nt) break;
-            if (!(ok = wait_bounded(p_half(t), j & 1, wc))) break;
+            if (!(ok = wait_bounded(p_first(t), j & 1, wc))) break;
             tc_fence_after();
-            mma_o_half(0, v_lo + v_at, L::col_p(t), L::col_o(t), j > 0);
-            mma_commit(o_half(t));
+            mma_o_part(0, v_lo + v_at, L::col_p(t), L::col_o(t), j > 0);
+            mma_commit(o_first(t));
             if (!(ok = wait_bounded(p_full(t), j & 1, wc))) break;
             tc_fence_after();
-            mma_o_half(1, v_lo + v_at, L::col_p(t), L::col_o(t), 1);
+            mma_o_part(1, v_lo + v_at, L::col_p(t), L::col_o(t), 1);
             if (more) mma_s(q_lo + t * (L::TILE >> 4), k_lo + k_at, L::col_s(t));
             mma_commit(more ? s_full(t) : o_full(t));
           }
@@ -471,15 +471,15 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
              // (the last tile's rows past the last key are cleared first)
              (j + 1 < n_iter || last_valid == kTileN || warp_wait(v_fixed, 0, wc));
     };
-    auto hand_half = [&](int j) {  // the first half of P, with V
+    auto hand_first = [&](int j) {  // P of the first keys, with V
       const bool got = warp != 5 || landed_v(j);
       tc_fence_before();
       __syncwarp();
-      if (got && lane == 0) mbar_arrive(p_half(t));
+      if (got && lane == 0) mbar_arrive(p_first(t));
       return got;
     };
     for (int j = 0; t < nt && j < n_iter; ++j) {
-      bool handed = false;  // the first half of P
+      bool handed = false;  // P of the first keys
       if (!(ok = warp_wait(s_full(L::OWN_P ? 0 : t), j & 1, wc))) break;
       tc_fence_after();
       if (warp_live) {
@@ -560,9 +560,9 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         } else {
           // Terms against the reference as it is, while their sum stays within
           // 2^8; else (and in a row's first tile) the maximum is taken. The
-          // products of the tiles before ended before this S. The first half's P
-          // is handed over while the second's is made
-          f = terms_of(integral_constant<int, 0>{}, integral_constant<int, 32>{});
+          // products of the tiles before ended before this S. P of the first
+          // keys is handed over while the others' is made
+          f = terms_of(integral_constant<int, 0>{}, integral_constant<int, kFirst / 2>{});
           bool again = !(f <= kSumMax) || (ref == -INFINITY && seen > 0);
           if (__any_sync(0xFFFFFFFFu, again)) {
             load_s();
@@ -571,40 +571,40 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             f = terms();
             again = false;  // (S of the whole tile was looked at)
           } else {
-            tmem_st16(tp, &p[0]);
-            tmem_st16(tp + 16, &p[16]);
+#pragma unroll
+            for (int q = 0; q < kFirst / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
             tmem_wait_st();
-            if (!hand_half(j)) {
+            if (!hand_first(j)) {
               ok = false;
               break;
             }
             handed = true;
-            float f2 = terms_of(integral_constant<int, 32>{}, integral_constant<int, 64>{});
+            float f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
             again = !(f2 <= kSumMax);
-            if (__any_sync(0xFFFFFFFFu, again)) {  // the second half's maximum; the first is in O by then
-              if (!(ok = warp_wait(o_half(t), j & 1, wc))) break;
+            if (__any_sync(0xFFFFFFFFu, again)) {  // the others' maximum; the first keys are in O by then
+              if (!(ok = warp_wait(o_first(t), j & 1, wc))) break;
               tc_fence_after();
 #pragma unroll
-              for (int q = 2; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+              for (int q = kFirst / 32; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
               tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 128; ++k)
-                if (k < 64 || k >= seen) s[k] = -INFINITY;
+                if (k < kFirst || k >= seen) s[k] = -INFINITY;
               l += f;
               f = 0.f;
               const float alpha = move_ref(again);
               scale_o(alpha);
-              f2 = terms_of(integral_constant<int, 32>{}, integral_constant<int, 64>{});
+              f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
             }
             f += f2;
           }
         }
         if (!handed) {
-          tmem_st16(tp, &p[0]);
-          tmem_st16(tp + 16, &p[16]);
+#pragma unroll
+          for (int q = 0; q < kFirst / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
         }
-        tmem_st16(tp + 32, &p[32]);
-        tmem_st16(tp + 48, &p[48]);
+#pragma unroll
+        for (int q = kFirst / 32; q < 4; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
         l += f;
         tmem_wait_st();
       } else if (L::OWN_P) {
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       // to spend (a wait takes the issuer 100 cycles between products, with the
       // data there)
       if (!L::OWN_P && !handed) {
-        if (!(ok = hand_half(j))) break;
+        if (!(ok = hand_first(j))) break;
       }
       if (warp == 5) {
         ok = L::OWN_P ? landed_v(j) : j + 1 == n_iter || landed_k(j + 1);

@@ -281,16 +281,17 @@ def test_large_logits_move_the_reference(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("d,n,rise", [(128, 100, 1), (128, 100, -1), (128, 60, 1), (64, 100, 1)])
-def test_logits_that_rise_within_a_tile(d, n, rise, dtype):
-    """Scores of even rows rise (odd ones fall) by about 10 from one run of 64 keys to the next, so that the reference
+@pytest.mark.parametrize("d,n,rise,run", [(128, 100, 1, 64), (128, 100, -1, 64), (128, 60, 1, 64), (64, 100, 1, 64),
+                                          (128, 100, 1, 32), (128, 100, -1, 32), (128, 300, 1, 96)])
+def test_logits_that_rise_within_a_tile(d, n, rise, run, dtype):
+    """Scores of even rows rise (odd ones fall) by about 10 from one run of keys to the next, so that the reference
     moves in the middle of a tile, for some rows of a warp; the last rows also at the sequence's ragged end."""
     dt = TYPES[dtype]
     c = Cache([700], 1, d, 16, dt, fill=False)
     g = torch.Generator().manual_seed(d + n)
     u = torch.randn(d, generator=g)
     u *= d ** 0.5 / u.norm()
-    steps = torch.arange(700) // 64 * rise * 10 / d ** 0.5
+    steps = torch.arange(700) // run * rise * 10 / d ** 0.5
     k = (steps[:, None, None] * u + 0.1 * torch.randn(700, 1, d, generator=g)).to(dt)
     v = torch.randn(700, 1, d, generator=g).to(dt)
     c.rows = [(k, v)]
