@@ -747,6 +747,83 @@ def test_debug_build_finds_nothing_and_gives_the_same():
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+# ------------------------------------------------- the softmax's reference
+def _put(c, b, k, v):
+    """Sequence b of the cache holds keys k and values v [length, HK, d]."""
+    n = k.shape[0]
+    page = c.k.shape[2]
+    at = torch.arange(n)
+    p, s = c.table[b, at.cuda() // page].long(), (at % page).cuda()
+    c.k[p, :, s], c.v[p, :, s] = k.cuda(), v.cuda()
+    c.rows[b] = (k, v)
+
+
+def _two_directions(d, g):
+    """Orthogonal vectors of d elements 1 and -1 that begin alike: a score is scale q k, so k = x / d^0.5 of the query's
+    own vector gives x."""
+    a = torch.where(torch.rand(d, generator=g) < 0.5, 1.0, -1.0)
+    return a, torch.cat((a[:d // 2], -a[d // 2:]))
+
+
+def _rising_keys(L, d, first, second, keys, rise, dt, g):
+    """Keys of small random scores, but for those at first[1] (second[1]) of every 128 from the 128th on, where the
+    score of queries along first[0] (second[0]) is `rise` times the tile's number."""
+    k = 0.05 * torch.randn(L, 1, d, generator=g)
+    for vec, place in (first, second):
+        for at in range(128 + place, L, 128):
+            if at < keys:
+                k[at, 0] += at // 128 * rise / d ** 0.5 * vec
+    return k.to(dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rise", [("fp16", 20.0), ("bf16", 100.0)])
+@pytest.mark.parametrize("d,n,splits", [(128, 150, 1), (128, 150, 2), (128, 40, 1), (64, 150, 1), (128, 16, 0), (64, 3, 0)])
+@pytest.mark.parametrize("places", [(40, 110), (100, 127), (95, 96)])
+def test_rows_of_a_warp_rise_at_different_keys_of_a_tile(d, n, splits, places, dtype, rise):
+    """Even rows (head 0) meet a score far above all before it at one key of a tile, odd rows (head 1) at another:
+    fp16 terms of 20 nats over the old reference (2^28) and bf16 terms of 100 (2^144) are infinite unless every row's
+    reference moves. Bounds as in _check_attn."""
+    dt = TYPES[dtype]
+    g = torch.Generator().manual_seed(d + n)
+    u, w = _two_directions(d, g)
+    c = Cache([700], 1, d, 16, dt, fill=False)
+    k = _rising_keys(700, d, (u, places[0]), (w, places[1]), 500, rise, dt, g)
+    _put(c, 0, k, torch.randn(700, 1, d, generator=g).to(dt))
+    q = torch.stack((u, w)).expand(n, 2, d).to(dt).cuda()
+    for causal in (True, False):
+        st = binding.new_status()
+        o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), max_kv_len=700, causal=causal,
+                                         num_splits=splits, dev_status=st)
+        binding.raise_on_device_status(st)
+        _check_attn(o, lse, q, c, [n], [700], d ** -0.5, causal, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rise", [("fp16", 20.0), ("bf16", 100.0)])
+@pytest.mark.parametrize("d,n,L,splits", [(128, 150, 700, 1), (128, 40, 700, 2), (128, 20, 700, 1), (64, 150, 700, 1)])
+def test_a_nan_query_leaves_the_other_rows_right(d, n, L, splits, dtype, rise):
+    """One row of NaN (the last token's head 2) beside rows whose scores rise in every tile."""
+    dt = TYPES[dtype]
+    g = torch.Generator().manual_seed(d + n)
+    u, w = _two_directions(d, g)
+    c = Cache([L], 1, d, 16, dt, fill=False)
+    k = _rising_keys(L, d, (u, 40), (w, 110), 600, rise, dt, g)
+    _put(c, 0, k, torch.randn(L, 1, d, generator=g).to(dt))
+    q = torch.stack((u, w, u, w)).repeat(n, 1, 1).to(dt).cuda()
+    q[-1, 2, 7] = float("nan")
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), max_kv_len=L, num_splits=splits,
+                                     dev_status=st)
+    binding.raise_on_device_status(st)
+    assert torch.all(torch.isnan(o[-1, 2])) and bool(torch.isnan(lse[-1, 2]))
+    rest = [0, 1, 3]
+    _check_attn(o[:, rest], lse[:, rest], q[:, rest], c, [n], [L], d ** -0.5, True, dt)
+    if n > 1:
+        _check_attn(o[:-1, 2:3], lse[:-1, 2:3], q[:-1, 2:3], type("", (), {"rows": [(k[:L - 1], c.rows[0][1][:L - 1])]}),
+                    [n - 1], [L - 1], d ** -0.5, True, dt)
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
