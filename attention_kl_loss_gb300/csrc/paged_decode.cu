@@ -470,13 +470,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         load_s();
         float f = 0.f;
         // as in paged_attn.cu: the reference stays while the sum is within 2^8
-        bool again = ref == -INFINITY && seen > 0;
-        if (!__any_sync(0xFFFFFFFFu, again)) {
+        bool again = __any_sync(0xFFFFFFFFu, ref == -INFINITY && seen > 0);
+        if (!again) {
           f = terms();
-          again = !(f <= kSumMax);
-          if (__any_sync(0xFFFFFFFFu, again)) load_s();
+          again = __any_sync(0xFFFFFFFFu, !(f <= kSumMax));
+          if (again) load_s();
         }
-        if (__any_sync(0xFFFFFFFFu, again)) {
+        if (again) {
           float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int e = 4; e < 124; e += 8) {
@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int q = 0; q < 4; ++q) m[q] = max3(m[q], s[e + 2 * q], s[e + 2 * q + 1]);
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
-          const bool move = again && (top > ref + kTau || (ref == -INFINITY && top > -INFINITY));
+          // (by its own maximum, whichever row of the warp asked: the others' sums may not have been looked at)
+          const bool move = top > ref + kTau || (ref == -INFINITY && top > -INFINITY);
           const float alpha = move ? ex2(ref - top) : 1.f;
           if (move) {
             ref = top;

@@ -801,7 +801,8 @@ def test_rows_of_a_warp_rise_at_different_keys_of_a_tile(d, n, splits, places, d
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,rise", [("fp16", 20.0), ("bf16", 100.0)])
-@pytest.mark.parametrize("d,n,L,splits", [(128, 150, 700, 1), (128, 40, 700, 2), (128, 20, 700, 1), (64, 150, 700, 1)])
+@pytest.mark.parametrize("d,n,L,splits", [(128, 1, 500, 0), (64, 1, 700, 0), (128, 2, 3000, 0), (64, 8, 400, 0),
+                                          (128, 150, 700, 1), (128, 40, 700, 2), (128, 20, 700, 1), (64, 150, 700, 1)])
 def test_a_nan_query_leaves_the_other_rows_right(d, n, L, splits, dtype, rise):
     """One row of NaN (the last token's head 2) beside rows whose scores rise in every tile."""
     dt = TYPES[dtype]
