@@ -300,10 +300,16 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
         dwk_at = dwk.data_ptr()
     length, rot, cos_at, sin_at = _tables(cos, sin, index)
     status, _keep = _status(dev_status, index)
-    if B * (NQ * HQ + NK * HK) == 0:
-        for w in (dwq, dwk):
-            if w is not None:
-                w.zero_()
+    # a side without rows is absent in the C call, which leaves its weight gradient
+    if B * NQ * HQ == 0:
+        NQ = HQ = wq = dwq_at = 0
+        if dwq is not None:
+            dwq.zero_()
+    if B * NK * HK == 0:
+        NK = HK = wk = dwk_at = 0
+        if dwk is not None:
+            dwk.zero_()
+    if NQ + NK == 0:
         return dq, dk, dwq, dwk
     lib = load()
     need = lib.streamkl_qk_norm_rope_bwd_workspace_size(B, NQ, NK, HQ, HK, d) if wq or wk else 0

@@ -372,6 +372,37 @@ def test_training_step_from_projection_to_its_gradients():
     assert rel(dwq, ws[0].grad) <= 3e-2 and rel(dwk, ws[1].grad) <= 3e-2
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("empty", ["tokens", "heads"])
+@pytest.mark.parametrize("side", ["q", "k"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_weight_gradient_of_an_empty_side_is_zero(side, empty, packed):
+    """Queries without a token or a head beside keys that have some, and the reverse: nothing to sum on that side, the
+    other side as alone. Memory that the outputs may get holds NaN."""
+    q, k, wq, wk, g = _inputs(2, 40, 40, 4, 2, 64, torch.bfloat16, packed)
+    x = {"q": q, "k": k}
+    x[side] = x[side][..., :0, :, :] if empty == "tokens" else x[side][..., :0, :]
+    cos, sin = _tables(40, 64, q.device)
+    pos = {n: torch.arange(t.shape[-3], dtype=torch.int32, device=t.device) for n, t in x.items()}
+    kw = dict(positions=pos["q"], k_positions=pos["k"], q_weight=wq, k_weight=wk)
+    y = skl.streamkl_qk_norm_rope_fwd(x["q"], x["k"], cos, sin, **kw)
+    dy = [torch.randn(t.shape, generator=g).bfloat16().cuda() for t in y]
+    for given in (False, True):
+        out = tuple(torch.empty_like(x[n], memory_format=torch.contiguous_format) for n in "qk") if given else None
+        junk = [torch.full((64,), float("nan"), device=q.device) for _ in range(64)]
+        del junk
+        st = binding.new_status(q.device)
+        dq, dk, dwq, dwk = skl.streamkl_qk_norm_rope_bwd(x["q"], x["k"], *dy, cos, sin, out=out, dev_status=st, **kw)
+        binding.raise_on_device_status(st)
+        assert dq.shape == x["q"].shape and dk.shape == x["k"].shape
+        if side == "q":
+            _, one, _, dw = skl.streamkl_qk_norm_rope_bwd(None, x["k"], None, dy[1], cos, sin, k_positions=pos["k"], k_weight=wk)
+            assert torch.all(dwq == 0) and torch.equal(dk, one) and torch.equal(dwk, dw)
+        else:
+            one, _, dw, _ = skl.streamkl_qk_norm_rope_bwd(x["q"], None, dy[0], None, cos, sin, positions=pos["q"], q_weight=wq)
+            assert torch.all(dwk == 0) and torch.equal(dq, one) and torch.equal(dwq, dw)
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
