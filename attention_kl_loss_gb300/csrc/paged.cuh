@@ -9,10 +9,20 @@ namespace skl {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTileN = 128;  // keys per tile
-// The softmax's reference of a row (log2 units) moves when a term would exceed
-// 2^kTau of it, or a tile's sum of terms 2^kTau = kSumMax.
-constexpr float kTau = 8.0f;
-constexpr float kSumMax = 256.0f;
+// The softmax's reference of a row (log2 units) is taken kBelow under the row's
+// maximum and moves when a term would exceed 2^kTau of it, or a tile's sum of
+// terms 2^kTau = kSumMax. bf16 has fp32's range, so its largest term may be 1.
+// In fp16 terms below 2^-14 lose bits and those below 2^-25 are gone, while the
+// fp32 sum keeps them: with 1 for the largest, 131,072 keys 17.7 nats below one
+// lost 0.3 % of max |v|. At 2^6 a term loses at most 2^-31 of the largest
+// (2^-14 over 131,072 keys, an eighth of the output's own half step), and the
+// largest of all, 2^14, stays two binary places under fp16's end.
+template <int TYPE>
+constexpr float kBelow = TYPE == kTypeF16 ? 6.0f : 0.0f;
+template <int TYPE>
+constexpr float kTau = 8.0f + kBelow<TYPE>;
+template <int TYPE>
+constexpr float kSumMax = TYPE == kTypeF16 ? 16384.0f : 256.0f;
 
 // A place in the ring of K and V stages and the parity of its turn.
 struct RingPos {

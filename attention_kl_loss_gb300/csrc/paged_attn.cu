@@ -12,9 +12,9 @@
 //   S (fp32, TMEM) -> registers -> P = 2^(c s - ref) in the inputs' type (TMEM,
 //   the PV product's A operand).
 // P has 8 (bf16) or 11 (fp16) bits: its rounding is the size of the output's
-// own. ref, the sum (of unrounded terms) and O are fp32. The reference moves
-// only when terms would exceed 2^8 of it, so O is seldom rescaled; the results
-// do not depend on it.
+// own (fp16's small terms: kBelow). ref, the sum (of unrounded terms) and O are
+// fp32. The reference moves only when terms would exceed 2^8 of it (2^14, fp16),
+// so O is seldom rescaled; the results do not depend on it.
 //
 // CTA: warp 0 loads (at d = 128 K, and warp 2 V; each lane one page's box of a
 // tile; pages are found through the block table), warp 1 issues MMAs, warps 4..
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         using std::integral_constant;
         auto terms = [&]() { return terms_of(integral_constant<int, 0>{}, integral_constant<int, 64>{}); };
         // the maximum of the tile moves the reference if it exceeds it by more
-        // than 2^8; by how much O and the sum scale then. Each row goes by its own
+        // than 2^kTau; by how much O and the sum scale then. Each row goes by its own
         // maximum, whichever row of the warp asked
         auto move_ref = [&]() {
           float m[4] = {s[0], s[1], s[2], s[3]};
@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
-          const bool move = top > ref + kTau || (ref == -INFINITY && top > -INFINITY);
-          const float alpha = move ? ex2(ref - top) : 1.f;
+          const bool move = top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY);
+          const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
           if (move) {
-            ref = top;
+            ref = top - kBelow<TYPE>;
             l *= alpha;
           }
           return alpha;
@@ -560,15 +560,15 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           }
         } else {
           // Terms against the reference as it is, while their sum stays within
-          // 2^8; else (and in a row's first tile) the maximum is taken. The
+          // kSumMax; else (and in a row's first tile) the maximum is taken. The
           // products of the tiles before ended before this S. P of the first
           // keys is handed over while the others' is made
           f = terms_of(integral_constant<int, 0>{}, integral_constant<int, kFirst / 2>{});
-          if (__any_sync(0xFFFFFFFFu, !(f <= kSumMax) || (ref == -INFINITY && seen > 0))) {
+          if (__any_sync(0xFFFFFFFFu, !(f <= kSumMax<TYPE>) || (ref == -INFINITY && seen > 0))) {
             load_s();
             const float alpha = move_ref();
             if (j > 0) scale_o(alpha);
-            f = terms();  // (the whole tile's maximum was taken: none exceeds 2^8)
+            f = terms();  // (the whole tile's maximum was taken: none exceeds 2^kTau)
           } else {
 #pragma unroll
             for (int q = 0; q < kFirst / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             }
             handed = true;
             float f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
-            if (__any_sync(0xFFFFFFFFu, !(f2 <= kSumMax))) {  // the others' maximum; the first keys are in O by then
+            if (__any_sync(0xFFFFFFFFu, !(f2 <= kSumMax<TYPE>))) {  // the others' maximum; the first keys are in O by then
               if (!(ok = warp_wait(o_first(t), j & 1, wc))) break;
               tc_fence_after();
 #pragma unroll

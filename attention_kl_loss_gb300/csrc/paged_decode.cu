@@ -469,11 +469,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         load_s();
         float f = 0.f;
-        // as in paged_attn.cu: the reference stays while the sum is within 2^8
+        // as in paged_attn.cu: the reference stays while the sum is within kSumMax
         bool again = __any_sync(0xFFFFFFFFu, ref == -INFINITY && seen > 0);
         if (!again) {
           f = terms();
-          again = __any_sync(0xFFFFFFFFu, !(f <= kSumMax));
+          again = __any_sync(0xFFFFFFFFu, !(f <= kSumMax<TYPE>));
           if (again) load_s();
         }
         if (again) {
@@ -485,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
           // (by its own maximum, whichever row of the warp asked: the others' sums may not have been looked at)
-          const bool move = top > ref + kTau || (ref == -INFINITY && top > -INFINITY);
-          const float alpha = move ? ex2(ref - top) : 1.f;
+          const bool move = top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY);
+          const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
           if (move) {
-            ref = top;
+            ref = top - kBelow<TYPE>;
             l *= alpha;
           }
           if (j > 0) {  // O holds the tiles before this one, all done before this S

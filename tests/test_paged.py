@@ -825,6 +825,39 @@ def test_a_nan_query_leaves_the_other_rows_right(d, n, L, splits, dtype, rise):
                     [n - 1], [L - 1], d ** -0.5, True, dt)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,n,L,splits,where", [(128, 1, 100_001, 0, 5), (64, 2, 100_001, 0, 99_000), (128, 20, 60_013, 1, 70_000),
+                                                (128, 40, 60_013, 3, 5), (128, 130, 20_011, 1, 5), (64, 130, 20_011, 1, 19_000)])
+def test_fp16_keeps_many_small_terms_beside_a_large_one(d, n, L, splits, where):
+    """One key (its value 0) 17.7 nats above all others: what the others add, terms of 2^-25.5 of the largest, is the
+    output. A term is at least 2^6 times that against the row's reference, where fp16 steps are 2^-24: off by 2^-25 at
+    most, 2^-31 of the largest term, which the sum of terms exceeds: L 2^-31 max |v| in all. The rest as in _check_attn,
+    relative to sum p |v|. (With the largest term at 2^0 all others are below 2^-25 and lost.)"""
+    dt = torch.float16
+    g = torch.Generator().manual_seed(n)
+    u, _ = _two_directions(d, g)
+    where = min(where, L - n)
+    c = Cache([L], 1, d, 64, dt, fill=False)
+    k = (-(1.5625 if d == 128 else 2.2109375) * u).expand(L, 1, d).clone()
+    v = 0.5 + torch.rand(L, 1, d, generator=g)
+    k[where], v[where] = 0, 0
+    _put(c, 0, k.to(dt), v.to(dt))
+    q = u.expand(n, 1, d).to(dt).cuda()
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), max_kv_len=L, causal=False,
+                                     num_splits=splits, dev_status=st)
+    binding.raise_on_device_status(st)
+    x, kk, vv = _np(q[:1]), _np(c.rows[0][0].transpose(0, 1)), _np(c.rows[0][1].transpose(0, 1))
+    ref, ref_lse, mag = orc.paged_attn(x, kk, vv, d ** -0.5, False)  # (all rows alike)
+    half = torch.finfo(dt).eps / 2
+    S = d ** -0.5 * float(np.max(np.abs(x[0, 0]) @ np.abs(kk[0]).T))
+    E = 2 * ((d + 12) * 2.0 ** -23 * S + 2.0 ** -21) + L * 2.0 ** -23
+    tol = half * np.abs(ref) + (half + E) * mag + L * 2.0 ** -31 * np.abs(vv).max() + 2.0 ** -25
+    err = np.abs(_np(o) - ref)
+    assert np.all(err <= tol), float((err / tol).max())
+    assert np.all(np.abs(_np(lse) - ref_lse) <= E + 2.0 ** -22 * np.abs(ref_lse))
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
