@@ -515,9 +515,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
         using std::integral_constant;
         auto terms = [&]() { return terms_of(integral_constant<int, 0>{}, integral_constant<int, 64>{}); };
         // the maximum of the tile moves the reference if it exceeds it by more
-        // than 2^kTau; by how much O and the sum scale then. Each row goes by its own
-        // maximum, whichever row of the warp asked
-        auto move_ref = [&]() {
+        // than 2^kTau, in the rows that may; by how much O and the sum scale then
+        auto move_ref = [&](bool may) {
           float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int k = 4; k < 124; k += 8) {
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
-          const bool move = top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY);
+          const bool move = may && (top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY));
           const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
           if (move) {
             ref = top - kBelow<TYPE>;
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           // S is in registers: the next tile's may come. P's columns and O are
           // touched once the product of the tile before has ended
           if (!(ok = hand_back_s(j))) break;
-          const float alpha = move_ref();
+          const float alpha = move_ref(true);
           f = terms();
           if (j > 0) {
             if (!(ok = warp_wait(p_read, (j - 1) & 1, wc))) break;
@@ -564,11 +563,13 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
           // products of the tiles before ended before this S. P of the first
           // keys is handed over while the others' is made
           f = terms_of(integral_constant<int, 0>{}, integral_constant<int, kFirst / 2>{});
-          if (__any_sync(0xFFFFFFFFu, !(f <= kSumMax<TYPE>) || (ref == -INFINITY && seen > 0))) {
+          bool again = !(f <= kSumMax<TYPE>) || (ref == -INFINITY && seen > 0);
+          if (__any_sync(0xFFFFFFFFu, again)) {
             load_s();
-            const float alpha = move_ref();
+            // (every row, whichever one asked: none has been asked about the other keys)
+            const float alpha = move_ref(true);
             if (j > 0) scale_o(alpha);
-            f = terms();  // (the whole tile's maximum was taken: none exceeds 2^kTau)
+            f = terms();
           } else {
 #pragma unroll
             for (int q = 0; q < kFirst / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
@@ -579,7 +580,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             }
             handed = true;
             float f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
-            if (__any_sync(0xFFFFFFFFu, !(f2 <= kSumMax<TYPE>))) {  // the others' maximum; the first keys are in O by then
+            again = !(f2 <= kSumMax<TYPE>);
+            if (__any_sync(0xFFFFFFFFu, again)) {  // the others' maximum; the first keys are in O by then
               if (!(ok = warp_wait(o_first(t), j & 1, wc))) break;
               tc_fence_after();
 #pragma unroll
@@ -590,7 +592,8 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
                 if (k < kFirst || k >= seen) s[k] = -INFINITY;
               l += f;
               f = 0.f;
-              const float alpha = move_ref();
+              // (the others' sums were within: 729 us, all rows by their maximum 739)
+              const float alpha = move_ref(again);
               scale_o(alpha);
               f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
             }
