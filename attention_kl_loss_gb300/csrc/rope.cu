@@ -326,14 +326,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   constexpr int SLOT = 4 * kChunkBytes<TYPE>;  // one repeat of a head: two chunks of dy, two of x with the first
   extern __shared__ __align__(16) uint8_t stage_mem[];
   __shared__ float red[2][kRopeWarps][D];
-  __shared__ float weights[2][D];
+  __shared__ float4 weights[2][D / 4];  // (read as such)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPR, l = lane % LPR;
   const uint32_t mem = smem_u32(stage_mem) + warp * STAGES * SLOT + lane * 16;
   const LaneChunks lc = lane_chunks(l, a.rot);
   const uint32_t stride = gridDim.x * kRopeWarps;
   if (threadIdx.x < 2 * D) {
     const float* w = a.side[threadIdx.x / D].w;
-    if (w != nullptr) weights[threadIdx.x / D][threadIdx.x % D] = __ldg(w + threadIdx.x % D);
+    if (w != nullptr) reinterpret_cast<float*>(weights[threadIdx.x / D])[threadIdx.x % D] = __ldg(w + threadIdx.x % D);
   }
   __syncthreads();
   // (no barrier from one side to the other: a warp that has no row of the first
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     const RopeSide& s = a.side[k];
     if (s.x == nullptr) continue;
     const bool norm = s.w != nullptr;
-    const float* ws = weights[k];
+    const float4* ws = weights[k];
     float dw0[8], dw1[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw0[e] = dw1[e] = 0.f;
@@ -434,10 +434,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
               }
             }
             float w0[8], w1[8];
-            *reinterpret_cast<float4*>(&w0[0]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c0]);
-            *reinterpret_cast<float4*>(&w0[4]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c0 + 4]);
-            *reinterpret_cast<float4*>(&w1[0]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c1]);
-            *reinterpret_cast<float4*>(&w1[4]) = *reinterpret_cast<const float4*>(&ws[8 * lc.c1 + 4]);
+            *reinterpret_cast<float4*>(&w0[0]) = ws[2 * lc.c0];
+            *reinterpret_cast<float4*>(&w0[4]) = ws[2 * lc.c0 + 1];
+            *reinterpret_cast<float4*>(&w1[0]) = ws[2 * lc.c1];
+            *reinterpret_cast<float4*>(&w1[4]) = ws[2 * lc.c1 + 1];
             float dot = 0.f, dot1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

@@ -358,3 +358,21 @@ def test_packed_batch_validation(lib):
     st = lib.streamkl_bwd_varlen(a, a, a, a, cu, cu, 2, 4, 300, 400, 200, 250, 64, 0.125, 1, a, a,
                                  a, a, None, None, None, None, a, None)
     assert st == 1 and b"no gradient" in lib.streamkl_last_error()
+
+
+def test_vector_reads_of_static_shared_memory_are_aligned_by_declaration():
+    """A static shared array is only as aligned as its element type unless its declaration says more: reading an array
+    of floats (or an alias of it) 16 bytes at a time faults wherever the compiler places it elsewhere."""
+    import glob
+
+    here = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "attention_kl_loss_gb300", "csrc")
+    files = sorted(glob.glob(os.path.join(here, "*.cu")) + glob.glob(os.path.join(here, "*.cuh")))
+    assert files
+    for path in files:
+        text = open(path).read()
+        names = set(re.findall(r"^\s*__shared__ (?:volatile )?(?:float|int|uint32_t|unsigned|long long|double) (\w+)\[", text, re.M))
+        for name in list(names):
+            names.update(re.findall(rf"\b(\w+) = &?{name}\b", text))
+        for name in names:
+            wide = re.findall(rf"reinterpret_cast<(?:const )?(?:float4|float2|uint4|int4) ?\*>\(&?{name}\b", text)
+            assert not wide, (os.path.basename(path), name)
