@@ -11,7 +11,9 @@ status word instead of issuing the access.
 
 ``build()`` also makes ``_lib/_marshal_<torch version>.so``, the Python module
 that takes tensors to the operators' C entries (``csrc/marshal.cpp``). It is
-tied to the version of PyTorch that it was built with, the library is not.
+tied to the version of PyTorch that it was built with, the library is not. It
+only saves host time, so where it cannot be built (it needs a C++ compiler, the
+headers of Python and of a CUDA build of PyTorch) ``build()`` says so and goes on.
 """
 from __future__ import annotations
 
@@ -71,6 +73,29 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_marshal(header: str, force: bool, verbose: bool) -> None:
+    """The native module, if stale. A failure is no failure of the build: calls
+    then go through ctypes, and a module of older sources is not left behind."""
+    target = marshal_path()
+    if not (force or _stale(target, [os.path.join(CSRC, "marshal.cpp"), header])):
+        return
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        output, failed = "no Python.h\n", True
+    else:
+        try:
+            p = subprocess.run(_marshal_cmd(), capture_output=True, text=True)
+            output, failed = p.stdout + p.stderr, p.returncode != 0
+        except OSError as error:  # no such compiler
+            output, failed = f"{error}\n", True
+    if verbose or failed:
+        sys.stderr.write(output)
+    if failed:
+        if os.path.exists(target):
+            os.remove(target)
+        sys.stderr.write(f"{os.path.basename(target)} was not built: calls around the KL will go through ctypes "
+                         "and take longer on the host\n")
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
           debug: bool = False) -> str:
     """Compile (if stale) and return the library path (the debug build with
@@ -92,21 +117,19 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
-        sys.stderr.write("no Python.h: calls around the KL will go through ctypes\n")
-    elif not debug and (force or _stale(marshal_path(), [os.path.join(CSRC, "marshal.cpp"), headers[-1]])):
-        jobs.append(_marshal_cmd())
-
     def run(cmd):
         p = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, p
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        marshal = None if debug else ex.submit(_build_marshal, headers[-1], force, verbose)
         for cmd, p in ex.map(run, jobs):
             if verbose or ptxas_info or p.returncode != 0:
                 sys.stderr.write(p.stdout + p.stderr)
             if p.returncode != 0:
                 raise RuntimeError(f"compiling failed: {' '.join(cmd)}")
+    if marshal is not None:
+        marshal.result()
     lib = lib_path(debug)
     if force or _stale(lib, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", lib, *objs]

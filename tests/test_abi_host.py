@@ -376,3 +376,19 @@ def test_vector_reads_of_static_shared_memory_are_aligned_by_declaration():
         for name in names:
             wide = re.findall(rf"reinterpret_cast<(?:const )?(?:float4|float2|uint4|int4) ?\*>\(&?{name}\b", text)
             assert not wide, (os.path.basename(path), name)
+
+
+@pytest.mark.parametrize("compiler", ["/bin/false", "/no/such/compiler"])
+def test_build_goes_on_without_the_native_module(compiler, tmp_path, monkeypatch, capfd):
+    """The module only saves host time: without a C++ compiler that makes it the library is built all the same, and a
+    module of older sources does not stay."""
+    from attention_kl_loss_gb300 import build
+    monkeypatch.setenv("CXX", compiler)
+    monkeypatch.setattr(build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "SOURCES", ["bwd.cu"])  # (a small one: the others are compiled elsewhere)
+    old = build.marshal_path()
+    open(old, "w").close()
+    os.utime(old, (0, 0))
+    lib = build.build()
+    assert os.path.dirname(lib) == str(tmp_path) and os.path.getsize(lib) > 0
+    assert not os.path.exists(old) and "ctypes" in capfd.readouterr().err
