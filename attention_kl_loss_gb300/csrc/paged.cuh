@@ -24,6 +24,15 @@ constexpr float kTau = 8.0f + kBelow<TYPE>;
 template <int TYPE>
 constexpr float kSumMax = TYPE == kTypeF16 ? 16384.0f : 256.0f;
 
+// How far over a row's reference a tile's maximum may be. From 2^24 on (log2
+// units) the maximum and the reference are themselves rounded by 1 and more, and
+// fp16 ends at 2^16: there less is allowed, from 2^26 on nothing, so that terms
+// stay finite up to maxima of 2^28.
+template <int TYPE>
+__device__ __forceinline__ float rise_allowed(float top) {
+  return TYPE == kTypeF16 ? fmaxf(0.0f, fmaf(fabsf(top), -0x1p-22f, kTau<TYPE>)) : kTau<TYPE>;
+}
+
 // A place in the ring of K and V stages and the parity of its turn.
 struct RingPos {
   int stage;

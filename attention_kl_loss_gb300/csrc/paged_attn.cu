@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
             for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
-          const bool move = may && (top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY));
+          const bool move = may && (top > ref + rise_allowed<TYPE>(top) || (ref == -INFINITY && top > -INFINITY));
           const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
           if (move) {
             ref = top - kBelow<TYPE>;

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
           // (by its own maximum, whichever row of the warp asked: the others' sums may not have been looked at)
-          const bool move = top > ref + kTau<TYPE> || (ref == -INFINITY && top > -INFINITY);
+          const bool move = top > ref + rise_allowed<TYPE>(top) || (ref == -INFINITY && top > -INFINITY);
           const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
           if (move) {
             ref = top - kBelow<TYPE>;

@@ -858,6 +858,38 @@ def test_fp16_keeps_many_small_terms_beside_a_large_one(d, n, L, splits, where):
     assert np.all(np.abs(_np(lse) - ref_lse) <= E + 2.0 ** -22 * np.abs(ref_lse))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("base", [4096, 8192, 16384, 20480])
+@pytest.mark.parametrize("d,n,splits", [(128, 1, 0), (64, 4, 0), (128, 20, 1), (128, 150, 1), (64, 150, 1)])
+def test_fp16_logits_whose_own_rounding_exceeds_a_term(d, n, splits, base):
+    """Scores of 2^25 to 2^28 (log2), of which fp32 keeps steps of 2 to 16, and a maximum that rises by a few of them from
+    tile to tile: fp16 ends 2^2 above the largest term that may stand against an old reference. All values are 1, so each
+    output is a sum of rounded terms over their sum: 2^-11 off, the half step of a term, and 2^-11 of its own, beside
+    fp32 sums of 24 tiles, 2^-17."""
+    dt, L = torch.float16, 24 * 128
+    g = torch.Generator().manual_seed(n)
+    u, _ = _two_directions(d, g)
+    u[0] = 1
+    c = Cache([L], 1, d, 16, dt, fill=False)
+    k = 0.5 * base * u.expand(L, 1, d).clone()
+    for j in range(24):
+        at = 128 * j + int(torch.randint(0, 128, (1,), generator=g))
+        k[at, 0] = base * u
+        k[at, 0, 0] = base * (1 + j / 512)
+    _put(c, 0, k.to(dt), torch.ones(L, 1, d).to(dt))
+    q = (480 * u * (128 / d) ** 0.5).repeat(n, 2, 1)
+    q[:, 0, 0] = torch.randint(1, 9, (n,), generator=g).float() * 8
+    q[:, 1, 0] = torch.randint(1, 400, (n,), generator=g).float()
+    q = q.to(dt).cuda()
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_attn(q, c.k, c.v, c.table, c.lens, cu_seqlens=_cu([n]), max_kv_len=L, causal=False,
+                                     num_splits=splits, dev_status=st)
+    binding.raise_on_device_status(st)
+    assert torch.all((o.float() - 1).abs() <= 2.0 ** -10 + 2.0 ** -17)
+    top = ((q.double() @ c.rows[0][0][:, 0].double().T.cuda()).amax(-1) * d ** -0.5)
+    assert torch.all((lse.double() - top).abs() <= 2.0 ** -20 * top + 24)
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
