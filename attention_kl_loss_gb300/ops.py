@@ -263,7 +263,7 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
     (``streamkl_bwd``'s dq, dk): (dq, dk, dq_weight, dk_weight). dq, dk have
     the shapes of q, k (``out`` = (dq, dk) may be slices of one buffer); the
     gradients of a key head's repeats are summed; weight gradients are fp32
-    [d], None where there is no weight."""
+    [d], made by the call, None where there is no weight."""
     if out is None and stream is None and (native := load().native) is not None:
         done = native.rope_bwd(q, k, dq_out, dk_out, cos, sin, positions, k_positions, q_weight, k_weight, eps, interleaved,
                                k_repeat, workspace, dev_status)
