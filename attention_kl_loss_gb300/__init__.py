@@ -11,6 +11,7 @@ from .binding import (  # noqa: F401
     STREAMKL_ERR_CUDA,
     STREAMKL_ERR_DEVICE_CHECK,
     STREAMKL_ERR_INVALID_ARG,
+    STREAMKL_ERR_NO_PAGES,
     STREAMKL_ERR_TIMEOUT,
     STREAMKL_ERR_UNSUPPORTED,
     STREAMKL_OK,
@@ -46,6 +47,12 @@ from .ops import (  # noqa: F401
     streamkl_paged_attn,
     streamkl_paged_attn_splits,
     streamkl_paged_attn_workspace_size,
+    streamkl_paged_compact,
+    streamkl_paged_copy,
+    streamkl_paged_fork,
+    streamkl_paged_resize,
+    streamkl_paged_tree_attn,
+    streamkl_paged_tree_attn_workspace_size,
     streamkl_qk_norm_rope_bwd,
     streamkl_qk_norm_rope_bwd_workspace_size,
     streamkl_qk_norm_rope_fwd,

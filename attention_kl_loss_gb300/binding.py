@@ -28,9 +28,10 @@ STREAMKL_ERR_UNSUPPORTED = 2
 STREAMKL_ERR_CUDA = 3
 STREAMKL_ERR_TIMEOUT = 4
 STREAMKL_ERR_DEVICE_CHECK = 5
+STREAMKL_ERR_NO_PAGES = 6
 
 _STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT",
-                 5: "DEVICE_CHECK"}
+                 5: "DEVICE_CHECK", 6: "NO_PAGES"}
 
 # loaded libraries: False = release build, True = debug build (device checks)
 _libs: dict = {}
@@ -79,6 +80,12 @@ _SIGNATURES = {
     "streamkl_paged_attn_splits": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_attn": (_I, [_P, _P]),
+    "streamkl_paged_tree_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "streamkl_paged_tree_attn": (_I, [_P, _P]),
+    "streamkl_paged_compact": (_I, [_P, _P]),
+    "streamkl_paged_copy": (_I, [_P, _P]),
+    "streamkl_paged_fork": (_I, [_P, _P]),
+    "streamkl_paged_resize": (_I, [_P, _P]),
 }
 
 
@@ -126,7 +133,8 @@ def _native_calls(path: str):
         return None
     entries = module.entries(path)
     return types.SimpleNamespace(**{name: functools.partial(getattr(module, name), entries)
-                                    for name in ("rope_fwd", "rope_bwd", "append", "attn")})
+                                    for name in ("rope_fwd", "rope_bwd", "append", "attn", "tree_attn", "compact", "copy",
+                                                 "fork", "resize")})
 
 
 def load(debug: Optional[bool] = None) -> ctypes.CDLL:
@@ -463,5 +471,6 @@ def raise_on_device_status(dev_status: torch.Tensor, where: str = "kernel"):
     if v != 0:
         why = {STREAMKL_ERR_TIMEOUT: "a bounded wait inside the kernel gave up",
                STREAMKL_ERR_INVALID_ARG: "malformed sequence offsets or causal rows without a key",
-               STREAMKL_ERR_DEVICE_CHECK: "a device-side range check failed (debug build)"}
+               STREAMKL_ERR_DEVICE_CHECK: "a device-side range check failed (debug build)",
+               STREAMKL_ERR_NO_PAGES: "free pages did not suffice for every sequence"}
         raise StreamKLError(v, where, why.get(v, "kernel failure"))

@@ -430,6 +430,7 @@ const char* streamkl_status_string(streamkl_status s) {
     case STREAMKL_ERR_CUDA: return "STREAMKL_ERR_CUDA";
     case STREAMKL_ERR_TIMEOUT: return "STREAMKL_ERR_TIMEOUT";
     case STREAMKL_ERR_DEVICE_CHECK: return "STREAMKL_ERR_DEVICE_CHECK";
+    case STREAMKL_ERR_NO_PAGES: return "STREAMKL_ERR_NO_PAGES";
   }
   return "STREAMKL_ERR_UNKNOWN";
 }

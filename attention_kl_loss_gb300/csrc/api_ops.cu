@@ -19,6 +19,7 @@ using namespace skl::host;
 static_assert(STREAMKL_BF16 == skl::kTypeBf16 && STREAMKL_FP16 == skl::kTypeF16 &&
                   STREAMKL_FP32 == skl::kTypeF32,
               "element types of the header and the kernels agree");
+static_assert(STREAMKL_ERR_NO_PAGES == skl::kStatusNoPages, "status codes of the header and the kernels agree");
 
 constexpr long long kMaxRows = 1LL << 30;  // rows (tokens x heads) of one tensor
 
@@ -143,24 +144,35 @@ streamkl_status rope_common(skl::RopeArgs* a, streamkl_rope_args* u, bool backwa
   return STREAMKL_OK;
 }
 
-streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* table, long long table_stride,
-                            const int* kv_lens, const int* cu_seqlens, int dtype, int B, int T, int HK, int d,
-                            int page_size, int num_pages, int max_pages) {
+streamkl_status check_page_size(int page_size) {
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "page size %d (supported: powers of two from 16 to 1024)", page_size);
+  return STREAMKL_OK;
+}
+
+streamkl_status check_cache_type(int dtype, int d) {
   if (dtype != STREAMKL_BF16 && dtype != STREAMKL_FP16)
     return fail(STREAMKL_ERR_UNSUPPORTED, "cache element type %d (supported: bf16, fp16)", dtype);
   if (d != 64 && d != 128) return fail(STREAMKL_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
+  return STREAMKL_OK;
+}
+
+streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* table, long long table_stride,
+                            const int* kv_lens, const int* cu_seqlens, int dtype, int B, int T, int HK, int d,
+                            int page_size, int num_pages, int max_pages) {
+  streamkl_status st = check_cache_type(dtype, d);
+  if (st != STREAMKL_OK) return st;
   if (B < 1 || T < 1 || HK < 1 || num_pages < 1 || max_pages < 1)
     return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (B=%d T=%d HK=%d num_pages=%d max_pages=%d)", B, T,
                 HK, num_pages, max_pages);
-  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
-    return fail(STREAMKL_ERR_UNSUPPORTED, "page size %d (supported: powers of two from 16 to 1024)", page_size);
+  if ((st = check_page_size(page_size)) != STREAMKL_OK) return st;
   if (static_cast<long long>(max_pages) * page_size > (1LL << 30))
     return fail(STREAMKL_ERR_UNSUPPORTED, "sequence length above 2^30");
   if (!table || !kv_lens) return fail(STREAMKL_ERR_INVALID_ARG, "block_table and kv_lens must be non-NULL");
   if (table_stride < 0) return fail(STREAMKL_ERR_INVALID_ARG, "block_table stride %lld", table_stride);
   if (!cu_seqlens && T != B)
     return fail(STREAMKL_ERR_INVALID_ARG, "without cu_seqlens each sequence has one token (T=%d B=%d)", T, B);
-  streamkl_status st = check_rows("k_cache", kc, num_pages, HK, page_size, d, dtype, true);
+  st = check_rows("k_cache", kc, num_pages, HK, page_size, d, dtype, true);
   return st != STREAMKL_OK ? st : check_rows("v_cache", vc, num_pages, HK, page_size, d, dtype, true);
 }
 
@@ -275,6 +287,104 @@ streamkl_status check_attn_sizes(int B, int T, int HQ, int HK, int d, int max_q,
   return STREAMKL_OK;
 }
 
+// The attention over the cache; `tree`: of drafted tokens.
+streamkl_status attn_call(streamkl_paged_attn_args& u, const streamkl_paged_tree_attn_args* tree, void* stream) {
+  streamkl_status st = check_cache(&u.k_cache, &u.v_cache, u.block_table, u.table_stride, u.kv_lens, u.cu_seqlens,
+                                   u.dtype, u.B, u.T, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
+  if (st != STREAMKL_OK) return st;
+  if ((st = check_attn_sizes(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len)) != STREAMKL_OK) return st;
+  if (u.max_kv_len > static_cast<long long>(u.max_pages) * u.page_size)
+    return fail(STREAMKL_ERR_INVALID_ARG, "max_kv_len %d above %d pages of %d", u.max_kv_len, u.max_pages, u.page_size);
+  if ((st = check_rows("q", &u.q, 0, u.T, u.HQ, u.d, u.dtype, false)) != STREAMKL_OK) return st;
+  if ((st = check_rows("out", &u.out, 0, u.T, u.HQ, u.d, u.dtype, true)) != STREAMKL_OK) return st;
+  if (!u.lse) return fail(STREAMKL_ERR_INVALID_ARG, "lse must be non-NULL");
+  if (u.causal != 0 && u.causal != 1) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (u.num_splits < 0) return fail(STREAMKL_ERR_INVALID_ARG, "num_splits must be >= 0");
+  if (!(u.scale > 0.f) || !std::isfinite(u.scale))
+    return fail(STREAMKL_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!u.dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
+  const AttnPlan p = attn_plan(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
+  if (p.splits > 65535) return fail(STREAMKL_ERR_UNSUPPORTED, "%d key splits (at most 65535)", p.splits);
+  const size_t need = attn_part_bytes(p, u.T, u.HQ, u.d);
+  if (need && (!u.workspace || u.ws_bytes < need))
+    return fail(STREAMKL_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", u.workspace ? u.ws_bytes : 0, need);
+  if (need && !aligned16(u.workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  CUtensorMap mk, mv;
+  if ((st = make_map_cache(&mk, u.k_cache, u.dtype, u.d, u.page_size, u.HK, u.num_pages, "k_cache")) != STREAMKL_OK)
+    return st;
+  if ((st = make_map_cache(&mv, u.v_cache, u.dtype, u.d, u.page_size, u.HK, u.num_pages, "v_cache")) != STREAMKL_OK)
+    return st;
+  skl::PagedAttnArgs a{};
+  a.tm_k = &mk;
+  a.tm_v = &mv;
+  a.q = u.q.data;
+  a.q_sn = u.q.stride[1], a.q_sh = u.q.stride[2];
+  a.o = u.out.data;
+  a.o_sn = u.out.stride[1], a.o_sh = u.out.stride[2];
+  a.lse = u.lse;
+  a.table = u.block_table;
+  a.table_sb = u.table_stride;
+  a.kv_lens = u.kv_lens;
+  a.cu = u.cu_seqlens;
+  a.B = u.B;
+  a.T = u.T;
+  a.HQ = u.HQ;
+  a.HK = u.HK;
+  a.d = u.d;
+  a.type = u.dtype;
+  a.causal = u.causal;
+  a.page_shift = __builtin_ctz(static_cast<unsigned>(u.page_size));
+  a.num_pages = u.num_pages;
+  a.max_pages = u.max_pages;
+  a.max_q = u.max_seqlen_q;
+  a.max_kv = u.max_kv_len;
+  a.scale = u.scale;
+  if (tree != nullptr) {
+    a.mask = tree->mask;
+    a.mask_sn = tree->mask_stride;
+    a.mask_words = tree->mask_words;
+  }
+  a.q_tiles = p.q_tiles;
+  a.row_tiles = p.row_tiles;
+  a.splits = p.splits;
+  a.split_tiles = p.split_tiles;
+  a.whole = p.whole;
+  // more than one CTA per SM one after the other: long ones first, so that the
+  // last to start are short (four ragged chunks of up to 2,048 rows over 16,384
+  // keys, d = 64: 250 us against 258)
+  a.by_length = u.B > 1 && u.B <= 32 && static_cast<long long>(p.q_tiles) * u.B * u.HK > num_sms();
+  a.part_o = static_cast<float*>(u.workspace);
+  a.part_lse = a.part_o ? a.part_o + attn_part_rows(p, u.T, u.HQ) * u.d : nullptr;
+  a.dev_status = u.dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  auto s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (tree != nullptr)
+    e = p.decode_ctas > 0 ? skl::launch_tree_decode(a, p.decode_ctas, s) : skl::launch_tree_attn(a, s);
+  else
+    e = p.decode_ctas > 0 ? skl::launch_paged_decode(a, p.decode_ctas, s) : skl::launch_paged_attn(a, s);
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "paged attention launch");
+}
+
+skl::CacheRows cache_rows(const streamkl_rows& r) {
+  return skl::CacheRows{r.data, r.stride[0] / 8, r.stride[1] / 8, r.stride[2] / 8};
+}
+
+// What a fork and a resize share.
+streamkl_status check_tables(const int* refs, const int* table, long long stride, const int* lens, const int* list,
+                                    const char* list_name, const int* status, int B, int num_pages, int max_pages) {
+  if (B < 1 || num_pages < 1 || max_pages < 1)
+    return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (B=%d num_pages=%d max_pages=%d)", B, num_pages, max_pages);
+  if (B > skl::kMaxTableRows || num_pages > (1 << 30) || static_cast<long long>(B) * max_pages > (1LL << 30))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "more than %d sequences, 2^30 pages or 2^30 entries", skl::kMaxTableRows);
+  if (!refs || !table || !lens || !list)
+    return fail(STREAMKL_ERR_INVALID_ARG, "page_refs, block_table, kv_lens and %s must be non-NULL", list_name);
+  if (stride < max_pages && B > 1)
+    return fail(STREAMKL_ERR_INVALID_ARG, "block_table rows overlap (stride %lld, %d pages)", stride, max_pages);
+  if (!status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
+  return STREAMKL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -379,72 +489,119 @@ size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, i
 streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* stream) {
   streamkl_paged_attn_args u;
   if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  return attn_call(u, nullptr, stream);
+}
+
+size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
+                                               int num_splits) {
+  return streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits);
+}
+
+streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* args, void* stream) {
+  streamkl_paged_tree_attn_args t;
+  if (!take_args(&t, args)) return STREAMKL_ERR_INVALID_ARG;
+  streamkl_paged_attn_args u;
+  if (!take_args(&u, &t.attn)) return STREAMKL_ERR_INVALID_ARG;
+  if (u.causal) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0: the masks say what a drafted token sees");
+  if (!t.mask || reinterpret_cast<uintptr_t>(t.mask) % 4)
+    return fail(STREAMKL_ERR_INVALID_ARG, "mask must be a 4-byte aligned address");
+  if (t.mask_words < 1 || t.mask_stride < 0 || u.max_seqlen_q > 32LL * t.mask_words)
+    return fail(STREAMKL_ERR_INVALID_ARG, "mask of %d words, %lld apart, for %d drafted tokens", t.mask_words,
+                t.mask_stride, u.max_seqlen_q);
+  return attn_call(u, &t, stream);
+}
+
+streamkl_status streamkl_paged_compact(const streamkl_compact_args* args, void* stream) {
+  streamkl_compact_args u;
+  if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  if (!u.cu_seqlens) return fail(STREAMKL_ERR_INVALID_ARG, "cu_seqlens must be non-NULL");
   streamkl_status st = check_cache(&u.k_cache, &u.v_cache, u.block_table, u.table_stride, u.kv_lens, u.cu_seqlens,
-                                   u.dtype, u.B, u.T, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
+                                   u.dtype, u.B, 1, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
   if (st != STREAMKL_OK) return st;
-  if ((st = check_attn_sizes(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len)) != STREAMKL_OK) return st;
-  if (u.max_kv_len > static_cast<long long>(u.max_pages) * u.page_size)
-    return fail(STREAMKL_ERR_INVALID_ARG, "max_kv_len %d above %d pages of %d", u.max_kv_len, u.max_pages, u.page_size);
-  if ((st = check_rows("q", &u.q, 0, u.T, u.HQ, u.d, u.dtype, false)) != STREAMKL_OK) return st;
-  if ((st = check_rows("out", &u.out, 0, u.T, u.HQ, u.d, u.dtype, true)) != STREAMKL_OK) return st;
-  if (!u.lse) return fail(STREAMKL_ERR_INVALID_ARG, "lse must be non-NULL");
-  if (u.causal != 0 && u.causal != 1) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0 or 1");
-  if (u.num_splits < 0) return fail(STREAMKL_ERR_INVALID_ARG, "num_splits must be >= 0");
-  if (!(u.scale > 0.f) || !std::isfinite(u.scale))
-    return fail(STREAMKL_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (static_cast<long long>(u.B) * u.HK > kMaxRows / 2) return fail(STREAMKL_ERR_UNSUPPORTED, "B x HK above 2^29");
+  if (!u.kept || !u.num_kept) return fail(STREAMKL_ERR_INVALID_ARG, "kept and num_kept must be non-NULL");
+  if (u.max_kept < 1 || (u.kept_stride < u.max_kept && u.B > 1) || u.kept_stride < 0)
+    return fail(STREAMKL_ERR_INVALID_ARG, "kept of %d tokens a sequence, rows %lld apart", u.max_kept, u.kept_stride);
   if (!u.dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
-  const AttnPlan p = attn_plan(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
-  if (p.splits > 65535) return fail(STREAMKL_ERR_UNSUPPORTED, "%d key splits (at most 65535)", p.splits);
-  const size_t need = attn_part_bytes(p, u.T, u.HQ, u.d);
-  if (need && (!u.workspace || u.ws_bytes < need))
-    return fail(STREAMKL_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", u.workspace ? u.ws_bytes : 0, need);
-  if (need && !aligned16(u.workspace)) return fail(STREAMKL_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
-  CUtensorMap mk, mv;
-  if ((st = make_map_cache(&mk, u.k_cache, u.dtype, u.d, u.page_size, u.HK, u.num_pages, "k_cache")) != STREAMKL_OK)
-    return st;
-  if ((st = make_map_cache(&mv, u.v_cache, u.dtype, u.d, u.page_size, u.HK, u.num_pages, "v_cache")) != STREAMKL_OK)
-    return st;
-  skl::PagedAttnArgs a{};
-  a.tm_k = &mk;
-  a.tm_v = &mv;
-  a.q = u.q.data;
-  a.q_sn = u.q.stride[1], a.q_sh = u.q.stride[2];
-  a.o = u.out.data;
-  a.o_sn = u.out.stride[1], a.o_sh = u.out.stride[2];
-  a.lse = u.lse;
+  skl::CompactArgs a{};
+  a.cache[0] = cache_rows(u.k_cache);
+  a.cache[1] = cache_rows(u.v_cache);
   a.table = u.block_table;
   a.table_sb = u.table_stride;
   a.kv_lens = u.kv_lens;
   a.cu = u.cu_seqlens;
+  a.kept = u.kept;
+  a.kept_sb = u.kept_stride;
+  a.num_kept = u.num_kept;
   a.B = u.B;
-  a.T = u.T;
-  a.HQ = u.HQ;
-  a.HK = u.HK;
-  a.d = u.d;
-  a.type = u.dtype;
-  a.causal = u.causal;
+  a.H = u.HK;
+  a.vshift = u.d == 128 ? 4 : 3;
   a.page_shift = __builtin_ctz(static_cast<unsigned>(u.page_size));
   a.num_pages = u.num_pages;
   a.max_pages = u.max_pages;
-  a.max_q = u.max_seqlen_q;
-  a.max_kv = u.max_kv_len;
-  a.scale = u.scale;
-  a.q_tiles = p.q_tiles;
-  a.row_tiles = p.row_tiles;
-  a.splits = p.splits;
-  a.split_tiles = p.split_tiles;
-  a.whole = p.whole;
-  // more than one CTA per SM one after the other: long ones first, so that the
-  // last to start are short (four ragged chunks of up to 2,048 rows over 16,384
-  // keys, d = 64: 250 us against 258)
-  a.by_length = u.B > 1 && u.B <= 32 && static_cast<long long>(p.q_tiles) * u.B * u.HK > num_sms();
-  a.part_o = static_cast<float*>(u.workspace);
-  a.part_lse = a.part_o ? a.part_o + attn_part_rows(p, u.T, u.HQ) * u.d : nullptr;
+  a.max_kept = u.max_kept;
   a.dev_status = u.dev_status;
-  a.timeout_ns = wait_timeout_ns();
-  cudaError_t e = p.decode_ctas > 0 ? skl::launch_paged_decode(a, p.decode_ctas, static_cast<cudaStream_t>(stream))
-                                    : skl::launch_paged_attn(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "paged attention launch");
+  cudaError_t e = skl::launch_compact(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "compact launch");
+}
+
+streamkl_status streamkl_paged_copy(const streamkl_page_copy_args* args, void* stream) {
+  streamkl_page_copy_args u;
+  if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  streamkl_status st = check_cache_type(u.dtype, u.d);
+  if (st != STREAMKL_OK) return st;
+  if ((st = check_page_size(u.page_size)) != STREAMKL_OK) return st;
+  if (u.n < 1 || u.HK < 1 || u.num_pages < 1)
+    return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (n=%d HK=%d num_pages=%d)", u.n, u.HK, u.num_pages);
+  if (u.HK > 65535 || static_cast<long long>(u.n) * u.HK * u.page_size > (1LL << 40))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "more than 65535 heads or 2^40 rows");
+  if ((st = check_rows("k_cache", &u.k_cache, u.num_pages, u.HK, u.page_size, u.d, u.dtype, true)) != STREAMKL_OK) return st;
+  if ((st = check_rows("v_cache", &u.v_cache, u.num_pages, u.HK, u.page_size, u.d, u.dtype, true)) != STREAMKL_OK) return st;
+  if (!u.pairs || reinterpret_cast<uintptr_t>(u.pairs) % 8)
+    return fail(STREAMKL_ERR_INVALID_ARG, "pairs must be an 8-byte aligned address");
+  if (!u.dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
+  skl::PageCopyArgs a{};
+  a.cache[0] = cache_rows(u.k_cache);
+  a.cache[1] = cache_rows(u.v_cache);
+  a.pairs = u.pairs;
+  a.n = u.n;
+  a.H = u.HK;
+  a.vshift = u.d == 128 ? 4 : 3;
+  a.page_shift = __builtin_ctz(static_cast<unsigned>(u.page_size));
+  a.num_pages = u.num_pages;
+  a.dev_status = u.dev_status;
+  cudaError_t e = skl::launch_page_copy(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "page copy launch");
+}
+
+streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream) {
+  streamkl_fork_args u;
+  if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  streamkl_status st = check_tables(u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.source, "source", u.dev_status,
+                                    u.B, u.num_pages, u.max_pages);
+  if (st != STREAMKL_OK) return st;
+  skl::ForkArgs a{u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.source, u.B, u.num_pages, u.max_pages, 0,
+                  u.dev_status};
+  cudaError_t e = skl::launch_fork(a, num_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "fork launch");
+}
+
+streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* stream) {
+  streamkl_resize_args u;
+  if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  streamkl_status st = check_tables(u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.new_lens, "new_lens",
+                                    u.dev_status, u.B, u.num_pages, u.max_pages);
+  if (st != STREAMKL_OK) return st;
+  if ((st = check_page_size(u.page_size)) != STREAMKL_OK) return st;
+  if (static_cast<long long>(u.max_pages) * u.page_size > (1LL << 30))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "sequence length above 2^30");
+  if (!aligned16(u.page_refs)) return fail(STREAMKL_ERR_INVALID_ARG, "page_refs is not 16-byte aligned");
+  if (!u.copies || reinterpret_cast<uintptr_t>(u.copies) % 8)
+    return fail(STREAMKL_ERR_INVALID_ARG, "copies must be an 8-byte aligned address");
+  skl::ResizeArgs a{u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.new_lens, reinterpret_cast<int2*>(u.copies), u.B,
+                    u.num_pages, u.max_pages, __builtin_ctz(static_cast<unsigned>(u.page_size)), u.dev_status};
+  cudaError_t e = skl::launch_resize(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "resize launch");
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -36,6 +37,12 @@ struct Entries {
   decltype(&streamkl_paged_append) append;
   decltype(&streamkl_paged_attn) attn;
   decltype(&streamkl_paged_attn_workspace_size) attn_size;
+  decltype(&streamkl_paged_tree_attn) tree;
+  decltype(&streamkl_paged_tree_attn_workspace_size) tree_size;
+  decltype(&streamkl_paged_compact) compact;
+  decltype(&streamkl_paged_copy) copy;
+  decltype(&streamkl_paged_fork) fork;
+  decltype(&streamkl_paged_resize) resize;
 };
 
 // An argument that is not for here.
@@ -412,47 +419,198 @@ PyObject* append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+// The attention over the cache, of drafted tokens (`tree`) or not.
+PyObject* attn_call(Args a, bool tree) {
+  const Entries& lib = a.entries();
+  const at::Tensor *q = a.tensor(), *kc = a.tensor(), *vc = a.tensor(), *table = a.tensor(), *lens = a.tensor();
+  const at::Tensor* mask = tree ? a.tensor() : nullptr;
+  const at::Tensor* cu = a.tensor(true);
+  streamkl_paged_tree_attn_args t{};
+  streamkl_paged_attn_args& u = t.attn;
+  u.max_seqlen_q = a.integer_or(INT_MIN), u.max_kv_len = a.integer_or(INT_MIN);
+  const bool scaled = *a.at != Py_None;
+  if (scaled)
+    u.scale = a.real();
+  else
+    a.next();
+  if (!tree) u.causal = a.flag();
+  u.num_splits = a.integer();
+  const at::Tensor *given = a.tensor(true), *status = a.tensor(true);
+  const Home home(*kc);
+  home.rows(*q, 3);
+  cache_args(&u, home, *kc, *vc, *table, *lens, cu, fits(q->size(0)), fits(q->size(2)));
+  u.HQ = fits(q->size(1));
+  want(u.HQ > 0 && u.HQ % u.HK == 0 && u.num_splits >= 0);
+  if (!scaled) u.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(u.d)));
+  if (u.max_seqlen_q == INT_MIN) {
+    u.max_seqlen_q = cu != nullptr ? u.T : 1;
+    if (tree && mask->dim() == 2) u.max_seqlen_q = static_cast<int>(std::min<int64_t>(u.max_seqlen_q, 32 * mask->size(1)));
+  }
+  if (u.max_kv_len == INT_MIN) u.max_kv_len = fits(static_cast<int64_t>(u.page_size) * u.max_pages);
+  if (tree) {
+    want(mask->dim() == 2 && mask->scalar_type() == at::kInt && mask->device() == home.device);
+    want(mask->size(0) == u.T && mask->size(1) > 0 && mask->stride(1) == 1);
+    t.struct_size = sizeof(t);
+    t.mask = static_cast<const int*>(mask->data_ptr());
+    t.mask_stride = mask->stride(0);
+    t.mask_words = fits(mask->size(1));
+  }
+  u.q = {q->data_ptr(), {0, q->stride(0), q->stride(1)}};
+  const at::Tensor o = home.make(q->sizes(), home.type), lse = home.make({u.T, u.HQ}, at::kFloat);
+  u.out = {o.data_ptr(), {0, static_cast<long long>(u.HQ) * u.d, u.d}};
+  u.lse = static_cast<float*>(lse.data_ptr());
+  at::Tensor word, space;
+  if (given != nullptr) {
+    want(given->device() == home.device && given->is_contiguous());
+    u.workspace = given->data_ptr(), u.ws_bytes = given->nbytes();
+  } else {
+    u.ws_bytes = (tree ? lib.tree_size : lib.attn_size)(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len,
+                                                        u.num_splits);
+    u.workspace = (space = home.make({static_cast<int64_t>(u.ws_bytes)}, at::kByte)).data_ptr();
+  }
+  u.dev_status = home.status(status, &word);
+  if (tree)
+    launch(lib.tree, t, home);
+  else
+    launch(lib.attn, u, home);
+  return tuple(o, lse);
+}
+
 // attn(entries, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
 //      num_splits, workspace, dev_status)
 PyObject* attn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     want(n == 14);
+    return attn_call(Args{argv}, false);
+  });
+}
+
+// tree_attn(entries, q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len, scale,
+//           num_splits, workspace, dev_status)
+PyObject* tree_attn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n == 14);
+    return attn_call(Args{argv}, true);
+  });
+}
+
+// compact(entries, k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status); True when done
+PyObject* compact(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n == 9);
     Args a{argv};
     const Entries& lib = a.entries();
-    const at::Tensor *q = a.tensor(), *kc = a.tensor(), *vc = a.tensor(), *table = a.tensor(), *lens = a.tensor(),
-                     *cu = a.tensor(true);
-    streamkl_paged_attn_args u{};
-    u.max_seqlen_q = a.integer_or(INT_MIN), u.max_kv_len = a.integer_or(INT_MIN);
-    const bool scaled = *a.at != Py_None;
-    if (scaled)
-      u.scale = a.real();
-    else
-      a.next();
-    u.causal = a.flag(), u.num_splits = a.integer();
-    const at::Tensor *given = a.tensor(true), *status = a.tensor(true);
+    const at::Tensor *kc = a.tensor(), *vc = a.tensor(), *table = a.tensor(), *lens = a.tensor(), *cu = a.tensor(),
+                     *kept = a.tensor(), *count = a.tensor(), *status = a.tensor(true);
     const Home home(*kc);
-    home.rows(*q, 3);
-    cache_args(&u, home, *kc, *vc, *table, *lens, cu, fits(q->size(0)), fits(q->size(2)));
-    u.HQ = fits(q->size(1));
-    want(u.HQ > 0 && u.HQ % u.HK == 0 && u.num_splits >= 0);
-    if (!scaled) u.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(u.d)));
-    if (u.max_seqlen_q == INT_MIN) u.max_seqlen_q = cu != nullptr ? u.T : 1;
-    if (u.max_kv_len == INT_MIN) u.max_kv_len = fits(static_cast<int64_t>(u.page_size) * u.max_pages);
-    u.q = {q->data_ptr(), {0, q->stride(0), q->stride(1)}};
-    const at::Tensor o = home.make(q->sizes(), home.type), lse = home.make({u.T, u.HQ}, at::kFloat);
-    u.out = {o.data_ptr(), {0, static_cast<long long>(u.HQ) * u.d, u.d}};
-    u.lse = static_cast<float*>(lse.data_ptr());
-    at::Tensor word, space;
-    if (given != nullptr) {
-      want(given->device() == home.device && given->is_contiguous());
-      u.workspace = given->data_ptr(), u.ws_bytes = given->nbytes();
-    } else {
-      u.ws_bytes = lib.attn_size(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
-      u.workspace = (space = home.make({static_cast<int64_t>(u.ws_bytes)}, at::kByte)).data_ptr();
-    }
+    want(kc->dim() == 4);
+    struct : streamkl_compact_args {  // (with the field of the calls that take tokens)
+      int T;
+    } u{};
+    cache_args(&u, home, *kc, *vc, *table, *lens, cu, 1, fits(kc->size(3)));
+    want(kept->dim() == 2 && kept->scalar_type() == at::kInt && kept->device() == home.device);
+    want(kept->size(0) == u.B && kept->size(1) > 0 && kept->stride(1) == 1);
+    home.list(*count, u.B, at::kInt);
+    u.kept = static_cast<const int*>(kept->data_ptr());
+    u.kept_stride = kept->stride(0);
+    u.max_kept = fits(kept->size(1));
+    u.num_kept = static_cast<const int*>(count->data_ptr());
+    at::Tensor word;
     u.dev_status = home.status(status, &word);
-    launch(lib.attn, u, home);
-    return tuple(o, lse);
+    streamkl_compact_args args = u;
+    args.struct_size = sizeof(args);
+    launch(lib.compact, args, home);
+    Py_RETURN_TRUE;
+  });
+}
+
+// copy(entries, k_cache, v_cache, pairs, dev_status); True when done
+PyObject* copy(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n == 5);
+    Args a{argv};
+    const Entries& lib = a.entries();
+    const at::Tensor *kc = a.tensor(), *vc = a.tensor(), *pairs = a.tensor(), *status = a.tensor(true);
+    const Home home(*kc);
+    home.rows(*kc, 4);
+    home.rows(*vc, 4);
+    want(kc->sizes() == vc->sizes() && (home.type == at::kBFloat16 || home.type == at::kHalf));
+    want(pairs->dim() == 2 && pairs->size(1) == 2 && pairs->scalar_type() == at::kInt && pairs->device() == home.device &&
+         pairs->is_contiguous());
+    streamkl_page_copy_args u{};
+    u.struct_size = sizeof(u);
+    u.k_cache = {kc->data_ptr(), {kc->stride(0), kc->stride(1), kc->stride(2)}};
+    u.v_cache = {vc->data_ptr(), {vc->stride(0), vc->stride(1), vc->stride(2)}};
+    u.pairs = static_cast<const int*>(pairs->data_ptr());
+    u.dtype = type_of(home.type);
+    u.n = fits(pairs->size(0)), u.HK = fits(kc->size(1)), u.d = fits(kc->size(3));
+    u.page_size = fits(kc->size(2)), u.num_pages = fits(kc->size(0));
+    want(u.n > 0 && u.HK > 0);
+    at::Tensor word;
+    u.dev_status = home.status(status, &word);
+    launch(lib.copy, u, home);
+    Py_RETURN_TRUE;
+  });
+}
+
+// The fields that fork and resize share.
+template <typename U>
+void table_args(U* u, const Home& home, const at::Tensor& refs, const at::Tensor& table, const at::Tensor& lens) {
+  want(home.type == at::kInt && refs.dim() == 1 && table.dim() == 2 && table.stride(1) == 1);
+  home.list(refs, refs.size(0), at::kInt);
+  u->struct_size = sizeof(*u);
+  u->page_refs = static_cast<int*>(refs.data_ptr());
+  u->block_table = static_cast<int*>(table.data_ptr());
+  u->table_stride = table.stride(0);
+  u->B = fits(table.size(0));
+  home.list(lens, u->B, at::kInt);
+  u->kv_lens = static_cast<int*>(lens.data_ptr());
+  u->num_pages = fits(refs.size(0)), u->max_pages = fits(table.size(1));
+  want(u->B > 0);
+}
+
+// fork(entries, page_refs, block_table, kv_lens, source, dev_status); True when done
+PyObject* fork(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n == 6);
+    Args a{argv};
+    const Entries& lib = a.entries();
+    const at::Tensor *refs = a.tensor(), *table = a.tensor(), *lens = a.tensor(), *source = a.tensor(),
+                     *status = a.tensor(true);
+    const Home home(*table);
+    streamkl_fork_args u{};
+    table_args(&u, home, *refs, *table, *lens);
+    home.list(*source, u.B, at::kInt);
+    u.source = static_cast<const int*>(source->data_ptr());
+    at::Tensor word;
+    u.dev_status = home.status(status, &word);
+    launch(lib.fork, u, home);
+    Py_RETURN_TRUE;
+  });
+}
+
+// resize(entries, page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
+PyObject* resize(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n == 7);
+    Args a{argv};
+    const Entries& lib = a.entries();
+    const at::Tensor *refs = a.tensor(), *table = a.tensor(), *lens = a.tensor(), *to = a.tensor();
+    streamkl_resize_args u{};
+    u.page_size = a.integer();
+    const at::Tensor* status = a.tensor(true);
+    const Home home(*table);
+    table_args(&u, home, *refs, *table, *lens);
+    home.list(*to, u.B, at::kInt);
+    u.new_lens = static_cast<const int*>(to->data_ptr());
+    const at::Tensor copies = home.make({u.B, 2}, at::kInt);
+    u.copies = static_cast<int*>(copies.data_ptr());
+    at::Tensor word;
+    u.dev_status = home.status(status, &word);
+    launch(lib.resize, u, home);
+    PyObject* o = THPVariable_Wrap(copies);
+    want(o != nullptr);
+    return o;
   });
 }
 
@@ -469,7 +627,11 @@ PyObject* entries(PyObject*, PyObject* path) {
   };
   if (!(find(&e->rope_fwd, "streamkl_qk_norm_rope_fwd") && find(&e->rope_bwd, "streamkl_qk_norm_rope_bwd") &&
         find(&e->rope_bwd_size, "streamkl_qk_norm_rope_bwd_workspace_size") && find(&e->append, "streamkl_paged_append") &&
-        find(&e->attn, "streamkl_paged_attn") && find(&e->attn_size, "streamkl_paged_attn_workspace_size"))) {
+        find(&e->attn, "streamkl_paged_attn") && find(&e->attn_size, "streamkl_paged_attn_workspace_size") &&
+        find(&e->tree, "streamkl_paged_tree_attn") &&
+        find(&e->tree_size, "streamkl_paged_tree_attn_workspace_size") && find(&e->compact, "streamkl_paged_compact") &&
+        find(&e->copy, "streamkl_paged_copy") && find(&e->fork, "streamkl_paged_fork") &&
+        find(&e->resize, "streamkl_paged_resize"))) {
     delete e;
     return PyErr_Format(PyExc_OSError, "%s lacks an entry", name);
   }
@@ -482,6 +644,11 @@ PyMethodDef kMethods[] = {{"entries", entries, METH_O, nullptr},
                           {"rope_bwd", FAST(rope_bwd), nullptr},
                           {"append", FAST(append), nullptr},
                           {"attn", FAST(attn), nullptr},
+                          {"tree_attn", FAST(tree_attn), nullptr},
+                          {"compact", FAST(compact), nullptr},
+                          {"copy", FAST(copy), nullptr},
+                          {"fork", FAST(fork), nullptr},
+                          {"resize", FAST(resize), nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 #undef FAST
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

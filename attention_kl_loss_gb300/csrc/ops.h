@@ -12,6 +12,8 @@ namespace skl {
 // Element types of the rows (== STREAMKL_BF16 and so on).
 constexpr int kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2;
 
+constexpr int kStatusNoPages = 6;  // == STREAMKL_ERR_NO_PAGES
+
 // Where rows of d elements lie: row (b, n, h) starts at element
 // b * sb + n * sn + h * sh.
 struct RowStrides {
@@ -85,6 +87,9 @@ struct PagedAttnArgs {
   int page_shift, num_pages, max_pages;
   int max_q, max_kv;
   float scale;
+  const int* mask;           // tree: row of token t at t * mask_sn, mask_words of 32 drafted tokens each
+  long long mask_sn;
+  int mask_words;
   int q_tiles;               // query tiles of a (sequence, key head)
   int row_tiles;             // 128-row tiles of a CTA (1 or 2)
   int splits, split_tiles;   // key splits and key tiles of one
@@ -95,6 +100,58 @@ struct PagedAttnArgs {
   int* dev_status;
   uint64_t timeout_ns;
 };
+
+// A paged cache whose rows are moved, 16 bytes a vector.
+struct CacheRows {
+  void* data;
+  long long sp, sh, ss;      // page, head and slot strides, vectors
+};
+
+struct PageCopyArgs {
+  CacheRows cache[2];
+  const int* pairs;          // [n][2]: source, destination; negative: nothing to do
+  int n, H, vshift;          // 1 << vshift vectors a row
+  int page_shift, num_pages;
+  int chunks;                // set by the launcher
+  int* dev_status;
+};
+
+struct CompactArgs {
+  CacheRows cache[2];
+  const int* table;
+  long long table_sb;
+  const int* kv_lens;
+  const int* cu;
+  const int* kept;           // [B][max_kept], rows kept_sb apart
+  long long kept_sb;
+  const int* num_kept;
+  int B, H, vshift, page_shift, num_pages, max_pages, max_kept;
+  int* dev_status;
+};
+
+struct ForkArgs {
+  int* refs;
+  int* table;
+  long long table_sb;
+  int* kv_lens;
+  const int* source;
+  int B, num_pages, max_pages;
+  int cols;                  // set by the launcher: columns of a block
+  int* dev_status;
+};
+
+struct ResizeArgs {
+  int* refs;
+  int* table;
+  long long table_sb;
+  int* kv_lens;
+  const int* new_lens;
+  int2* copies;
+  int B, num_pages, max_pages, page_shift;
+  int* dev_status;
+};
+
+constexpr int kMaxTableRows = 8192;  // sequences of a fork or resize call
 
 // Blocks of the backward's persistent grid (its partials' row count).
 int rope_bwd_blocks(int B, int NQ, int HQ, int NK, int HK, int d, int sms);
@@ -109,5 +166,13 @@ cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream);
 constexpr int kDecodeRows = 32;
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+// The same for rows that see the drafted tokens of their masks.
+cudaError_t launch_tree_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_tree_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
+cudaError_t launch_page_copy(PageCopyArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream);
 
 }  // namespace skl

@@ -57,4 +57,54 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
+// Whether what the status word held before stops a call: a failure does, but not
+// a bad number of some sequence, which may come from this very call, nor pages
+// that did not suffice.
+__device__ __forceinline__ bool status_stops(int before) {
+  return before != 0 && before != kStatusInvalidArg && before != kStatusNoPages;
+}
+
+// A row of a drafted tree: which of 32 keys it sees, bit k for drafted token t + k
+// of its sequence's n. Tokens before the drafted ones (t + k < 0) are seen by
+// every row, those from n on (past the sequence's end) by none.
+__device__ __forceinline__ uint32_t tree_bits(const int* mask, int words, int n, int t) {
+  auto word = [&](int i) {
+    if (i < 0) return ~0u;
+    const int left = n - 32 * i;
+    if (i >= words || left <= 0) return 0u;
+    const uint32_t w = static_cast<uint32_t>(__ldg(mask + i));
+    return left < 32 ? w & ((1u << left) - 1) : w;
+  };
+  const int i = t >> 5;
+  return __funnelshift_r(word(i), word(i + 1), t & 31);
+}
+
+// The keys of a tile that a row sees: the first `seen`, or with TREE those whose
+// bit is set (`all`: every one of them).
+template <bool TREE>
+struct TileMask;
+template <>
+struct TileMask<false> {
+  int seen;
+  __device__ __forceinline__ TileMask(const PagedAttnArgs&, bool, int, int, int, int lim, int key0) : seen(lim - key0) {}
+  __device__ __forceinline__ bool partial() const { return seen < kTileN; }
+  __device__ __forceinline__ bool some() const { return seen > 0; }
+  __device__ __forceinline__ bool hides(int k) const { return k >= seen; }
+};
+template <>
+struct TileMask<true> {
+  uint32_t bits[4];
+  bool all;
+  __device__ __forceinline__ TileMask(const PagedAttnArgs& a, bool live, int token, int n, int len, int, int key0) {
+    const int t = key0 - (len - n);
+    all = live && t + kTileN <= 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      bits[q] = !live ? 0u : all ? ~0u : tree_bits(a.mask + token * a.mask_sn, a.mask_words, n, t + 32 * q);
+  }
+  __device__ __forceinline__ bool partial() const { return !all; }
+  __device__ __forceinline__ bool some() const { return (bits[0] | bits[1] | bits[2] | bits[3]) != 0; }
+  __device__ __forceinline__ bool hides(int k) const { return !(bits[k >> 5] >> (k & 31) & 1); }
+};
+
 }  // namespace skl

@@ -1,0 +1,501 @@
+// What a serving step does with the pages of a cache beside attention: drafted
+// tokens that were accepted move to the front (compact), pages are copied (copy),
+// sequences go on from others' pages (fork), take pages and give them back (resize).
+//
+// Rows and pages are moved 16 bytes a lane; tables and counts are whole numbers, so
+// results do not depend on the order of the atomics.
+#include <algorithm>
+#include <atomic>
+#include <cooperative_groups.h>
+
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace skl {
+
+namespace {
+
+// ------------------------------------------------------------------ copy
+// Page `dst` of both caches becomes page `src`, for each pair. A block moves
+// kCopyVectors vectors of one pair and cache: every lane has its 8 loads in flight
+// before the first store.
+constexpr int kCopyThreads = 256, kCopyRun = 8, kCopyVectors = kCopyThreads * kCopyRun;
+
+__global__ void __launch_bounds__(kCopyThreads) streamkl_page_copy_kernel(const __grid_constant__ PageCopyArgs a) {
+  const int pair = static_cast<int>(blockIdx.x / a.chunks), chunk = static_cast<int>(blockIdx.x - pair * a.chunks);
+  const int src = __ldg(a.pairs + 2LL * pair), dst = __ldg(a.pairs + 2LL * pair + 1);
+  if ((src < 0 && dst < 0) || src == dst) return;
+  if (src < 0 || dst < 0 || src >= a.num_pages || dst >= a.num_pages) {
+    if (chunk == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    return;
+  }
+  const CacheRows& c = a.cache[blockIdx.y];
+  const uint4* from = static_cast<const uint4*>(c.data) + src * c.sp;
+  uint4* to = static_cast<uint4*>(c.data) + dst * c.sp;
+  const int page = 1 << a.page_shift, total = (a.H << a.page_shift) << a.vshift;
+  uint4 v[kCopyRun];
+  long long at[kCopyRun];
+#pragma unroll
+  for (int i = 0; i < kCopyRun; ++i) {
+    const int e = chunk * kCopyVectors + i * kCopyThreads + static_cast<int>(threadIdx.x);
+    const int row = e >> a.vshift;
+    at[i] = e < total ? (row >> a.page_shift) * c.sh + (row & (page - 1)) * c.ss + (e & ((1 << a.vshift) - 1)) : -1;
+    if (at[i] >= 0) v[i] = from[at[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyRun; ++i)
+    if (at[i] >= 0) to[at[i]] = v[i];
+}
+
+// --------------------------------------------------------------- compact
+// Row kept[i] of a sequence's last n becomes row i of them, i rising, in place. The
+// kept rows rise too, so row i is at most kept[i]: what a batch of rows writes lies
+// before all that later batches read, and within a batch every load comes before
+// the first store. Columns do not meet, so an item is one (sequence, cache, head).
+constexpr int kCompactRun = 8;
+
+struct CompactSeq {
+  int n, first, count;  // last tokens, position of the first of them, kept ones
+  bool ok;
+};
+
+__device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int b) {
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.kv_lens + b);
+  CompactSeq s;
+  s.n = c1 - c0;
+  s.first = len - s.n;
+  s.count = __ldg(a.num_kept + b);
+  s.ok = c0 >= 0 && c1 >= c0 && s.first >= 0 && s.count >= 0 && s.count <= s.n && s.count <= a.max_kept &&
+         len <= (static_cast<long long>(a.max_pages) << a.page_shift);
+  return s;
+}
+
+// THREADS threads an item: a warp each where few rows are kept, else a block.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
+    streamkl_paged_compact_kernel(const __grid_constant__ CompactArgs a) {
+  constexpr bool WARP = THREADS == 32;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const long long item = WARP ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
+  if (item >= 2LL * a.B * a.H) return;
+  auto together = [](bool p) { return WARP ? __all_sync(0xFFFFFFFFu, p) != 0 : __syncthreads_and(p) != 0; };
+  const int b = static_cast<int>(item / (2 * a.H)), rest = static_cast<int>(item - b * 2LL * a.H);
+  const int h = rest >> 1;
+  const CacheRows& c = a.cache[rest & 1];
+  const CompactSeq s = compact_seq(a, b);
+  const int* kept = a.kept + b * a.kept_sb;
+  bool good = s.ok;
+  // the list, before anything moves
+  for (int i = tid; good && i < s.count; i += THREADS) {
+    const int k = __ldg(kept + i);
+    good = k < s.n && k >= (i > 0 ? __ldg(kept + i - 1) + 1 : 0);
+  }
+  if (!together(good)) {
+    if (tid == 0 && rest == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    return;
+  }
+  const int* table = a.table + b * a.table_sb;
+  const int page = 1 << a.page_shift, lane = tid & ((1 << a.vshift) - 1);
+  uint4* data = static_cast<uint4*>(c.data) + h * c.sh + lane;
+  auto place = [&](int i) -> uint4* {  // row i of the last n
+    const int pos = s.first + i;
+    const int p = __ldg(table + (pos >> a.page_shift));
+    if (p < 0 || p >= a.num_pages) {
+      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+      return nullptr;
+    }
+    return data + p * c.sp + (pos & (page - 1)) * c.ss;
+  };
+  const int per = THREADS >> a.vshift;  // rows at once
+  for (int i0 = 0; i0 < s.count; i0 += per * kCompactRun) {
+    uint4 v[kCompactRun];
+    uint4* to[kCompactRun];
+#pragma unroll
+    for (int u = 0; u < kCompactRun; ++u) {
+      const int i = i0 + u * per + (tid >> a.vshift);
+      to[u] = nullptr;
+      if (i < s.count) {
+        const int k = __ldg(kept + i);
+        if (k != i) {
+          const uint4* from = place(k);
+          if (from != nullptr) {
+            v[u] = *from;
+            to[u] = place(i);
+          }
+        }
+      }
+    }
+    if (WARP)
+      __syncwarp();
+    else
+      __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kCompactRun; ++u)
+      if (to[u] != nullptr) *to[u] = v[u];
+  }
+}
+
+// ------------------------------------------------------------------ fork
+// table[b] = table[source[b]] for all b at once. A block takes a slab of columns of
+// every row: all of it is read before any is written, and other slabs do not meet
+// it. A page of the row b is afterwards held by as many rows more as there are
+// sequences that go on from b, less the row b itself: one atomic an entry.
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ int sm[];
+  int *source = sm, *more = sm + a.B, *old = more + a.B;  // old: [B][cols], block 0 first uses it for the lengths
+  for (int b = threadIdx.x; b < a.B; b += kForkThreads) more[b] = -1;
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.B; b += kForkThreads) {
+    int s = __ldg(a.source + b);
+    if (s < 0 || s >= a.B) {
+      if (blockIdx.x == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+      s = b;  // it stays
+    }
+    source[b] = s;
+    atomicAdd(&more[s], 1);
+    if (blockIdx.x == 0) old[b] = a.kv_lens[b];
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < a.B; b += kForkThreads)
+      if (source[b] != b) a.kv_lens[b] = old[source[b]];
+    __syncthreads();
+  }
+  const int j0 = static_cast<int>(blockIdx.x) * a.cols, cols = min(a.cols, a.max_pages - j0);
+  for (int e = threadIdx.x; e < a.B * a.cols; e += kForkThreads) {
+    const int b = e / a.cols, j = e - b * a.cols;
+    if (j >= cols || (source[b] == b && more[b] == 0)) continue;  // nobody takes it, and it stays
+    const int p = a.table[b * a.table_sb + j0 + j];
+    old[e] = p;
+    if (more[b] != 0 && p != -1) {
+      if (p < 0 || p >= a.num_pages)
+        atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+      else
+        atomicAdd(a.refs + p, more[b]);
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.B * a.cols; e += kForkThreads) {
+    const int b = e / a.cols, j = e - b * a.cols;
+    if (j < cols && source[b] != b) a.table[b * a.table_sb + j0 + j] = old[source[b] * a.cols + j];
+  }
+}
+
+// ---------------------------------------------------------------- resize
+// One cluster: what is asked of a sequence hangs on those before it, and which page
+// it gets on all pages before that one, so the whole call is two prefix sums, over
+// the sequences (every block makes them for itself) and over the free pages (the
+// blocks share them, a bit each in registers, and exchange their counts).
+constexpr int kResizeThreads = 1024, kResizeWarps = kResizeThreads / 32;
+constexpr int kBlockPages = kResizeThreads * 32;  // a block's pages of a round
+
+// Exclusive sums of value(b) over b < B into out[0 .. B]; returns the total. All
+// threads; two barriers, and one before the next use of `sums`.
+template <typename F>
+__device__ __forceinline__ int scan_sequences(int B, int* out, int* sums, F&& value) {
+  const int per = (B + kResizeThreads - 1) / kResizeThreads;
+  const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += value(b);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int upto = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+    if (lane >= m) upto += up;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  const int w = sums[lane];  // (32 warps)
+  int before = lane < warp ? w : 0, total = w;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, m);
+    total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+  }
+  int at = before + upto - mine;
+  for (int b = b0; b < b1; ++b) {
+    out[b] = at;
+    at += value(b);
+  }
+  if (threadIdx.x == 0) out[B] = total;
+  __syncthreads();
+  return total;
+}
+
+// The sequence in whose part of the exclusive sums x lies.
+__device__ __forceinline__ int find_sequence(const int* sums, int B, int x) {
+  int lo = 0, hi = B;  // sums[lo] <= x < sums[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kernel(const __grid_constant__ ResizeArgs a) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
+  extern __shared__ int sm[];
+  int* sums = sm;              // [B + 1]
+  int* delta = sums + a.B + 1; // pages more than before
+  int* first = delta + a.B;    // the first entry that comes or goes
+  int* last = first + a.B;     // a last page to be copied; kNone, kKeeps: the last of those that hold it
+  constexpr int kNone = -1, kKeeps = -2;
+  __shared__ int scratch[kResizeWarps];
+  __shared__ int counts[2][8];  // free pages of the blocks, by the round's parity
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int page = 1 << a.page_shift;
+  const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
+  auto lengths = [&](int b, int& from, int& to) {
+    from = a.kv_lens[b];
+    to = __ldg(a.new_lens + b);
+    return from >= 0 && from <= most && to >= 0 && to <= most;
+  };
+  for (int b = tid; b < a.B; b += kResizeThreads) {
+    int from, to;
+    delta[b] = first[b] = 0;
+    last[b] = kNone;
+    if (lengths(b, from, to)) {
+      const int have = (from + page - 1) >> a.page_shift, need = (to + page - 1) >> a.page_shift;
+      delta[b] = need - have;
+      first[b] = min(have, need);
+    } else if (me == 0) {
+      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    }
+  }
+  __syncthreads();
+  // ---- what is given back
+  const int back = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, -delta[b]); });
+  for (int i = me * kResizeThreads + tid; i < back; i += blocks * kResizeThreads) {
+    const int b = find_sequence(sums, a.B, i);
+    int* entry = a.table + b * a.table_sb + first[b] + (i - sums[b]);
+    const int p = *entry;
+    *entry = -1;
+    if (p >= 0 && p < a.num_pages)
+      atomicSub(a.refs + p, 1);
+    else
+      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+  }
+  __threadfence();
+  cluster.sync();
+  // ---- last pages that others hold too
+  bool any = false;
+  for (int b = tid; b < a.B; b += kResizeThreads) {
+    int from, to;
+    if (!lengths(b, from, to) || to <= from || (from & (page - 1)) == 0) continue;
+    const int p = __ldcg(a.table + b * a.table_sb + (from >> a.page_shift));
+    if (p < 0 || p >= a.num_pages) {
+      if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    } else if (__ldcg(a.refs + p) > 1) {
+      last[b] = p;
+      any = true;
+    }
+  }
+  if (__syncthreads_or(any)) {
+    // in their order, each takes a copy while another holds the page
+    for (int b0 = 0; b0 < a.B; b0 += kResizeThreads) {  // (from the back, so that those before are as they were)
+      const int b = a.B - 1 - b0 - tid;
+      bool keeps = false;
+      if (b >= 0 && last[b] >= 0) {
+        int before = 0;
+        for (int i = 0; i < b; ++i) before += last[i] == last[b];
+        keeps = __ldcg(a.refs + last[b]) - before <= 1;
+      }
+      __syncthreads();
+      if (keeps) last[b] = kKeeps;
+    }
+    __syncthreads();
+  }
+  const int asked = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, delta[b]) + (last[b] >= 0); });
+  // ---- free pages, lowest numbers first
+  uint32_t free_bits = 0;  // bit 4 i + e: page base + 128 i + 4 lane + e of this warp's 1,024
+  auto look = [&](int round) {
+    const long long base = (static_cast<long long>(round) * blocks + me) * kBlockPages + warp * 1024 + lane * 4;
+    int4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long p = base + 128 * i;
+      v[i] = make_int4(1, 1, 1, 1);
+      if (p + 4 <= a.num_pages)
+        v[i] = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
+      else if (p < a.num_pages) {
+        v[i].x = __ldcg(a.refs + p);
+        if (p + 1 < a.num_pages) v[i].y = __ldcg(a.refs + p + 1);
+        if (p + 2 < a.num_pages) v[i].z = __ldcg(a.refs + p + 2);
+      }
+    }
+    free_bits = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      free_bits |= static_cast<uint32_t>((v[i].x == 0) | (v[i].y == 0) << 1 | (v[i].z == 0) << 2 | (v[i].w == 0) << 3)
+                   << (4 * i);
+  };
+  // this round's free pages: before this warp's, in all
+  auto count = [&](int round, int& before, int& total) {
+    const int mine = __reduce_add_sync(0xFFFFFFFFu, __popc(free_bits));
+    if (lane == 0) scratch[warp] = mine;
+    __syncthreads();
+    const int w = scratch[lane];
+    before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
+    const int block = __reduce_add_sync(0xFFFFFFFFu, w);
+    if (tid < blocks) *cluster.map_shared_rank(&counts[round & 1][me], tid) = block;
+    cluster.sync();  // (and `scratch` may be used again)
+    total = 0;
+    for (int i = 0; i < blocks; ++i) {
+      if (i < me) before += counts[round & 1][i];
+      total += counts[round & 1][i];
+    }
+  };
+  const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
+                                      (static_cast<long long>(blocks) * kBlockPages));
+  int found = 0, before = 0, total = 0;
+  int round = 0;
+  for (; round < rounds && found < asked; ++round) {
+    look(round);
+    count(round, before, total);
+    found += total;
+  }
+  // ---- who is served: all that is asked up to a sequence has to be there
+  auto wants = [&](int b) { return sums[b + 1] > sums[b] || last[b] == kKeeps; };
+  auto served = [&](int b) { return !wants(b) || sums[b + 1] <= found; };
+  int limit = asked;
+  if (found < asked) {  // (the sums do not fall: the largest that is there)
+    int lo = 0, hi = a.B;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sums[mid] <= found)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    limit = sums[lo];
+  }
+  // ---- pages to their places
+  auto assign = [&](int p, int slot) {
+    const int b = find_sequence(sums, a.B, slot);
+    int* entry = a.table + b * a.table_sb + first[b] + (slot - sums[b]);
+    a.refs[p] = 1;
+    if (last[b] >= 0) {
+      --entry;  // the copy comes first, in the last page's place
+      if (slot == sums[b]) {
+        a.copies[b] = make_int2(last[b], p);
+        atomicSub(a.refs + last[b], 1);
+      }
+    }
+    *entry = p;
+  };
+  const bool kept = round == 1;  // the only round's bits are still there
+  int base = 0;
+  for (int r = 0; r < round && base < limit; ++r) {
+    if (!kept) {
+      look(r);
+      count(round + r, before, total);
+    }
+    int at = base + before;  // rank of this warp's first free page
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t mine = free_bits >> (4 * i) & 15;
+      int below = 0, all = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, mine >> e & 1);
+        below += __popc(lanes & ((1u << lane) - 1));
+        all += __popc(lanes);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(mine >> e & 1)) continue;
+        const int slot = at + below + __popc(mine & ((1u << e) - 1));
+        if (slot < limit) assign((r * blocks + me) * kBlockPages + warp * 1024 + 128 * i + 4 * lane + e, slot);
+      }
+      at += all;
+    }
+    base += total;
+  }
+  // ---- lengths (which every block has read by then, as it has the others' counts)
+  cluster.sync();
+  if (me == 0) {
+    for (int b = tid; b < a.B; b += kResizeThreads) {
+      int from, to;
+      const bool good = lengths(b, from, to), is_served = served(b);
+      if (!good || last[b] < 0 || !is_served) a.copies[b] = make_int2(-1, -1);
+      if (good && is_served) a.kv_lens[b] = to;
+      if (!is_served) atomicCAS(a.dev_status, 0, kStatusNoPages);
+    }
+  }
+}
+
+int resize_shared(int B) { return (4 * B + 1) * static_cast<int>(sizeof(int)); }
+
+template <typename K>
+cudaError_t allow_shared(K kern, std::atomic<unsigned long long>& done, int bytes) {  // once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_page_copy(PageCopyArgs& a, cudaStream_t stream) {
+  const long long vectors = (static_cast<long long>(a.H) << a.page_shift) << a.vshift;
+  a.chunks = static_cast<int>((vectors + kCopyVectors - 1) / kCopyVectors);
+  const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.n) * a.chunks), 2);
+  streamkl_page_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
+  const long long items = 2LL * a.B * a.H;
+  // a warp moves 16 rows of 256 bytes at once; longer lists get a block
+  if (a.max_kept <= 2 * kCompactRun * (32 >> a.vshift))
+    streamkl_paged_compact_kernel<32><<<static_cast<unsigned>((items + 3) / 4), 128, 0, stream>>>(a);
+  else
+    streamkl_paged_compact_kernel<512><<<static_cast<unsigned>(items), 512, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  constexpr int kMost = (kMaxTableRows * 6) * static_cast<int>(sizeof(int));
+  cudaError_t e = allow_shared(streamkl_paged_fork_kernel, done, kMost);
+  if (e != cudaSuccess) return e;
+  // 32 columns (a line of each row), fewer for more blocks or where the slab would not fit
+  a.cols = 32;
+  while (a.cols > 4 && (a.max_pages < a.cols * 2 * sms || a.B * (a.cols + 2) > kMaxTableRows * 6)) a.cols >>= 1;
+  const int bytes = a.B * (a.cols + 2) * static_cast<int>(sizeof(int));
+  streamkl_paged_fork_kernel<<<(a.max_pages + a.cols - 1) / a.cols, kForkThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_shared(streamkl_paged_resize_kernel, done, resize_shared(kMaxTableRows));
+  if (e != cudaSuccess) return e;
+  int blocks = 1;
+  while (blocks < 8 && static_cast<long long>(blocks) * kBlockPages < a.num_pages) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kResizeThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, streamkl_paged_resize_kernel, a);
+}
+
+}  // namespace skl

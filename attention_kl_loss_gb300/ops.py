@@ -5,7 +5,11 @@ projection to the layout that ``streamkl_fwd`` reads (norm and rotation of
 every head in one pass, grouped key heads repeated on request) and the KL's
 gradients back. ``streamkl_paged_append`` puts a trained student's new keys
 and values into a paged cache, ``streamkl_paged_attn`` is the attention of new
-tokens (one, or a chunk) over it. As in ``binding``: argument marshalling only,
+tokens (one, or a chunk) over it, ``streamkl_paged_tree_attn`` that of a tree of
+drafted ones. ``streamkl_paged_compact`` keeps the accepted of these,
+``streamkl_paged_resize`` gives sequences pages and takes them back,
+``streamkl_paged_fork`` lets sequences share them and ``streamkl_paged_copy``
+copies them. As in ``binding``: argument marshalling only,
 PyTorch provides device memory and the current stream.
 
 Each call tries ``csrc/marshal.cpp`` first, which takes ordinary arguments in a
@@ -34,6 +38,11 @@ _ROWS = "Pqqq"
 _ROPE = struct.Struct("N" + 6 * _ROWS + "PPPqPqPPPPPNP11if")
 _APPEND = struct.Struct("N" + 4 * _ROWS + "PqPPPPPP11if")
 _ATTN = struct.Struct("N" + 4 * _ROWS + "PqPPPPNP13if")
+_TREE = struct.Struct("N" + _ATTN.format + "Pqi0q")  # (0q: padded to 8 bytes)
+_COMPACT = struct.Struct("N" + 2 * _ROWS + "PqPPPqPP8i0q")
+_COPY = struct.Struct("N" + 2 * _ROWS + "PP6i0q")
+_FORK = struct.Struct("NPPqPPP3i0q")
+_RESIZE = struct.Struct("NPPqPPPP4i0q")
 
 
 def _pack(fields, *values):
@@ -403,37 +412,25 @@ def streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len
     return int(load().streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits))
 
 
-def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None,
-                        max_seqlen_q: Optional[int] = None, max_kv_len: Optional[int] = None,
-                        scale: Optional[float] = None, causal: bool = True, num_splits: int = 0, out=None,
-                        workspace=None, dev_status=None, stream=None):
-    """Attention of new tokens over a paged cache: (out [total, H, d], lse
-    fp32 [total, H]).
-
-    q [total, H, d]: the new tokens of B sequences (cu_seqlens int32 [B + 1];
-    None: one token a sequence), the last ones of kv_lens int32 [B] keys, which
-    lie in the caches as ``streamkl_paged_append`` puts them (append first).
-    H is a multiple of the caches' heads. max_seqlen_q, max_kv_len: bounds of
-    the sequences' new tokens and lengths (default: every token, every page of
-    block_table); close ones give a better grid. Rows that see no key get
-    zeros and -inf; rows behind the last sequence stay as they were."""
-    if out is None and stream is None and (native := load().native) is not None:
-        done = native.attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
-                           num_splits, workspace, dev_status)
-        if done is not None:
-            return done
-    index, dtype = k_cache.get_device(), k_cache.dtype
-    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
-        return _elsewhere(streamkl_paged_attn, k_cache.device, stream, dict(
-            q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
-            max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, causal=causal, num_splits=num_splits,
-            out=out, workspace=workspace, dev_status=dev_status))
+def _attn(tree_mask, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
+          num_splits, out, workspace, dev_status, index):
+    """The attention over the cache, of drafted tokens where there is a mask."""
+    dtype = k_cache.dtype
     q0, q1, _ = _rows("q", q, 3, dtype, index)
     total, HQ, d = shape = q.shape
     HK, dim, pages, B, offsets, cache = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, total, dtype, index)
     if dim != d or HK < 1 or HQ % HK:
         raise ValueError(f"q [total, H, d] needs d = {dim} and H a multiple of {HK}, got {list(shape)}")
-    max_q = (total if offsets else 1) if max_seqlen_q is None else max_seqlen_q
+    if tree_mask is not None:
+        m0, _ = _rows("tree_mask", tree_mask, 2, torch.int32, index)
+        if tree_mask.shape[0] != total or tree_mask.shape[1] < 1:
+            raise ValueError(f"tree_mask must be [{total}, words], got {list(tree_mask.shape)}")
+        mask = tree_mask.data_ptr(), m0, tree_mask.shape[1]
+    max_q = max_seqlen_q
+    if max_q is None:
+        max_q = total if offsets else 1
+        if tree_mask is not None:
+            max_q = min(max_q, 32 * tree_mask.shape[1])
     max_kv = pages[0] * pages[2] if max_kv_len is None else max_kv_len
     dev = q.device
     o, lse = (None, None) if out is None else out
@@ -453,21 +450,233 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
     if total == 0 or HQ == 0:
         return o, lse
     lib = load()
+    name = "streamkl_paged_attn" if tree_mask is None else "streamkl_paged_tree_attn"
+    size_of = getattr(lib, name + "_workspace_size")
     if workspace is None:
-        need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+        need = size_of(B, total, HQ, HK, d, max_q, max_kv, num_splits)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    args = _pack(_ATTN, q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(),
-                      workspace.data_ptr(), workspace.nbytes, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q,
-                      max_kv, bool(causal), num_splits, 1.0 / math.sqrt(d) if scale is None else scale)
-    st = lib.streamkl_paged_attn(args, _raw_stream(index))
+    fields = (q.data_ptr(), 0, q0, q1, o.data_ptr(), 0, o0, o1, *cache, lse.data_ptr(), workspace.data_ptr(),
+              workspace.nbytes, status, _DTYPES[dtype], B, total, HQ, HK, d, *pages, max_q, max_kv, causal, num_splits,
+              1.0 / math.sqrt(d) if scale is None else scale)
+    args = _pack(_ATTN, *fields) if tree_mask is None else _pack(_TREE, _ATTN.size, *fields, *mask)
+    st = getattr(lib, name)(args, _raw_stream(index))
     if st:
         try:
-            _check(st, "streamkl_paged_attn")
+            _check(st, name)
         except StreamKLError as error:
-            need = lib.streamkl_paged_attn_workspace_size(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+            need = size_of(B, total, HQ, HK, d, max_q, max_kv, num_splits)
             if workspace.nbytes < need:
                 raise ValueError(f"workspace too small: need {need} bytes") from error
             raise
     return o, lse
+
+
+def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None,
+                        max_seqlen_q: Optional[int] = None, max_kv_len: Optional[int] = None,
+                        scale: Optional[float] = None, causal: bool = True, num_splits: int = 0, out=None,
+                        workspace=None, dev_status=None, stream=None):
+    """Attention of new tokens over a paged cache: (out [total, H, d], lse
+    fp32 [total, H]).
+
+    q [total, H, d]: the new tokens of B sequences (cu_seqlens int32 [B + 1];
+    None: one token a sequence), the last ones of kv_lens int32 [B] keys, which
+    lie in the caches as ``streamkl_paged_append`` puts them (append first).
+    H is a multiple of the caches' heads. max_seqlen_q, max_kv_len: bounds of
+    the sequences' new tokens and lengths (default: every token, every page of
+    block_table); close ones give a better grid. Rows that see no key get
+    zeros and -inf; rows behind the last sequence stay as they were."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
+                           num_splits, workspace, dev_status)
+        if done is not None:
+            return done
+    index = k_cache.get_device()
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_attn, k_cache.device, stream, dict(
+            q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
+            max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, causal=causal, num_splits=num_splits,
+            out=out, workspace=workspace, dev_status=dev_status))
+    return _attn(None, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale,
+                 bool(causal), num_splits, out, workspace, dev_status, index)
+
+
+def streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits=0) -> int:
+    return int(load().streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits))
+
+
+def streamkl_paged_tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens=None,
+                             max_seqlen_q: Optional[int] = None, max_kv_len: Optional[int] = None,
+                             scale: Optional[float] = None, num_splits: int = 0, out=None, workspace=None,
+                             dev_status=None, stream=None):
+    """Attention of drafted tokens over a paged cache: (out [total, H, d], lse
+    fp32 [total, H]).
+
+    As ``streamkl_paged_attn``, but the new tokens of a sequence are a tree of
+    guesses (append them first; their rotation goes by depth, not by place): each
+    sees all keys before the drafted ones, and of these those that its row of
+    tree_mask names: int32 [total, words], bit t % 32 of word t // 32 for its
+    sequence's drafted token t (itself and its ancestors, or any others).
+    max_seqlen_q is at most 32 * words (and that, or every token, by default)."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len,
+                                scale, num_splits, workspace, dev_status)
+        if done is not None:
+            return done
+    index = k_cache.get_device()
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_tree_attn, k_cache.device, stream, dict(
+            q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, tree_mask=tree_mask,
+            cu_seqlens=cu_seqlens, max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, num_splits=num_splits,
+            out=out, workspace=workspace, dev_status=dev_status))
+    if tree_mask is None:
+        raise ValueError("tree_mask must be given")
+    return _attn(tree_mask, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, False,
+                 num_splits, out, workspace, dev_status, index)
+
+
+def streamkl_paged_compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status=None,
+                           stream=None):
+    """Keep some of the last tokens of each sequence, in place.
+
+    cu_seqlens int32 [B + 1]: how many last tokens of kv_lens int32 [B] are in
+    question (as ``streamkl_paged_append`` put them, say). Of these, token
+    kept[b, i] moves to the place of token i, for i < num_kept[b]; kept int32
+    [B, most], rising in each row, num_kept int32 [B]. Lengths are left to
+    ``streamkl_paged_resize``. Returns the caches."""
+    if stream is None and (native := load().native) is not None:
+        if native.compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status):
+            return k_cache, v_cache
+    index, dtype = k_cache.get_device(), k_cache.dtype
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_compact, k_cache.device, stream, dict(
+            k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens, kept=kept,
+            num_kept=num_kept, dev_status=dev_status))
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens must be given")
+    HK, d, pages, B, _, cache = _cache(k_cache, v_cache, block_table, kv_lens, cu_seqlens, 0, dtype, index)
+    k0, _ = _rows("kept", kept, 2, torch.int32, index)
+    if kept.shape[0] != B or num_kept is None:
+        raise ValueError(f"kept must be [{B}, most] and num_kept [{B}]")
+    count = _vector("num_kept", num_kept, B, torch.int32, index)
+    status, _keep = _status(dev_status, index)
+    if B == 0 or HK == 0 or kept.shape[1] == 0:
+        return k_cache, v_cache
+    args = _pack(_COMPACT, *cache, kept.data_ptr(), k0, count, status, _DTYPES[dtype], B, HK, d, *pages, kept.shape[1])
+    st = load().streamkl_paged_compact(args, _raw_stream(index))
+    if st:
+        _check(st, "streamkl_paged_compact")
+    return k_cache, v_cache
+
+
+def streamkl_paged_copy(k_cache, v_cache, pairs, dev_status=None, stream=None):
+    """Copy pages of both caches [pages, HK, page size, d]: pairs int32 [n, 2] of
+    (source, destination); a pair of negative numbers copies nothing. No page may
+    be the destination of two pairs, or of one and the source of another. What
+    ``streamkl_paged_resize`` returns, once for each layer. Returns the caches."""
+    if stream is None and (native := load().native) is not None:
+        if native.copy(k_cache, v_cache, pairs, dev_status):
+            return k_cache, v_cache
+    index, dtype = k_cache.get_device(), k_cache.dtype
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_copy, k_cache.device, stream, dict(
+            k_cache=k_cache, v_cache=v_cache, pairs=pairs, dev_status=dev_status))
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"unsupported cache type {dtype} (bf16, fp16)")
+    k0, k1, k2, _ = _rows("k_cache", k_cache, 4, dtype, index)
+    v0, v1, v2, _ = _rows("v_cache", v_cache, 4, dtype, index)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [pages, heads, page size, d]")
+    _rows("pairs", pairs, 2, torch.int32, index)
+    if pairs.shape[1] != 2 or not pairs.is_contiguous():
+        raise ValueError(f"pairs must be contiguous [n, 2], got {list(pairs.shape)}")
+    num_pages, HK, page, d = k_cache.shape
+    status, _keep = _status(dev_status, index)
+    if pairs.shape[0] == 0 or HK == 0:
+        return k_cache, v_cache
+    args = _pack(_COPY, k_cache.data_ptr(), k0, k1, k2, v_cache.data_ptr(), v0, v1, v2, pairs.data_ptr(), status,
+                 _DTYPES[dtype], pairs.shape[0], HK, d, page, num_pages)
+    st = load().streamkl_paged_copy(args, _raw_stream(index))
+    if st:
+        _check(st, "streamkl_paged_copy")
+    return k_cache, v_cache
+
+
+def _held(page_refs, block_table, kv_lens, index):
+    """Checks of pages' counts and the tables that hold them: (B, the C
+    struct's fields up to kv_lens, pages, entries of a sequence)."""
+    if not isinstance(page_refs, torch.Tensor) or page_refs.dim() != 1:
+        raise ValueError("page_refs must be int32 [pages]")
+    refs = _vector("page_refs", page_refs, page_refs.shape[0], torch.int32, index)
+    t0, _ = _rows("block_table", block_table, 2, torch.int32, index)
+    B, width = block_table.shape
+    if kv_lens is None:
+        raise ValueError("kv_lens must be given")
+    return B, (refs, block_table.data_ptr(), t0, _vector("kv_lens", kv_lens, B, torch.int32, index)), page_refs.shape[0], width
+
+
+def streamkl_paged_fork(page_refs, block_table, kv_lens, source, dev_status=None, stream=None):
+    """Every sequence b goes on from source[b] (int32 [B]; its own number: it
+    stays), all at once and in place: entries, length, and in page_refs int32
+    [pages] how many entries hold each page. No page is copied:
+    ``streamkl_paged_resize`` says which have to be. block_table int32 [B, width]
+    with -1 where an entry holds no page, kv_lens int32 [B]. Returns page_refs,
+    block_table and kv_lens."""
+    if stream is None and (native := load().native) is not None:
+        if native.fork(page_refs, block_table, kv_lens, source, dev_status):
+            return page_refs, block_table, kv_lens
+    index = block_table.get_device()
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_fork, block_table.device, stream, dict(
+            page_refs=page_refs, block_table=block_table, kv_lens=kv_lens, source=source, dev_status=dev_status))
+    B, tables, pages, width = _held(page_refs, block_table, kv_lens, index)
+    if source is None:
+        raise ValueError("source must be given")
+    at = _vector("source", source, B, torch.int32, index)
+    status, _keep = _status(dev_status, index)
+    if B == 0:
+        return page_refs, block_table, kv_lens
+    st = load().streamkl_paged_fork(_pack(_FORK, *tables, at, status, B, pages, width), _raw_stream(index))
+    if st:
+        _check(st, "streamkl_paged_fork")
+    return page_refs, block_table, kv_lens
+
+
+def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: int, out=None, dev_status=None,
+                          stream=None):
+    """Sequences get the pages of new_lens int32 [B] tokens, or give back those
+    behind them, in place (page_refs, block_table, kv_lens as for
+    ``streamkl_paged_fork``; begin with zeros, -1 and zeros).
+
+    The free pages (page_refs 0) of the lowest numbers go out in the order of the
+    sequences. A longer sequence whose last page is partly filled and held by
+    others too gets one in its place: the call returns int32 [B, 2], (old, new) or
+    (-1, -1), for ``streamkl_paged_copy`` to copy in every layer. Where pages do
+    not suffice, sequences keep their lengths (that of the first one, and of all
+    after it that ask for pages), and dev_status is STREAMKL_ERR_NO_PAGES."""
+    if out is None and stream is None and (native := load().native) is not None:
+        done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
+        if done is not None:
+            return done
+    index = block_table.get_device()
+    if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
+        return _elsewhere(streamkl_paged_resize, block_table.device, stream, dict(
+            page_refs=page_refs, block_table=block_table, kv_lens=kv_lens, new_lens=new_lens, page_size=page_size, out=out,
+            dev_status=dev_status))
+    B, tables, pages, width = _held(page_refs, block_table, kv_lens, index)
+    if new_lens is None:
+        raise ValueError("new_lens must be given")
+    at = _vector("new_lens", new_lens, B, torch.int32, index)
+    if out is None:
+        out = torch.empty((B, 2), dtype=torch.int32, device=block_table.device)
+    elif out.shape != (B, 2) or out.dtype is not torch.int32 or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous int32 [{B}, 2] on cuda:{index}")
+    status, _keep = _status(dev_status, index)
+    if B == 0:
+        return out
+    args = _pack(_RESIZE, *tables, at, out.data_ptr(), status, B, pages, width, page_size)
+    st = load().streamkl_paged_resize(args, _raw_stream(index))
+    if st:
+        _check(st, "streamkl_paged_resize")
+    return out

@@ -53,7 +53,10 @@ typedef enum {
    * TMA copy, TMEM access or mbarrier outside its layout, skipped that access
    * and stopped (the first failing source line is printed from the device).
    * The release build never writes it. */
-  STREAMKL_ERR_DEVICE_CHECK = 5
+  STREAMKL_ERR_DEVICE_CHECK = 5,
+  /* Written to dev_status by streamkl_paged_resize: free pages did not suffice
+   * for every sequence (those that got none keep their lengths). */
+  STREAMKL_ERR_NO_PAGES = 6
 } streamkl_status;
 
 /* Human-readable name of a status code (static string). */
@@ -481,6 +484,124 @@ int streamkl_paged_attn_splits(int B, int T, int HQ, int HK, int d, int max_seql
 size_t streamkl_paged_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
                                           int num_splits);
 streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* stream);
+
+/*
+ * Attention of drafted tokens: as streamkl_paged_attn, but the n new tokens of a
+ * sequence are a tree (or any set) of guesses, and a row sees all keys before
+ * them (j < length - n) and those of them whose bit its mask has: bit t % 32 of
+ * word t / 32 for the sequence's drafted token t, its own and its ancestors' in a
+ * tree. Bits from n on say nothing. A row that sees no key gets zeros and -inf.
+ * With fewer keys than drafted tokens the first of these have no key.
+ *   attn: the arguments of streamkl_paged_attn, struct_size and all; causal must
+ *   be 0. mask: device words [T, mask_words], rows mask_stride words apart, for
+ *   the tokens in q's order; max_seqlen_q is at most 32 mask_words.
+ *   workspace as there, of streamkl_paged_tree_attn_workspace_size(...) bytes.
+ */
+typedef struct {
+  size_t struct_size;
+  streamkl_paged_attn_args attn;
+  const int* mask;
+  long long mask_stride;
+  int mask_words;
+} streamkl_paged_tree_attn_args;
+
+size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
+                                               int num_splits);
+streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* args, void* stream);
+
+/*
+ * Keep some of the last tokens of each sequence: of its n = cu_seqlens[b + 1] -
+ * cu_seqlens[b] last ones, token kept[b][i] (of 0 .. n - 1) moves to the place of
+ * token i, for i < num_kept[b], in both caches and in place. kept[b] rises; places
+ * from num_kept[b] on are left as they are. The lengths are not changed, so that a
+ * call for each layer can follow (streamkl_paged_resize then gives the rest back).
+ * Pages that other sequences hold change for these too. A list that does not rise
+ * or leaves 0 .. n - 1 and numbers that do not fit are reported, and that sequence
+ * is left as it was; a row whose page number is none is reported and not moved.
+ */
+typedef struct {
+  size_t struct_size;
+  streamkl_rows k_cache, v_cache; /* strides: page, head, slot */
+  const int* block_table;
+  long long table_stride;
+  const int *kv_lens, *cu_seqlens; /* lengths with these tokens; [B + 1] */
+  const int* kept;                 /* device [B, max_kept], rows kept_stride apart */
+  long long kept_stride;
+  const int* num_kept; /* device [B] */
+  int* dev_status;
+  int dtype, B, HK, d, page_size, num_pages, max_pages, max_kept;
+} streamkl_compact_args;
+
+streamkl_status streamkl_paged_compact(const streamkl_compact_args* args, void* stream);
+
+/*
+ * Copy pages of both caches: pairs [n, 2] of (source, destination), device,
+ * 8-byte aligned. A pair of negative numbers copies nothing. No page may be the
+ * destination of two pairs, or of one and the source of another. A pair with one
+ * number that is no page is reported and not copied.
+ */
+typedef struct {
+  size_t struct_size;
+  streamkl_rows k_cache, v_cache; /* strides: page, head, slot */
+  const int* pairs;
+  int* dev_status;
+  int dtype, n, HK, d, page_size, num_pages;
+} streamkl_page_copy_args;
+
+streamkl_status streamkl_paged_copy(const streamkl_page_copy_args* args, void* stream);
+
+/*
+ * Sequences that share pages. page_refs[p] is the number of entries of
+ * block_table [B, max_pages] that hold page p (0: free); entries that hold none
+ * are -1, and a sequence's pages are its first ceil(length / page_size) entries.
+ * The two calls below keep that so; a table is filled by streamkl_paged_resize
+ * from lengths of 0, counts of 0 and entries of -1. Both change their arguments
+ * in place; a call that sets STREAMKL_ERR_INVALID_ARG has found numbers that do
+ * not fit, left those out and done the rest. B is at most 8192.
+ *
+ * streamkl_paged_fork: every sequence b becomes a copy of what source[b] was, for
+ * all b at once (source[b] = b: it stays): entries, length and the pages' counts.
+ */
+typedef struct {
+  size_t struct_size;
+  int* page_refs;   /* device [num_pages] */
+  int* block_table; /* device [B, max_pages], rows table_stride apart */
+  long long table_stride;
+  int* kv_lens;      /* device [B] */
+  const int* source; /* device [B]; a number that is no sequence is reported, that sequence stays */
+  int* dev_status;
+  int B, num_pages, max_pages;
+} streamkl_fork_args;
+
+streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream);
+
+/*
+ * streamkl_paged_resize: lengths become new_lens. A shorter sequence gives the
+ * pages past its new end back. Then, in the order of the sequences, a longer one
+ * gets the free pages of the lowest numbers: first, where its last page is partly
+ * filled and others hold it too, one in that page's place (the last of those that
+ * grow in one call keeps it if no other is left), then those that it lacks.
+ *   copies [B, 2]: (old, new) of the page so replaced, whose slots
+ *   streamkl_paged_copy has to copy in every layer before new tokens are written;
+ *   (-1, -1) for the others.
+ * Where free pages do not suffice, a sequence is served if all that is asked up to
+ * and with it is there, or it asks for none (and grows into no shared page); the
+ * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set.
+ * page_refs and copies are 16 and 8-byte aligned; B * max_pages is at most 2^30.
+ */
+typedef struct {
+  size_t struct_size;
+  int* page_refs;
+  int* block_table;
+  long long table_stride;
+  int* kv_lens;
+  const int* new_lens; /* device [B], 0 .. max_pages * page_size */
+  int* copies;
+  int* dev_status;
+  int B, num_pages, max_pages, page_size;
+} streamkl_resize_args;
+
+streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* stream);
 
 /*
  * Self-test of the bounded-wait path: launches one tiny kernel that waits on
