@@ -80,7 +80,7 @@ _SIGNATURES = {
     "streamkl_paged_attn_splits": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_attn": (_I, [_P, _P]),
-    "streamkl_paged_tree_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "streamkl_paged_tree_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "streamkl_paged_tree_attn": (_I, [_P, _P]),
     "streamkl_paged_compact": (_I, [_P, _P]),
     "streamkl_paged_copy": (_I, [_P, _P]),

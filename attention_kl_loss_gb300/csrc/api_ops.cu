@@ -183,7 +183,7 @@ streamkl_status check_cache(streamkl_rows* kc, streamkl_rows* vc, const int* tab
 // `splits` ranges of split_tiles 128-key tiles (counted from a sequence's
 // start, so a short one uses fewer ranges).
 struct AttnPlan {
-  int decode_ctas;  // 0: not the persistent kernel
+  int decode_ctas;  // 0: not a persistent kernel
   bool whole;       // there: each CTA takes whole (sequence, key head) pairs
   int row_tiles, q_tiles, splits, split_tiles;
 };
@@ -240,9 +240,23 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
   return p;
 }
 
+// Of drafted tokens: few rows as above, more on one persistent CTA an SM.
+AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
+  const long long rows = static_cast<long long>(max_q) * (HQ / HK);
+  if (rows <= skl::kDecodeRows) return attn_plan(B, B, HQ, HK, d, max_q, max_kv, 0);
+  AttnPlan p{};
+  p.row_tiles = rows > 128 ? 2 : 1;
+  const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
+  const long long tiles = std::max(1, (max_kv + 127) / 128);
+  p.split_tiles = 2;
+  p.decode_ctas = static_cast<int>(std::min<long long>(B * HK * blocks * tiles, num_sms()));
+  return p;
+}
+
 // Rows of the partial results.
 size_t attn_part_rows(const AttnPlan& p, int T, int HQ) {
   if (p.whole) return 0;
+  if (p.decode_ctas > 0 && p.row_tiles > 0) return static_cast<size_t>(2) * p.decode_ctas * 128 * p.row_tiles;
   if (p.decode_ctas > 0) return static_cast<size_t>(2) * p.decode_ctas * skl::kDecodeRows;
   return p.splits > 1 ? static_cast<size_t>(p.splits) * T * HQ : 0;
 }
@@ -303,7 +317,8 @@ streamkl_status attn_call(streamkl_paged_attn_args& u, const streamkl_paged_tree
   if (!(u.scale > 0.f) || !std::isfinite(u.scale))
     return fail(STREAMKL_ERR_INVALID_ARG, "scale must be finite and > 0");
   if (!u.dev_status) return fail(STREAMKL_ERR_INVALID_ARG, "dev_status must be non-NULL");
-  const AttnPlan p = attn_plan(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
+  const AttnPlan p = tree ? tree_plan(u.B, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len)
+                          : attn_plan(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
   if (p.splits > 65535) return fail(STREAMKL_ERR_UNSUPPORTED, "%d key splits (at most 65535)", p.splits);
   const size_t need = attn_part_bytes(p, u.T, u.HQ, u.d);
   if (need && (!u.workspace || u.ws_bytes < need))
@@ -360,7 +375,7 @@ streamkl_status attn_call(streamkl_paged_attn_args& u, const streamkl_paged_tree
   auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (tree != nullptr)
-    e = p.decode_ctas > 0 ? skl::launch_tree_decode(a, p.decode_ctas, s) : skl::launch_tree_attn(a, s);
+    e = p.row_tiles > 0 ? skl::launch_tree(a, p.decode_ctas, s) : skl::launch_tree_decode(a, p.decode_ctas, s);
   else
     e = p.decode_ctas > 0 ? skl::launch_paged_decode(a, p.decode_ctas, s) : skl::launch_paged_attn(a, s);
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "paged attention launch");
@@ -492,9 +507,9 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
   return attn_call(u, nullptr, stream);
 }
 
-size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
-                                               int num_splits) {
-  return streamkl_paged_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits);
+size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len) {
+  if (check_attn_sizes(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) != STREAMKL_OK) return 0;
+  return attn_part_bytes(tree_plan(B, HQ, HK, d, max_seqlen_q, max_kv_len), T, HQ, d);
 }
 
 streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* args, void* stream) {
@@ -502,7 +517,8 @@ streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* ar
   if (!take_args(&t, args)) return STREAMKL_ERR_INVALID_ARG;
   streamkl_paged_attn_args u;
   if (!take_args(&u, &t.attn)) return STREAMKL_ERR_INVALID_ARG;
-  if (u.causal) return fail(STREAMKL_ERR_INVALID_ARG, "causal must be 0: the masks say what a drafted token sees");
+  if (u.causal || u.num_splits)
+    return fail(STREAMKL_ERR_INVALID_ARG, "causal and num_splits must be 0: the masks say what a drafted token sees");
   if (!t.mask || reinterpret_cast<uintptr_t>(t.mask) % 4)
     return fail(STREAMKL_ERR_INVALID_ARG, "mask must be a 4-byte aligned address");
   if (t.mask_words < 1 || t.mask_stride < 0 || u.max_seqlen_q > 32LL * t.mask_words)

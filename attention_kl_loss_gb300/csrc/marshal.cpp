@@ -433,8 +433,7 @@ PyObject* attn_call(Args a, bool tree) {
     u.scale = a.real();
   else
     a.next();
-  if (!tree) u.causal = a.flag();
-  u.num_splits = a.integer();
+  if (!tree) u.causal = a.flag(), u.num_splits = a.integer();
   const at::Tensor *given = a.tensor(true), *status = a.tensor(true);
   const Home home(*kc);
   home.rows(*q, 3);
@@ -464,8 +463,8 @@ PyObject* attn_call(Args a, bool tree) {
     want(given->device() == home.device && given->is_contiguous());
     u.workspace = given->data_ptr(), u.ws_bytes = given->nbytes();
   } else {
-    u.ws_bytes = (tree ? lib.tree_size : lib.attn_size)(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len,
-                                                        u.num_splits);
+    u.ws_bytes = tree ? lib.tree_size(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len)
+                      : lib.attn_size(u.B, u.T, u.HQ, u.HK, u.d, u.max_seqlen_q, u.max_kv_len, u.num_splits);
     u.workspace = (space = home.make({static_cast<int64_t>(u.ws_bytes)}, at::kByte)).data_ptr();
   }
   u.dev_status = home.status(status, &word);
@@ -486,10 +485,10 @@ PyObject* attn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
 }
 
 // tree_attn(entries, q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len, scale,
-//           num_splits, workspace, dev_status)
+//           workspace, dev_status)
 PyObject* tree_attn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n == 14);
+    want(n == 13);
     return attn_call(Args{argv}, true);
   });
 }

@@ -166,9 +166,10 @@ cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t stream);
 constexpr int kDecodeRows = 32;
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
-// The same for rows that see the drafted tokens of their masks.
+// Rows that see the drafted tokens of their masks: launch_paged_decode's kernel,
+// and one for more rows (row_tiles x 128 at once; part_o [2 ctas][128 row_tiles][d]).
 cudaError_t launch_tree_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
-cudaError_t launch_tree_attn(const PagedAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_tree(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 
 cudaError_t launch_page_copy(PageCopyArgs& a, cudaStream_t stream);
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);

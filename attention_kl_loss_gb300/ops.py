@@ -451,9 +451,9 @@ def _attn(tree_mask, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_
         return o, lse
     lib = load()
     name = "streamkl_paged_attn" if tree_mask is None else "streamkl_paged_tree_attn"
-    size_of = getattr(lib, name + "_workspace_size")
+    sizes = (B, total, HQ, HK, d, max_q, max_kv) + ((num_splits,) if tree_mask is None else ())
     if workspace is None:
-        need = size_of(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+        need = getattr(lib, name + "_workspace_size")(*sizes)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -466,7 +466,7 @@ def _attn(tree_mask, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_
         try:
             _check(st, name)
         except StreamKLError as error:
-            need = size_of(B, total, HQ, HK, d, max_q, max_kv, num_splits)
+            need = getattr(lib, name + "_workspace_size")(*sizes)
             if workspace.nbytes < need:
                 raise ValueError(f"workspace too small: need {need} bytes") from error
             raise
@@ -502,14 +502,13 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
                  bool(causal), num_splits, out, workspace, dev_status, index)
 
 
-def streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits=0) -> int:
-    return int(load().streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len, num_splits))
+def streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len) -> int:
+    return int(load().streamkl_paged_tree_attn_workspace_size(B, T, HQ, HK, d, max_seqlen_q, max_kv_len))
 
 
 def streamkl_paged_tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens=None,
                              max_seqlen_q: Optional[int] = None, max_kv_len: Optional[int] = None,
-                             scale: Optional[float] = None, num_splits: int = 0, out=None, workspace=None,
-                             dev_status=None, stream=None):
+                             scale: Optional[float] = None, out=None, workspace=None, dev_status=None, stream=None):
     """Attention of drafted tokens over a paged cache: (out [total, H, d], lse
     fp32 [total, H]).
 
@@ -521,19 +520,19 @@ def streamkl_paged_tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mas
     max_seqlen_q is at most 32 * words (and that, or every token, by default)."""
     if out is None and stream is None and (native := load().native) is not None:
         done = native.tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len,
-                                scale, num_splits, workspace, dev_status)
+                                scale, workspace, dev_status)
         if done is not None:
             return done
     index = k_cache.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_tree_attn, k_cache.device, stream, dict(
             q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, tree_mask=tree_mask,
-            cu_seqlens=cu_seqlens, max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, num_splits=num_splits,
-            out=out, workspace=workspace, dev_status=dev_status))
+            cu_seqlens=cu_seqlens, max_seqlen_q=max_seqlen_q, max_kv_len=max_kv_len, scale=scale, out=out,
+            workspace=workspace, dev_status=dev_status))
     if tree_mask is None:
         raise ValueError("tree_mask must be given")
     return _attn(tree_mask, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, False,
-                 num_splits, out, workspace, dev_status, index)
+                 0, out, workspace, dev_status, index)
 
 
 def streamkl_paged_compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status=None,

@@ -492,8 +492,8 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
  * word t / 32 for the sequence's drafted token t, its own and its ancestors' in a
  * tree. Bits from n on say nothing. A row that sees no key gets zeros and -inf.
  * With fewer keys than drafted tokens the first of these have no key.
- *   attn: the arguments of streamkl_paged_attn, struct_size and all; causal must
- *   be 0. mask: device words [T, mask_words], rows mask_stride words apart, for
+ *   attn: the arguments of streamkl_paged_attn, struct_size and all; causal and
+ *   num_splits must be 0. mask: device words [T, mask_words], rows mask_stride words apart, for
  *   the tokens in q's order; max_seqlen_q is at most 32 mask_words.
  *   workspace as there, of streamkl_paged_tree_attn_workspace_size(...) bytes.
  */
@@ -505,8 +505,7 @@ typedef struct {
   int mask_words;
 } streamkl_paged_tree_attn_args;
 
-size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len,
-                                               int num_splits);
+size_t streamkl_paged_tree_attn_workspace_size(int B, int T, int HQ, int HK, int d, int max_seqlen_q, int max_kv_len);
 streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* args, void* stream);
 
 /*

@@ -77,30 +77,30 @@ def _check(o, lse, q, c, bits, new, lens, scale, dt):
 
 
 TREE = [
-    # new, lens, HQ, HK, d, page, type, masks, splits, layout
-    ([1], [1], 1, 1, 64, 16, "bf16", "tree", 0, "heads"),
-    ([1], [300], 4, 1, 128, 16, "bf16", "none", 0, "heads"),
-    ([8], [2048], 8, 2, 128, 16, "bf16", "tree", 0, "heads"),
-    ([5, 0, 8, 1], [5, 17, 700, 129], 6, 2, 64, 32, "fp16", "any", 0, "slots"),
-    ([7, 3, 8], [7, 3, 8], 4, 1, 128, 64, "bf16", "holes", 0, "slots"),      # no key before the drafted: empty rows
-    ([16, 9], [1000, 128], 8, 2, 128, 16, "fp16", "tree", 0, "heads"),
-    ([33, 20], [700, 20], 3, 1, 128, 16, "bf16", "any", 1, "slots"),
-    ([31, 32, 33], [159, 160, 161], 2, 1, 64, 16, "bf16", "tree", 0, "heads"),  # a tile's border in every place
-    ([64, 1, 40], [300, 2000, 64], 8, 8, 64, 128, "fp16", "tree", 0, "heads"),
-    ([64, 63], [128, 127], 4, 2, 128, 16, "bf16", "holes", 2, "heads"),
-    ([130], [900], 1, 1, 128, 256, "bf16", "tree", 3, "heads"),
-    ([100, 257], [2000, 300], 4, 4, 128, 16, "fp16", "any", 0, "slots"),
-    ([300, 4], [300, 513], 6, 2, 64, 32, "bf16", "tree", 0, "heads"),
-    ([290], [3000], 2, 1, 128, 1024, "bf16", "holes", 0, "slots"),
-    ([12, 30], [5, 0], 4, 2, 128, 16, "bf16", "causal", 0, "heads"),          # fewer keys than drafted tokens
-    ([150], [40], 2, 1, 64, 16, "fp16", "any", 2, "heads"),
-    ([6], [77], 160, 1, 64, 32, "bf16", "tree", 0, "heads"),                  # one token's group wider than a tile
+    # new, lens, HQ, HK, d, page, type, masks, layout
+    ([1], [1], 1, 1, 64, 16, "bf16", "tree", "heads"),
+    ([1], [300], 4, 1, 128, 16, "bf16", "none", "heads"),
+    ([8], [2048], 8, 2, 128, 16, "bf16", "tree", "heads"),
+    ([5, 0, 8, 1], [5, 17, 700, 129], 6, 2, 64, 32, "fp16", "any", "slots"),
+    ([7, 3, 8], [7, 3, 8], 4, 1, 128, 64, "bf16", "holes", "slots"),      # no key before the drafted: empty rows
+    ([16, 9], [1000, 128], 8, 2, 128, 16, "fp16", "tree", "heads"),
+    ([33, 20], [700, 20], 3, 1, 128, 16, "bf16", "any", "slots"),
+    ([31, 32, 33], [159, 160, 161], 2, 1, 64, 16, "bf16", "tree", "heads"),  # a tile's border in every place
+    ([64, 1, 40], [300, 2000, 64], 8, 8, 64, 128, "fp16", "tree", "heads"),
+    ([64, 63], [128, 127], 4, 2, 128, 16, "bf16", "holes", "heads"),
+    ([130], [900], 1, 1, 128, 256, "bf16", "tree", "heads"),
+    ([100, 257], [2000, 300], 4, 4, 128, 16, "fp16", "any", "slots"),
+    ([300, 4], [300, 513], 6, 2, 64, 32, "bf16", "tree", "heads"),
+    ([290], [3000], 2, 1, 128, 1024, "bf16", "holes", "slots"),
+    ([12, 30], [5, 0], 4, 2, 128, 16, "bf16", "causal", "heads"),          # fewer keys than drafted tokens
+    ([150], [40], 2, 1, 64, 16, "fp16", "any", "heads"),
+    ([6], [77], 160, 1, 64, 32, "bf16", "tree", "heads"),                  # one token's group wider than a tile
 ]
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("new,lens,HQ,HK,d,page,dtype,kind,splits,layout", TREE)
-def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, splits, layout):
+@pytest.mark.parametrize("new,lens,HQ,HK,d,page,dtype,kind,layout", TREE)
+def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, layout):
     dt = TYPES[dtype]
     c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
     g = torch.Generator().manual_seed(HQ + d)
@@ -115,7 +115,7 @@ def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, sp
     scale = d ** -0.5
     kw = dict(cu_seqlens=_cu(new), dev_status=st)
     ret = skl.streamkl_paged_tree_attn(q, c.k, c.v, c.table, c.lens, mask, max_seqlen_q=max(new), max_kv_len=max(lens),
-                                       num_splits=splits, out=(o, lse), **kw)
+                                       out=(o, lse), **kw)
     binding.raise_on_device_status(st)
     assert ret[0] is o and ret[1] is lse
     assert torch.all(o[total:] == 3) and torch.all(lse[total:] == 3)  # rows behind the last sequence
@@ -461,10 +461,10 @@ class TreeArgs(ctypes.Structure):
 
 @pytest.mark.parametrize("over,status", CACHE_REFUSED + [
     (dict(HQ=3), 1), (dict(max_seqlen_q=0), 1), (dict(max_seqlen_q=6), 1), (dict(max_kv_len=65), 1), (dict(q__data=4104), 1),
-    (dict(out__data=None), 1), (dict(lse=None), 1), (dict(causal=1), 1), (dict(num_splits=-1), 1), (dict(scale=0.0), 1),
+    (dict(out__data=None), 1), (dict(lse=None), 1), (dict(causal=1), 1), (dict(num_splits=2), 1), (dict(scale=0.0), 1),
     (dict(scale=float("nan")), 1), (dict(out__stride=(0, 128, 64)), 1)])
 def test_tree_c_call_refuses_what_the_attention_does(lib, over, status):
-    base = dict(HQ=4, max_seqlen_q=4, max_kv_len=64, scale=0.1, causal=0, num_splits=1, lse=4096)
+    base = dict(HQ=4, max_seqlen_q=4, max_kv_len=64, scale=0.1, causal=0, num_splits=0, lse=4096)
     attn = _raw(AttnArgs, over, **base)._obj
     t = TreeArgs(ctypes.sizeof(TreeArgs), attn, 4096, 1, 1)
     assert lib.streamkl_paged_tree_attn(ctypes.byref(t), None) == status and lib.streamkl_last_error()
@@ -475,7 +475,7 @@ def test_tree_c_call_refuses_what_the_attention_does(lib, over, status):
 def test_tree_c_call_refuses_masks(lib, over):
     over = dict(over)
     T = over.pop("T", 5)
-    attn = _raw(AttnArgs, dict(T=T), HQ=4, max_seqlen_q=T - 1, max_kv_len=64, scale=0.1, causal=0, num_splits=1, lse=4096)._obj
+    attn = _raw(AttnArgs, dict(T=T), HQ=4, max_seqlen_q=T - 1, max_kv_len=64, scale=0.1, causal=0, num_splits=0, lse=4096)._obj
     t = TreeArgs(ctypes.sizeof(TreeArgs), attn, 4096, 1, 1)
     for n, v in over.items():
         setattr(t, n, v)
