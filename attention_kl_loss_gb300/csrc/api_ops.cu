@@ -249,7 +249,8 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
   const long long tiles = std::max(1, (max_kv + 127) / 128);
   p.split_tiles = 2;
-  p.decode_ctas = static_cast<int>(std::min<long long>(B * HK * blocks * tiles, num_sms()));
+  const int per_sm = d == 64 && p.row_tiles == 1 ? 2 : 1;
+  p.decode_ctas = static_cast<int>(std::min<long long>(B * HK * blocks * tiles, per_sm * num_sms()));
   return p;
 }
 
@@ -262,7 +263,8 @@ size_t attn_part_rows(const AttnPlan& p, int T, int HQ) {
 }
 
 size_t attn_part_bytes(const AttnPlan& p, int T, int HQ, int d) {
-  return (attn_part_rows(p, T, HQ) * (d + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+  const size_t cuts = p.decode_ctas > 0 && p.row_tiles > 0 ? p.decode_ctas * sizeof(skl::TreeCut) : 0;
+  return (attn_part_rows(p, T, HQ) * (d + 1) * sizeof(float) + cuts + 255) & ~static_cast<size_t>(255);
 }
 
 // 4-D map {d, page size, HK, pages} of a cache, 64-column boxes of one page's
@@ -370,6 +372,7 @@ streamkl_status attn_call(streamkl_paged_attn_args& u, const streamkl_paged_tree
   a.by_length = u.B > 1 && u.B <= 32 && static_cast<long long>(p.q_tiles) * u.B * u.HK > num_sms();
   a.part_o = static_cast<float*>(u.workspace);
   a.part_lse = a.part_o ? a.part_o + attn_part_rows(p, u.T, u.HQ) * u.d : nullptr;
+  a.cuts = a.part_o ? reinterpret_cast<skl::TreeCut*>(a.part_lse + attn_part_rows(p, u.T, u.HQ)) : nullptr;
   a.dev_status = u.dev_status;
   a.timeout_ns = wait_timeout_ns();
   auto s = static_cast<cudaStream_t>(stream);

@@ -71,6 +71,13 @@ struct AppendArgs {
   int* dev_status;
 };
 
+// An item of the tree attention that CTAs share, as the first of them writes it down.
+struct TreeCut {
+  int tok0, hk, row0, rows;  // rows 0: none
+  int parts;                 // of consecutive CTAs, this one's first
+  int inside;                // its part lies in the second of this CTA's slots
+};
+
 struct PagedAttnArgs {
   const CUtensorMap* tm_k;
   const CUtensorMap* tm_v;
@@ -97,6 +104,7 @@ struct PagedAttnArgs {
   int whole;                 // few rows: each CTA takes whole (sequence, key head) pairs, no parts
   float* part_o;             // [splits][T][HQ][d]; null without splits
   float* part_lse;           // [splits][T][HQ], log2 units
+  TreeCut* cuts;             // tree: [CTAs]
   int* dev_status;
   uint64_t timeout_ns;
 };

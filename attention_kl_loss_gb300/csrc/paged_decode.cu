@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Join the parts of the items that the CTAs' stretches cut: block c takes the
-// item that starts in CTA c's stretch and goes on in the next, its warps the
-// rows in turn; the parts of a row lie in the slots of consecutive CTAs.
+// item that starts in CTA c's stretch and goes on in the next, its warps (of the
+// blocks (c, ..)) the rows in turn; the parts of a row lie in the slots of consecutive CTAs.
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads)
     streamkl_paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads)
   grid_dependency_wait();
   if (none) return;
   const int G = a.HQ / a.HK, lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < s.n * G; r += kThreads / 32) {
+  for (int r = (blockIdx.y * kThreads + threadIdx.x) >> 5; r < s.n * G; r += gridDim.y * kThreads / 32) {
     // parts whose loads are in flight, the first ones beside the lse's (one token
     // over 4,096 keys, both kernels: 12.2 us, 12.5 with 8, 13.9 with 8 after the lse)
     constexpr int RUN = 16;
@@ -667,7 +667,9 @@ cudaError_t decode_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || a.whole) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  // a warp a row of the trees, which have many; else four
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas),
+                     TREE ? static_cast<unsigned>((a.max_q * (a.HQ / a.HK) + kThreads / 32 - 1) / (kThreads / 32)) : 1);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -35,7 +35,7 @@ namespace {
 constexpr int kTileM = 128;  // rows per tile
 constexpr int kFirst = 96;   // keys of a tile whose P is handed over first (P in S's place)
 constexpr int kSegs = 4;     // items whose numbers are known ahead
-constexpr int kJoinThreads = 128, kJoinRows = 32;
+constexpr int kJoinWarps = 8;  // rows of a block of the join kernel
 
 // A CTA's part of an item: key tiles [t0, t0 + n_iter) of rows from rb * 128 NT on.
 struct Seg {
@@ -49,7 +49,10 @@ struct TreeLayout {
   static constexpr int KB = D / 64;          // 64-column (128-byte) boxes per row
   static constexpr int BOX = kTileN * 128;   // 128 rows of one box
   static constexpr int TILE = kTileN * D * 2;
-  static constexpr int STAGES = D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 10 : 12);
+  // CTAs of an SM: two where shared memory and half of TMEM hold what one needs
+  static constexpr int PER_SM = D == 64 && NT == 1 ? 2 : 1;
+  static constexpr int STAGES = D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 10 : 6);
+  static constexpr int TMEM = 512 / PER_SM;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = NT * TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
@@ -62,11 +65,11 @@ struct TreeLayout {
   static constexpr int OFF_MISC = (OFF_SEG + kSegs * static_cast<int>(sizeof(Seg)) + 15) / 16 * 16;
   static constexpr int THREADS = 128 + 128 * NT;
   static constexpr int BYTES = OFF_MISC + 32 + THREADS / 32 * 8;
-  static_assert(BYTES <= 232448, "shared memory budget");
+  static_assert(PER_SM == 1 ? BYTES <= 232448 : 2 * (BYTES + 1024) <= 233472, "shared memory budget");
   static constexpr int col_s(int t) { return 128 * t; }
   static constexpr int col_p(int t) { return OWN_P ? 128 * NT + 64 * t : 128 * t; }
   static constexpr int col_o(int t) { return (OWN_P ? 192 : 128) * NT + D * t; }
-  static_assert(col_o(NT - 1) + D <= 512, "TMEM columns");
+  static_assert(col_o(NT - 1) + D <= TMEM, "TMEM columns");
 };
 
 // What is known of a sequence.
@@ -90,15 +93,15 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnArgs& a, int b, int rows_
 }
 
 // The whole block finds its way in the line of tiles: each thread sums a run of
-// consecutive sequences, a scan adds them up; the thread in whose run tile
-// place(chunk) lies writes where that is to *at (left alone past the line's end).
+// consecutive sequences, a scan adds them up; the thread in whose run this CTA's
+// first tile lies writes where that is to *at (left alone past the line's end).
 // Returns the tiles of a CTA's stretch. One barrier; *at is there after the next.
 struct Place {
   int b, hk, rb, tile;
 };
-template <int THREADS, typename F, typename V>
-__device__ __forceinline__ long long locate(const PagedAttnArgs& a, int ctas, int rows_block, long long* scratch,
-                                            volatile Place* at, long long* total, F&& place, V&& visit) {
+template <int THREADS, typename V>
+__device__ __forceinline__ long long locate(const PagedAttnArgs& a, int rows_block, long long* scratch,
+                                            volatile Place* at, long long* total, V&& visit) {
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
@@ -123,8 +126,8 @@ __device__ __forceinline__ long long locate(const PagedAttnArgs& a, int ctas, in
     if (i < warp) base += scratch[i];
     sum += scratch[i];
   }
-  const long long chunk = max((sum + ctas - 1) / ctas, static_cast<long long>(a.split_tiles));
-  const long long x = place(chunk);
+  const long long chunk = max((sum + gridDim.x - 1) / gridDim.x, static_cast<long long>(a.split_tiles));
+  const long long x = blockIdx.x * chunk;
   long long first = base + upto - mine;
   if (first <= x && x < first + mine)
     for (int b = b0; b < b1; ++b) {
@@ -150,7 +153,7 @@ __device__ __forceinline__ T* shfl_ptr(T* p, int from) {
 }
 
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
+__global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>::PER_SM)
     streamkl_paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v,
                                const __grid_constant__ PagedAttnArgs a) {
@@ -220,29 +223,27 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
     tma_prefetch_desc(&tm_v);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), L::TMEM);
     tmem_relinquish();
   }
   // this CTA's stretch of the line of tiles; sequences without a key on the way
   long long total;
-  const long long chunk = locate<L::THREADS>(
-      a, gridDim.x, kRows, scratch, start, &total, [&](long long per_cta) { return blockIdx.x * per_cta; },
-      [&](int b, const Seq& s) {
-        if (blockIdx.x == 0 && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-        if (s.n == 0 || s.tiles > 0 || b % gridDim.x != blockIdx.x) return;
-        for (int r = 0; r < s.n * a.HQ; ++r) {
-          const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
-          for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-          a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
-        }
-      });
+  const long long chunk = locate<L::THREADS>(a, kRows, scratch, start, &total, [&](int b, const Seq& s) {
+    if (blockIdx.x == 0 && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    if (s.n == 0 || s.tiles > 0 || b % gridDim.x != blockIdx.x) return;
+    for (int r = 0; r < s.n * a.HQ; ++r) {
+      const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
+      for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+      a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
+    }
+  });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
   ck.tmem = tmem;
-  ck.tmem_cols = 512;
+  ck.tmem_cols = L::TMEM;
   const WaitCtx wc{abort_flag, a.dev_status, a.timeout_ns};
 
   // Place of key tile j's K and V among an item's 2 n loads, in the order in which the
@@ -270,13 +271,16 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
   };
 
   if (warp < 4) {
-  // NT = 2: 128 threads with 88 registers and 256 with 208 make up the launch's
-  // 384 x 168; a softmax thread holds a row of S (128)
+  // A softmax thread holds a row of S (128). NT = 2: 128 threads with 88 registers
+  // and 256 with 208 make up the launch's 384 x 168; two CTAs an SM: 128 with 48 and
+  // 128 with 208 its 256 x 128
   if (NT == 2) regs_dec<88>();
+  if (L::PER_SM == 2) regs_dec<48>();
   if (warp == 3) {
     // ------------------------------------------------------------ items
     long long left = *skip_flag ? 0 : max(0LL, min(total - blockIdx.x * chunk, chunk));
     int b = 0, hk = 0, rb = 0, tile = 0;
+    TreeCut cut{};  // the item that goes on in the next stretch
     if (left > 0) b = start->b, hk = start->hk, rb = start->rb, tile = start->tile;
     for (int it = 0;; ++it) {
       Seg sg{};
@@ -285,6 +289,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
         while (s.tiles == 0) s = load_seq(a, ++b, kRows);  // (b < B: tiles are left)
         sg = {b, hk, rb, tile, static_cast<int>(min(left, static_cast<long long>(s.tiles - tile))), s.tok0, s.n, s.len, 0};
         sg.slot = sg.n_iter == s.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (it > 0);
+        // (an item that began before this stretch is not its to join)
+        if (tile + sg.n_iter < s.tiles && tile == 0)
+          cut = {s.tok0, hk, rb * kRows, min(kRows, s.n * G - rb * kRows),
+                 1 + static_cast<int>((s.tiles - sg.n_iter + chunk - 1) / chunk), it > 0};
         left -= sg.n_iter;
         tile += sg.n_iter;
         if (tile == s.tiles) {
@@ -315,6 +323,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
       __syncwarp();
       if (sg.n_iter == 0) break;
     }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
   } else if (warp != 1) {
     // ------------------------------------------------------ loads of K or V
     const bool is_v = warp == 2;
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
         mma_bf16_ts(tmem + L::col_o(t), tmem + L::col_p(t) + 8 * k, desc(v_lo + v_at + k * (2048 >> 4)), id_o,
                     k > 0 ? 1 : add);
     };
-    bool ok = check_tmem(ck, tmem, 128, 512, __LINE__);
+    bool ok = check_tmem(ck, tmem, 128, L::TMEM, __LINE__);
     uint32_t tiles = 0;  // so far
     for (int it = 0; ok; ++it) {
       Seg sg;
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax
-    if (NT == 2) regs_inc<208>();
+    if (NT == 2 || L::PER_SM == 2) regs_inc<208>();
     const int t = (warp - 4) >> 2;               // row tile
     const int r_tile = (warp & 3) * 32 + lane;   // TMEM lane
     const float c = a.scale * kLog2e;
@@ -781,82 +790,64 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, L::TMEM);
   }
 }
 
-// Join the parts of the items that the CTAs' stretches cut: blocks (c, ..) take the
-// item that starts in CTA c's stretch and goes on in the next, kJoinRows of its rows
-// each; the parts of a row lie in the slots of consecutive CTAs.
+// Join the parts of an item that the CTAs' stretches cut, one warp a row: blocks
+// (c, ..) take the item that starts in CTA c's stretch and goes on in the next, as
+// that CTA has written it down; the parts lie in the slots of consecutive CTAs.
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     streamkl_paged_tree_join_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
   constexpr int kRows = kTileM * NT;
-  __shared__ long long scratch[kJoinThreads / 32];
-  __shared__ Place where;
-  long long total;
+  grid_dependency_wait();  // launched while the tree kernel ends
   const int c0 = static_cast<int>(blockIdx.x);
-  const long long chunk = locate<kJoinThreads>(
-      a, gridDim.x, kRows, scratch, &where, &total, [&](long long per_cta) { return (c0 + 1) * per_cta; },
-      [](int, const Seq&) {});
-  __syncthreads();
-  const long long cut = (c0 + 1) * chunk;  // the first tile of the next stretch
-  // nothing after it, or an item that starts there, or before this stretch
-  const bool none = cut >= total || where.tile == 0 || where.tile > chunk;
-  const Seq s = load_seq(a, none ? 0 : where.b, kRows);
-  const int inside = where.tile < chunk ? 1 : 0;  // the item starts inside this stretch: its last part
-  const int parts = 1 + static_cast<int>((s.tiles - where.tile + chunk - 1) / chunk);
-  auto slot = [&](int i) { return static_cast<long long>(2 * (c0 + i) + (i == 0 ? inside : 0)) * kRows; };
-  // launched while the tree kernel ends; every block waits for its end, since
-  // what comes after this kernel counts on both
-  grid_dependency_wait();
-  if (none) return;
-  const int G = a.HQ / a.HK, lane = threadIdx.x & 31;
-  const int r0 = static_cast<int>(blockIdx.y) * kJoinRows;
-  const int rows = min(kRows, s.n * G - where.rb * kRows);
-  for (int r = r0 + static_cast<int>(threadIdx.x >> 5); r < min(rows, r0 + kJoinRows); r += kJoinThreads / 32) {
-    constexpr int RUN = 8;  // parts whose loads are in flight, the first ones beside the lse's
-    float p[RUN][V];
-    auto fetch = [&](int i0) {
+  const TreeCut cut = a.cuts[c0];
+  const int lane = threadIdx.x & 31, r = static_cast<int>(blockIdx.y) * kJoinWarps + static_cast<int>(threadIdx.x >> 5);
+  if (r >= cut.rows) return;
+  auto slot = [&](int i) { return static_cast<long long>(2 * (c0 + i) + (i == 0 ? cut.inside : 0)) * kRows + r; };
+  constexpr int RUN = 8;  // parts whose loads are in flight, the first ones beside the lse's
+  float p[RUN][V];
+  auto fetch = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
+    for (int i = 0; i < RUN; ++i) {
 #pragma unroll
-        for (int x = 0; x < V; ++x) p[i][x] = 0.f;
-        if (i0 + i < parts) {
-          const float* src = a.part_o + (slot(i0 + i) + r) * D + lane * V;
-          if constexpr (V == 4)
-            *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(src);
-          else
-            *reinterpret_cast<float2*>(p[i]) = *reinterpret_cast<const float2*>(src);
-        }
-      }
-    };
-    fetch(0);
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_lse[slot(i) + r]);
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    const float t0 = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o[V] = {};
-    for (int i0 = 0; i0 < parts; i0 += RUN) {
-      if (i0 > 0) fetch(i0);
-      const float mine = lane < RUN && i0 + lane < parts ? ex2(a.part_lse[slot(i0 + lane) + r] - t0) : 0.f;
-#pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        const float w = __shfl_sync(0xFFFFFFFFu, mine, i);  // 0 past the last part
-        sum += w;
-#pragma unroll
-        for (int x = 0; x < V; ++x) o[x] = fmaf(w, p[i][x], o[x]);
+      for (int x = 0; x < V; ++x) p[i][x] = 0.f;
+      if (i0 + i < cut.parts) {
+        const float* src = a.part_o + slot(i0 + i) * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(p[i]) = *reinterpret_cast<const float2*>(src);
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int row = where.rb * kRows + r, token = s.tok0 + row / G, head = where.hk * G + row % G;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
+  };
+  fetch(0);
+  float top = -INFINITY;
+  for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, a.part_lse[slot(i)]);
 #pragma unroll
-    for (int x = 0; x < V / 2; ++x) dst[x] = pack2<TYPE>(o[2 * x] * inv, o[2 * x + 1] * inv);
-    if (lane == 0) a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+  const float t0 = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, o[V] = {};
+  for (int i0 = 0; i0 < cut.parts; i0 += RUN) {
+    if (i0 > 0) fetch(i0);
+    const float mine = lane < RUN && i0 + lane < cut.parts ? ex2(a.part_lse[slot(i0 + lane)] - t0) : 0.f;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      const float w = __shfl_sync(0xFFFFFFFFu, mine, i);  // 0 past the last part
+      sum += w;
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[x] = fmaf(w, p[i][x], o[x]);
+    }
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int G = a.HQ / a.HK, row = cut.row0 + r, token = cut.tok0 + row / G, head = cut.hk * G + row % G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
+#pragma unroll
+  for (int x = 0; x < V / 2; ++x) dst[x] = pack2<TYPE>(o[2 * x] * inv, o[2 * x + 1] * inv);
+  if (lane == 0) a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int TYPE, int D, int NT>
@@ -879,8 +870,8 @@ cudaError_t tree_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long most = std::min<long long>(static_cast<long long>(a.max_q) * (a.HQ / a.HK), kTileM * NT);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((most + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
