@@ -51,16 +51,18 @@ struct TreeLayout {
   static constexpr int TILE = kTileN * D * 2;
   // CTAs of an SM: two where shared memory and half of TMEM hold what one needs
   static constexpr int PER_SM = D == 64 && NT == 1 ? 2 : 1;
-  static constexpr int STAGES = D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 10 : 6);
+  static constexpr int STAGES = D == 64 && NT == 2 ? 10 : 5;
   static constexpr int TMEM = 512 / PER_SM;
+  // Q of the next item beside this one's, where there is room for it
+  static constexpr int QBUFS = D == 128 && NT == 2 ? 1 : 2;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_KV = NT * TILE;
+  static constexpr int OFF_KV = QBUFS * NT * TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
   // P in columns of its own, where TMEM has room for them; else in S's place
   static constexpr bool OWN_P = D == 64 || NT == 1;
-  // q_full, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], s_read, p_read,
+  // q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], s_read, p_read,
   // drain, p_first[2], o_first[2], seg_full[kSegs], seg_empty[kSegs]
-  static constexpr int NBAR = 1 + 2 * STAGES + 13 + 2 * kSegs;
+  static constexpr int NBAR = 2 + 2 * STAGES + 13 + 2 * kSegs;
   static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = (OFF_SEG + kSegs * static_cast<int>(sizeof(Seg)) + 15) / 16 * 16;
   static constexpr int THREADS = 128 + 128 * NT;
@@ -146,6 +148,13 @@ __device__ __forceinline__ long long locate(const PagedAttnArgs& a, int rows_blo
   return chunk;
 }
 
+// 16 bytes from global to shared memory, past the registers; and the wait for all
+// of this thread's.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Lane `from`'s pointer.
 template <typename T>
 __device__ __forceinline__ T* shfl_ptr(T* p, int from) {
@@ -164,10 +173,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.HQ / a.HK;
   const uint32_t bar0 = sb + L::OFF_BAR;
-  const uint32_t q_full = bar0;
-  auto kv_full = [&](int s) { return bar0 + 8u * (1 + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (1 + L::STAGES + s); };
-  const uint32_t rest = bar0 + 8u * (1 + 2 * L::STAGES);
+  auto q_full = [&](int it) { return bar0 + 8u * (it % L::QBUFS); };
+  auto kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (2 + L::STAGES + s); };
+  const uint32_t rest = bar0 + 8u * (2 + 2 * L::STAGES);
   auto s_full = [&](int k) { return rest + 8u * k; };
   auto p_full = [&](int k) { return rest + 8u * (2 + k); };
   auto o_full = [&](int k) { return rest + 8u * (4 + k); };
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
   auto o_first = [&](int k) { return rest + 8u * (11 + k); };
   auto seg_full = [&](int k) { return rest + 8u * (13 + k); };
   auto seg_empty = [&](int k) { return rest + 8u * (13 + kSegs + k); };
-  static_assert(1 + 2 * L::STAGES + 13 + 2 * kSegs == L::NBAR, "barrier region holds every barrier");
+  static_assert(2 + 2 * L::STAGES + 13 + 2 * kSegs == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
   volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
@@ -193,7 +202,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     if (kDeviceChecks)
       for (int i = 0; i < L::NBAR; ++i) lay_ok = lay_ok && check_bar(ck, bar0 + 8u * i, __LINE__);
     if (lay_ok) {
-      mbar_init(q_full, 4 * NT);  // one arrival per softmax warp
+      for (int k = 0; k < 2; ++k) mbar_init(bar0 + 8u * k, 4 * NT);  // q_full: one arrival per softmax warp
       for (int s = 0; s < L::STAGES; ++s) {
         mbar_init(kv_full(s), 1);
         mbar_init(kv_empty(s), NT);
@@ -401,11 +410,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       ring.step(L::STAGES);
       return at;
     };
-    auto mma_s = [&](int t, uint32_t k_at) {  // S = Q_t K_j^T
+    auto mma_s = [&](int t, uint32_t q_at, uint32_t k_at) {  // S = Q_t K_j^T
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t off = ((i >> 2) * L::BOX + (i & 3) * 32) >> 4;
-        mma_bf16(tmem + L::col_s(t), desc(q_lo + t * (L::TILE >> 4) + off), desc(k_lo + k_at + off), id_s, i > 0);
+        mma_bf16(tmem + L::col_s(t), desc(q_at + t * (L::TILE >> 4) + off), desc(k_lo + k_at + off), id_s, i > 0);
       }
     };
     auto mma_o = [&](int t, int from, int to, uint32_t v_at, uint32_t add) {  // O_t += P V_j, of keys [from, to)
@@ -419,12 +428,16 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     for (int it = 0; ok; ++it) {
       Seg sg;
       if (!(ok = take_seg(it, sg, true)) || sg.n_iter == 0) break;
-      if (!(ok = wait_bounded(q_full, it & 1, wc) && wait_bounded(kv_full(ring.stage), ring.phase, wc))) break;
+      if (!(ok = wait_bounded(q_full(it), (it / L::QBUFS) & 1, wc) && wait_bounded(kv_full(ring.stage), ring.phase, wc)))
+        break;
+      // (with Q there early, the last item's S may still be read)
+      if (L::QBUFS == 2 && it > 0 && !(ok = wait_bounded(s_read, (tiles - 1) & 1, wc))) break;
       tc_fence_after();
+      const uint32_t q_at = q_lo + it % L::QBUFS * (NT * L::TILE >> 4);
       uint32_t k_at = next();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        mma_s(t, k_at);
+        mma_s(t, q_at, k_at);
         if (!L::OWN_P || t == NT - 1) mma_commit(s_full(L::OWN_P ? 0 : t));
       }
 #pragma unroll 1
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             if (!(ok = wait_bounded(p_full(t), tiles & 1, wc))) break;
             tc_fence_after();
             mma_o(t, kFirst, kTileN, v_at, 1);
-            if (more) mma_s(t, k_at);
+            if (more) mma_s(t, q_at, k_at);
             mma_commit(more ? s_full(t) : o_full(t));
           }
           if (!ok) break;
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             if (!(ok = wait_bounded(s_read, tiles & 1, wc))) break;
             tc_fence_after();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_s(t, k_at);
+            for (int t = 0; t < NT; ++t) mma_s(t, q_at, k_at);
             mma_commit(s_full(0));
           }
           const uint32_t v_at = next();
@@ -480,30 +493,47 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     // this warp's rows of Q, D / 8 lanes a row, 128-byte swizzled as TMA would
     // place them; rows that are not there are zero
     constexpr int LPR = D / 8, RPI = 32 / LPR;
-    auto fetch_q = [&](const Seg& s, uint4 (&v)[LPR]) {
+    auto row_of_q = [&](const Seg& s) -> const uint16_t* {  // this thread's, null where there is none
       const int row = s.rb * kRows + t * kTileM + r_tile, tok = row / G;
-      const uint16_t* mine = s.n_iter > 0 && row < s.n * G
-                                 ? static_cast<const uint16_t*>(a.q) + (s.tok0 + tok) * a.q_sn +
-                                       (s.hk * G + row - tok * G) * a.q_sh
-                                 : nullptr;
+      return s.n_iter > 0 && row < s.n * G ? static_cast<const uint16_t*>(a.q) + (s.tok0 + tok) * a.q_sn +
+                                                 (s.hk * G + row - tok * G) * a.q_sh
+                                           : nullptr;
+    };
+    const int cq = lane % LPR;
+    auto place_q = [&](int i, int it) {  // of this lane's chunk of the warp's rows i * RPI ..
+      const int r = (warp & 3) * 32 + i * RPI + lane / LPR;
+      return sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + (cq >> 3) * L::BOX + r * 128 + (((cq & 7) ^ (r & 7)) << 4);
+    };
+    // into registers and from there, or past them where Q has two places
+    auto fetch_q = [&](const Seg& s, uint4 (&v)[LPR]) {
+      const uint16_t* mine = row_of_q(s);
 #pragma unroll
       for (int i = 0; i < LPR; ++i) {
         const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
         v[i] = make_uint4(0, 0, 0, 0);
-        if (row_q != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(row_q) + lane % LPR);
+        if (row_q != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(row_q) + cq);
       }
     };
-    auto put_q = [&](const uint4 (&v)[LPR]) {
-      const int cq = lane % LPR;
-#pragma unroll
-      for (int i = 0; i < LPR; ++i) {
-        const int r = (warp & 3) * 32 + i * RPI + lane / LPR;
-        st_shared_v4(sb + L::OFF_Q + t * L::TILE + (cq >> 3) * L::BOX + r * 128 + (((cq & 7) ^ (r & 7)) << 4), v[i].x,
-                     v[i].y, v[i].z, v[i].w);
-      }
+    auto give_q = [&](int it) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(q_full(it));
+    };
+    auto put_q = [&](const uint4 (&v)[LPR], int it) {
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) st_shared_v4(place_q(i, it), v[i].x, v[i].y, v[i].z, v[i].w);
+      give_q(it);
+    };
+    auto copy_q = [&](const Seg& s, int it) {
+      const uint16_t* mine = row_of_q(s);
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
+        if (row_q != nullptr)
+          copy16_async(place_q(i, it), row_q + 8 * cq);
+        else
+          st_shared_v4(place_q(i, it), 0, 0, 0, 0);
+      }
     };
     int base = 0;        // loads of the items before
     uint32_t tiles = 0;  // of the items before
@@ -513,7 +543,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     if (ok && sg.n_iter > 0) {
       uint4 v[LPR];
       fetch_q(sg, v);
-      put_q(v);
+      put_q(v, 0);
     }
     for (int it = 0; ok && sg.n_iter > 0; ++it) {
       const int n_iter = sg.n_iter, rows = sg.n * G;
@@ -525,6 +555,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       // keys of the last tile that are there; the rest of its V rows are cleared
       const int last_valid = min(kTileN, sg.len - (sg.t0 + n_iter - 1) * kTileN);
       float ref = -INFINITY, l = 0.f;
+      Seg after{};  // the next item
+      if (L::QBUFS == 2) {
+        if (!(ok = take_seg(it + 1, after, false))) break;
+        if (after.n_iter > 0) copy_q(after, it + 1);
+      }
       auto landed_k = [&](int j) {
         const int i = base + idx_k(j);
         return warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc);
@@ -711,14 +746,19 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             mbar_arrive(kv_empty((base + idx_k(j)) % L::STAGES));
           }
         }
+        if (L::QBUFS == 2 && j == 0 && after.n_iter > 0) {
+          copy_async_wait();
+          give_q(it + 1);
+        }
       }
       if (!ok) break;
       // ---------------------------------------------------------- output
-      // The next item's rows of Q are on their way meanwhile
-      Seg after;
+      // With one place for Q the next item's rows are on their way meanwhile
       uint4 next_q[LPR];
-      if (!(ok = take_seg(it + 1, after, false))) break;
-      fetch_q(after, next_q);
+      if (L::QBUFS == 1) {
+        if (!(ok = take_seg(it + 1, after, false))) break;
+        fetch_q(after, next_q);
+      }
       if (!(ok = warp_wait(o_full(L::OWN_P ? 0 : t), it & 1, wc))) break;
       tc_fence_after();
       if ((warp & 3) == 0 && lane == 0) mbar_arrive(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
@@ -730,7 +770,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         // The rows go out through shared memory (this warp's part of Q's tile,
         // which no product reads any more), 128 bytes of each at a time, so that
         // eight lanes write a row's line together
-        const uint32_t stage = sb + L::OFF_Q + t * L::TILE + (warp & 3) * 32 * 128;
+        const uint32_t stage = sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + (warp & 3) * 32 * 128;
         const bool parts = sg.slot >= 0;
         uint8_t* mine = !live  ? nullptr
                         : parts ? reinterpret_cast<uint8_t*>(a.part_o + part * D)
@@ -777,7 +817,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             a.lse[e] = lse2 * kLn2;
         }
       }
-      if (after.n_iter > 0) put_q(next_q);
+      if (L::QBUFS == 1 && after.n_iter > 0) put_q(next_q, it + 1);
       base += 2 * n_iter;
       tiles += n_iter;
       reads += n_iter - 1;
