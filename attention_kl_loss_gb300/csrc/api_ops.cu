@@ -393,8 +393,9 @@ streamkl_status check_tables(const int* refs, const int* table, long long stride
                                     const char* list_name, const int* status, int B, int num_pages, int max_pages) {
   if (B < 1 || num_pages < 1 || max_pages < 1)
     return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (B=%d num_pages=%d max_pages=%d)", B, num_pages, max_pages);
-  if (B > skl::kMaxTableRows || num_pages > (1 << 30) || static_cast<long long>(B) * max_pages > (1LL << 30))
-    return fail(STREAMKL_ERR_UNSUPPORTED, "more than %d sequences, 2^30 pages or 2^30 entries", skl::kMaxTableRows);
+  if (B > skl::kMaxTableRows || num_pages > skl::kMaxPages || static_cast<long long>(B) * max_pages > (1LL << 30))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "more than %d sequences, %d pages or 2^30 entries", skl::kMaxTableRows,
+                skl::kMaxPages);
   if (!refs || !table || !lens || !list)
     return fail(STREAMKL_ERR_INVALID_ARG, "page_refs, block_table, kv_lens and %s must be non-NULL", list_name);
   if (stride < max_pages && B > 1)

@@ -144,7 +144,7 @@ struct ForkArgs {
   int* kv_lens;
   const int* source;
   int B, num_pages, max_pages;
-  int cols;                  // set by the launcher: columns of a block
+  int cols;                  // set by the launcher: 1 << cols columns a block
   int* dev_status;
 };
 
@@ -159,7 +159,8 @@ struct ResizeArgs {
   int* dev_status;
 };
 
-constexpr int kMaxTableRows = 8192;  // sequences of a fork or resize call
+constexpr int kMaxTableRows = 8192;    // sequences of a fork or resize call
+constexpr int kMaxPages = 1 << 23;     // pages of a cache that resize looks after
 
 // Blocks of the backward's persistent grid (its partials' row count).
 int rope_bwd_blocks(int B, int NQ, int HQ, int NK, int HK, int d, int sms);

@@ -70,13 +70,17 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int b) {
   return s;
 }
 
-// THREADS threads an item: a warp each where few rows are kept, else a block.
+// THREADS threads an item: a warp each where few rows are kept, else a block for
+// 64 bytes of its columns (whole sequences are pruned: the longest one decides, and
+// in whole rows 16 blocks would have it to themselves: 8 sequences of up to 4,100
+// kept rows, 8 heads of 128, 73 us). The next rows' numbers are loaded beside the rows.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     streamkl_paged_compact_kernel(const __grid_constant__ CompactArgs a) {
   constexpr bool WARP = THREADS == 32;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const long long item = WARP ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
+  const int split = WARP ? 0 : a.vshift - 2, vshift = a.vshift - split;  // column groups; vectors a row in one
+  const long long item = WARP ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x >> split;
   if (item >= 2LL * a.B * a.H) return;
   auto together = [](bool p) { return WARP ? __all_sync(0xFFFFFFFFu, p) != 0 : __syncthreads_and(p) != 0; };
   const int b = static_cast<int>(item / (2 * a.H)), rest = static_cast<int>(item - b * 2LL * a.H);
@@ -95,8 +99,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     return;
   }
   const int* table = a.table + b * a.table_sb;
-  const int page = 1 << a.page_shift, lane = tid & ((1 << a.vshift) - 1);
-  uint4* data = static_cast<uint4*>(c.data) + h * c.sh + lane;
+  const int page = 1 << a.page_shift;
+  const int column = (tid & ((1 << vshift) - 1)) + (WARP ? 0 : (blockIdx.x & ((1 << split) - 1)) << vshift);
+  uint4* data = static_cast<uint4*>(c.data) + h * c.sh + column;
   auto place = [&](int i) -> uint4* {  // row i of the last n
     const int pos = s.first + i;
     const int p = __ldg(table + (pos >> a.page_shift));
@@ -106,25 +111,32 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     }
     return data + p * c.sp + (pos & (page - 1)) * c.ss;
   };
-  const int per = THREADS >> a.vshift;  // rows at once
+  const int per = THREADS >> vshift, mine = tid >> vshift;  // rows at once
+  int k[kCompactRun];
+  auto numbers = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kCompactRun; ++u) {
+      const int i = i0 + u * per + mine;
+      k[u] = i < s.count ? __ldg(kept + i) : i;  // (which moves nothing)
+    }
+  };
+  numbers(0);
   for (int i0 = 0; i0 < s.count; i0 += per * kCompactRun) {
     uint4 v[kCompactRun];
     uint4* to[kCompactRun];
 #pragma unroll
     for (int u = 0; u < kCompactRun; ++u) {
-      const int i = i0 + u * per + (tid >> a.vshift);
+      const int i = i0 + u * per + mine;
       to[u] = nullptr;
-      if (i < s.count) {
-        const int k = __ldg(kept + i);
-        if (k != i) {
-          const uint4* from = place(k);
-          if (from != nullptr) {
-            v[u] = *from;
-            to[u] = place(i);
-          }
+      if (k[u] != i) {
+        const uint4* from = place(k[u]);
+        if (from != nullptr) {
+          v[u] = *from;
+          to[u] = place(i);
         }
       }
     }
+    numbers(i0 + per * kCompactRun);
     if (WARP)
       __syncwarp();
     else
@@ -140,11 +152,11 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
 // every row: all of it is read before any is written, and other slabs do not meet
 // it. A page of the row b is afterwards held by as many rows more as there are
 // sequences that go on from b, less the row b itself: one atomic an entry.
-constexpr int kForkThreads = 256;
+constexpr int kForkThreads = 256, kForkRun = 8;  // entries whose loads are in flight
 
 __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const __grid_constant__ ForkArgs a) {
   extern __shared__ int sm[];
-  int *source = sm, *more = sm + a.B, *old = more + a.B;  // old: [B][cols], block 0 first uses it for the lengths
+  int *source = sm, *more = sm + a.B, *old = more + a.B;  // old: [B][columns], block 0 first uses it for the lengths
   for (int b = threadIdx.x; b < a.B; b += kForkThreads) more[b] = -1;
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += kForkThreads) {
@@ -163,23 +175,35 @@ __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const
       if (source[b] != b) a.kv_lens[b] = old[source[b]];
     __syncthreads();
   }
-  const int j0 = static_cast<int>(blockIdx.x) * a.cols, cols = min(a.cols, a.max_pages - j0);
-  for (int e = threadIdx.x; e < a.B * a.cols; e += kForkThreads) {
-    const int b = e / a.cols, j = e - b * a.cols;
-    if (j >= cols || (source[b] == b && more[b] == 0)) continue;  // nobody takes it, and it stays
-    const int p = a.table[b * a.table_sb + j0 + j];
-    old[e] = p;
-    if (more[b] != 0 && p != -1) {
-      if (p < 0 || p >= a.num_pages)
-        atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-      else
-        atomicAdd(a.refs + p, more[b]);
+  const int j0 = static_cast<int>(blockIdx.x) << a.cols, cols = min(1 << a.cols, a.max_pages - j0);
+  const int entries = a.B << a.cols;
+  for (int e0 = threadIdx.x; e0 < entries; e0 += kForkThreads * kForkRun) {
+    int p[kForkRun];
+#pragma unroll
+    for (int u = 0; u < kForkRun; ++u) {
+      const int e = e0 + u * kForkThreads, b = e >> a.cols, j = e & ((1 << a.cols) - 1);
+      p[u] = -1;
+      // (nothing to do where nobody takes it and it stays)
+      if (e < entries && j < cols && (source[b] != b || more[b] != 0)) p[u] = a.table[b * a.table_sb + j0 + j];
+    }
+#pragma unroll
+    for (int u = 0; u < kForkRun; ++u) {
+      const int e = e0 + u * kForkThreads;
+      if (e >= entries) break;
+      old[e] = p[u];
+      const int change = more[e >> a.cols];
+      if (change != 0 && p[u] != -1) {
+        if (p[u] < 0 || p[u] >= a.num_pages)
+          atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+        else
+          atomicAdd(a.refs + p[u], change);
+      }
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.B * a.cols; e += kForkThreads) {
-    const int b = e / a.cols, j = e - b * a.cols;
-    if (j < cols && source[b] != b) a.table[b * a.table_sb + j0 + j] = old[source[b] * a.cols + j];
+  for (int e = threadIdx.x; e < entries; e += kForkThreads) {
+    const int b = e >> a.cols, j = e & ((1 << a.cols) - 1);
+    if (j < cols && source[b] != b) a.table[b * a.table_sb + j0 + j] = old[(source[b] << a.cols) + j];
   }
 }
 
@@ -187,9 +211,13 @@ __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const
 // One cluster: what is asked of a sequence hangs on those before it, and which page
 // it gets on all pages before that one, so the whole call is two prefix sums, over
 // the sequences (every block makes them for itself) and over the free pages (the
-// blocks share them, a bit each in registers, and exchange their counts).
+// blocks share them, one bit each, and exchange their counts). Between them lies what
+// has to be in that order: pages given back, the counts of last pages, free pages.
 constexpr int kResizeThreads = 1024, kResizeWarps = kResizeThreads / 32;
 constexpr int kBlockPages = kResizeThreads * 32;  // a block's pages of a round
+constexpr int kResizeBlocks = 16;                 // most of a cluster
+static_assert(kMaxPages % (kBlockPages * kResizeBlocks) == 0);
+constexpr int kResizeRounds = kMaxPages / (kBlockPages * kResizeBlocks);
 
 // Exclusive sums of value(b) over b < B into out[0 .. B]; returns the total. All
 // threads; two barriers, and one before the next use of `sums`.
@@ -209,12 +237,7 @@ __device__ __forceinline__ int scan_sequences(int B, int* out, int* sums, F&& va
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
   const int w = sums[lane];  // (32 warps)
-  int before = lane < warp ? w : 0, total = w;
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, m);
-    total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
-  }
+  const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0), total = __reduce_add_sync(0xFFFFFFFFu, w);
   int at = before + upto - mine;
   for (int b = b0; b < b1; ++b) {
     out[b] = at;
@@ -225,15 +248,14 @@ __device__ __forceinline__ int scan_sequences(int B, int* out, int* sums, F&& va
   return total;
 }
 
-// The sequence in whose part of the exclusive sums x lies.
-__device__ __forceinline__ int find_sequence(const int* sums, int B, int x) {
-  int lo = 0, hi = B;  // sums[lo] <= x < sums[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+// The sequence of lo .. hi in whose part of the exclusive sums x lies.
+__device__ __forceinline__ int find_sequence(const int* sums, int lo, int hi, int x) {
+  while (lo < hi) {  // sums[lo] <= x < sums[hi + 1]
+    const int mid = (lo + hi + 1) >> 1;
     if (sums[mid] <= x)
       lo = mid;
     else
-      hi = mid;
+      hi = mid - 1;
   }
   return lo;
 }
@@ -243,60 +265,94 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
   extern __shared__ int sm[];
-  int* sums = sm;              // [B + 1]
-  int* delta = sums + a.B + 1; // pages more than before
-  int* first = delta + a.B;    // the first entry that comes or goes
-  int* last = first + a.B;     // a last page to be copied; kNone, kKeeps: the last of those that hold it
+  int* sums = sm;            // [B + 1]
+  int* from = sums + a.B + 1;  // lengths; a sequence whose numbers do not fit stays
+  int* to = from + a.B;
+  int* last = to + a.B;      // a last page to be copied; kNone, kKeeps: the last of those that hold it
+  uint32_t* bits = reinterpret_cast<uint32_t*>(last + a.B);  // [rounds][threads]: free pages
   constexpr int kNone = -1, kKeeps = -2;
   __shared__ int scratch[kResizeWarps];
-  __shared__ int counts[2][8];  // free pages of the blocks, by the round's parity
+  __shared__ int counts[2][kResizeBlocks];  // free pages of the blocks, by the round's parity
+  __shared__ int ranks[kResizeRounds + 1];  // of a round's first free page in this block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << a.page_shift;
   const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
-  auto lengths = [&](int b, int& from, int& to) {
-    from = a.kv_lens[b];
-    to = __ldg(a.new_lens + b);
-    return from >= 0 && from <= most && to >= 0 && to <= most;
-  };
+  auto pages_of = [&](int length) { return (length + page - 1) >> a.page_shift; };
   for (int b = tid; b < a.B; b += kResizeThreads) {
-    int from, to;
-    delta[b] = first[b] = 0;
-    last[b] = kNone;
-    if (lengths(b, from, to)) {
-      const int have = (from + page - 1) >> a.page_shift, need = (to + page - 1) >> a.page_shift;
-      delta[b] = need - have;
-      first[b] = min(have, need);
-    } else if (me == 0) {
-      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    int f = a.kv_lens[b], t = __ldg(a.new_lens + b), p = kNone;
+    if (f < 0 || f > most || t < 0 || t > most) {
+      if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+      f = t = 0;
+    } else if (t > f && (f & (page - 1)) != 0) {  // it grows into its last page
+      p = a.table[b * a.table_sb + (f >> a.page_shift)];
+      if (p < 0 || p >= a.num_pages) {
+        if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+        p = kNone;
+      }
     }
+    from[b] = f;
+    to[b] = t;
+    last[b] = p;
   }
   __syncthreads();
-  // ---- what is given back
-  const int back = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, -delta[b]); });
-  for (int i = me * kResizeThreads + tid; i < back; i += blocks * kResizeThreads) {
-    const int b = find_sequence(sums, a.B, i);
-    int* entry = a.table + b * a.table_sb + first[b] + (i - sums[b]);
-    const int p = *entry;
-    *entry = -1;
-    if (p >= 0 && p < a.num_pages)
-      atomicSub(a.refs + p, 1);
-    else
-      atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+  // ---- what is given back: runs of 128 entries a warp, most of one sequence
+  const int back = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, pages_of(from[b]) - pages_of(to[b])); });
+  for (int i0 = (me * kResizeWarps + warp) * 128; i0 < back; i0 += blocks * kResizeWarps * 128) {
+    const int lo = find_sequence(sums, 0, a.B - 1, i0);
+    const int hi = find_sequence(sums, lo, a.B - 1, min(back, i0 + 128) - 1);
+    int p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i >= back) continue;
+      const int b = find_sequence(sums, lo, hi, i);
+      int* entry = a.table + b * a.table_sb + pages_of(to[b]) + (i - sums[b]);
+      p[u] = *entry;
+      *entry = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + 32 * u + lane >= back) continue;
+      if (p[u] >= 0 && p[u] < a.num_pages)
+        atomicSub(a.refs + p[u], 1);
+      else
+        atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+    }
   }
-  __threadfence();
+  if (back > 0) __threadfence();
   cluster.sync();
-  // ---- last pages that others hold too
+  // ---- free pages: bit 4 i + e of a thread: page base + 128 i + 4 lane + e of its warp's 1,024
+  auto look = [&](int round) {
+    const long long base = (static_cast<long long>(round) * blocks + me) * kBlockPages + warp * 1024 + lane * 4;
+    int4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long p = base + 128 * i;
+      v[i] = make_int4(1, 1, 1, 1);
+      if (p + 4 <= a.num_pages)
+        v[i] = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
+      else if (p < a.num_pages) {
+        v[i].x = __ldcg(a.refs + p);
+        if (p + 1 < a.num_pages) v[i].y = __ldcg(a.refs + p + 1);
+        if (p + 2 < a.num_pages) v[i].z = __ldcg(a.refs + p + 2);
+      }
+    }
+    uint32_t free = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      free |= static_cast<uint32_t>((v[i].x == 0) | (v[i].y == 0) << 1 | (v[i].z == 0) << 2 | (v[i].w == 0) << 3) << (4 * i);
+    bits[round * kResizeThreads + tid] = free;
+    return __popc(free);
+  };
+  // ---- last pages that others hold too (beside the first look at the counts)
+  const int held = tid < a.B && last[tid] >= 0 ? __ldcg(a.refs + last[tid]) : 0;
+  int seen = look(0);
   bool any = false;
   for (int b = tid; b < a.B; b += kResizeThreads) {
-    int from, to;
-    if (!lengths(b, from, to) || to <= from || (from & (page - 1)) == 0) continue;
-    const int p = __ldcg(a.table + b * a.table_sb + (from >> a.page_shift));
-    if (p < 0 || p >= a.num_pages) {
-      if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-    } else if (__ldcg(a.refs + p) > 1) {
-      last[b] = p;
-      any = true;
-    }
+    if (last[b] < 0) continue;
+    const bool shared = (b == tid ? held : __ldcg(a.refs + last[b])) > 1;
+    any = any || shared;
+    if (!shared) last[b] = kNone;
   }
   if (__syncthreads_or(any)) {
     // in their order, each takes a copy while another holds the page
@@ -313,58 +369,31 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     }
     __syncthreads();
   }
-  const int asked = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, delta[b]) + (last[b] >= 0); });
-  // ---- free pages, lowest numbers first
-  uint32_t free_bits = 0;  // bit 4 i + e: page base + 128 i + 4 lane + e of this warp's 1,024
-  auto look = [&](int round) {
-    const long long base = (static_cast<long long>(round) * blocks + me) * kBlockPages + warp * 1024 + lane * 4;
-    int4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long p = base + 128 * i;
-      v[i] = make_int4(1, 1, 1, 1);
-      if (p + 4 <= a.num_pages)
-        v[i] = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
-      else if (p < a.num_pages) {
-        v[i].x = __ldcg(a.refs + p);
-        if (p + 1 < a.num_pages) v[i].y = __ldcg(a.refs + p + 1);
-        if (p + 2 < a.num_pages) v[i].z = __ldcg(a.refs + p + 2);
-      }
-    }
-    free_bits = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      free_bits |= static_cast<uint32_t>((v[i].x == 0) | (v[i].y == 0) << 1 | (v[i].z == 0) << 2 | (v[i].w == 0) << 3)
-                   << (4 * i);
-  };
-  // this round's free pages: before this warp's, in all
-  auto count = [&](int round, int& before, int& total) {
-    const int mine = __reduce_add_sync(0xFFFFFFFFu, __popc(free_bits));
+  const int asked = scan_sequences(a.B, sums, scratch, [&](int b) {
+    return max(0, pages_of(to[b]) - pages_of(from[b])) + (last[b] >= 0);
+  });
+  // ---- enough of the free pages, lowest numbers first
+  const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
+                                      (static_cast<long long>(blocks) * kBlockPages));
+  int found = 0, round = 0;
+  for (; round < rounds && found < asked; ++round) {
+    if (round > 0) seen = look(round);
+    const int mine = __reduce_add_sync(0xFFFFFFFFu, seen);
     if (lane == 0) scratch[warp] = mine;
     __syncthreads();
-    const int w = scratch[lane];
-    before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
-    const int block = __reduce_add_sync(0xFFFFFFFFu, w);
+    const int block = __reduce_add_sync(0xFFFFFFFFu, scratch[lane]);
     if (tid < blocks) *cluster.map_shared_rank(&counts[round & 1][me], tid) = block;
     cluster.sync();  // (and `scratch` may be used again)
-    total = 0;
+    int before = found, total = found;
     for (int i = 0; i < blocks; ++i) {
       if (i < me) before += counts[round & 1][i];
       total += counts[round & 1][i];
     }
-  };
-  const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
-                                      (static_cast<long long>(blocks) * kBlockPages));
-  int found = 0, before = 0, total = 0;
-  int round = 0;
-  for (; round < rounds && found < asked; ++round) {
-    look(round);
-    count(round, before, total);
-    found += total;
+    if (tid == 0) ranks[round] = before;
+    found = total;
   }
   // ---- who is served: all that is asked up to a sequence has to be there
-  auto wants = [&](int b) { return sums[b + 1] > sums[b] || last[b] == kKeeps; };
-  auto served = [&](int b) { return !wants(b) || sums[b + 1] <= found; };
+  auto served = [&](int b) { return (sums[b + 1] == sums[b] && last[b] != kKeeps) || sums[b + 1] <= found; };
   int limit = asked;
   if (found < asked) {  // (the sums do not fall: the largest that is there)
     int lo = 0, hi = a.B;
@@ -378,71 +407,79 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     limit = sums[lo];
   }
   // ---- pages to their places
-  auto assign = [&](int p, int slot) {
-    const int b = find_sequence(sums, a.B, slot);
-    int* entry = a.table + b * a.table_sb + first[b] + (slot - sums[b]);
-    a.refs[p] = 1;
-    if (last[b] >= 0) {
-      --entry;  // the copy comes first, in the last page's place
-      if (slot == sums[b]) {
-        a.copies[b] = make_int2(last[b], p);
-        atomicSub(a.refs + last[b], 1);
-      }
-    }
-    *entry = p;
-  };
-  const bool kept = round == 1;  // the only round's bits are still there
-  int base = 0;
-  for (int r = 0; r < round && base < limit; ++r) {
-    if (!kept) {
-      look(r);
-      count(round + r, before, total);
-    }
-    int at = base + before;  // rank of this warp's first free page
+  __syncthreads();  // (ranks)
+  for (int r = 0; r < round; ++r) {
+    if (ranks[r] >= limit) break;
+    const uint32_t free = bits[r * kResizeThreads + tid];
+    const int mine = __reduce_add_sync(0xFFFFFFFFu, __popc(free));
+    if (lane == 0) scratch[warp] = mine;
+    __syncthreads();
+    int at = ranks[r] + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scratch[lane] : 0);  // of this warp's first free page
+    __syncthreads();
+    if (mine == 0 || at >= limit) continue;
+    const int lo = find_sequence(sums, 0, a.B - 1, at);
+    const int hi = find_sequence(sums, lo, a.B - 1, min(limit, at + mine) - 1);
+    const int base = (r * blocks + me) * kBlockPages + warp * 1024 + 4 * lane;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t mine = free_bits >> (4 * i) & 15;
+      const uint32_t four = free >> (4 * i) & 15;
       int below = 0, all = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, mine >> e & 1);
+        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, four >> e & 1);
         below += __popc(lanes & ((1u << lane) - 1));
         all += __popc(lanes);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (!(mine >> e & 1)) continue;
-        const int slot = at + below + __popc(mine & ((1u << e) - 1));
-        if (slot < limit) assign((r * blocks + me) * kBlockPages + warp * 1024 + 128 * i + 4 * lane + e, slot);
+        const int slot = at + below + __popc(four & ((1u << e) - 1));
+        if (!(four >> e & 1) || slot >= limit) continue;
+        const int p = base + 128 * i + e;
+        const int b = find_sequence(sums, lo, hi, slot);
+        int* entry = a.table + b * a.table_sb + pages_of(from[b]) + (slot - sums[b]);
+        a.refs[p] = 1;
+        if (last[b] >= 0) {
+          --entry;  // the copy comes first, in the last page's place
+          if (slot == sums[b]) {
+            a.copies[b] = make_int2(last[b], p);
+            atomicSub(a.refs + last[b], 1);
+          }
+        }
+        *entry = p;
       }
       at += all;
     }
-    base += total;
   }
-  // ---- lengths (which every block has read by then, as it has the others' counts)
-  cluster.sync();
+  // ---- lengths (which every block has read, before the barriers above)
   if (me == 0) {
     for (int b = tid; b < a.B; b += kResizeThreads) {
-      int from, to;
-      const bool good = lengths(b, from, to), is_served = served(b);
-      if (!good || last[b] < 0 || !is_served) a.copies[b] = make_int2(-1, -1);
-      if (good && is_served) a.kv_lens[b] = to;
+      const bool is_served = served(b);
+      if (last[b] < 0 || !is_served) a.copies[b] = make_int2(-1, -1);
+      if (is_served && from[b] != to[b]) a.kv_lens[b] = to[b];
       if (!is_served) atomicCAS(a.dev_status, 0, kStatusNoPages);
     }
   }
 }
 
-int resize_shared(int B) { return (4 * B + 1) * static_cast<int>(sizeof(int)); }
+int resize_shared(int B, int rounds) { return (4 * B + 1 + rounds * kResizeThreads) * static_cast<int>(sizeof(int)); }
 
-template <typename K>
-cudaError_t allow_shared(K kern, std::atomic<unsigned long long>& done, int bytes) {  // once per device
+template <typename F>
+cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (done.load() & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = set();
   if (e == cudaSuccess) done.fetch_or(bit);
   return e;
+}
+
+template <typename K>
+cudaError_t allow_shared(K kern, std::atomic<unsigned long long>& done, int bytes) {
+  return once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
 }
 
 }  // namespace
@@ -461,7 +498,7 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
   if (a.max_kept <= 2 * kCompactRun * (32 >> a.vshift))
     streamkl_paged_compact_kernel<32><<<static_cast<unsigned>((items + 3) / 4), 128, 0, stream>>>(a);
   else
-    streamkl_paged_compact_kernel<512><<<static_cast<unsigned>(items), 512, 0, stream>>>(a);
+    streamkl_paged_compact_kernel<256><<<static_cast<unsigned>(items << (a.vshift - 2)), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -471,23 +508,31 @@ cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e = allow_shared(streamkl_paged_fork_kernel, done, kMost);
   if (e != cudaSuccess) return e;
   // 32 columns (a line of each row), fewer for more blocks or where the slab would not fit
-  a.cols = 32;
-  while (a.cols > 4 && (a.max_pages < a.cols * 2 * sms || a.B * (a.cols + 2) > kMaxTableRows * 6)) a.cols >>= 1;
-  const int bytes = a.B * (a.cols + 2) * static_cast<int>(sizeof(int));
-  streamkl_paged_fork_kernel<<<(a.max_pages + a.cols - 1) / a.cols, kForkThreads, bytes, stream>>>(a);
+  a.cols = 5;
+  while (a.cols > 2 && (a.max_pages >> a.cols < 2 * sms || a.B * ((1 << a.cols) + 2) > kMaxTableRows * 6)) --a.cols;
+  const int cols = 1 << a.cols, bytes = a.B * (cols + 2) * static_cast<int>(sizeof(int));
+  streamkl_paged_fork_kernel<<<(a.max_pages + cols - 1) / cols, kForkThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream) {
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_shared(streamkl_paged_resize_kernel, done, resize_shared(kMaxTableRows));
+  static std::atomic<unsigned long long> done{0}, wide{0};
+  cudaError_t e = allow_shared(streamkl_paged_resize_kernel, done, resize_shared(kMaxTableRows, kResizeRounds));
   if (e != cudaSuccess) return e;
+  // as many blocks as look at all pages in one round; sixteen of a cluster have to be asked for
   int blocks = 1;
-  while (blocks < 8 && static_cast<long long>(blocks) * kBlockPages < a.num_pages) blocks *= 2;
+  while (blocks < kResizeBlocks && static_cast<long long>(blocks) * kBlockPages < a.num_pages) blocks *= 2;
+  if (blocks > 8 && (e = once_per_device(wide, [] {
+                       return cudaFuncSetAttribute(streamkl_paged_resize_kernel,
+                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                     })) != cudaSuccess)
+    return e;
+  const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
+                                      (static_cast<long long>(blocks) * kBlockPages));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kResizeThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B));
+  cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B, rounds));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -556,7 +556,8 @@ streamkl_status streamkl_paged_copy(const streamkl_page_copy_args* args, void* s
  * The two calls below keep that so; a table is filled by streamkl_paged_resize
  * from lengths of 0, counts of 0 and entries of -1. Both change their arguments
  * in place; a call that sets STREAMKL_ERR_INVALID_ARG has found numbers that do
- * not fit, left those out and done the rest. B is at most 8192.
+ * not fit, left those out and done the rest. B is at most 8192, num_pages 2^23,
+ * B * max_pages 2^30.
  *
  * streamkl_paged_fork: every sequence b becomes a copy of what source[b] was, for
  * all b at once (source[b] = b: it stays): entries, length and the pages' counts.
@@ -586,7 +587,7 @@ streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream
  * Where free pages do not suffice, a sequence is served if all that is asked up to
  * and with it is there, or it asks for none (and grows into no shared page); the
  * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set.
- * page_refs and copies are 16 and 8-byte aligned; B * max_pages is at most 2^30.
+ * page_refs and copies are 16 and 8-byte aligned.
  */
 typedef struct {
   size_t struct_size;
