@@ -159,7 +159,7 @@ struct ResizeArgs {
   int* dev_status;
 };
 
-constexpr int kMaxTableRows = 8192;    // sequences of a fork or resize call
+constexpr int kMaxTableRows = 4096;    // sequences of a fork or resize call
 constexpr int kMaxPages = 1 << 23;     // pages of a cache that resize looks after
 
 // Blocks of the backward's persistent grid (its partials' row count).

@@ -265,11 +265,12 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
   extern __shared__ int sm[];
-  int* sums = sm;            // [B + 1]
+  int* sums = sm;              // [B + 1]
   int* from = sums + a.B + 1;  // lengths; a sequence whose numbers do not fit stays
   int* to = from + a.B;
-  int* last = to + a.B;      // a last page to be copied; kNone, kKeeps: the last of those that hold it
-  uint32_t* bits = reinterpret_cast<uint32_t*>(last + a.B);  // [rounds][threads]: free pages
+  int* last = to + a.B;        // a last page to be copied; kNone, kKeeps: the last of those that hold it
+  uint16_t* lists = reinterpret_cast<uint16_t*>(last + a.B);  // [warps][1,024] pages of a warp's
+  uint32_t* bits = reinterpret_cast<uint32_t*>(lists + kResizeWarps * 1024);  // [rounds][threads]: free pages
   constexpr int kNone = -1, kKeeps = -2;
   __shared__ int scratch[kResizeWarps];
   __shared__ int counts[2][kResizeBlocks];  // free pages of the blocks, by the round's parity
@@ -417,9 +418,10 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     int at = ranks[r] + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scratch[lane] : 0);  // of this warp's first free page
     __syncthreads();
     if (mine == 0 || at >= limit) continue;
-    const int lo = find_sequence(sums, 0, a.B - 1, at);
-    const int hi = find_sequence(sums, lo, a.B - 1, min(limit, at + mine) - 1);
-    const int base = (r * blocks + me) * kBlockPages + warp * 1024 + 4 * lane;
+    // in a list first, so that the lanes take one page each (most threads have none
+    // or several of their own, 32 turns a warp: a step of 64 sequences 14.0 us)
+    uint16_t* list = lists + warp * 1024;
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t four = free >> (4 * i) & 15;
@@ -431,24 +433,29 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
         all += __popc(lanes);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int slot = at + below + __popc(four & ((1u << e) - 1));
-        if (!(four >> e & 1) || slot >= limit) continue;
-        const int p = base + 128 * i + e;
-        const int b = find_sequence(sums, lo, hi, slot);
-        int* entry = a.table + b * a.table_sb + pages_of(from[b]) + (slot - sums[b]);
-        a.refs[p] = 1;
-        if (last[b] >= 0) {
-          --entry;  // the copy comes first, in the last page's place
-          if (slot == sums[b]) {
-            a.copies[b] = make_int2(last[b], p);
-            atomicSub(a.refs + last[b], 1);
-          }
-        }
-        *entry = p;
-      }
-      at += all;
+      for (int e = 0; e < 4; ++e)
+        if (four >> e & 1) list[n + below + __popc(four & ((1u << e) - 1))] = static_cast<uint16_t>(128 * i + 4 * lane + e);
+      n += all;
     }
+    __syncwarp();
+    n = min(n, limit - at);
+    const int lo = find_sequence(sums, 0, a.B - 1, at), hi = find_sequence(sums, lo, a.B - 1, at + n - 1);
+    const int base = (r * blocks + me) * kBlockPages + warp * 1024;
+    for (int x = lane; x < n; x += 32) {
+      const int p = base + list[x], slot = at + x;
+      const int b = find_sequence(sums, lo, hi, slot);
+      int* entry = a.table + b * a.table_sb + pages_of(from[b]) + (slot - sums[b]);
+      a.refs[p] = 1;
+      if (last[b] >= 0) {
+        --entry;  // the copy comes first, in the last page's place
+        if (slot == sums[b]) {
+          a.copies[b] = make_int2(last[b], p);
+          atomicSub(a.refs + last[b], 1);
+        }
+      }
+      *entry = p;
+    }
+    __syncwarp();
   }
   // ---- lengths (which every block has read, before the barriers above)
   if (me == 0) {
@@ -461,7 +468,9 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   }
 }
 
-int resize_shared(int B, int rounds) { return (4 * B + 1 + rounds * kResizeThreads) * static_cast<int>(sizeof(int)); }
+int resize_shared(int B, int rounds) {
+  return (4 * B + 1 + (rounds + 16) * kResizeThreads) * static_cast<int>(sizeof(int));  // (lists: 2 KB a warp)
+}
 
 template <typename F>
 cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {

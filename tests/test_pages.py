@@ -85,7 +85,7 @@ def test_oracle_keeps_the_invariant_and_runs_dry():
     (1, 1, 1, 16, None), (1, 5, 7, 16, 9), (3, 4, 13, 1024, None), (7, 33, 130, 32, 40), (64, 20, 700, 16, None),
     (65, 17, 33001, 64, 19), (300, 9, 1025, 16, None), (1100, 6, 4096, 16, None), (40, 1000, 70003, 16, None),
     (30, 9000, 300001, 16, None),
-    (20, 40000, 1100000, 16, None), (8192, 3, 20000, 16, None),
+    (20, 40000, 1100000, 16, None), (4096, 3, 9000, 16, None),
 ])
 def test_random_steps(B, width, pages, page, stride):
     """Sequences grow, shrink, end and go on from one another; some steps ask for more pages than there are."""
@@ -443,7 +443,7 @@ CACHES = [(dict(struct_size=8), 1), (dict(dtype=2), 2), (dict(d=80), 2), (dict(H
           (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=2048), 2), (dict(k_cache__data=None), 1),
           (dict(v_cache__data=4100), 1), (dict(k_cache__stride=(2048, 1024, 60)), 1), (dict(v_cache__stride=(0, 1024, 64)), 1),
           (dict(k_cache__stride=(1024, 1024, 64)), 1), (dict(dev_status=None), 1)]
-TABLES = [(dict(struct_size=8), 1), (dict(B=0), 1), (dict(B=8193), 2), (dict(num_pages=0), 1), (dict(num_pages=(1 << 23) + 1), 2), (dict(max_pages=0), 1),
+TABLES = [(dict(struct_size=8), 1), (dict(B=0), 1), (dict(B=4097), 2), (dict(num_pages=0), 1), (dict(num_pages=(1 << 23) + 1), 2), (dict(max_pages=0), 1),
           (dict(max_pages=1 << 30, table_stride=1 << 30), 2), (dict(page_refs=None), 1), (dict(block_table=None), 1),
           (dict(kv_lens=None), 1), (dict(table_stride=3), 1), (dict(dev_status=None), 1)]
 
