@@ -619,8 +619,8 @@ streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* st
   if (!u.copies || reinterpret_cast<uintptr_t>(u.copies) % 8)
     return fail(STREAMKL_ERR_INVALID_ARG, "copies must be an 8-byte aligned address");
   skl::ResizeArgs a{u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.new_lens, reinterpret_cast<int2*>(u.copies), u.B,
-                    u.num_pages, u.max_pages, __builtin_ctz(static_cast<unsigned>(u.page_size)), u.dev_status};
-  cudaError_t e = skl::launch_resize(a, static_cast<cudaStream_t>(stream));
+                    u.num_pages, u.max_pages, __builtin_ctz(static_cast<unsigned>(u.page_size)), 0, u.dev_status};
+  cudaError_t e = skl::launch_resize(a, num_sms(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "resize launch");
 }
 

@@ -156,6 +156,7 @@ struct ResizeArgs {
   const int* new_lens;
   int2* copies;
   int B, num_pages, max_pages, page_shift;
+  int released;              // set by the launcher: pages are given back by a kernel before
   int* dev_status;
 };
 
@@ -183,6 +184,6 @@ cudaError_t launch_tree(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_page_copy(PageCopyArgs& a, cudaStream_t stream);
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
 cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream);
+cudaError_t launch_resize(ResizeArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace skl

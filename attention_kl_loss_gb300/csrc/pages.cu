@@ -220,10 +220,10 @@ static_assert(kMaxPages % (kBlockPages * kResizeBlocks) == 0);
 constexpr int kResizeRounds = kMaxPages / (kBlockPages * kResizeBlocks);
 
 // Exclusive sums of value(b) over b < B into out[0 .. B]; returns the total. All
-// threads; two barriers, and one before the next use of `sums`.
-template <typename F>
+// threads; two barriers, and one before the next use of `sums` [32].
+template <int THREADS, typename F>
 __device__ __forceinline__ int scan_sequences(int B, int* out, int* sums, F&& value) {
-  const int per = (B + kResizeThreads - 1) / kResizeThreads;
+  const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += value(b);
@@ -236,12 +236,13 @@ __device__ __forceinline__ int scan_sequences(int B, int* out, int* sums, F&& va
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  const int w = sums[lane];  // (32 warps)
+  const int w = lane < THREADS / 32 ? sums[lane] : 0;
   const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0), total = __reduce_add_sync(0xFFFFFFFFu, w);
   int at = before + upto - mine;
   for (int b = b0; b < b1; ++b) {
+    const int v = value(b);  // (it may lie in out)
     out[b] = at;
-    at += value(b);
+    at += v;
   }
   if (threadIdx.x == 0) out[B] = total;
   __syncthreads();
@@ -260,6 +261,67 @@ __device__ __forceinline__ int find_sequence(const int* sums, int lo, int hi, in
   return lo;
 }
 
+// What a sequence's numbers ask for; false where they do not fit.
+__device__ __forceinline__ bool lengths_fit(const ResizeArgs& a, int from, int to) {
+  const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
+  return from >= 0 && from <= most && to >= 0 && to <= most;
+}
+
+__device__ __forceinline__ void take_back(const ResizeArgs& a, int p) {
+  if (p >= 0 && p < a.num_pages)
+    atomicSub(a.refs + p, 1);
+  else
+    atomicCAS(a.dev_status, 0, kStatusInvalidArg);
+}
+
+// Entries from_pages(b) + i, i below the sums' differences, of all sequences: runs of
+// 128 a warp, most of which lie in one sequence.
+template <typename F>
+__device__ __forceinline__ void give_back(const ResizeArgs& a, const int* sums, int total, int warp, int warps, F&& first) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = warp * 128; i0 < total; i0 += warps * 128) {
+    const int lo = find_sequence(sums, 0, a.B - 1, i0);
+    const int hi = find_sequence(sums, lo, a.B - 1, min(total, i0 + 128) - 1);
+    int p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i >= total) continue;
+      const int b = find_sequence(sums, lo, hi, i);
+      int* entry = a.table + b * a.table_sb + first(b) + (i - sums[b]);
+      p[u] = *entry;
+      *entry = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + 32 * u + lane < total) take_back(a, p[u]);
+  }
+}
+
+// Large tables: what is given back, by blocks on every SM before the cluster (an SM
+// makes an atomic on scattered counts every three cycles: 667,000 of them on sixteen
+// SMs took 68 of 99 us).
+constexpr int kReleaseThreads = 256;
+constexpr long long kReleaseEntries = 1 << 18;  // of the tables, from which on
+
+__global__ void __launch_bounds__(kReleaseThreads) streamkl_paged_release_kernel(const __grid_constant__ ResizeArgs a) {
+  extern __shared__ int sm[];
+  __shared__ int scratch[32];
+  int *sums = sm, *first = sm + a.B + 1;
+  grid_launch_dependents();
+  const int page = 1 << a.page_shift;
+  for (int b = threadIdx.x; b < a.B; b += kReleaseThreads) {
+    const int from = a.kv_lens[b], to = __ldg(a.new_lens + b);
+    const bool fits = lengths_fit(a, from, to);
+    first[b] = fits ? (to + page - 1) >> a.page_shift : 0;
+    sums[b] = fits ? max(0, ((from + page - 1) >> a.page_shift) - first[b]) : 0;
+  }
+  __syncthreads();
+  const int total = scan_sequences<kReleaseThreads>(a.B, sums, scratch, [&](int b) { return sums[b]; });
+  give_back(a, sums, total, static_cast<int>(blockIdx.x * (kReleaseThreads / 32) + (threadIdx.x >> 5)),
+            static_cast<int>(gridDim.x * (kReleaseThreads / 32)), [&](int b) { return first[b]; });
+}
+
 __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kernel(const __grid_constant__ ResizeArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -272,55 +334,56 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   uint16_t* lists = reinterpret_cast<uint16_t*>(last + a.B);  // [warps][1,024] pages of a warp's
   uint32_t* bits = reinterpret_cast<uint32_t*>(lists + kResizeWarps * 1024);  // [rounds][threads]: free pages
   constexpr int kNone = -1, kKeeps = -2;
+  constexpr int kShort = 4;  // entries given back that a sequence's own thread takes
   __shared__ int scratch[kResizeWarps];
   __shared__ int counts[2][kResizeBlocks];  // free pages of the blocks, by the round's parity
   __shared__ int ranks[kResizeRounds + 1];  // of a round's first free page in this block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << a.page_shift;
-  const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
   auto pages_of = [&](int length) { return (length + page - 1) >> a.page_shift; };
+  auto back_of = [&](int b) { return max(0, pages_of(from[b]) - pages_of(to[b])); };
+  bool many = false;  // entries of some sequence to be given back
   for (int b = tid; b < a.B; b += kResizeThreads) {
     int f = a.kv_lens[b], t = __ldg(a.new_lens + b), p = kNone;
-    if (f < 0 || f > most || t < 0 || t > most) {
+    int* row = a.table + b * a.table_sb;
+    if (!lengths_fit(a, f, t)) {
       if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
       f = t = 0;
     } else if (t > f && (f & (page - 1)) != 0) {  // it grows into its last page
-      p = a.table[b * a.table_sb + (f >> a.page_shift)];
+      p = row[f >> a.page_shift];
       if (p < 0 || p >= a.num_pages) {
         if (me == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
         p = kNone;
+      }
+    } else if (!a.released) {
+      const int n = pages_of(f) - pages_of(t);
+      many = many || n > kShort;
+      if (n > 0 && n <= kShort && me == 0) {
+        int old[kShort];
+        row += pages_of(t);
+#pragma unroll
+        for (int i = 0; i < kShort; ++i)
+          if (i < n) old[i] = row[i];
+#pragma unroll
+        for (int i = 0; i < kShort; ++i)
+          if (i < n) {
+            row[i] = -1;
+            take_back(a, old[i]);
+          }
       }
     }
     from[b] = f;
     to[b] = t;
     last[b] = p;
   }
-  __syncthreads();
-  // ---- what is given back: runs of 128 entries a warp, most of one sequence
-  const int back = scan_sequences(a.B, sums, scratch, [&](int b) { return max(0, pages_of(from[b]) - pages_of(to[b])); });
-  for (int i0 = (me * kResizeWarps + warp) * 128; i0 < back; i0 += blocks * kResizeWarps * 128) {
-    const int lo = find_sequence(sums, 0, a.B - 1, i0);
-    const int hi = find_sequence(sums, lo, a.B - 1, min(back, i0 + 128) - 1);
-    int p[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + 32 * u + lane;
-      if (i >= back) continue;
-      const int b = find_sequence(sums, lo, hi, i);
-      int* entry = a.table + b * a.table_sb + pages_of(to[b]) + (i - sums[b]);
-      p[u] = *entry;
-      *entry = -1;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (i0 + 32 * u + lane >= back) continue;
-      if (p[u] >= 0 && p[u] < a.num_pages)
-        atomicSub(a.refs + p[u], 1);
-      else
-        atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-    }
+  if (__syncthreads_or(many)) {
+    const int back = scan_sequences<kResizeThreads>(a.B, sums, scratch, [&](int b) {
+      const int n = back_of(b);
+      return n > kShort ? n : 0;
+    });
+    give_back(a, sums, back, me * kResizeWarps + warp, blocks * kResizeWarps, [&](int b) { return pages_of(to[b]); });
   }
-  if (back > 0) __threadfence();
+  if (a.released) grid_dependency_wait();  // the other kernel has given back
   cluster.sync();
   // ---- free pages: bit 4 i + e of a thread: page base + 128 i + 4 lane + e of its warp's 1,024
   auto look = [&](int round) {
@@ -361,16 +424,18 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
       const int b = a.B - 1 - b0 - tid;
       bool keeps = false;
       if (b >= 0 && last[b] >= 0) {
+        const int p = last[b];
         int before = 0;
-        for (int i = 0; i < b; ++i) before += last[i] == last[b];
-        keeps = __ldcg(a.refs + last[b]) - before <= 1;
+#pragma unroll 8
+        for (int i = 0; i < b; ++i) before += last[i] == p;
+        keeps = __ldcg(a.refs + p) - before <= 1;
       }
       __syncthreads();
       if (keeps) last[b] = kKeeps;
     }
     __syncthreads();
   }
-  const int asked = scan_sequences(a.B, sums, scratch, [&](int b) {
+  const int asked = scan_sequences<kResizeThreads>(a.B, sums, scratch, [&](int b) {
     return max(0, pages_of(to[b]) - pages_of(from[b])) + (last[b] >= 0);
   });
   // ---- enough of the free pages, lowest numbers first
@@ -524,7 +589,7 @@ cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream) {
+cudaError_t launch_resize(ResizeArgs& a, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0}, wide{0};
   cudaError_t e = allow_shared(streamkl_paged_resize_kernel, done, resize_shared(kMaxTableRows, kResizeRounds));
   if (e != cudaSuccess) return e;
@@ -538,17 +603,25 @@ cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t stream) {
     return e;
   const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
                                       (static_cast<long long>(blocks) * kBlockPages));
+  a.released = static_cast<long long>(a.B) * a.max_pages > kReleaseEntries && a.num_pages > kReleaseEntries / 4;
+  if (a.released) {
+    const size_t bytes = (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
+    streamkl_paged_release_kernel<<<2 * sms, kReleaseThreads, bytes, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kResizeThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B, rounds));
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.released ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, streamkl_paged_resize_kernel, a);
 }
 
