@@ -243,12 +243,18 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
 // Of drafted tokens: few rows as above, more on one persistent CTA an SM.
 AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   const long long rows = static_cast<long long>(max_q) * (HQ / HK);
-  if (rows <= skl::kDecodeRows) return attn_plan(B, B, HQ, HK, d, max_q, max_kv, 0);
+  // (one tile at least for a CTA: one sequence of 2,048 keys, 32 rows 12.8 us, with two
+  // 13.6, with four 15.4; four of 1,024 keys, 64 rows of d = 64 12.3, 15.4 and 18.5)
+  if (rows <= skl::kDecodeRows) {
+    AttnPlan p = attn_plan(B, B, HQ, HK, d, max_q, max_kv, 0);
+    p.split_tiles = 1;
+    return p;
+  }
   AttnPlan p{};
+  p.split_tiles = 1;
   p.row_tiles = rows > 128 ? 2 : 1;
   const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
   const long long tiles = std::max(1, (max_kv + 127) / 128);
-  p.split_tiles = 2;
   const int per_sm = d == 64 && p.row_tiles == 1 ? 2 : 1;
   p.decode_ctas = static_cast<int>(std::min<long long>(B * HK * blocks * tiles, per_sm * num_sms()));
   return p;

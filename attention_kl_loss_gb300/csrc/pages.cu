@@ -71,15 +71,15 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int b) {
 }
 
 // THREADS threads an item: a warp each where few rows are kept, else a block for
-// 64 bytes of its columns (whole sequences are pruned: the longest one decides, and
-// in whole rows 16 blocks would have it to themselves: 8 sequences of up to 4,100
-// kept rows, 8 heads of 128, 73 us). The next rows' numbers are loaded beside the rows.
+// 32 bytes of its columns (whole sequences are pruned, and the longest one decides: 8
+// sequences of up to 4,100 kept rows, 8 heads of 128 take 27 us, 30 by 64 bytes, 73
+// by whole rows and 512 threads). The next rows' numbers are loaded beside the rows.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
+__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ? 1 : 3)
     streamkl_paged_compact_kernel(const __grid_constant__ CompactArgs a) {
   constexpr bool WARP = THREADS == 32;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int split = WARP ? 0 : a.vshift - 2, vshift = a.vshift - split;  // column groups; vectors a row in one
+  const int split = WARP ? 0 : a.vshift - 1, vshift = a.vshift - split;  // column groups; vectors a row in one
   const long long item = WARP ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x >> split;
   if (item >= 2LL * a.B * a.H) return;
   auto together = [](bool p) { return WARP ? __all_sync(0xFFFFFFFFu, p) != 0 : __syncthreads_and(p) != 0; };
@@ -89,10 +89,19 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
   const CompactSeq s = compact_seq(a, b);
   const int* kept = a.kept + b * a.kept_sb;
   bool good = s.ok;
-  // the list, before anything moves
-  for (int i = tid; good && i < s.count; i += THREADS) {
-    const int k = __ldg(kept + i);
-    good = k < s.n && k >= (i > 0 ? __ldg(kept + i - 1) + 1 : 0);
+  // the list, before anything moves (eight numbers in flight: a block of its own
+  // columns looks at all of it)
+  for (int i0 = tid; good && i0 < s.count; i0 += THREADS * 8) {
+    int now[8], before[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * THREADS;
+      now[u] = i < s.count ? __ldg(kept + i) : 0;
+      before[u] = i < s.count && i > 0 ? __ldg(kept + i - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u * THREADS < s.count) good = good && now[u] < s.n && now[u] > before[u] && now[u] >= 0;
   }
   if (!together(good)) {
     if (tid == 0 && rest == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
@@ -572,7 +581,7 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
   if (a.max_kept <= 2 * kCompactRun * (32 >> a.vshift))
     streamkl_paged_compact_kernel<32><<<static_cast<unsigned>((items + 3) / 4), 128, 0, stream>>>(a);
   else
-    streamkl_paged_compact_kernel<256><<<static_cast<unsigned>(items << (a.vshift - 2)), 256, 0, stream>>>(a);
+    streamkl_paged_compact_kernel<256><<<static_cast<unsigned>(items << (a.vshift - 1)), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
