@@ -222,11 +222,12 @@ __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const
 // the sequences (every block makes them for itself) and over the free pages (the
 // blocks share them, one bit each, and exchange their counts). Between them lies what
 // has to be in that order: pages given back, the counts of last pages, free pages.
-constexpr int kResizeThreads = 1024, kResizeWarps = kResizeThreads / 32;
-constexpr int kBlockPages = kResizeThreads * 32;  // a block's pages of a round
-constexpr int kResizeBlocks = 16;                 // most of a cluster
-static_assert(kMaxPages % (kBlockPages * kResizeBlocks) == 0);
-constexpr int kResizeRounds = kMaxPages / (kBlockPages * kResizeBlocks);
+//
+// 1,024 threads a block, or one block of 256 where tables and pages are few: barriers,
+// scans and looks of warps that have nothing to do are most of such a call.
+constexpr int kResizeBlocks = 16;  // most of a cluster
+constexpr int kResizeRounds = kMaxPages / (1024 * 32 * kResizeBlocks);  // a bit a page and thread, 32 in each
+static_assert(kMaxPages % (1024 * 32 * kResizeBlocks) == 0);
 
 // Exclusive sums of value(b) over b < B into out[0 .. B]; returns the total. All
 // threads; two barriers, and one before the next use of `sums` [32].
@@ -283,11 +284,21 @@ __device__ __forceinline__ void take_back(const ResizeArgs& a, int p) {
     atomicCAS(a.dev_status, 0, kStatusInvalidArg);
 }
 
-// Entries from_pages(b) + i, i below the sums' differences, of all sequences: runs of
-// 128 a warp, most of which lie in one sequence.
+// Entries first(b) + i, i below the sums' differences, of all sequences: a lane each
+// where that is enough, else runs of 128 a warp, most of which lie in one sequence.
 template <typename F>
 __device__ __forceinline__ void give_back(const ResizeArgs& a, const int* sums, int total, int warp, int warps, F&& first) {
   const int lane = threadIdx.x & 31;
+  if (total <= warps * 32) {
+    const int i = warp * 32 + lane;
+    if (i >= total) return;
+    const int b = find_sequence(sums, 0, a.B - 1, i);
+    int* entry = a.table + b * a.table_sb + first(b) + (i - sums[b]);
+    const int p = *entry;
+    *entry = -1;
+    take_back(a, p);
+    return;
+  }
   for (int i0 = warp * 128; i0 < total; i0 += warps * 128) {
     const int lo = find_sequence(sums, 0, a.B - 1, i0);
     const int hi = find_sequence(sums, lo, a.B - 1, min(total, i0 + 128) - 1);
@@ -331,8 +342,10 @@ __global__ void __launch_bounds__(kReleaseThreads) streamkl_paged_release_kernel
             static_cast<int>(gridDim.x * (kReleaseThreads / 32)), [&](int b) { return first[b]; });
 }
 
-__global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kernel(const __grid_constant__ ResizeArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) streamkl_paged_resize_kernel(const __grid_constant__ ResizeArgs a) {
   namespace cg = cooperative_groups;
+  constexpr int kWarps = THREADS / 32, kBlockPages = THREADS * 32;  // (a block's of a round)
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
   extern __shared__ int sm[];
@@ -340,11 +353,11 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   int* from = sums + a.B + 1;  // lengths; a sequence whose numbers do not fit stays
   int* to = from + a.B;
   int* last = to + a.B;        // a last page to be copied; kNone, kKeeps: the last of those that hold it
-  uint16_t* lists = reinterpret_cast<uint16_t*>(last + a.B);  // [warps][1,024] pages of a warp's
-  uint32_t* bits = reinterpret_cast<uint32_t*>(lists + kResizeWarps * 1024);  // [rounds][threads]: free pages
+  uint16_t* list = reinterpret_cast<uint16_t*>(last + a.B);  // [block's pages]: free ones of a round, in their order
+  uint32_t* bits = reinterpret_cast<uint32_t*>(list + kBlockPages);  // [rounds][threads]: free pages
   constexpr int kNone = -1, kKeeps = -2;
   constexpr int kShort = 4;  // entries given back that a sequence's own thread takes
-  __shared__ int scratch[kResizeWarps];
+  __shared__ int scratch[kWarps];
   __shared__ int counts[2][kResizeBlocks];  // free pages of the blocks, by the round's parity
   __shared__ int ranks[kResizeRounds + 1];  // of a round's first free page in this block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   auto pages_of = [&](int length) { return (length + page - 1) >> a.page_shift; };
   auto back_of = [&](int b) { return max(0, pages_of(from[b]) - pages_of(to[b])); };
   bool many = false;  // entries of some sequence to be given back
-  for (int b = tid; b < a.B; b += kResizeThreads) {
+  for (int b = tid; b < a.B; b += THREADS) {
     int f = a.kv_lens[b], t = __ldg(a.new_lens + b), p = kNone;
     int* row = a.table + b * a.table_sb;
     if (!lengths_fit(a, f, t)) {
@@ -386,42 +399,47 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     last[b] = p;
   }
   if (__syncthreads_or(many)) {
-    const int back = scan_sequences<kResizeThreads>(a.B, sums, scratch, [&](int b) {
+    const int back = scan_sequences<THREADS>(a.B, sums, scratch, [&](int b) {
       const int n = back_of(b);
       return n > kShort ? n : 0;
     });
-    give_back(a, sums, back, me * kResizeWarps + warp, blocks * kResizeWarps, [&](int b) { return pages_of(to[b]); });
+    give_back(a, sums, back, me * kWarps + warp, blocks * kWarps, [&](int b) { return pages_of(to[b]); });
   }
   if (a.released) grid_dependency_wait();  // the other kernel has given back
   cluster.sync();
   // ---- free pages: bit 4 i + e of a thread: page base + 128 i + 4 lane + e of its warp's 1,024
   auto look = [&](int round) {
-    const long long base = (static_cast<long long>(round) * blocks + me) * kBlockPages + warp * 1024 + lane * 4;
-    int4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long p = base + 128 * i;
-      v[i] = make_int4(1, 1, 1, 1);
-      if (p + 4 <= a.num_pages)
-        v[i] = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
-      else if (p < a.num_pages) {
-        v[i].x = __ldcg(a.refs + p);
-        if (p + 1 < a.num_pages) v[i].y = __ldcg(a.refs + p + 1);
-        if (p + 2 < a.num_pages) v[i].z = __ldcg(a.refs + p + 2);
-      }
-    }
+    const int base = (round * blocks + me) * kBlockPages + warp * 1024;
     uint32_t free = 0;
+    if (base < a.num_pages) {
+      const int* refs = a.refs + base + lane * 4;
+      int4 v[8];
+      if (base + 1024 <= a.num_pages) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      free |= static_cast<uint32_t>((v[i].x == 0) | (v[i].y == 0) << 1 | (v[i].z == 0) << 2 | (v[i].w == 0) << 3) << (4 * i);
-    bits[round * kResizeThreads + tid] = free;
+        for (int i = 0; i < 8; ++i) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + 128 * i));
+      } else {
+        const int left = a.num_pages - base - lane * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i].x = 128 * i < left ? __ldcg(refs + 128 * i) : 1;
+          v[i].y = 128 * i + 1 < left ? __ldcg(refs + 128 * i + 1) : 1;
+          v[i].z = 128 * i + 2 < left ? __ldcg(refs + 128 * i + 2) : 1;
+          v[i].w = 128 * i + 3 < left ? __ldcg(refs + 128 * i + 3) : 1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        free |= static_cast<uint32_t>((v[i].x == 0) | (v[i].y == 0) << 1 | (v[i].z == 0) << 2 | (v[i].w == 0) << 3)
+                << (4 * i);
+    }
+    bits[round * THREADS + tid] = free;
     return __popc(free);
   };
   // ---- last pages that others hold too (beside the first look at the counts)
   const int held = tid < a.B && last[tid] >= 0 ? __ldcg(a.refs + last[tid]) : 0;
   int seen = look(0);
   bool any = false;
-  for (int b = tid; b < a.B; b += kResizeThreads) {
+  for (int b = tid; b < a.B; b += THREADS) {
     if (last[b] < 0) continue;
     const bool shared = (b == tid ? held : __ldcg(a.refs + last[b])) > 1;
     any = any || shared;
@@ -429,7 +447,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   }
   if (__syncthreads_or(any)) {
     // in their order, each takes a copy while another holds the page
-    for (int b0 = 0; b0 < a.B; b0 += kResizeThreads) {  // (from the back, so that those before are as they were)
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {  // (from the back, so that those before are as they were)
       const int b = a.B - 1 - b0 - tid;
       bool keeps = false;
       if (b >= 0 && last[b] >= 0) {
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     }
     __syncthreads();
   }
-  const int asked = scan_sequences<kResizeThreads>(a.B, sums, scratch, [&](int b) {
+  const int asked = scan_sequences<THREADS>(a.B, sums, scratch, [&](int b) {
     return max(0, pages_of(to[b]) - pages_of(from[b])) + (last[b] >= 0);
   });
   // ---- enough of the free pages, lowest numbers first
@@ -456,7 +474,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
     const int mine = __reduce_add_sync(0xFFFFFFFFu, seen);
     if (lane == 0) scratch[warp] = mine;
     __syncthreads();
-    const int block = __reduce_add_sync(0xFFFFFFFFu, scratch[lane]);
+    const int block = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? scratch[lane] : 0);
     if (tid < blocks) *cluster.map_shared_rank(&counts[round & 1][me], tid) = block;
     cluster.sync();  // (and `scratch` may be used again)
     int before = found, total = found;
@@ -485,38 +503,43 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   __syncthreads();  // (ranks)
   for (int r = 0; r < round; ++r) {
     if (ranks[r] >= limit) break;
-    const uint32_t free = bits[r * kResizeThreads + tid];
+    // in a list first, so that all threads take one page each, whichever they found
+    const uint32_t free = bits[r * THREADS + tid];
     const int mine = __reduce_add_sync(0xFFFFFFFFu, __popc(free));
+    __syncthreads();  // (the list of the round before has been read)
     if (lane == 0) scratch[warp] = mine;
     __syncthreads();
-    int at = ranks[r] + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scratch[lane] : 0);  // of this warp's first free page
-    __syncthreads();
-    if (mine == 0 || at >= limit) continue;
-    // in a list first, so that the lanes take one page each (most threads have none
-    // or several of their own, 32 turns a warp: a step of 64 sequences 14.0 us)
-    uint16_t* list = lists + warp * 1024;
-    int n = 0;
+    const int count = lane < kWarps ? scratch[lane] : 0;
+    const int all = __reduce_add_sync(0xFFFFFFFFu, count);
+    int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? count : 0);  // of this warp's first free page
+    const int n = min(all, limit - ranks[r]);
+    if (mine > 0 && at < n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t four = free >> (4 * i) & 15;
-      int below = 0, all = 0;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t four = free >> (4 * i) & 15;
+        int below = 0, sum = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, four >> e & 1);
-        below += __popc(lanes & ((1u << lane) - 1));
-        all += __popc(lanes);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, four >> e & 1);
+          below += __popc(lanes & ((1u << lane) - 1));
+          sum += __popc(lanes);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (four >> e & 1)
+            list[at + below + __popc(four & ((1u << e) - 1))] = static_cast<uint16_t>(warp * 1024 + 128 * i + 4 * lane + e);
+        at += sum;
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (four >> e & 1) list[n + below + __popc(four & ((1u << e) - 1))] = static_cast<uint16_t>(128 * i + 4 * lane + e);
-      n += all;
     }
-    __syncwarp();
-    n = min(n, limit - at);
-    const int lo = find_sequence(sums, 0, a.B - 1, at), hi = find_sequence(sums, lo, a.B - 1, at + n - 1);
-    const int base = (r * blocks + me) * kBlockPages + warp * 1024;
-    for (int x = lane; x < n; x += 32) {
-      const int p = base + list[x], slot = at + x;
+    __syncthreads();
+    const int base = (r * blocks + me) * kBlockPages;
+    int lo = 0, hi = a.B - 1;
+    if (n > 2 * THREADS) {  // few sequences of them all, to be found once
+      lo = find_sequence(sums, lo, hi, ranks[r]);
+      hi = find_sequence(sums, lo, hi, ranks[r] + n - 1);
+    }
+    for (int x = tid; x < n; x += THREADS) {
+      const int p = base + list[x], slot = ranks[r] + x;
       const int b = find_sequence(sums, lo, hi, slot);
       int* entry = a.table + b * a.table_sb + pages_of(from[b]) + (slot - sums[b]);
       a.refs[p] = 1;
@@ -529,11 +552,10 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
       }
       *entry = p;
     }
-    __syncwarp();
   }
   // ---- lengths (which every block has read, before the barriers above)
   if (me == 0) {
-    for (int b = tid; b < a.B; b += kResizeThreads) {
+    for (int b = tid; b < a.B; b += THREADS) {
       const bool is_served = served(b);
       if (last[b] < 0 || !is_served) a.copies[b] = make_int2(-1, -1);
       if (is_served && from[b] != to[b]) a.kv_lens[b] = to[b];
@@ -542,8 +564,8 @@ __global__ void __launch_bounds__(kResizeThreads, 1) streamkl_paged_resize_kerne
   }
 }
 
-int resize_shared(int B, int rounds) {
-  return (4 * B + 1 + (rounds + 16) * kResizeThreads) * static_cast<int>(sizeof(int));  // (lists: 2 KB a warp)
+int resize_shared(int B, int rounds, int threads) {
+  return (4 * B + 1 + (rounds + 16) * threads) * static_cast<int>(sizeof(int));  // (the list: two bytes a page)
 }
 
 template <typename F>
@@ -600,18 +622,20 @@ cudaError_t launch_fork(ForkArgs& a, int sms, cudaStream_t stream) {
 
 cudaError_t launch_resize(ResizeArgs& a, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0}, wide{0};
-  cudaError_t e = allow_shared(streamkl_paged_resize_kernel, done, resize_shared(kMaxTableRows, kResizeRounds));
+  cudaError_t e = allow_shared(streamkl_paged_resize_kernel<1024>, done, resize_shared(kMaxTableRows, kResizeRounds, 1024));
   if (e != cudaSuccess) return e;
+  // 256 threads as long as they look at all pages in one round
+  const int threads = a.num_pages <= 256 * 32 && a.B <= 256 ? 256 : 1024;
   // as many blocks as look at all pages in one round; sixteen of a cluster have to be asked for
+  const long long block_pages = threads * 32;
   int blocks = 1;
-  while (blocks < kResizeBlocks && static_cast<long long>(blocks) * kBlockPages < a.num_pages) blocks *= 2;
+  while (blocks < kResizeBlocks && blocks * block_pages < a.num_pages) blocks *= 2;
   if (blocks > 8 && (e = once_per_device(wide, [] {
-                       return cudaFuncSetAttribute(streamkl_paged_resize_kernel,
+                       return cudaFuncSetAttribute(streamkl_paged_resize_kernel<1024>,
                                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
                      })) != cudaSuccess)
     return e;
-  const int rounds = static_cast<int>((a.num_pages + static_cast<long long>(blocks) * kBlockPages - 1) /
-                                      (static_cast<long long>(blocks) * kBlockPages));
+  const int rounds = static_cast<int>((a.num_pages + blocks * block_pages - 1) / (blocks * block_pages));
   a.released = static_cast<long long>(a.B) * a.max_pages > kReleaseEntries && a.num_pages > kReleaseEntries / 4;
   if (a.released) {
     const size_t bytes = (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
@@ -620,8 +644,8 @@ cudaError_t launch_resize(ResizeArgs& a, int sms, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kResizeThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B, rounds));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(resize_shared(a.B, rounds, threads));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -631,7 +655,8 @@ cudaError_t launch_resize(ResizeArgs& a, int sms, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.released ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, streamkl_paged_resize_kernel, a);
+  return threads == 256 ? cudaLaunchKernelEx(&cfg, streamkl_paged_resize_kernel<256>, a)
+                        : cudaLaunchKernelEx(&cfg, streamkl_paged_resize_kernel<1024>, a);
 }
 
 }  // namespace skl
