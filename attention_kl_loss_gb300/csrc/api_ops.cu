@@ -200,7 +200,10 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
     // the other way; 64 sequences of up to 256 keys, two a CTA, 19.1 -> 16.7, 100 of
     // up to 512 34.8 -> 32.3, of 1,024 50.8 -> 52.5 the other way)
     p.split_tiles = 2;  // (one tile each is level: one sequence of 4,096 keys 18.7 us against 18.4)
-    p.whole = (items + ctas - 1) / ctas * tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
+    // Whole items, nothing cut and nothing to join, unless the longest row of them is
+  // much more than an equal share
+  const long long row = (items + ctas - 1) / ctas * tiles, share = (items * tiles + ctas - 1) / ctas;
+  p.whole = row <= share + std::min<long long>(3 + 3 * share / 10, 8);
     p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
     return p;
   }
@@ -255,8 +258,10 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   p.row_tiles = rows > 128 ? 2 : 1;
   const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
   const long long tiles = std::max(1, (max_kv + 127) / 128);
-  const int per_sm = d == 64 && p.row_tiles == 1 ? 2 : 1;
-  p.decode_ctas = static_cast<int>(std::min<long long>(B * HK * blocks * tiles, per_sm * num_sms()));
+  const long long ctas = (d == 64 && p.row_tiles == 1 ? 2 : 1) * num_sms(), items = B * HK * blocks;
+  p.q_tiles = static_cast<int>(blocks);
+  p.whole = (items + ctas - 1) / ctas * tiles <= (items * tiles + ctas - 1) / ctas + 2;
+  p.decode_ctas = static_cast<int>(std::min(p.whole ? items : items * tiles, ctas));
   return p;
 }
 
@@ -269,7 +274,7 @@ size_t attn_part_rows(const AttnPlan& p, int T, int HQ) {
 }
 
 size_t attn_part_bytes(const AttnPlan& p, int T, int HQ, int d) {
-  const size_t cuts = p.decode_ctas > 0 && p.row_tiles > 0 ? p.decode_ctas * sizeof(skl::TreeCut) : 0;
+  const size_t cuts = p.decode_ctas > 0 && p.row_tiles > 0 && !p.whole ? p.decode_ctas * sizeof(skl::TreeCut) : 0;
   return (attn_part_rows(p, T, HQ) * (d + 1) * sizeof(float) + cuts + 255) & ~static_cast<size_t>(255);
 }
 

@@ -64,21 +64,6 @@ __device__ __forceinline__ bool status_stops(int before) {
   return before != 0 && before != kStatusInvalidArg && before != kStatusNoPages;
 }
 
-// A row of a drafted tree: which of 32 keys it sees, bit k for drafted token t + k
-// of its sequence's n. Tokens before the drafted ones (t + k < 0) are seen by
-// every row, those from n on (past the sequence's end) by none.
-__device__ __forceinline__ uint32_t tree_bits(const int* mask, int words, int n, int t) {
-  auto word = [&](int i) {
-    if (i < 0) return ~0u;
-    const int left = n - 32 * i;
-    if (i >= words || left <= 0) return 0u;
-    const uint32_t w = static_cast<uint32_t>(__ldg(mask + i));
-    return left < 32 ? w & ((1u << left) - 1) : w;
-  };
-  const int i = t >> 5;
-  return __funnelshift_r(word(i), word(i + 1), t & 31);
-}
-
 // The keys of a tile that a row sees: the first `seen`, or with TREE those whose
 // bit is set (`all`: every one of them).
 template <bool TREE>
@@ -94,13 +79,33 @@ struct TileMask<false> {
 template <>
 struct TileMask<true> {
   uint32_t bits[4];
-  bool all;
+  bool all;  // (the same in all rows that are there)
+  // Bit k of word q: key key0 + 32 q + k, which is drafted token t + k of the
+  // sequence's n. Tokens before the drafted ones (t + k < 0) are seen by every row,
+  // those from n on (past the sequence's end) by none.
   __device__ __forceinline__ TileMask(const PagedAttnArgs& a, bool live, int token, int n, int len, int, int key0) {
     const int t = key0 - (len - n);
     all = live && t + kTileN <= 0;
+    if (t + kTileN <= 0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      bits[q] = !live ? 0u : all ? ~0u : tree_bits(a.mask + token * a.mask_sn, a.mask_words, n, t + 32 * q);
+      for (int q = 0; q < 4; ++q) bits[q] = live ? ~0u : 0u;
+      return;
+    }
+    const int* row = a.mask + token * a.mask_sn;
+    const int first = t >> 5;  // (t may be negative)
+    uint32_t w[5];
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+      const int i = first + x, left = n - 32 * i;
+      w[x] = i >= 0 && i < a.mask_words && left > 0 && live ? static_cast<uint32_t>(__ldg(row + i)) : i < 0 && live ? ~0u : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+      const int left = n - 32 * (first + x);
+      if (left < 32) w[x] &= left > 0 ? (1u << left) - 1 : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) bits[q] = __funnelshift_r(w[q], w[q + 1], t & 31);
   }
   __device__ __forceinline__ bool partial() const { return !all; }
   __device__ __forceinline__ bool some() const { return (bits[0] | bits[1] | bits[2] | bits[3]) != 0; }

@@ -22,6 +22,7 @@
 // bits, shifted into place, before that tile's S is there.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "ops.h"
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     tmem_alloc(smem_u32(tmem_slot), L::TMEM);
     tmem_relinquish();
   }
-  // this CTA's stretch of the line of tiles; sequences without a key on the way
-  long long total;
-  const long long chunk = locate<L::THREADS>(a, kRows, scratch, start, &total, [&](int b, const Seq& s) {
+  // this CTA's stretch of the line of tiles, or whole items; sequences without a key on
+  // the way
+  auto visit = [&](int b, const Seq& s) {
     if (blockIdx.x == 0 && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
     if (s.n == 0 || s.tiles > 0 || b % gridDim.x != blockIdx.x) return;
     for (int r = 0; r < s.n * a.HQ; ++r) {
@@ -246,7 +247,14 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
       a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
     }
-  });
+  };
+  long long total = 0, chunk = 0;
+  if (a.whole) {
+    for (int b = threadIdx.x; b < a.B; b += L::THREADS)
+      if (blockIdx.x == 0 || b % gridDim.x == blockIdx.x) visit(b, load_seq(a, b, kRows));
+  } else {
+    chunk = locate<L::THREADS>(a, kRows, scratch, start, &total, visit);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -289,11 +297,19 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     // ------------------------------------------------------------ items
     long long left = *skip_flag ? 0 : max(0LL, min(total - blockIdx.x * chunk, chunk));
     int b = 0, hk = 0, rb = 0, tile = 0;
+    int item = *skip_flag ? INT_MAX : static_cast<int>(blockIdx.x);  // with whole items, every gridDim.x-th
     TreeCut cut{};  // the item that goes on in the next stretch
     if (left > 0) b = start->b, hk = start->hk, rb = start->rb, tile = start->tile;
     for (int it = 0;; ++it) {
       Seg sg{};
-      if (left > 0) {
+      if (a.whole) {
+        for (; item < a.B * a.HK * a.q_tiles && sg.n_iter == 0; item += gridDim.x) {
+          // (all first blocks of rows, then the second ones that there are, ..)
+          rb = item / (a.B * a.HK), b = item / a.HK - rb * a.B, hk = item % a.HK;
+          const Seq s = load_seq(a, b, kRows);
+          if (rb < s.blocks) sg = {b, hk, rb, 0, s.tiles, s.tok0, s.n, s.len, -1};
+        }
+      } else if (left > 0) {
         Seq s = load_seq(a, b, kRows);
         while (s.tiles == 0) s = load_seq(a, ++b, kRows);  // (b < B: tiles are left)
         sg = {b, hk, rb, tile, static_cast<int>(min(left, static_cast<long long>(s.tiles - tile))), s.tok0, s.n, s.len, 0};
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       __syncwarp();
       if (sg.n_iter == 0) break;
     }
-    if (lane == 0) a.cuts[blockIdx.x] = cut;
+    if (!a.whole && lane == 0) a.cuts[blockIdx.x] = cut;
   } else if (warp != 1) {
     // ------------------------------------------------------ loads of K or V
     const bool is_v = warp == 2;
@@ -775,25 +791,37 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         uint8_t* mine = !live  ? nullptr
                         : parts ? reinterpret_cast<uint8_t*>(a.part_o + part * D)
                                 : reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
+        uint8_t* row_out[8];  // of the rows that this lane writes a piece of
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row_out[i] = shfl_ptr(mine, 4 * i + (lane >> 3));
         auto write_out = [&](int byte) {  // 128 bytes of each row from this one on
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const int r = i + (lane >> 3);
-            uint8_t* row_out = shfl_ptr(mine, r);
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
             uint4 v;
             ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-            if (row_out != nullptr) *reinterpret_cast<uint4*>(row_out + byte + (lane & 7) * 16) = v;
+            if (row_out[i] != nullptr) *reinterpret_cast<uint4*>(row_out[i] + byte + (lane & 7) * 16) = v;
           }
           __syncwarp();
         };
+        // (a row that saw no key holds 0 times whatever V's rows are)
+        const bool any_none = __any_sync(0xFFFFFFFFu, none);
+        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           float o[32];
           tmem_ld32(to + 32 * q, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = none ? 0.f : o[k] * inv;
+          for (int k = 0; k < 32; k += 2) {
+            const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), inv2);
+            o[k] = x.x, o[k + 1] = x.y;
+          }
+          if (any_none) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = none ? 0.f : o[k];
+          }
           if (parts) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -907,7 +935,7 @@ cudaError_t tree_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   }
   kern<<<ctas, L::THREADS, L::BYTES, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole) return e;
   const long long most = std::min<long long>(static_cast<long long>(a.max_q) * (a.HQ / a.HK), kTileM * NT);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((most + kJoinWarps - 1) / kJoinWarps));
