@@ -203,7 +203,7 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
     // Whole items, nothing cut and nothing to join, unless the longest row of them is
   // much more than an equal share
   const long long row = (items + ctas - 1) / ctas * tiles, share = (items * tiles + ctas - 1) / ctas;
-  p.whole = row <= share + std::min<long long>(3 + 3 * share / 10, 8);
+  p.whole = items < (1 << 30) && row <= share + std::min<long long>(3 + 3 * share / 10, 8);
     p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
     return p;
   }

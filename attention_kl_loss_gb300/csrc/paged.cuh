@@ -66,7 +66,7 @@ __device__ __forceinline__ bool status_stops(int before) {
 
 // The keys of a tile that a row sees: the first `seen`, or with TREE those whose
 // bit is set (`all`: every one of them).
-template <bool TREE>
+template <bool TREE, int WORDS = kTileN / 32>
 struct TileMask;
 template <>
 struct TileMask<false> {
@@ -76,39 +76,44 @@ struct TileMask<false> {
   __device__ __forceinline__ bool some() const { return seen > 0; }
   __device__ __forceinline__ bool hides(int k) const { return k >= seen; }
 };
-template <>
-struct TileMask<true> {
-  uint32_t bits[4];
+template <int WORDS>  // of 32 keys, from key0 on
+struct TileMask<true, WORDS> {
+  uint32_t bits[WORDS];
   bool all;  // (the same in all rows that are there)
   // Bit k of word q: key key0 + 32 q + k, which is drafted token t + k of the
   // sequence's n. Tokens before the drafted ones (t + k < 0) are seen by every row,
   // those from n on (past the sequence's end) by none.
   __device__ __forceinline__ TileMask(const PagedAttnArgs& a, bool live, int token, int n, int len, int, int key0) {
     const int t = key0 - (len - n);
-    all = live && t + kTileN <= 0;
-    if (t + kTileN <= 0) {
+    all = live && t + 32 * WORDS <= 0;
+    if (t + 32 * WORDS <= 0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) bits[q] = live ? ~0u : 0u;
+      for (int q = 0; q < WORDS; ++q) bits[q] = live ? ~0u : 0u;
       return;
     }
     const int* row = a.mask + token * a.mask_sn;
     const int first = t >> 5;  // (t may be negative)
-    uint32_t w[5];
+    uint32_t w[WORDS + 1];
 #pragma unroll
-    for (int x = 0; x < 5; ++x) {
+    for (int x = 0; x < WORDS + 1; ++x) {
       const int i = first + x, left = n - 32 * i;
       w[x] = i >= 0 && i < a.mask_words && left > 0 && live ? static_cast<uint32_t>(__ldg(row + i)) : i < 0 && live ? ~0u : 0u;
     }
 #pragma unroll
-    for (int x = 0; x < 5; ++x) {
+    for (int x = 0; x < WORDS + 1; ++x) {
       const int left = n - 32 * (first + x);
       if (left < 32) w[x] &= left > 0 ? (1u << left) - 1 : 0u;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) bits[q] = __funnelshift_r(w[q], w[q + 1], t & 31);
+    for (int q = 0; q < WORDS; ++q) bits[q] = __funnelshift_r(w[q], w[q + 1], t & 31);
   }
   __device__ __forceinline__ bool partial() const { return !all; }
-  __device__ __forceinline__ bool some() const { return (bits[0] | bits[1] | bits[2] | bits[3]) != 0; }
+  __device__ __forceinline__ bool some() const {
+    uint32_t any = 0;
+#pragma unroll
+    for (int q = 0; q < WORDS; ++q) any |= bits[q];
+    return any != 0;
+  }
   __device__ __forceinline__ bool hides(int k) const { return !(bits[k >> 5] >> (k & 31) & 1); }
 };
 

@@ -61,13 +61,20 @@ struct TreeLayout {
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
   // P in columns of its own, where TMEM has room for them; else in S's place
   static constexpr bool OWN_P = D == 64 || NT == 1;
+  // Softmax warpgroups of a row tile, each with half of a key tile's columns where
+  // there are two: one warp of a scheduler waits for its own instructions most of
+  // the time
+  static constexpr int HALVES = D == 128 && NT == 1 ? 2 : 1;
+  static constexpr int CW = kTileN / HALVES;      // columns of S of a thread
+  static constexpr int WARPS = 4 * NT * HALVES;   // of the softmax
   // q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], s_read, p_read,
-  // drain, p_first[2], o_first[2], seg_full[kSegs], seg_empty[kSegs]
-  static constexpr int NBAR = 2 + 2 * STAGES + 13 + 2 * kSegs;
+  // drain, p_first[2], o_first[2], seg_full[kSegs], seg_empty[kSegs], pair[4]
+  static constexpr int NBAR = 2 + 2 * STAGES + 13 + 2 * kSegs + 4;
   static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = (OFF_SEG + kSegs * static_cast<int>(sizeof(Seg)) + 15) / 16 * 16;
-  static constexpr int THREADS = 128 + 128 * NT;
-  static constexpr int BYTES = OFF_MISC + 32 + THREADS / 32 * 8;
+  static constexpr int THREADS = 128 + 32 * WARPS;
+  static constexpr int OFF_PAIR = OFF_MISC + 32 + THREADS / 32 * 8;  // [2][halves][rows] floats
+  static constexpr int BYTES = OFF_PAIR + (HALVES == 2 ? 2 * 2 * kTileM * 4 : 0);
   static_assert(PER_SM == 1 ? BYTES <= 232448 : 2 * (BYTES + 1024) <= 233472, "shared memory budget");
   static constexpr int col_s(int t) { return 128 * t; }
   static constexpr int col_p(int t) { return OWN_P ? 128 * NT + 64 * t : 128 * t; }
@@ -156,6 +163,15 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+__device__ __forceinline__ void st_shared_f32(uint32_t at, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
 // Lane `from`'s pointer.
 template <typename T>
 __device__ __forceinline__ T* shfl_ptr(T* p, int from) {
@@ -186,7 +202,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
   auto o_first = [&](int k) { return rest + 8u * (11 + k); };
   auto seg_full = [&](int k) { return rest + 8u * (13 + k); };
   auto seg_empty = [&](int k) { return rest + 8u * (13 + kSegs + k); };
-  static_assert(2 + 2 * L::STAGES + 13 + 2 * kSegs == L::NBAR, "barrier region holds every barrier");
+  auto pair = [&](int k) { return rest + 8u * (13 + 2 * kSegs + k); };
+  static_assert(2 + 2 * L::STAGES + 13 + 2 * kSegs + 4 == L::NBAR, "barrier region holds every barrier");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 4);
   volatile int* skip_flag = reinterpret_cast<volatile int*>(gb + L::OFF_MISC + 8);
@@ -203,24 +220,25 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     if (kDeviceChecks)
       for (int i = 0; i < L::NBAR; ++i) lay_ok = lay_ok && check_bar(ck, bar0 + 8u * i, __LINE__);
     if (lay_ok) {
-      for (int k = 0; k < 2; ++k) mbar_init(bar0 + 8u * k, 4 * NT);  // q_full: one arrival per softmax warp
+      for (int k = 0; k < 2; ++k) mbar_init(bar0 + 8u * k, L::WARPS);  // q_full: one arrival per softmax warp
       for (int s = 0; s < L::STAGES; ++s) {
         mbar_init(kv_full(s), 1);
         mbar_init(kv_empty(s), NT);
       }
       for (int k = 0; k < 2; ++k) {
         mbar_init(s_full(k), 1);
-        mbar_init(p_full(k), L::OWN_P ? 4 * NT : 4);
+        mbar_init(p_full(k), L::OWN_P ? L::WARPS : 4);
         mbar_init(o_full(k), 1);
         mbar_init(p_first(k), 4);
         mbar_init(o_first(k), 1);
       }
-      mbar_init(s_read, 4 * NT);
+      mbar_init(s_read, L::WARPS);
       mbar_init(p_read, 1);
       mbar_init(drain, 1);
+      for (int k = 0; k < 4; ++k) mbar_init(pair(k), 2);
       for (int k = 0; k < kSegs; ++k) {
         mbar_init(seg_full(k), 1);
-        mbar_init(seg_empty(k), 3 + 4 * NT);  // loads of K and of V, MMAs, softmax warps
+        mbar_init(seg_empty(k), 3 + L::WARPS);  // loads of K and of V, MMAs, softmax warps
       }
     }
     // a failure recorded earlier, or a failed layout check, skips the work
@@ -288,10 +306,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
   };
 
   if (warp < 4) {
-  // A softmax thread holds a row of S (128). NT = 2: 128 threads with 88 registers
-  // and 256 with 208 make up the launch's 384 x 168; two CTAs an SM: 128 with 48 and
-  // 128 with 208 its 256 x 128
-  if (NT == 2) regs_dec<88>();
+  // A softmax thread holds a row of S (128, or half of one). 128 threads with 88
+  // registers and 256 with 208 make up the launch's 384 x 168; two CTAs an SM: 128
+  // with 48 and 128 with 208 its 256 x 128
+  if (L::WARPS == 8) regs_dec<88>();
   if (L::PER_SM == 2) regs_dec<48>();
   if (warp == 3) {
     // ------------------------------------------------------------ items
@@ -500,15 +518,30 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
   }
   } else {
     // ------------------------------------------------------------ softmax
-    if (NT == 2 || L::PER_SM == 2) regs_inc<208>();
-    const int t = (warp - 4) >> 2;               // row tile
+    if (L::WARPS == 8 || L::PER_SM == 2) regs_inc<208>();
+    const int t = L::HALVES == 1 ? (warp - 4) >> 2 : 0;     // row tile
+    const int half = L::HALVES == 2 ? (warp - 4) >> 2 : 0;  // of its columns
     const int r_tile = (warp & 3) * 32 + lane;   // TMEM lane
     const float c = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + L::col_s(t) + lanes, tp = tmem + L::col_p(t) + lanes, to = tmem + L::col_o(t) + lanes;
+    const uint32_t ts = tmem + L::col_s(t) + L::CW * half + lanes, tp = tmem + L::col_p(t) + L::CW / 2 * half + lanes,
+                   to = tmem + L::col_o(t) + D / L::HALVES * half + lanes;
+    // the other half's number of the same row
+    uint32_t swaps = 0;  // so far
+    auto swap = [&](float mine, float* other) {
+      const uint32_t at = sb + L::OFF_PAIR + ((swaps & 1) * 2 * kTileM + r_tile) * 4;
+      st_shared_f32(at + half * kTileM * 4, mine);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair(warp & 3));
+      if (!warp_wait(pair(warp & 3), swaps & 1, wc)) return false;
+      *other = ld_shared_f32(at + (1 - half) * kTileM * 4);
+      ++swaps;
+      return true;
+    };
     // this warp's rows of Q, D / 8 lanes a row, 128-byte swizzled as TMA would
     // place them; rows that are not there are zero
-    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    constexpr int LPR = D / 8, RPI = 32 / LPR, QI = LPR / L::HALVES;
+    const int i0_q = half * QI;
     auto row_of_q = [&](const Seg& s) -> const uint16_t* {  // this thread's, null where there is none
       const int row = s.rb * kRows + t * kTileM + r_tile, tok = row / G;
       return s.n_iter > 0 && row < s.n * G ? static_cast<const uint16_t*>(a.q) + (s.tok0 + tok) * a.q_sn +
@@ -521,11 +554,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       return sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + (cq >> 3) * L::BOX + r * 128 + (((cq & 7) ^ (r & 7)) << 4);
     };
     // into registers and from there, or past them where Q has two places
-    auto fetch_q = [&](const Seg& s, uint4 (&v)[LPR]) {
+    auto fetch_q = [&](const Seg& s, uint4 (&v)[QI]) {
       const uint16_t* mine = row_of_q(s);
 #pragma unroll
-      for (int i = 0; i < LPR; ++i) {
-        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
+      for (int i = 0; i < QI; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, (i0_q + i) * RPI + lane / LPR);
         v[i] = make_uint4(0, 0, 0, 0);
         if (row_q != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(row_q) + cq);
       }
@@ -535,20 +568,20 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(it));
     };
-    auto put_q = [&](const uint4 (&v)[LPR], int it) {
+    auto put_q = [&](const uint4 (&v)[QI], int it) {
 #pragma unroll
-      for (int i = 0; i < LPR; ++i) st_shared_v4(place_q(i, it), v[i].x, v[i].y, v[i].z, v[i].w);
+      for (int i = 0; i < QI; ++i) st_shared_v4(place_q(i0_q + i, it), v[i].x, v[i].y, v[i].z, v[i].w);
       give_q(it);
     };
     auto copy_q = [&](const Seg& s, int it) {
       const uint16_t* mine = row_of_q(s);
 #pragma unroll
-      for (int i = 0; i < LPR; ++i) {
-        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
+      for (int i = 0; i < QI; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, (i0_q + i) * RPI + lane / LPR);
         if (row_q != nullptr)
-          copy16_async(place_q(i, it), row_q + 8 * cq);
+          copy16_async(place_q(i0_q + i, it), row_q + 8 * cq);
         else
-          st_shared_v4(place_q(i, it), 0, 0, 0, 0);
+          st_shared_v4(place_q(i0_q + i, it), 0, 0, 0, 0);
       }
     };
     int base = 0;        // loads of the items before
@@ -557,7 +590,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     Seg sg;
     bool ok = take_seg(0, sg, false);
     if (ok && sg.n_iter > 0) {
-      uint4 v[LPR];
+      uint4 v[QI];
       fetch_q(sg, v);
       put_q(v, 0);
     }
@@ -612,23 +645,24 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       for (int j = 0; j < n_iter; ++j) {
         const uint32_t parity = (tiles + j) & 1;
         bool handed = false;  // P of the first keys
-        const TileMask<true> mask(a, live, token, sg.n, sg.len, 0, (sg.t0 + j) * kTileN);
+        const TileMask<true, L::CW / 32> mask(a, live, token, sg.n, sg.len, 0, (sg.t0 + j) * kTileN + L::CW * half);
         if (!(ok = warp_wait(s_full(L::OWN_P ? 0 : t), parity, wc))) break;
         tc_fence_after();
         if (warp_live) {
           if (!(ok = check_tmem(ck, ts, 32, 128, __LINE__) && check_tmem(ck, tp, 32, 64, __LINE__))) break;
-          float s[128];
+          constexpr int CW = L::CW;
+          float s[CW];
           auto load_s = [&]() {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+            for (int q = 0; q < CW / 32; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
             tmem_wait_ld();
             if (mask.partial()) {
 #pragma unroll
-              for (int k = 0; k < 128; ++k)
+              for (int k = 0; k < CW; ++k)
                 if (mask.hides(k)) s[k] = -INFINITY;
             }
           };
-          uint32_t p[64];
+          uint32_t p[CW / 2];
           auto terms_of = [&](auto first, auto last) {  // P against ref, in the inputs' type; its fp32 sum
             const float r0 = ref == -INFINITY ? 0.f : ref;
             const float2 c2 = make_float2(c, c), nr = make_float2(-r0, -r0);
@@ -644,28 +678,34 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             return f.x + f.y;
           };
           using std::integral_constant;
-          auto terms = [&]() { return terms_of(integral_constant<int, 0>{}, integral_constant<int, 64>{}); };
+          auto terms = [&]() { return terms_of(integral_constant<int, 0>{}, integral_constant<int, CW / 2>{}); };
           // the maximum of the tile moves the reference if it exceeds it by more
           // than is allowed; by how much O and the sum scale then
-          auto move_ref = [&](bool may) {
+          auto move_ref = [&](bool may, float* alpha) {
             float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 4; k < 124; k += 8) {
+            for (int k = 4; k < CW - 4; k += 8) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[k + 2 * i], s[k + 2 * i + 1]);
             }
-            const float top = max3(max3(m[0], m[1], m[2]), max3(m[3], s[124], s[125]), fmaxf(s[126], s[127])) * c;
+            float most = max3(max3(m[0], m[1], m[2]), max3(m[3], s[CW - 4], s[CW - 3]), fmaxf(s[CW - 2], s[CW - 1]));
+            if constexpr (L::HALVES == 2) {
+              float other;
+              if (!swap(most, &other)) return false;
+              most = fmaxf(most, other);
+            }
+            const float top = most * c;
             const bool move = may && (top > ref + rise_allowed<TYPE>(top) || (ref == -INFINITY && top > -INFINITY));
-            const float alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
+            *alpha = move ? ex2(ref - (top - kBelow<TYPE>)) : 1.f;
             if (move) {
               ref = top - kBelow<TYPE>;
-              l *= alpha;
+              l *= *alpha;
             }
-            return alpha;
+            return true;
           };
           auto scale_o = [&](float alpha) {  // (all of its products so far have ended)
 #pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
+            for (int q = 0; q < D / L::HALVES / 16; ++q) {
               float o[16];
               tmem_ld16(to + 16 * q, o);
               tmem_wait_ld();
@@ -675,13 +715,12 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
               tmem_st16(to + 16 * q, r);
             }
           };
-          float f;
+          float f, alpha;
           load_s();
-          if (L::OWN_P) {
+          if constexpr (L::OWN_P) {
             // S is in registers: the next tile's may come. P's columns and O are
             // touched once the product of the tile before has ended
-            if (!(ok = hand_back_s(j))) break;
-            const float alpha = move_ref(true);
+            if (!(ok = hand_back_s(j) && move_ref(true, &alpha))) break;
             f = terms();
             if (j > 0) {
               if (!(ok = warp_wait(p_read, (reads + j - 1) & 1, wc))) break;
@@ -697,7 +736,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             bool again = !(f <= kSumMax<TYPE>) || (ref == -INFINITY && mask.some());
             if (__any_sync(0xFFFFFFFFu, again)) {
               load_s();
-              const float alpha = move_ref(true);
+              move_ref(true, &alpha);
               if (j > 0) scale_o(alpha);
               f = terms();
             } else {
@@ -722,19 +761,20 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
                   if (k < kFirst || mask.hides(k)) s[k] = -INFINITY;
                 l += f;
                 f = 0.f;
-                const float alpha = move_ref(again);
+                move_ref(again, &alpha);
                 scale_o(alpha);
                 f2 = terms_of(integral_constant<int, kFirst / 2>{}, integral_constant<int, 64>{});
               }
               f += f2;
             }
           }
+          constexpr int kLate = L::OWN_P ? 0 : kFirst / 32;  // handed over with the rest
           if (!handed) {
 #pragma unroll
-            for (int q = 0; q < kFirst / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
+            for (int q = 0; q < kLate; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
           }
 #pragma unroll
-          for (int q = kFirst / 32; q < 4; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
+          for (int q = kLate; q < CW / 32; ++q) tmem_st16(tp + 16 * q, &p[16 * q]);
           l += f;
           tmem_wait_st();
         } else if (L::OWN_P) {
@@ -757,7 +797,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
           mbar_arrive(p_full(L::OWN_P ? 0 : t));
           // S of this tile came from K's stage, the product of the V before it
           // has ended: both are free
-          if ((warp & 3) == 0) {
+          if ((warp & 3) == 0 && half == 0) {
             if (j > 0) mbar_arrive(kv_empty((base + idx_v(j - 1, n_iter)) % L::STAGES));
             mbar_arrive(kv_empty((base + idx_k(j)) % L::STAGES));
           }
@@ -770,15 +810,20 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       if (!ok) break;
       // ---------------------------------------------------------- output
       // With one place for Q the next item's rows are on their way meanwhile
-      uint4 next_q[LPR];
+      uint4 next_q[QI];
       if (L::QBUFS == 1) {
         if (!(ok = take_seg(it + 1, after, false))) break;
         fetch_q(after, next_q);
       }
       if (!(ok = warp_wait(o_full(L::OWN_P ? 0 : t), it & 1, wc))) break;
       tc_fence_after();
-      if ((warp & 3) == 0 && lane == 0) mbar_arrive(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
+      if ((warp & 3) == 0 && half == 0 && lane == 0) mbar_arrive(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
       if (warp_live) {
+        if constexpr (L::HALVES == 2) {
+          float other;
+          if (!(ok = swap(l, &other))) break;
+          l += other;
+        }
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (NaN stays NaN)
         const bool none = l == 0.f;
         const long long e = static_cast<long long>(token) * a.HQ + head;
@@ -786,7 +831,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         // The rows go out through shared memory (this warp's part of Q's tile,
         // which no product reads any more), 128 bytes of each at a time, so that
         // eight lanes write a row's line together
-        const uint32_t stage = sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + (warp & 3) * 32 * 128;
+        const uint32_t stage =
+            sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + half * L::BOX + (warp & 3) * 32 * 128;
         const bool parts = sg.slot >= 0;
         uint8_t* mine = !live  ? nullptr
                         : parts ? reinterpret_cast<uint8_t*>(a.part_o + part * D)
@@ -809,7 +855,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         const bool any_none = __any_sync(0xFFFFFFFFu, none);
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = 0; q < D / L::HALVES / 32; ++q) {
           float o[32];
           tmem_ld32(to + 32 * q, o);
           tmem_wait_ld();
@@ -827,17 +873,17 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
             for (int k = 0; k < 8; ++k)
               st_shared_v4(stage + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]),
                            __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
-            write_out(128 * q);
+            write_out(D / L::HALVES * 4 * half + 128 * q);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               st_shared_v4(stage + lane * 128 + (((4 * (q & 1) + k) ^ (lane & 7)) << 4),
                            pack2<TYPE>(o[8 * k], o[8 * k + 1]), pack2<TYPE>(o[8 * k + 2], o[8 * k + 3]),
                            pack2<TYPE>(o[8 * k + 4], o[8 * k + 5]), pack2<TYPE>(o[8 * k + 6], o[8 * k + 7]));
-            if (q & 1) write_out(64 * (q - 1));
+            if (q & 1) write_out(D / L::HALVES * 2 * half + 64 * (q - 1));
           }
         }
-        if (live) {
+        if (live && half == 0) {
           const float lse2 = none ? -INFINITY : ref + log2f(l);
           if (parts)
             a.part_lse[part] = lse2;
