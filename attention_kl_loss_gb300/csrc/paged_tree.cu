@@ -538,27 +538,28 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       ++swaps;
       return true;
     };
-    // this warp's rows of Q, D / 8 lanes a row, 128-byte swizzled as TMA would
-    // place them; rows that are not there are zero
-    constexpr int LPR = D / 8, RPI = 32 / LPR, QI = LPR / L::HALVES;
-    const int i0_q = half * QI;
+    // this warp's rows of Q, its half's columns of them (the part of Q's place that it
+    // stages its output in, too), 128-byte swizzled as TMA would place them; rows that
+    // are not there are zero
+    constexpr int LPR = D / L::HALVES / 8, RPI = 32 / LPR;  // lanes of a row, rows at once
+    static_assert(L::HALVES == 1 || D / L::HALVES == 64, "a half is one box");
     auto row_of_q = [&](const Seg& s) -> const uint16_t* {  // this thread's, null where there is none
       const int row = s.rb * kRows + t * kTileM + r_tile, tok = row / G;
       return s.n_iter > 0 && row < s.n * G ? static_cast<const uint16_t*>(a.q) + (s.tok0 + tok) * a.q_sn +
                                                  (s.hk * G + row - tok * G) * a.q_sh
                                            : nullptr;
     };
-    const int cq = lane % LPR;
+    const int cq = half * LPR + lane % LPR;
     auto place_q = [&](int i, int it) {  // of this lane's chunk of the warp's rows i * RPI ..
       const int r = (warp & 3) * 32 + i * RPI + lane / LPR;
       return sb + L::OFF_Q + (it % L::QBUFS * NT + t) * L::TILE + (cq >> 3) * L::BOX + r * 128 + (((cq & 7) ^ (r & 7)) << 4);
     };
     // into registers and from there, or past them where Q has two places
-    auto fetch_q = [&](const Seg& s, uint4 (&v)[QI]) {
+    auto fetch_q = [&](const Seg& s, uint4 (&v)[LPR]) {
       const uint16_t* mine = row_of_q(s);
 #pragma unroll
-      for (int i = 0; i < QI; ++i) {
-        const uint16_t* row_q = shfl_ptr(mine, (i0_q + i) * RPI + lane / LPR);
+      for (int i = 0; i < LPR; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
         v[i] = make_uint4(0, 0, 0, 0);
         if (row_q != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(row_q) + cq);
       }
@@ -568,20 +569,20 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(it));
     };
-    auto put_q = [&](const uint4 (&v)[QI], int it) {
+    auto put_q = [&](const uint4 (&v)[LPR], int it) {
 #pragma unroll
-      for (int i = 0; i < QI; ++i) st_shared_v4(place_q(i0_q + i, it), v[i].x, v[i].y, v[i].z, v[i].w);
+      for (int i = 0; i < LPR; ++i) st_shared_v4(place_q(i, it), v[i].x, v[i].y, v[i].z, v[i].w);
       give_q(it);
     };
     auto copy_q = [&](const Seg& s, int it) {
       const uint16_t* mine = row_of_q(s);
 #pragma unroll
-      for (int i = 0; i < QI; ++i) {
-        const uint16_t* row_q = shfl_ptr(mine, (i0_q + i) * RPI + lane / LPR);
+      for (int i = 0; i < LPR; ++i) {
+        const uint16_t* row_q = shfl_ptr(mine, i * RPI + lane / LPR);
         if (row_q != nullptr)
-          copy16_async(place_q(i0_q + i, it), row_q + 8 * cq);
+          copy16_async(place_q(i, it), row_q + 8 * cq);
         else
-          st_shared_v4(place_q(i0_q + i, it), 0, 0, 0, 0);
+          st_shared_v4(place_q(i, it), 0, 0, 0, 0);
       }
     };
     int base = 0;        // loads of the items before
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     Seg sg;
     bool ok = take_seg(0, sg, false);
     if (ok && sg.n_iter > 0) {
-      uint4 v[QI];
+      uint4 v[LPR];
       fetch_q(sg, v);
       put_q(v, 0);
     }
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       if (!ok) break;
       // ---------------------------------------------------------- output
       // With one place for Q the next item's rows are on their way meanwhile
-      uint4 next_q[QI];
+      uint4 next_q[LPR];
       if (L::QBUFS == 1) {
         if (!(ok = take_seg(it + 1, after, false))) break;
         fetch_q(after, next_q);
