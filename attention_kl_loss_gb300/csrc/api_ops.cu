@@ -342,7 +342,7 @@ streamkl_status attn_call(streamkl_paged_attn_args& u, const streamkl_paged_tree
     return st;
   if ((st = make_map_cache(&mv, u.v_cache, u.dtype, u.d, u.page_size, u.HK, u.num_pages, "v_cache")) != STREAMKL_OK)
     return st;
-  skl::PagedAttnArgs a{};
+  skl::TreeAttnArgs a{};
   a.tm_k = &mk;
   a.tm_v = &mv;
   a.q = u.q.data;

@@ -94,9 +94,6 @@ struct PagedAttnArgs {
   int page_shift, num_pages, max_pages;
   int max_q, max_kv;
   float scale;
-  const int* mask;           // tree: row of token t at t * mask_sn, mask_words of 32 drafted tokens each
-  long long mask_sn;
-  int mask_words;
   int q_tiles;               // query tiles of a (sequence, key head)
   int row_tiles;             // 128-row tiles of a CTA (1 or 2)
   int splits, split_tiles;   // key splits and key tiles of one
@@ -104,9 +101,15 @@ struct PagedAttnArgs {
   int whole;                 // few rows: each CTA takes whole (sequence, key head) pairs, no parts
   float* part_o;             // [splits][T][HQ][d]; null without splits
   float* part_lse;           // [splits][T][HQ], log2 units
-  TreeCut* cuts;             // tree: [CTAs]
   int* dev_status;
   uint64_t timeout_ns;
+};
+
+struct TreeAttnArgs : PagedAttnArgs {
+  const int* mask;           // row of token t at t * mask_sn, mask_words of 32 drafted tokens each
+  long long mask_sn;
+  int mask_words;
+  TreeCut* cuts;             // [CTAs]
 };
 
 // A paged cache whose rows are moved, 16 bytes a vector.
@@ -178,8 +181,8 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t s
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 // Rows that see the drafted tokens of their masks: launch_paged_decode's kernel,
 // and one for more rows (row_tiles x 128 at once; part_o [2 ctas][128 row_tiles][d]).
-cudaError_t launch_tree_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
-cudaError_t launch_tree(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_tree_decode(const TreeAttnArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_tree(const TreeAttnArgs& a, int ctas, cudaStream_t stream);
 
 cudaError_t launch_page_copy(PageCopyArgs& a, cudaStream_t stream);
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);

@@ -83,7 +83,7 @@ struct TileMask<true, WORDS> {
   // Bit k of word q: key key0 + 32 q + k, which is drafted token t + k of the
   // sequence's n. Tokens before the drafted ones (t + k < 0) are seen by every row,
   // those from n on (past the sequence's end) by none.
-  __device__ __forceinline__ TileMask(const PagedAttnArgs& a, bool live, int token, int n, int len, int, int key0) {
+  __device__ __forceinline__ TileMask(const TreeAttnArgs& a, bool live, int token, int n, int len, int, int key0) {
     const int t = key0 - (len - n);
     all = live && t + 32 * WORDS <= 0;
     if (t + 32 * WORDS <= 0) {

@@ -22,6 +22,7 @@
 // of K and V, warp 2 MMAs, warp 3 Q and the items' numbers.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ops.h"
 #include "paged.cuh"
@@ -181,11 +182,14 @@ __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Stretch& st
   return true;
 }
 
+template <bool TREE>
+using Args = std::conditional_t<TREE, TreeAttnArgs, PagedAttnArgs>;
+
 template <int TYPE, int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
     streamkl_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v,
-                                 const __grid_constant__ PagedAttnArgs a) {
+                                 const __grid_constant__ Args<TREE> a) {
   using L = DecodeLayout<D>;
   extern __shared__ __align__(1024) uint8_t gb[];
   const uint32_t sb = smem_u32(gb);
@@ -649,7 +653,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <bool TREE, int TYPE, int D>
-cudaError_t decode_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t decode_t(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   using L = DecodeLayout<D>;
   auto kern = streamkl_paged_decode_kernel<TYPE, D, TREE>;
   // the shared-memory attribute, once per device
@@ -677,11 +681,11 @@ cudaError_t decode_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, streamkl_paged_join_kernel<TYPE, D>, a);
+  return cudaLaunchKernelEx(&cfg, streamkl_paged_join_kernel<TYPE, D>, static_cast<const PagedAttnArgs&>(a));
 }
 
 template <bool TREE>
-cudaError_t launch_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_decode(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   if (a.type == kTypeBf16)
     return a.d == 128 ? decode_t<TREE, kTypeBf16, 128>(a, ctas, stream) : decode_t<TREE, kTypeBf16, 64>(a, ctas, stream);
   return a.d == 128 ? decode_t<TREE, kTypeF16, 128>(a, ctas, stream) : decode_t<TREE, kTypeF16, 64>(a, ctas, stream);
@@ -693,7 +697,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t s
   return launch_decode<false>(a, ctas, stream);
 }
 
-cudaError_t launch_tree_decode(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_tree_decode(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   return launch_decode<true>(a, ctas, stream);
 }
 

@@ -182,7 +182,7 @@ template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>::PER_SM)
     streamkl_paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v,
-                               const __grid_constant__ PagedAttnArgs a) {
+                               const __grid_constant__ TreeAttnArgs a) {
   using L = TreeLayout<D, NT>;
   constexpr int kRows = kTileM * NT;
   extern __shared__ __align__(1024) uint8_t gb[];
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
 // that CTA has written it down; the parts lie in the slots of consecutive CTAs.
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    streamkl_paged_tree_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+    streamkl_paged_tree_join_kernel(const __grid_constant__ TreeAttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
   constexpr int kRows = kTileM * NT;
   grid_dependency_wait();  // launched while the tree kernel ends
@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 }
 
 template <int TYPE, int D, int NT>
-cudaError_t tree_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t tree_t(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   using L = TreeLayout<D, NT>;
   auto kern = streamkl_paged_tree_kernel<TYPE, D, NT>;
   // the shared-memory attribute, once per device
@@ -997,13 +997,13 @@ cudaError_t tree_t(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
 }
 
 template <int TYPE, int D>
-cudaError_t tree_d(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t tree_d(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   return a.row_tiles == 2 ? tree_t<TYPE, D, 2>(a, ctas, stream) : tree_t<TYPE, D, 1>(a, ctas, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_tree(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   if (a.type == kTypeBf16)
     return a.d == 128 ? tree_d<kTypeBf16, 128>(a, ctas, stream) : tree_d<kTypeBf16, 64>(a, ctas, stream);
   return a.d == 128 ? tree_d<kTypeF16, 128>(a, ctas, stream) : tree_d<kTypeF16, 64>(a, ctas, stream);
