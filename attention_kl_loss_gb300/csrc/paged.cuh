@@ -57,13 +57,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
-// Whether what the status word held before stops a call: a failure does, but not
-// a bad number of some sequence, which may come from this very call, nor pages
-// that did not suffice.
-__device__ __forceinline__ bool status_stops(int before) {
-  return before != 0 && before != kStatusInvalidArg && before != kStatusNoPages;
-}
-
 // The keys of a tile that a row sees: the first `seen`, or with TREE those whose
 // bit is set (`all`: every one of them).
 template <bool TREE, int WORDS = kTileN / 32>

@@ -212,9 +212,10 @@ __global__ void __launch_bounds__(AttnLayout<D, NT>::THREADS, 1)
       mbar_init(p_read, 1);
       mbar_init(drain, 1);
     }
-    // a failure recorded earlier, or a failed layout check, skips the work
+    // a failure recorded earlier, or a failed layout check, skips the work; not a
+    // bad number of some sequence, which may come from this very call
     const int before = *reinterpret_cast<volatile int*>(a.dev_status);
-    *skip_flag = !lay_ok || status_stops(before);
+    *skip_flag = !lay_ok || (before != 0 && before != kStatusInvalidArg);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {

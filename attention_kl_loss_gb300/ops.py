@@ -653,7 +653,8 @@ def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: 
     others too gets one in its place: the call returns int32 [B, 2], (old, new) or
     (-1, -1), for ``streamkl_paged_copy`` to copy in every layer. Where pages do
     not suffice, sequences keep their lengths (that of the first one, and of all
-    after it that ask for pages), and dev_status is STREAMKL_ERR_NO_PAGES."""
+    after it that ask for pages), and dev_status is STREAMKL_ERR_NO_PAGES: a word
+    of its own where the step goes on, since attention does nothing after a failure."""
     if out is None and stream is None and (native := load().native) is not None:
         done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
         if done is not None:

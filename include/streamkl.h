@@ -586,7 +586,9 @@ streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream
  *   (-1, -1) for the others.
  * Where free pages do not suffice, a sequence is served if all that is asked up to
  * and with it is there, or it asks for none (and grows into no shared page); the
- * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set.
+ * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set (in a word of its
+ * own where the step goes on: attention that is given a word with a failure in it
+ * does nothing).
  * page_refs and copies are 16 and 8-byte aligned.
  */
 typedef struct {
