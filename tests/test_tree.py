@@ -239,7 +239,11 @@ def _random(B, n, L, HQ, HK, d, page, dt, seed):
 @pytest.mark.parametrize("B,n,L,HQ,HK,d,page,dtype", [
     (32, 8, 9000, 16, 4, 128, 16, "bf16"), (20, 16, 12000, 16, 4, 128, 32, "bf16"), (9, 61, 7000, 16, 8, 64, 16, "fp16"),
     (40, 32, 3000, 8, 2, 128, 128, "fp16"), (3, 200, 15000, 8, 4, 128, 64, "bf16"), (100, 30, 800, 4, 4, 64, 64, "bf16"),
-    (150, 33, 400, 2, 1, 128, 16, "bf16"), (1, 128, 40000, 1, 1, 128, 16, "bf16"), (2, 100, 30000, 8, 8, 64, 16, "bf16")])
+    (150, 33, 400, 2, 1, 128, 16, "bf16"), (1, 128, 40000, 1, 1, 128, 16, "bf16"), (2, 100, 30000, 8, 8, 64, 16, "bf16"),
+    # three or four items to a CTA, cut where an equal share ends; and whole ones in turn
+    (230, 40, 1500, 2, 2, 128, 16, "bf16"), (230, 150, 1500, 2, 2, 128, 32, "fp16"), (460, 40, 1500, 2, 2, 64, 16, "bf16"),
+    (230, 140, 1500, 2, 2, 64, 64, "bf16"), (150, 50, 300, 4, 2, 128, 16, "bf16"), (300, 70, 300, 4, 2, 64, 16, "fp16"),
+    (100, 90, 400, 8, 2, 128, 64, "bf16")])
 def test_long_and_many_sequences(B, n, L, HQ, HK, d, page, dtype):
     """Loads that arrive late and items of every length. The relative 2-norm of o: rounding P gives at most eps / 2 of
     sum p |v| a term, in the norm at most eps / 2 of the norm of p v's parts (test_paged.py), o's own rounding eps / 2,
@@ -319,6 +323,96 @@ def test_captured_on_another_stream_and_both_ways(n, HQ, monkeypatch):
     graph.replay()
     binding.raise_on_device_status(st)
     _check(out[0], out[1], q, c, bits, [n, n], [440, 299], 64 ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,HQ,L", [(6, 4, 300), (25, 4, 300), (25, 4, 20000), (90, 4, 300), (90, 4, 9000)])
+def test_rows_in_front_of_the_first_sequence_stay(n, HQ, L):
+    c = Cache([L, 100], 1, 64, 16, torch.bfloat16, seed=n)
+    new = [n, 3]
+    total = sum(new) + 7
+    q = torch.randn(total, HQ, 64, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    bits = _masks(new, "tree", seed=2)
+    mask = torch.zeros(total, -(-n // 32), dtype=torch.int32, device="cuda")
+    mask[4:4 + sum(new)] = _words(bits, -(-n // 32))
+    o = torch.full((total, HQ, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((total, HQ), 3.0, device="cuda")
+    st = binding.new_status()
+    skl.streamkl_paged_tree_attn(q, c.k, c.v, c.table, c.lens, mask, cu_seqlens=_cu(new) + 4, max_seqlen_q=n, max_kv_len=L,
+                                 out=(o, lse), dev_status=st)
+    binding.raise_on_device_status(st)
+    for rows in (slice(0, 4), slice(4 + sum(new), None)):
+        assert torch.all(o[rows] == 3) and torch.all(lse[rows] == 3)
+    own = slice(4, 4 + sum(new))
+    _check(o[own], lse[own], q[own], c, bits, new, [L, 100], 64 ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,n", [(128, 2), (64, 8), (128, 12), (64, 20), (128, 40), (64, 40)])
+def test_a_nan_query_leaves_the_other_rows_right(d, n):
+    """Scores rise by 100 (log: of bf16's terms to infinity) along the keys; one row, the last token's head 2, is NaN."""
+    dt, L, HQ = torch.bfloat16, 600, 4
+    g = torch.Generator().manual_seed(d + n)
+    u, w = _two_directions(d, g)
+    c = Cache([L], 1, d, 16, dt, fill=False)
+    k = 0.05 * torch.randn(L, 1, d, generator=g)
+    for at in range(40, L, 90):
+        k[at, 0] += at / 6 / d ** 0.5 * (u if at % 4 else w)
+    _put(c, 0, k.to(dt), torch.randn(L, 1, d, generator=g).to(dt))
+    q = torch.stack((u, w, u, w)).repeat(n, 1, 1).to(dt).cuda()
+    q[-1, 2, 7] = float("nan")
+    bits = _masks([n], "causal")
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_tree_attn(q, c.k, c.v, c.table, c.lens, _words(bits, -(-n // 32)), cu_seqlens=_cu([n]),
+                                          max_kv_len=L, dev_status=st)
+    binding.raise_on_device_status(st)
+    assert torch.all(torch.isnan(o[-1, 2])) and bool(torch.isnan(lse[-1, 2]))
+    rest = [0, 1, 3]
+    _check(o[:, rest], lse[:, rest], q[:, rest], c, bits, [n], [L], d ** -0.5, dt)
+    if n > 1:
+        one = type("", (), {"rows": [(c.rows[0][0][:L - 1], c.rows[0][1][:L - 1])]})
+        _check(o[:-1, 2:3], lse[:-1, 2:3], q[:-1, 2:3], one, [bits[0][:-1, :-1]], [n - 1], [L - 1], d ** -0.5, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,HQ,L", [(6, 4, 4000), (25, 4, 9000), (90, 4, 3000)])
+def test_two_captured_calls_at_once(n, HQ, L):
+    """Two graphs, each with the workspace that its capture made, replayed on two streams at the same time."""
+    parts = []
+    for seed in (0, 1):
+        k, v, table, lens, new, q = _random(5, n, L, HQ, 1, 128, 16, torch.bfloat16, seed)
+        args = (q, k, v, table, lens, _words(_masks(new, "tree", seed), -(-n // 32)))
+        kw = dict(cu_seqlens=_cu(new), max_seqlen_q=n, max_kv_len=L, dev_status=binding.new_status())
+        want = skl.streamkl_paged_tree_attn(*args, **kw)
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            out = skl.streamkl_paged_tree_attn(*args, **kw)
+        parts.append((graph, stream, want, out, kw["dev_status"], args, kw))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream, *_ in parts:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, want, out, st, *_ in parts:
+        binding.raise_on_device_status(st)
+        assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+
+
+def test_workspace_sizes_on_the_host(lib):
+    size = skl.streamkl_paged_tree_attn_workspace_size
+    assert size(1, 8, 32, 8, 128, 8, 512) == 0                           # few rows of few tiles: whole ones
+    assert size(1, 8, 32, 8, 128, 8, 2048) == 2 * 128 * 32 * 129 * 4      # few rows, cut: two parts of 32 rows a CTA
+    assert size(1, 9, 32, 8, 128, 9, 512) == 0 and size(64, 64 * 16, 32, 8, 128, 16, 128) == 0
+
+    def parts(ctas, rows, d):
+        return (2 * ctas * rows * (d + 1) * 4 + ctas * 24 + 255) // 256 * 256
+
+    assert size(64, 64 * 16, 32, 8, 128, 16, 16384) == parts(152, 128, 128)
+    assert size(4, 4 * 256, 32, 8, 128, 256, 16384) == parts(152, 256, 128)
+    assert size(24, 24 * 61, 8, 8, 64, 61, 5000) == parts(304, 128, 64)    # two CTAs an SM
+    assert size(1, 40, 1, 1, 128, 40, 1000) == parts(8, 128, 128)          # no more CTAs than key tiles
+    assert size(1, 40, 3, 2, 128, 40, 1000) == 0 and size(1, 40, 1, 1, 80, 40, 1000) == 0  # no sizes of a call
 
 
 @pytest.mark.gpu
