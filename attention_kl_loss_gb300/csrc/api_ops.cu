@@ -200,17 +200,8 @@ AttnPlan attn_plan(int B, int T, int HQ, int HK, int d, int max_q, int max_kv, i
     // the other way; 64 sequences of up to 256 keys, two a CTA, 19.1 -> 16.7, 100 of
     // up to 512 34.8 -> 32.3, of 1,024 50.8 -> 52.5 the other way)
     p.split_tiles = 2;  // (one tile each is level: one sequence of 4,096 keys 18.7 us against 18.4)
-    // Whole items, nothing cut and nothing to join, while the longest row of them (with
-  // what sequences of different lengths make of it) is no more tiles over an equal
-  // share than cutting costs: that is 9 to 14 tiles, less where a share is small. At
-  // most 1.08 times the better of the two over 96 shapes of 6 to 48 tiles (290 items of
-  // up to 6 tiles, 240 rows of d = 128 34 us, cut 62; of 48 tiles cut 147, whole 169)
-  const long long turns = (items + ctas - 1) / ctas;
-  const double share = std::max(1.0, static_cast<double>(items) * tiles / ctas);
-  const double ragged = B > 1 ? 0.3 * tiles * std::sqrt(static_cast<double>(turns)) : 0.0;
-  const double cut = std::min(share + 3.0, p.row_tiles == 1 ? 9.0 : d == 64 ? 11.0 : 14.0);
-  p.whole = items < (1 << 30) && turns * tiles - share + ragged <= cut;
-  p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
+    p.whole = (items + ctas - 1) / ctas * tiles <= std::max<long long>(4, (all + ctas - 1) / ctas + 1);
+    p.decode_ctas = static_cast<int>(std::min(p.whole ? items : all, ctas));
     return p;
   }
   p.row_tiles = rows > 128 ? 2 : 1;
@@ -266,13 +257,16 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   const long long tiles = std::max(1, (max_kv + 127) / 128);
   const long long ctas = (d == 64 && p.row_tiles == 1 ? 2 : 1) * num_sms(), items = B * HK * blocks;
   p.q_tiles = static_cast<int>(blocks);
-  // Whole items, nothing cut and nothing to join, unless the longest row of them is
-  // much more than an equal share of the tiles: a cut item costs as much as three to
-  // eight tiles (16 sequences of up to 458 keys, 1,132 rows, 8 key heads, 20 tiles for
-  // 17: 47 us, cut 80; 21 of 1,439 keys, 184 rows, 12 for 7: 27.9 and 32.5; one of 512
-  // keys, 64 rows, 4 for 1: level; of 1,024, 8 for 1: 16.8 and 12.4)
-  const long long row = (items + ctas - 1) / ctas * tiles, share = (items * tiles + ctas - 1) / ctas;
-  p.whole = items < (1 << 30) && row <= share + std::min<long long>(3 + 3 * share / 10, 8);
+  // Whole items, nothing cut and nothing to join, while the longest row of them (with
+  // what sequences of different lengths make of it) is no more tiles over an equal
+  // share than cutting costs: that is 9 to 14 tiles, less where a share is small. At
+  // most 1.08 times the better of the two over 96 shapes of 6 to 48 tiles (290 items of
+  // up to 6 tiles, 240 rows of d = 128 34 us, cut 62; of 48 tiles cut 147, whole 169)
+  const long long turns = (items + ctas - 1) / ctas;
+  const double share = std::max(1.0, static_cast<double>(items) * tiles / ctas);
+  const double ragged = B > 1 ? 0.3 * tiles * std::sqrt(static_cast<double>(turns)) : 0.0;
+  const double cut = std::min(share + 3.0, p.row_tiles == 1 ? 9.0 : d == 64 ? 11.0 : 14.0);
+  p.whole = items < (1 << 30) && turns * tiles - share + ragged <= cut;
   p.decode_ctas = static_cast<int>(std::min(p.whole ? items : items * tiles, ctas));
   return p;
 }
