@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const
 // blocks share them, one bit each, and exchange their counts). Between them lies what
 // has to be in that order: pages given back, the counts of last pages, free pages.
 // A step of 64 sequences takes 6.2 us, a chain of loads and barriers; 667,000 pages
-// given back and 608,000 given out of two million 45 us, of which 9 give back, 8 look
-// for free pages and 25 write them down, on the cluster's sixteen SMs.
+// given back and 608,000 given out of two million 38 us: 9 give back, 7 look for free
+// pages and some 20 write them down, at what sixteen SMs store (a page's count and its
+// entry, in other lines for every warp).
 //
 // 1,024 threads a block, or one block of 256 where tables and pages are few: barriers,
 // scans and looks of warps that have nothing to do are most of such a call.
@@ -329,9 +330,8 @@ __device__ __forceinline__ void give_back(const ResizeArgs& a, const int* sums, 
   }
 }
 
-// Large tables: what is given back, by blocks on every SM before the cluster (an SM
-// makes an atomic on scattered counts every three cycles: 667,000 of them on sixteen
-// SMs took 68 of 99 us).
+// Large tables: what is given back, by blocks on every SM before the cluster (scattered
+// atomics: 667,000 of them take 9 us so, and 25 on the cluster's sixteen SMs).
 constexpr int kReleaseThreads = 256;
 constexpr long long kReleaseEntries = 1 << 18;  // of the tables, from which on
 
@@ -525,33 +525,34 @@ __global__ void __launch_bounds__(THREADS, 1) streamkl_paged_resize_kernel(const
     int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? count : 0);  // of this warp's first free page
     const int n = min(all, limit - ranks[r]);
     if (mine > 0 && at < n) {
+      // counts of the eight groups of 128 pages, a byte each, summed over the lanes together
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t four = free >> (4 * i) & 15;
-        int below = 0, sum = 0;
+      for (int w = 0; w < 2; ++w) {
+        uint32_t ones = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, four >> e & 1);
-          below += __popc(lanes & ((1u << lane) - 1));
-          sum += __popc(lanes);
+        for (int i = 0; i < 4; ++i) ones |= __popc(free >> (16 * w + 4 * i) & 15) << (8 * i);
+        uint32_t upto = ones;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+          if (lane >= m) upto += up;
         }
+        const uint32_t sums_of = __shfl_sync(0xFFFFFFFFu, upto, 31), before = upto - ones;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (four >> e & 1)
-            list[at + below + __popc(four & ((1u << e) - 1))] = static_cast<uint16_t>(warp * 1024 + 128 * i + 4 * lane + e);
-        at += sum;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t four = free >> (16 * w + 4 * i) & 15;
+          int to_place = at + static_cast<int>(before >> (8 * i) & 255);
+          const int number = warp * 1024 + 128 * (4 * w + i) + 4 * lane;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (four >> e & 1) list[to_place++] = static_cast<uint16_t>(number + e);
+          at += static_cast<int>(sums_of >> (8 * i) & 255);
+        }
       }
     }
     __syncthreads();
     const int base = (r * blocks + me) * kBlockPages;
-    int lo = 0, hi = a.B - 1;
-    if (n > 2 * THREADS) {  // few sequences of them all, to be found once
-      lo = find_sequence(sums, lo, hi, ranks[r]);
-      hi = find_sequence(sums, lo, hi, ranks[r] + n - 1);
-    }
-    for (int x = tid; x < n; x += THREADS) {
-      const int p = base + list[x], slot = ranks[r] + x;
-      const int b = find_sequence(sums, lo, hi, slot);
+    auto give = [&](int slot, int p, int b) {
       int* entry = a.table + b * a.table_sb + pages_of(from[b]) + (slot - sums[b]);
       a.refs[p] = 1;
       if (last[b] >= 0) {
@@ -562,6 +563,33 @@ __global__ void __launch_bounds__(THREADS, 1) streamkl_paged_resize_kernel(const
         }
       }
       *entry = p;
+    };
+    if (n <= 2 * THREADS) {
+      for (int x = tid; x < n; x += THREADS)
+        give(ranks[r] + x, base + list[x], find_sequence(sums, 0, a.B - 1, ranks[r] + x));
+      continue;
+    }
+    // runs of 128 a warp, most of which lie in one sequence: no search, no branch
+    int hi = 0;
+    for (int x0 = warp * 128; x0 < n; x0 += kWarps * 128) {
+      const int x1 = min(n, x0 + 128) - 1, slot = ranks[r] + x0 + lane;
+      const int lo = find_sequence(sums, hi, a.B - 1, ranks[r] + x0);
+      hi = find_sequence(sums, lo, a.B - 1, ranks[r] + x1);
+      if (lo == hi && last[lo] < 0) {
+        int* entry = a.table + lo * a.table_sb + pages_of(from[lo]) + (slot - sums[lo]);
+        int p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) p[u] = base + list[min(x1, x0 + 32 * u + lane)];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (x0 + 32 * u + lane <= x1) {
+            a.refs[p[u]] = 1;
+            entry[32 * u] = p[u];
+          }
+      } else {
+        for (int x = x0 + lane; x <= x1; x += 32)
+          give(ranks[r] + x, base + list[x], find_sequence(sums, lo, hi, ranks[r] + x));
+      }
     }
   }
   // ---- lengths (which every block has read, before the barriers above)
