@@ -555,7 +555,8 @@ streamkl_status streamkl_paged_compact(const streamkl_compact_args* args, void* 
   streamkl_status st = check_cache(&u.k_cache, &u.v_cache, u.block_table, u.table_stride, u.kv_lens, u.cu_seqlens,
                                    u.dtype, u.B, 1, u.HK, u.d, u.page_size, u.num_pages, u.max_pages);
   if (st != STREAMKL_OK) return st;
-  if (static_cast<long long>(u.B) * u.HK > kMaxRows / 2) return fail(STREAMKL_ERR_UNSUPPORTED, "B x HK above 2^29");
+  // (16 blocks for each where lists are long)
+  if (static_cast<long long>(u.B) * u.HK > (1LL << 26)) return fail(STREAMKL_ERR_UNSUPPORTED, "B x HK above 2^26");
   if (!u.kept || !u.num_kept) return fail(STREAMKL_ERR_INVALID_ARG, "kept and num_kept must be non-NULL");
   if (u.max_kept < 1 || (u.kept_stride < u.max_kept && u.B > 1) || u.kept_stride < 0)
     return fail(STREAMKL_ERR_INVALID_ARG, "kept of %d tokens a sequence, rows %lld apart", u.max_kept, u.kept_stride);
@@ -590,8 +591,9 @@ streamkl_status streamkl_paged_copy(const streamkl_page_copy_args* args, void* s
   if ((st = check_page_size(u.page_size)) != STREAMKL_OK) return st;
   if (u.n < 1 || u.HK < 1 || u.num_pages < 1)
     return fail(STREAMKL_ERR_INVALID_ARG, "sizes must be >= 1 (n=%d HK=%d num_pages=%d)", u.n, u.HK, u.num_pages);
-  if (u.HK > 65535 || static_cast<long long>(u.n) * u.HK * u.page_size > (1LL << 40))
-    return fail(STREAMKL_ERR_UNSUPPORTED, "more than 65535 heads or 2^40 rows");
+  // (a block moves 128 rows or more of a pair: no more blocks than a grid can have)
+  if (u.HK > 65535 || u.n > (1 << 30) || static_cast<long long>(u.n) * u.HK * u.page_size > (1LL << 36))
+    return fail(STREAMKL_ERR_UNSUPPORTED, "more than 65535 heads, 2^30 pairs or 2^36 rows");
   if ((st = check_rows("k_cache", &u.k_cache, u.num_pages, u.HK, u.page_size, u.d, u.dtype, true)) != STREAMKL_OK) return st;
   if ((st = check_rows("v_cache", &u.v_cache, u.num_pages, u.HK, u.page_size, u.d, u.dtype, true)) != STREAMKL_OK) return st;
   if (!u.pairs || reinterpret_cast<uintptr_t>(u.pairs) % 8)

@@ -542,7 +542,8 @@ def streamkl_paged_compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, k
     cu_seqlens int32 [B + 1]: how many last tokens of kv_lens int32 [B] are in
     question (as ``streamkl_paged_append`` put them, say). Of these, token
     kept[b, i] moves to the place of token i, for i < num_kept[b]; kept int32
-    [B, most], rising in each row, num_kept int32 [B]. Lengths are left to
+    [B, most], rising in each row, num_kept int32 [B]. No two sequences of a call
+    may have last tokens in the same page. Lengths are left to
     ``streamkl_paged_resize``. Returns the caches."""
     if stream is None and (native := load().native) is not None:
         if native.compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status):

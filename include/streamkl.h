@@ -514,9 +514,11 @@ streamkl_status streamkl_paged_tree_attn(const streamkl_paged_tree_attn_args* ar
  * token i, for i < num_kept[b], in both caches and in place. kept[b] rises; places
  * from num_kept[b] on are left as they are. The lengths are not changed, so that a
  * call for each layer can follow (streamkl_paged_resize then gives the rest back).
- * Pages that other sequences hold change for these too. A list that does not rise
- * or leaves 0 .. n - 1 and numbers that do not fit are reported, and that sequence
- * is left as it was; a row whose page number is none is reported and not moved.
+ * Pages that other sequences hold change for these too, and no two sequences of a
+ * call may have last tokens in the same page (streamkl_paged_resize, by which they
+ * came, sees to that). A list that does not rise or leaves 0 .. n - 1 and numbers
+ * that do not fit are reported, and that sequence is left as it was; a row whose
+ * page number is none is reported and not moved. B * HK is at most 2^26.
  */
 typedef struct {
   size_t struct_size;
@@ -537,7 +539,8 @@ streamkl_status streamkl_paged_compact(const streamkl_compact_args* args, void* 
  * Copy pages of both caches: pairs [n, 2] of (source, destination), device,
  * 8-byte aligned. A pair of negative numbers copies nothing. No page may be the
  * destination of two pairs, or of one and the source of another. A pair with one
- * number that is no page is reported and not copied.
+ * number that is no page is reported and not copied. At most 2^30 pairs and 2^36
+ * rows (pairs, heads and slots of a page).
  */
 typedef struct {
   size_t struct_size;

@@ -452,13 +452,15 @@ TABLES = [(dict(struct_size=8), 1), (dict(B=0), 1), (dict(B=4097), 2), (dict(num
     (dict(B=0), 1), (dict(max_pages=1 << 27), 2), (dict(table_stride=-1), 1), (dict(block_table=None), 1),
     (dict(kv_lens=None), 1), (dict(cu_seqlens=None), 1), (dict(kept=None), 1), (dict(num_kept=None), 1), (dict(max_kept=0), 1),
     (dict(kept_stride=3), 1), (dict(kept_stride=-1, B=1), 1), (dict(B=1 << 28, HK=8, k_cache__stride=(8192, 1024, 64),
-                                                                   v_cache__stride=(8192, 1024, 64)), 2)])
+                                                                   v_cache__stride=(8192, 1024, 64)), 2),
+    (dict(B=(1 << 25) + 1), 2)])
 def test_compact_c_call_refuses(lib, over, status):
     assert lib.streamkl_paged_compact(_raw(CompactArgs, over), None) == status and lib.streamkl_last_error()
 
 
 @pytest.mark.parametrize("over,status", CACHES + [(dict(n=0), 1), (dict(pairs=None), 1), (dict(pairs=4100), 1),
-                                                  (dict(HK=65536), 2), (dict(n=1 << 30, HK=4096), 2)])
+                                                  (dict(HK=65536), 2), (dict(n=1 << 30, HK=4096), 2),
+                                                  (dict(n=(1 << 30) + 1, HK=1), 2), (dict(n=1 << 28, HK=17), 2)])
 def test_copy_c_call_refuses(lib, over, status):
     assert lib.streamkl_paged_copy(_raw(CopyArgs, over), None) == status and lib.streamkl_last_error()
 
