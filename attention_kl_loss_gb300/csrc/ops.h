@@ -1,6 +1,6 @@
 // Internal launch interface of the operators around the attention-KL call:
-// norm and rotation of queries and keys, the paged cache's append and the
-// attention over it.
+// norm and rotation of queries and keys, the paged cache's append, the attention
+// over it, and what is done with its pages.
 #pragma once
 
 #include <cstdint>

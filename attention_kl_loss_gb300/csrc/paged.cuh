@@ -1,4 +1,4 @@
-// What the two kernels of the attention over a paged cache share.
+// What the kernels of the attention over a paged cache share.
 #pragma once
 
 #include "ops.h"

@@ -18,6 +18,9 @@
 //     past the 32nd are never looked at.
 // 64 sequences of 4,096 to 16,384 keys, 32 heads over 8 key heads of 128: 0.39 ms
 // for 2.6 GB, 6.7 TB/s (one CTA per (sequence, key head) and key split: 0.54 ms).
+// With TREE the rows are drafted tokens, whose masks say which of these they see;
+// stretches may be one tile long there, and the join has a warp for each row (32 rows
+// over 2,048 keys, 8 heads: 12.9 us both, 18.1 with four rows a warp and two tiles).
 // CTA: warp 0 softmax and output (thread = row, TMEM lanes 0..31), warp 1 loads
 // of K and V, warp 2 MMAs, warp 3 Q and the items' numbers.
 #include <algorithm>

@@ -13,13 +13,29 @@
 // very different lengths with one or a few row tiles each, so the key tiles of all
 // items (a sequence, a key head, a block of rows) form one line that persistent CTAs
 // share evenly, as in paged_decode.cu: one CTA an SM, of NT row tiles that share each
-// K and V tile. A CTA's stretch cuts at most its first and its last item; a join
-// kernel adds those parts by their lse. Loads run on from item to item (a warp
-// publishes the coming items' numbers), so HBM is kept busy while an item's output
-// leaves; the next item's rows of Q are fetched into registers beside that.
+// K and V tile (two CTAs, where one tile of d = 64 is all). A CTA's stretch cuts at
+// most its first and its last item; a join kernel adds those parts by their lse.
+// Where that is near an equal share each CTA takes whole items instead, and nothing
+// is joined. Loads run on from item to item (a warp publishes the coming items'
+// numbers), so HBM is kept busy while an item's output leaves; the next item's rows
+// of Q are copied into a second place of theirs meanwhile, or held in registers where
+// there is only one.
 //
 // The mask is looked at only in tiles that hold drafted keys: four words of a row's
 // bits, shifted into place, before that tile's S is there.
+//
+// What bounds it (one GB300, both kernels; a turn is one key tile of a CTA):
+//   d = 128, one row tile: HBM. 64 sequences of up to 16,384 keys, 16 drafted tokens,
+//     32 heads over 8: 451 us, 6.6 TB/s; 1.48 us a turn, some 20 us start, end and join.
+//   d = 128, two: the chain S, P, O of a row tile, 1.8 us a turn for 1.3 of products.
+//     4 sequences of up to 16,384 keys with 256 drafted tokens 131 us, 1.1 PFLOP/s.
+//   d = 64: the softmax, 0.80 us a turn of one row tile (two CTAs an SM), 1.35 of two.
+//     24 sequences of up to 5,000 keys, up to 61 tokens, 8 heads 48 us, 3.2 TB/s.
+//   One sequence of 2,048 keys, 32 rows a head (by paged_decode.cu): 12.9 us of loads
+//     that wait for one another (length, page, K, parts), first fetches of the code.
+// No faster, each measured: softmax by two halves of the columns at d = 64 with two
+// row tiles (125 us for 104), barriers per row tile there (no change), two CTAs of one
+// row tile for more than 128 rows of d = 64 (200 for 189), the output's loops rolled.
 #include <algorithm>
 #include <atomic>
 #include <climits>

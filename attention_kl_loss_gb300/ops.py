@@ -655,7 +655,9 @@ def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: 
     (-1, -1), for ``streamkl_paged_copy`` to copy in every layer. Where pages do
     not suffice, sequences keep their lengths (that of the first one, and of all
     after it that ask for pages), and dev_status is STREAMKL_ERR_NO_PAGES: a word
-    of its own where the step goes on, since attention does nothing after a failure."""
+    of its own where the step goes on, since attention does nothing after a failure.
+    Such a sequence has no places for new tokens: leave it out of the step (an
+    append would write over its last tokens)."""
     if out is None and stream is None and (native := load().native) is not None:
         done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
         if done is not None:

@@ -591,7 +591,8 @@ streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream
  * and with it is there, or it asks for none (and grows into no shared page); the
  * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set (in a word of its
  * own where the step goes on: attention that is given a word with a failure in it
- * does nothing).
+ * does nothing). They have no places for new tokens: appended all the same, these
+ * would be written over their last ones.
  * page_refs and copies are 16 and 8-byte aligned.
  */
 typedef struct {
