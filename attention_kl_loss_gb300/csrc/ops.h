@@ -110,6 +110,7 @@ struct TreeAttnArgs : PagedAttnArgs {
   long long mask_sn;
   int mask_words;
   TreeCut* cuts;             // [CTAs]
+  int cluster;               // few rows: CTAs of a cluster that shares one item (whole is set), or 0
 };
 
 // A paged cache whose rows are moved, 16 bytes a vector.

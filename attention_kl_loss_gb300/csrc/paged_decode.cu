@@ -20,7 +20,12 @@
 // for 2.6 GB, 6.7 TB/s (one CTA per (sequence, key head) and key split: 0.54 ms).
 // With TREE the rows are drafted tokens, whose masks say which of these they see;
 // stretches may be one tile long there, and the join has a warp for each row (32 rows
-// over 2,048 keys, 8 heads: 12.9 us both, 18.1 with four rows a warp and two tiles).
+// over 2,048 keys, 8 heads: 12.8 us both, 18.1 with four rows a warp and two tiles).
+// With CLUSTER (of these) up to 16 CTAs take an item's tiles in turn and join their
+// parts through shared memory: no search, no parts in HBM, no second kernel, the first
+// page numbers loaded beside the length. 10.7 us for the same; 4 sequences of 4,096 keys
+// 19.9 for 25.8. Clusters of 16 with two CTAs on an SM wait for places (19.8 us where
+// those of 8 take 11.6).
 // CTA: warp 0 softmax and output (thread = row, TMEM lanes 0..31), warp 1 loads
 // of K and V, warp 2 MMAs, warp 3 Q and the items' numbers.
 #include <algorithm>
@@ -37,6 +42,7 @@ namespace {
 
 constexpr int kRows = kDecodeRows;
 constexpr int kThreads = 128;
+constexpr int kMostCluster = 16;  // CTAs
 
 template <int D>
 struct DecodeLayout {
@@ -188,7 +194,7 @@ __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Stretch& st
 template <bool TREE>
 using Args = std::conditional_t<TREE, TreeAttnArgs, PagedAttnArgs>;
 
-template <int TYPE, int D, bool TREE>
+template <int TYPE, int D, bool TREE, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2)
     streamkl_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v,
@@ -261,7 +267,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   Stretch st;
-  if (a.whole) {  // every gridDim-th item
+  // With CLUSTER the CTAs of a cluster take the key tiles of one item in turn and join
+  // what they have through shared memory
+  int ranks = 1, rank = 0, page0 = -1;
+  Seq whole_seq{};  // the item's sequence
+  if constexpr (CLUSTER) {
+    ranks = a.cluster;
+    rank = static_cast<int>(cluster_ctarank());
+    const int item = static_cast<int>(blockIdx.x) / ranks;
+    st.b = item / a.HK;
+    st.hk = item - st.b * a.HK;
+    st.left = 1;
+    if (warp == 1) {  // the first tile's pages, before the length is known
+      const int box_rows = min(1 << a.page_shift, kTileN);
+      const long long at = (static_cast<long long>(rank) * kTileN + lane * box_rows) >> a.page_shift;
+      if (at < a.max_pages) page0 = __ldg(a.table + st.b * a.table_sb + at);
+    }
+    whole_seq = load_seq(a, st.b);
+    if (threadIdx.x == 0 && rank == 0 && st.hk == 0) visit(st.b, whole_seq, true, true);
+  } else if (a.whole) {  // every gridDim-th item
     st.item = static_cast<int>(blockIdx.x);
     st.left = 1;
     for (int i = st.item + static_cast<int>(threadIdx.x) * gridDim.x; i < a.B * a.HK; i += kThreads * gridDim.x)
@@ -289,13 +313,24 @@ __global__ void __launch_bounds__(kThreads, 2)
   ck.tmem_cols = 256;
   const WaitCtx wc{abort_flag, a.dev_status, a.timeout_ns};
   constexpr int COL_O = 128;  // S, and P over it, in [0, 128)
+  auto next = [&](Stretch& at, Segment& sg, bool first) {
+    if constexpr (CLUSTER) {
+      if (at.left == 0 || rank >= whole_seq.tiles) return false;
+      at.left = 0;
+      sg = {at.b, at.hk, rank, (whole_seq.tiles - rank + ranks - 1) / ranks, whole_seq.tok0, whole_seq.n, whole_seq.len,
+            whole_seq.tiles == 1 ? -1 : 0};
+      return true;
+    } else {
+      return next_segment(a, at, sg, first);
+    }
+  };
 
   if (warp == 3) {
     // ------------------------------------------------------------ Q, items
     Segment sg;
     bool first = true;
     for (int i = 0;; ++i) {
-      const bool more = next_segment(a, st, sg, first);
+      const bool more = next(st, sg, first);
       first = false;
       const int k = i & 1;
       if (!warp_wait(q_empty(k), ((i >> 1) & 1) ^ 1, wc)) break;
@@ -335,15 +370,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     RingPos ring{0, 0};
     bool ok = true, first = true;
     int issued = 0;
-    while (ok && next_segment(a, st, sg, first)) {
+    while (ok && next(st, sg, first)) {
       first = false;
       const int* table = a.table + static_cast<long long>(sg.b) * a.table_sb;
       // the page this lane loads of tile j; a number that is none is reported
       // and page 0 read in its place
       auto page_of = [&](int j) {
-        const int key = (sg.t0 + j) * kTileN + lane * box_rows;
+        const int key = (sg.t0 + j * ranks) * kTileN + lane * box_rows;
         if (j >= sg.n_iter || lane * box_rows >= kTileN || key >= sg.len) return -1;
-        int p = __ldg(table + (key >> a.page_shift));
+        int p = CLUSTER && j == 0 ? page0 : __ldg(table + (key >> a.page_shift));
         if (p < 0 || p >= a.num_pages) {
           atomicCAS(a.dev_status, 0, kStatusInvalidArg);
           p = 0;
@@ -353,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto load = [&](const CUtensorMap* map, int j, int pg) {
         const int s = ring.stage;
         if (!warp_wait(kv_empty(s), ring.phase ^ 1, wc)) return false;
-        const int key0 = (sg.t0 + j) * kTileN;
+        const int key0 = (sg.t0 + j * ranks) * kTileN;
         const int pages = (min(kTileN, sg.len - key0) + box_rows - 1) / box_rows;
         const uint32_t dst = sb + L::OFF_KV + s * L::TILE + lane * box_rows * 128;
         if (lane == 0) mbar_arrive_expect_tx(kv_full(s), static_cast<uint32_t>(pages * box_rows * D * 2));
@@ -444,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int lim = !live ? 0 : a.causal ? min(len, len - n + tok + 1) : len;
       float ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n_iter; ++j, ++tiles) {
-        const TileMask<TREE> mask(a, live, token, n, len, lim, (t0 + j) * kTileN);
+        const TileMask<TREE> mask(a, live, token, n, len, lim, (t0 + j * ranks) * kTileN);
         if (!(ok = warp_wait(s_full, tiles & 1, wc))) break;
         tc_fence_after();
         if (!(ok = check_tmem(ck, tmem, 32, 128, __LINE__))) break;
@@ -517,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         l += f;
         // V's rows past the last key (the slots there hold anything, and
         // 0 x NaN is NaN): cleared once it has landed
-        const int valid = len - (t0 + j) * kTileN;
+        const int valid = len - (t0 + j * ranks) * kTileN;
         if (valid < kTileN) {
           if (!(ok = warp_wait(kv_full(ring.stage), ring.phase, wc))) break;
           uint8_t* v = gb + L::OFF_KV + ring.stage * L::TILE;
@@ -548,7 +583,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = none ? 0.f : o[x] * inv;
         if (live) {
-          if (slot >= 0) {
+          if (CLUSTER && slot >= 0) {
+            // over the ring, which nothing uses any more: a row's 16-byte pieces turned
+            // by its number
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              st_shared_v4(sb + L::OFF_KV + (lane * (D / 4) + ((8 * q + x) ^ (lane & 7))) * 16, __float_as_uint(o[4 * x]),
+                           __float_as_uint(o[4 * x + 1]), __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3]));
+          } else if (slot >= 0) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kRows + lane) * D + 32 * q);
 #pragma unroll
             for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
@@ -563,7 +605,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (live) {
         const float lse2 = none ? -INFINITY : ref + log2f(l);
-        if (slot >= 0)
+        if (CLUSTER && slot >= 0)
+          *reinterpret_cast<float*>(gb + L::OFF_KV + kRows * D * 4 + lane * 4) = lse2;
+        else if (slot >= 0)
           a.part_lse[slot * kRows + lane] = lse2;
         else
           a.lse[e] = lse2 * kLn2;
@@ -579,6 +623,44 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
+  }
+  if constexpr (CLUSTER) {
+    // a warp a row, dealt to the cluster's; rows of O lie in D / 32 columns a lane
+    constexpr int V = D / 32, MOST = kMostCluster;
+    const int parts = min(ranks, whole_seq.tiles), rows = whole_seq.n * G;
+    cluster_sync();
+    for (int r = rank * (kThreads / 32) + warp; parts > 1 && r < rows && !*skip_flag; r += ranks * (kThreads / 32)) {
+      const uint32_t mine = sb + L::OFF_KV + (r * (D / 4) + ((lane * V / 4) ^ (r & 7))) * 16 + lane * V % 4 * 4;
+      const float lse = lane < parts ? ld_cluster_f32(mapa_shared(sb + L::OFF_KV + kRows * D * 4 + r * 4, lane)) : -INFINITY;
+      float p[MOST][V];
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) p[i][x] = 0.f;
+        if (i < parts) ld_cluster_f32(mapa_shared(mine, i), p[i]);
+      }
+      float top = lse;
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+      const float weight = ex2(lse - (top == -INFINITY ? 0.f : top));  // 0 past the last part
+      float sum = 0.f, o[V] = {};
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
+        sum += w;
+#pragma unroll
+        for (int x = 0; x < V; ++x) o[x] = fmaf(w, p[i][x], o[x]);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int tok = r / G, token = whole_seq.tok0 + tok, head = st.hk * G + r - tok * G;
+      uint32_t* dst =
+          reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
+#pragma unroll
+      for (int x = 0; x < V / 2; ++x) dst[x] = pack2<TYPE>(o[2 * x] * inv, o[2 * x + 1] * inv);
+      if (lane == 0)
+        a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // (this CTA's part may still be read)
   }
 }
 
@@ -656,10 +738,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <bool TREE, int TYPE, int D>
+template <bool TREE, int TYPE, int D, bool CLUSTER = false>
 cudaError_t decode_t(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   using L = DecodeLayout<D>;
-  auto kern = streamkl_paged_decode_kernel<TYPE, D, TREE>;
+  auto kern = streamkl_paged_decode_kernel<TYPE, D, TREE, CLUSTER>;
   // the shared-memory attribute, once per device
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
@@ -669,7 +751,23 @@ cudaError_t decode_t(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   if (!(done.load() & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
+    if (CLUSTER && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
     done.fetch_or(bit);
+  }
+  if constexpr (CLUSTER) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, *a.tm_k, *a.tm_v, a);
   }
   kern<<<ctas, kThreads, L::BYTES, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
@@ -688,11 +786,13 @@ cudaError_t decode_t(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, streamkl_paged_join_kernel<TYPE, D>, static_cast<const PagedAttnArgs&>(a));
 }
 
-template <bool TREE>
+template <bool TREE, bool CLUSTER = false>
 cudaError_t launch_decode(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   if (a.type == kTypeBf16)
-    return a.d == 128 ? decode_t<TREE, kTypeBf16, 128>(a, ctas, stream) : decode_t<TREE, kTypeBf16, 64>(a, ctas, stream);
-  return a.d == 128 ? decode_t<TREE, kTypeF16, 128>(a, ctas, stream) : decode_t<TREE, kTypeF16, 64>(a, ctas, stream);
+    return a.d == 128 ? decode_t<TREE, kTypeBf16, 128, CLUSTER>(a, ctas, stream)
+                      : decode_t<TREE, kTypeBf16, 64, CLUSTER>(a, ctas, stream);
+  return a.d == 128 ? decode_t<TREE, kTypeF16, 128, CLUSTER>(a, ctas, stream)
+                    : decode_t<TREE, kTypeF16, 64, CLUSTER>(a, ctas, stream);
 }
 
 }  // namespace
@@ -702,7 +802,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, int ctas, cudaStream_t s
 }
 
 cudaError_t launch_tree_decode(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
-  return launch_decode<true>(a, ctas, stream);
+  return a.cluster > 0 ? launch_decode<true, true>(a, ctas, stream) : launch_decode<true>(a, ctas, stream);
 }
 
 }  // namespace skl

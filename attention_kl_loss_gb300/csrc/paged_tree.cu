@@ -31,8 +31,6 @@
 //     4 sequences of up to 16,384 keys with 256 drafted tokens 131 us, 1.1 PFLOP/s.
 //   d = 64: the softmax, 0.80 us a turn of one row tile (two CTAs an SM), 1.35 of two.
 //     24 sequences of up to 5,000 keys, up to 61 tokens, 8 heads 48 us, 3.2 TB/s.
-//   One sequence of 2,048 keys, 32 rows a head (by paged_decode.cu): 12.9 us of loads
-//     that wait for one another (length, page, K, parts), first fetches of the code.
 // No faster, each measured: softmax by two halves of the columns at d = 64 with two
 // row tiles (125 us for 104), barriers per row tile there (no change), two CTAs of one
 // row tile for more than 128 rows of d = 64 (200 for 189), the output's loops rolled.

@@ -133,6 +133,33 @@ def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, la
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new,lens,most,HQ,HK,d,page,dtype,kind,layout", [
+    ([8], [8200], 8200, 16, 4, 128, 16, "bf16", "tree", "heads"),            # sixteen CTAs, five tiles each or four
+    ([32], [4096], 5000, 2, 2, 64, 1024, "fp16", "any", "slots"),
+    ([5, 0, 8, 1, 7], [5, 17, 1300, 129, 0], 8192, 8, 2, 128, 16, "bf16", "any", "heads"),  # fewer tiles than CTAs, or none
+    ([8, 3], [3, 0], 4000, 4, 1, 128, 64, "fp16", "holes", "slots"),
+    ([16, 11, 16, 9], [2000, 1025, 897, 896], 2000, 8, 4, 64, 32, "bf16", "holes", "heads"),
+    ([8, 7, 6], [400, 385, 384], 400, 32, 8, 128, 16, "fp16", "tree", "slots"),
+    ([4] * 20, list(range(250, 1250, 50)), 1200, 8, 4, 128, 128, "bf16", "tree", "heads"),
+    ([1] * 9, [1, 2, 127, 128, 129, 255, 256, 257, 1000], 1000, 8, 4, 128, 16, "bf16", "tree", "heads"),
+])
+def test_few_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, layout):
+    dt = TYPES[dtype]
+    c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
+    width = -(-most // page)
+    table = torch.full((len(lens), width), 2 ** 30, dtype=torch.int32, device="cuda")  # behind the pages: anything
+    table[:, :c.table.shape[1]] = torch.where(c.table < 0, 2 ** 30, c.table)[:, :width]
+    q = torch.randn(sum(new), HQ, d, generator=torch.Generator().manual_seed(d)).to(dt).cuda()
+    bits = _masks(new, kind, seed=len(lens))
+    st = binding.new_status()
+    ret = [skl.streamkl_paged_tree_attn(q, c.k, c.v, table, c.lens, _words(bits, 1), cu_seqlens=_cu(new),
+                                        max_seqlen_q=max(new), max_kv_len=most, dev_status=st) for _ in range(2)]
+    binding.raise_on_device_status(st)
+    _check(*ret[0], q, c, bits, new, lens, d ** -0.5, dt)
+    assert torch.equal(ret[0][0], ret[1][0]) and torch.equal(ret[0][1], ret[1][1])
+
+
+@pytest.mark.gpu
 def test_single_tokens_without_offsets():
     """One drafted token a sequence: its bit says whether it sees itself."""
     lens = [1, 16, 17, 129, 400]
@@ -402,7 +429,8 @@ def test_two_captured_calls_at_once(n, HQ, L):
 def test_workspace_sizes_on_the_host(lib):
     size = skl.streamkl_paged_tree_attn_workspace_size
     assert size(1, 8, 32, 8, 128, 8, 512) == 0                           # few rows of few tiles: whole ones
-    assert size(1, 8, 32, 8, 128, 8, 2048) == 2 * 128 * 32 * 129 * 4      # few rows, cut: two parts of 32 rows a CTA
+    assert size(1, 8, 32, 8, 128, 8, 65536) == 2 * 304 * 32 * 129 * 4     # few rows, cut: two parts of 32 rows a CTA
+    assert size(1, 8, 32, 8, 128, 8, 2048) == 0                            # a cluster for each item
     assert size(1, 9, 32, 8, 128, 9, 512) == 0 and size(64, 64 * 16, 32, 8, 128, 16, 128) == 0
 
     def parts(ctas, rows, d):
