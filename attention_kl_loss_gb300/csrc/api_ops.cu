@@ -290,6 +290,31 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   const double cut = std::min(share + 3.0, p.row_tiles == 1 ? 9.0 : d == 64 ? 11.0 : 14.0);
   p.whole = items < (1 << 30) && turns * tiles - share + ragged <= cut;
   p.decode_ctas = static_cast<int>(std::min(p.whole ? items : items * tiles, ctas));
+  // Or a cluster for each item, its CTAs the item's tiles in turn, the parts joined in
+  // shared memory. Clusters of 8 with one CTA an SM find places for 8 of them at once
+  // (16 take a second wave, 19.2 us for 13.2), of 4 for 32. Times in us, by d and row
+  // tiles: a start, a tile, the join of rows by fewer CTAs; with items cut a start (with
+  // search and join; of one sequence or of more), a tile, what of max_kv ragged sequences
+  // have; whole items. From 200 shapes (1 to 16 sequences of up to 512 to 8,192 keys):
+  // on average 0.7 % from the better way, 12 % at worst, 7 % under what it was without,
+  // 1.4 times at best (8 ragged sequences of up to 1,024 keys, 240 rows of d = 128 31.6
+  // us -> 22.6)
+  static constexpr double kTimes[2][2][9] = {
+      {{6.1, 1.76, 6.1, 11.0, 12.1, 1.81, 0.97, 7.4, 1.08}, {6.2, 1.68, 7.0, 11.0, 11.65, 1.70, 1.0, 7.2, 1.33}},
+      {{7.3, 1.44, 3.6, 11.2, 13.4, 1.74, 0.76, 6.2, 1.09}, {12.75, 1.47, 4.9, 12.9, 19.5, 1.62, 0.92, 8.3, 1.60}}};
+  const double(&us)[9] = kTimes[d == 128][p.row_tiles - 1];
+  const long long places = ctas > num_sms() ? 256 : 128;
+  int cluster = ctas == num_sms() && items > 8 ? 4 : 8;
+  while (cluster > 1 && (cluster > tiles || items * cluster > places)) cluster /= 2;
+  const double alone = us[0] + us[1] * static_cast<double>((tiles + cluster - 1) / cluster) + us[2] / cluster;
+  const double other =
+      p.whole ? us[7] + us[8] * static_cast<double>(turns * tiles)
+              : us[B > 1 ? 4 : 3] + us[5] * std::max(1.0, static_cast<double>(items * tiles) / ctas * (B > 1 ? us[6] : 1.0));
+  if (cluster > 1 && tiles > 2 && alone < other) {
+    p.cluster = cluster;
+    p.whole = true;
+    p.decode_ctas = static_cast<int>(items * cluster);
+  }
   return p;
 }
 

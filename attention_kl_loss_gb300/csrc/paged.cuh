@@ -9,6 +9,7 @@ namespace skl {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTileN = 128;  // keys per tile
+constexpr int kMostCluster = 16;  // CTAs that share an item and join their parts
 // The softmax's reference of a row (log2 units) is taken kBelow under the row's
 // maximum and moves when a term would exceed 2^kTau of it, or a tile's sum of
 // terms 2^kTau = kSumMax. bf16 has fp32's range, so its largest term may be 1.
@@ -55,6 +56,60 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
 template <int TYPE>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+}
+
+// Rows of an item whose parts lie in the shared memory of a cluster's CTAs, joined by
+// their lse: O in fp32 [part_rows][D] from `part` on, a row's 16-byte pieces turned by
+// its number (^ row & 7), then the rows' lse in log2 units. Warp `at` of `warps` takes
+// kMostCluster / MOST rows at once (a lane D / 32 columns of each), of at most MOST parts.
+template <int TYPE, int D, int MOST>
+__device__ __forceinline__ void join_cluster(const PagedAttnArgs& a, uint32_t part, int part_rows, int parts, int at, int warps,
+                                             int rows, int row0, int tok0, int hk) {
+  constexpr int V = D / 32, ROWS = kMostCluster / MOST;
+  const int lane = threadIdx.x & 31, G = a.HQ / a.HK;
+  for (int r0 = at * ROWS; r0 < rows; r0 += warps * ROWS) {
+    const int my_row = r0 + lane / MOST, my_part = lane % MOST;
+    float lse = -INFINITY;
+    if (lane < ROWS * MOST && my_row < rows && my_part < parts)
+      lse = ld_cluster_f32(mapa_shared(part + (part_rows * D + my_row) * 4, my_part));
+    float p[ROWS][MOST][V];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int r = r0 + u;
+      const uint32_t mine = part + (r * (D / 4) + ((lane * V / 4) ^ (r & 7))) * 16 + lane * V % 4 * 4;
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) p[u][i][x] = 0.f;
+        if (r < rows && i < parts) ld_cluster_f32(mapa_shared(mine, i), p[u][i]);
+      }
+    }
+    float top = lse;
+#pragma unroll
+    for (int m = MOST / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    const float weight = ex2(lse - (top == -INFINITY ? 0.f : top));  // 0 past the last part
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      float sum = 0.f, o[V] = {};
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, weight, u * MOST + i);
+        sum += w;
+#pragma unroll
+        for (int x = 0; x < V; ++x) o[x] = fmaf(w, p[u][i][x], o[x]);
+      }
+      const float most = __shfl_sync(0xFFFFFFFFu, top, u * MOST);
+      if (r0 + u >= rows) break;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int row = row0 + r0 + u, tok = row / G, token = tok0 + tok, head = hk * G + row - tok * G;
+      uint32_t* dst =
+          reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
+#pragma unroll
+      for (int x = 0; x < V / 2; ++x) dst[x] = pack2<TYPE>(o[2 * x] * inv, o[2 * x + 1] * inv);
+      if (lane == 0)
+        a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (most + log2f(sum)) * kLn2;
+    }
+  }
 }
 
 // The keys of a tile that a row sees: the first `seen`, or with TREE those whose

@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kRows = kDecodeRows;
 constexpr int kThreads = 128;
-constexpr int kMostCluster = 16;  // CTAs
 
 template <int D>
 struct DecodeLayout {
@@ -625,41 +624,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_dealloc(tmem, 256);
   }
   if constexpr (CLUSTER) {
-    // a warp a row, dealt to the cluster's; rows of O lie in D / 32 columns a lane
-    constexpr int V = D / 32, MOST = kMostCluster;
-    const int parts = min(ranks, whole_seq.tiles), rows = whole_seq.n * G;
+    const int parts = min(ranks, whole_seq.tiles);
     cluster_sync();
-    for (int r = rank * (kThreads / 32) + warp; parts > 1 && r < rows && !*skip_flag; r += ranks * (kThreads / 32)) {
-      const uint32_t mine = sb + L::OFF_KV + (r * (D / 4) + ((lane * V / 4) ^ (r & 7))) * 16 + lane * V % 4 * 4;
-      const float lse = lane < parts ? ld_cluster_f32(mapa_shared(sb + L::OFF_KV + kRows * D * 4 + r * 4, lane)) : -INFINITY;
-      float p[MOST][V];
-#pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-#pragma unroll
-        for (int x = 0; x < V; ++x) p[i][x] = 0.f;
-        if (i < parts) ld_cluster_f32(mapa_shared(mine, i), p[i]);
-      }
-      float top = lse;
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-      const float weight = ex2(lse - (top == -INFINITY ? 0.f : top));  // 0 past the last part
-      float sum = 0.f, o[V] = {};
-#pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-        const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
-        sum += w;
-#pragma unroll
-        for (int x = 0; x < V; ++x) o[x] = fmaf(w, p[i][x], o[x]);
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int tok = r / G, token = whole_seq.tok0 + tok, head = st.hk * G + r - tok * G;
-      uint32_t* dst =
-          reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh + lane * V);
-#pragma unroll
-      for (int x = 0; x < V / 2; ++x) dst[x] = pack2<TYPE>(o[2 * x] * inv, o[2 * x + 1] * inv);
-      if (lane == 0)
-        a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    }
+    if (parts > 1 && !*skip_flag)
+      join_cluster<TYPE, D, kMostCluster>(a, sb + L::OFF_KV, kRows, parts, rank * (kThreads / 32) + warp,
+                                          ranks * (kThreads / 32), whole_seq.n * G, 0, whole_seq.tok0, st.hk);
     cluster_sync();  // (this CTA's part may still be read)
   }
 }

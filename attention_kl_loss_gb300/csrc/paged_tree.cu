@@ -16,7 +16,9 @@
 // K and V tile (two CTAs, where one tile of d = 64 is all). A CTA's stretch cuts at
 // most its first and its last item; a join kernel adds those parts by their lse.
 // Where that is near an equal share each CTA takes whole items instead, and nothing
-// is joined. Loads run on from item to item (a warp publishes the coming items'
+// is joined; where items are few, short and large enough for it a cluster takes each,
+// its CTAs the tiles in turn, and joins their parts out of shared memory (CLUSTER: no
+// search, no second kernel, first page numbers loaded beside the length). Loads run on from item to item (a warp publishes the coming items'
 // numbers), so HBM is kept busy while an item's output leaves; the next item's rows
 // of Q are copied into a second place of theirs meanwhile, or held in registers where
 // there is only one.
@@ -192,7 +194,7 @@ __device__ __forceinline__ T* shfl_ptr(T* p, int from) {
   return reinterpret_cast<T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(p), from));
 }
 
-template <int TYPE, int D, int NT>
+template <int TYPE, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>::PER_SM)
     streamkl_paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v,
@@ -282,6 +284,19 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     }
   };
   long long total = 0, chunk = 0;
+  // With CLUSTER the CTAs of a cluster take the key tiles of one item in turn
+  int ranks = 1, rank = 0, one_b = 0, one_hk = 0, one_rb = 0, page0 = -1;
+  if constexpr (CLUSTER) {
+    ranks = a.cluster;
+    rank = static_cast<int>(cluster_ctarank());
+    const int item = static_cast<int>(blockIdx.x) / ranks;
+    one_rb = item / (a.B * a.HK), one_b = item / a.HK - one_rb * a.B, one_hk = item % a.HK;
+    if (warp == 0 || warp == 2) {  // the first tile's pages, before the length is known
+      const int box_rows = min(1 << a.page_shift, kTileN);
+      const long long at = (static_cast<long long>(rank) * kTileN + lane * box_rows) >> a.page_shift;
+      if (at < a.max_pages) page0 = __ldg(a.table + one_b * a.table_sb + at);
+    }
+  }
   if (a.whole) {
     for (int b = threadIdx.x; b < a.B; b += L::THREADS)
       if (blockIdx.x == 0 || b % gridDim.x == blockIdx.x) visit(b, load_seq(a, b, kRows));
@@ -335,7 +350,14 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     if (left > 0) b = start->b, hk = start->hk, rb = start->rb, tile = start->tile;
     for (int it = 0;; ++it) {
       Seg sg{};
-      if (a.whole) {
+      if constexpr (CLUSTER) {
+        if (it == 0) {
+          const Seq s = load_seq(a, one_b, kRows);
+          const bool mine = !*skip_flag && one_rb < s.blocks && rank < s.tiles;
+          sg = {one_b,  one_hk, one_rb, rank, mine ? (s.tiles - rank + ranks - 1) / ranks : 0,
+                s.tok0, s.n,    s.len,  s.tiles == 1 ? -1 : 0};
+        }
+      } else if (a.whole) {
         for (; item < a.B * a.HK * a.q_tiles && sg.n_iter == 0; item += gridDim.x) {
           // (all first blocks of rows, then the second ones that there are, ..)
           rb = item / (a.B * a.HK), b = item / a.HK - rb * a.B, hk = item % a.HK;
@@ -398,9 +420,9 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       // the page this lane loads of tile j; a number that is none is reported
       // and page 0 read in its place
       auto page_of = [&](int j) {
-        const int key = (sg.t0 + j) * kTileN + lane * box_rows;
+        const int key = (sg.t0 + j * ranks) * kTileN + lane * box_rows;
         if (j >= sg.n_iter || lane * box_rows >= kTileN || key >= sg.len) return -1;
-        int p = __ldg(table + (key >> a.page_shift));
+        int p = CLUSTER && j == 0 ? page0 : __ldg(table + (key >> a.page_shift));
         if (p < 0 || p >= a.num_pages) {
           atomicCAS(a.dev_status, 0, kStatusInvalidArg);
           p = 0;
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         // lies at most three back, and the ring is longer than that by two
         const int i = base + (is_v ? idx_v(j, sg.n_iter) : idx_k(j)), s = i % L::STAGES;
         if (!(ok = warp_wait(kv_empty(s), ((i / L::STAGES) & 1) ^ 1, wc))) break;
-        const int key0 = (sg.t0 + j) * kTileN;
+        const int key0 = (sg.t0 + j * ranks) * kTileN;
         const int pages = (min(kTileN, sg.len - key0) + box_rows - 1) / box_rows;
         const uint32_t dst = sb + L::OFF_KV + s * L::TILE + lane * box_rows * 128;
         if (lane == 0) mbar_arrive_expect_tx(kv_full(s), static_cast<uint32_t>(pages * box_rows * D * 2));
@@ -531,6 +553,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     mma_commit(drain);
     wait_drain(drain, 0, a.timeout_ns);
   }
+  if constexpr (CLUSTER) {  // (the parts are there; they have been read)
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   } else {
     // ------------------------------------------------------------ softmax
     if (L::WARPS == 8 || L::PER_SM == 2) regs_inc<208>();
@@ -605,6 +632,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     uint32_t reads = 0;  // of P, commits so far
     Seg sg;
     bool ok = take_seg(0, sg, false);
+    const int one_tok0 = sg.tok0, one_rows = ok ? min(kRows, sg.n * G - sg.rb * kRows) : 0, one_tiles = (sg.len + kTileN - 1) / kTileN;
     if (ok && sg.n_iter > 0) {
       uint4 v[LPR];
       fetch_q(sg, v);
@@ -618,7 +646,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       const int token = sg.tok0 + tok, head = sg.hk * G + (live ? row - tok * G : 0);
       const bool warp_live = sg.rb * kRows + t * kTileM + (warp & 3) * 32 < rows;
       // keys of the last tile that are there; the rest of its V rows are cleared
-      const int last_valid = min(kTileN, sg.len - (sg.t0 + n_iter - 1) * kTileN);
+      const int last_valid = min(kTileN, sg.len - (sg.t0 + (n_iter - 1) * ranks) * kTileN);
       float ref = -INFINITY, l = 0.f;
       Seg after{};  // the next item
       if (L::QBUFS == 2) {
@@ -661,7 +689,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       for (int j = 0; j < n_iter; ++j) {
         const uint32_t parity = (tiles + j) & 1;
         bool handed = false;  // P of the first keys
-        const TileMask<true, L::CW / 32> mask(a, live, token, sg.n, sg.len, 0, (sg.t0 + j) * kTileN + L::CW * half);
+        const TileMask<true, L::CW / 32> mask(a, live, token, sg.n, sg.len, 0,
+                                                 (sg.t0 + j * ranks) * kTileN + L::CW * half);
         if (!(ok = warp_wait(s_full(L::OWN_P ? 0 : t), parity, wc))) break;
         tc_fence_after();
         if (warp_live) {
@@ -832,6 +861,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         fetch_q(after, next_q);
       }
       if (!(ok = warp_wait(o_full(L::OWN_P ? 0 : t), it & 1, wc))) break;
+      if (CLUSTER && !L::OWN_P && NT == 2 && !(ok = warp_wait(o_full(1 - t), it & 1, wc))) break;  // (the ring is free)
       tc_fence_after();
       if ((warp & 3) == 0 && half == 0 && lane == 0) mbar_arrive_relaxed(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
       if (warp_live) {
@@ -884,7 +914,18 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = none ? 0.f : o[k];
           }
-          if (parts) {
+          if (CLUSTER && parts) {
+            // over the ring, which nothing uses any more: a row's 16-byte pieces turned
+            // by its number
+            const int piece = (D / L::HALVES * half + 32 * q) / 4;
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                st_shared_v4(sb + L::OFF_KV + ((t * kTileM + r_tile) * (D / 4) + ((piece + k) ^ (lane & 7))) * 16,
+                             __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                             __float_as_uint(o[4 * k + 3]));
+            }
+          } else if (parts) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               st_shared_v4(stage + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]),
@@ -901,7 +942,9 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         }
         if (live && half == 0) {
           const float lse2 = none ? -INFINITY : ref + log2f(l);
-          if (parts)
+          if (CLUSTER && parts)
+            st_shared_f32(sb + L::OFF_KV + (kRows * D + t * kTileM + r_tile) * 4, lse2);
+          else if (parts)
             a.part_lse[part] = lse2;
           else
             a.lse[e] = lse2 * kLn2;
@@ -912,6 +955,18 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       tiles += n_iter;
       reads += n_iter - 1;
       sg = after;
+    }
+    if constexpr (CLUSTER) {
+      static_assert(kRows * (D + 1) * 4 <= L::STAGES * L::TILE, "parts lie in the ring");
+      const int parts = min(ranks, one_tiles), at = rank * L::WARPS + warp - 4;
+      cluster_sync();
+      if (parts > 1 && !*skip_flag) {
+        if (parts <= 4)
+          join_cluster<TYPE, D, 4>(a, sb + L::OFF_KV, kRows, parts, at, ranks * L::WARPS, one_rows, one_rb * kRows, one_tok0, one_hk);
+        else
+          join_cluster<TYPE, D, 16>(a, sb + L::OFF_KV, kRows, parts, at, ranks * L::WARPS, one_rows, one_rb * kRows, one_tok0, one_hk);
+      }
+      cluster_sync();  // (this CTA's part may still be read)
     }
   }
 
@@ -980,10 +1035,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (lane == 0) a.lse[static_cast<long long>(token) * a.HQ + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int TYPE, int D, int NT>
+template <int TYPE, int D, int NT, bool CLUSTER>
 cudaError_t tree_t(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   using L = TreeLayout<D, NT>;
-  auto kern = streamkl_paged_tree_kernel<TYPE, D, NT>;
+  auto kern = streamkl_paged_tree_kernel<TYPE, D, NT, CLUSTER>;
   // the shared-memory attribute, once per device
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
@@ -993,7 +1048,23 @@ cudaError_t tree_t(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
   if (!(done.load() & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
+    if (CLUSTER && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
     done.fetch_or(bit);
+  }
+  if constexpr (CLUSTER) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, *a.tm_k, *a.tm_v, a);
   }
   kern<<<ctas, L::THREADS, L::BYTES, stream>>>(*a.tm_k, *a.tm_v, a);
   e = cudaGetLastError();
@@ -1013,7 +1084,9 @@ cudaError_t tree_t(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
 
 template <int TYPE, int D>
 cudaError_t tree_d(const TreeAttnArgs& a, int ctas, cudaStream_t stream) {
-  return a.row_tiles == 2 ? tree_t<TYPE, D, 2>(a, ctas, stream) : tree_t<TYPE, D, 1>(a, ctas, stream);
+  if (a.cluster > 0)
+    return a.row_tiles == 2 ? tree_t<TYPE, D, 2, true>(a, ctas, stream) : tree_t<TYPE, D, 1, true>(a, ctas, stream);
+  return a.row_tiles == 2 ? tree_t<TYPE, D, 2, false>(a, ctas, stream) : tree_t<TYPE, D, 1, false>(a, ctas, stream);
 }
 
 }  // namespace

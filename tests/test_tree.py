@@ -134,16 +134,26 @@ def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, la
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("new,lens,most,HQ,HK,d,page,dtype,kind,layout", [
-    ([8], [8200], 8200, 16, 4, 128, 16, "bf16", "tree", "heads"),            # sixteen CTAs, five tiles each or four
+    ([8], [8100], 8192, 16, 4, 128, 16, "bf16", "tree", "heads"),            # sixteen CTAs, four tiles each
     ([32], [4096], 5000, 2, 2, 64, 1024, "fp16", "any", "slots"),
-    ([5, 0, 8, 1, 7], [5, 17, 1300, 129, 0], 8192, 8, 2, 128, 16, "bf16", "any", "heads"),  # fewer tiles than CTAs, or none
+    ([5, 0, 8, 1, 7], [5, 17, 1300, 129, 0], 4096, 8, 2, 128, 16, "bf16", "any", "heads"),  # fewer tiles than CTAs, or none
     ([8, 3], [3, 0], 4000, 4, 1, 128, 64, "fp16", "holes", "slots"),
     ([16, 11, 16, 9], [2000, 1025, 897, 896], 2000, 8, 4, 64, 32, "bf16", "holes", "heads"),
     ([8, 7, 6], [400, 385, 384], 400, 32, 8, 128, 16, "fp16", "tree", "slots"),
     ([4] * 20, list(range(250, 1250, 50)), 1200, 8, 4, 128, 128, "bf16", "tree", "heads"),
     ([1] * 9, [1, 2, 127, 128, 129, 255, 256, 257, 1000], 1000, 8, 4, 128, 16, "bf16", "tree", "heads"),
+    # more than 32 rows: one and two row tiles, clusters of 8, 4 and 2
+    ([16], [1000], 1024, 16, 4, 128, 16, "bf16", "tree", "heads"),
+    ([30, 2, 0, 5], [1100, 1, 60, 0], 1200, 8, 2, 128, 32, "fp16", "any", "slots"),
+    ([20] * 6, [1000, 129, 128, 640, 20, 7], 1024, 16, 8, 128, 64, "bf16", "holes", "heads"),
+    ([64, 33, 1], [2000, 1500, 130], 2048, 8, 8, 64, 16, "bf16", "tree", "slots"),
+    ([40] * 8, [1900, 1, 50, 128, 129, 700, 1024, 1999], 2048, 8, 8, 64, 128, "fp16", "any", "heads"),
+    ([60, 17, 40], [1000, 300, 40], 1024, 32, 8, 128, 16, "bf16", "tree", "heads"),
+    ([100, 90], [1024, 700], 1024, 24, 4, 128, 256, "fp16", "holes", "heads"),  # blocks of rows; the last of few
+    ([200, 130, 3], [900, 513, 600], 1024, 4, 4, 64, 64, "bf16", "any", "slots"),
+    ([100, 90, 70, 100], [900, 90, 512, 1023], 1024, 16, 4, 128, 32, "bf16", "any", "slots"),
 ])
-def test_few_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, layout):
+def test_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, layout):
     dt = TYPES[dtype]
     c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
     width = -(-most // page)
@@ -152,9 +162,10 @@ def test_few_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, 
     q = torch.randn(sum(new), HQ, d, generator=torch.Generator().manual_seed(d)).to(dt).cuda()
     bits = _masks(new, kind, seed=len(lens))
     st = binding.new_status()
-    ret = [skl.streamkl_paged_tree_attn(q, c.k, c.v, table, c.lens, _words(bits, 1), cu_seqlens=_cu(new),
+    ret = [skl.streamkl_paged_tree_attn(q, c.k, c.v, table, c.lens, _words(bits, -(-max(new) // 32)), cu_seqlens=_cu(new),
                                         max_seqlen_q=max(new), max_kv_len=most, dev_status=st) for _ in range(2)]
     binding.raise_on_device_status(st)
+    assert skl.streamkl_paged_tree_attn_workspace_size(len(new), sum(new), HQ, HK, d, max(new), most) == 0
     _check(*ret[0], q, c, bits, new, lens, d ** -0.5, dt)
     assert torch.equal(ret[0][0], ret[1][0]) and torch.equal(ret[0][1], ret[1][1])
 
@@ -439,7 +450,8 @@ def test_workspace_sizes_on_the_host(lib):
     assert size(64, 64 * 16, 32, 8, 128, 16, 16384) == parts(152, 128, 128)
     assert size(4, 4 * 256, 32, 8, 128, 256, 16384) == parts(152, 256, 128)
     assert size(24, 24 * 61, 8, 8, 64, 61, 5000) == parts(304, 128, 64)    # two CTAs an SM
-    assert size(1, 40, 1, 1, 128, 40, 1000) == parts(8, 128, 128)          # no more CTAs than key tiles
+    assert size(1, 40, 1, 1, 128, 40, 16384) == parts(128, 128, 128)       # no more CTAs than key tiles
+    assert size(1, 40, 1, 1, 128, 40, 1000) == 0                           # a cluster of them
     assert size(1, 40, 3, 2, 128, 40, 1000) == 0 and size(1, 40, 1, 1, 80, 40, 1000) == 0  # no sizes of a call
 
 
