@@ -18,10 +18,10 @@
 // Where that is near an equal share each CTA takes whole items instead, and nothing
 // is joined; where items are few, short and large enough for it a cluster takes each,
 // its CTAs the tiles in turn, and joins their parts out of shared memory (CLUSTER: no
-// search, no second kernel, first page numbers loaded beside the length). Loads run on from item to item (a warp publishes the coming items'
-// numbers), so HBM is kept busy while an item's output leaves; the next item's rows
-// of Q are copied into a second place of theirs meanwhile, or held in registers where
-// there is only one.
+// search, no second kernel, first page numbers loaded beside the length). Loads run on
+// from item to item (a warp publishes the coming items' numbers), so HBM is kept busy
+// while an item's output leaves; the next item's rows of Q are copied into a second
+// place of theirs meanwhile, or held in registers where there is only one.
 //
 // The mask is looked at only in tiles that hold drafted keys: four words of a row's
 // bits, shifted into place, before that tile's S is there.
