@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Join the parts of the items that the CTAs' stretches cut: block c takes the
 // item that starts in CTA c's stretch and goes on in the next, its warps (of the
 // blocks (c, ..)) the rows in turn; the parts of a row lie in the slots of consecutive CTAs.
-template <int TYPE, int D>
+template <int TYPE, int D, bool TREE>
 __global__ void __launch_bounds__(kThreads)
     streamkl_paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(kThreads)
   grid_dependency_wait();
   if (none) return;
   const int G = a.HQ / a.HK, lane = threadIdx.x & 31;
-  for (int r = (blockIdx.y * kThreads + threadIdx.x) >> 5; r < s.n * G; r += gridDim.y * kThreads / 32) {
+  for (int r = ((TREE ? blockIdx.y * kThreads : 0) + threadIdx.x) >> 5; r < s.n * G;
+       r += (TREE ? gridDim.y : 1) * kThreads / 32) {
     // parts whose loads are in flight, the first ones beside the lse's (one token
     // over 4,096 keys, both kernels: 12.2 us, 12.5 with 8, 13.9 with 8 after the lse)
     constexpr int RUN = 16;
@@ -752,7 +753,7 @@ cudaError_t decode_t(const Args<TREE>& a, int ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, streamkl_paged_join_kernel<TYPE, D>, static_cast<const PagedAttnArgs&>(a));
+  return cudaLaunchKernelEx(&cfg, streamkl_paged_join_kernel<TYPE, D, TREE>, static_cast<const PagedAttnArgs&>(a));
 }
 
 template <bool TREE, bool CLUSTER = false>
