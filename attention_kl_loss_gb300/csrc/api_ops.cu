@@ -274,9 +274,15 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   }
   AttnPlan p{};
   p.split_tiles = 1;
-  p.row_tiles = rows > 128 ? 2 : 1;
-  const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
   const long long tiles = std::max(1, (max_kv + 127) / 128);
+  // Two row tiles, which share the keys they read, once there is enough to do: calls of
+  // at most an item an SM and 7 key tiles a CTA are faster by single ones (one sequence of
+  // 1,024 keys, 400 rows of d = 128, 8 key heads 13.6 us, by two 18.1; 8 of 512 keys, 160
+  // rows 12.7 and 14.5; of 4,096 keys 53.2 and 44.7; 16 of 512 19.7 and 15.0)
+  const long long singles = B * HK * ((rows + 127) / 128);
+  const double turns_of_singles = static_cast<double>(singles * tiles) / ((d == 64 ? 2 : 1) * num_sms()) * (B > 1 ? 0.75 : 1.0);
+  p.row_tiles = rows > 128 && (singles > num_sms() || turns_of_singles > 7.0) ? 2 : 1;
+  const long long blocks = (rows + 128 * p.row_tiles - 1) / (128 * p.row_tiles);
   const long long ctas = (d == 64 && p.row_tiles == 1 ? 2 : 1) * num_sms(), items = B * HK * blocks;
   p.q_tiles = static_cast<int>(blocks);
   // Whole items, nothing cut and nothing to join, while the longest row of them (with

@@ -156,9 +156,7 @@ def test_tree_attention_matches_fp64(new, lens, HQ, HK, d, page, dtype, kind, la
 def test_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, layout):
     dt = TYPES[dtype]
     c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
-    width = -(-most // page)
-    table = torch.full((len(lens), width), 2 ** 30, dtype=torch.int32, device="cuda")  # behind the pages: anything
-    table[:, :c.table.shape[1]] = torch.where(c.table < 0, 2 ** 30, c.table)[:, :width]
+    table = _wide(c.table, page, most)
     q = torch.randn(sum(new), HQ, d, generator=torch.Generator().manual_seed(d)).to(dt).cuda()
     bits = _masks(new, kind, seed=len(lens))
     st = binding.new_status()
@@ -168,6 +166,56 @@ def test_rows_over_a_cluster(new, lens, most, HQ, HK, d, page, dtype, kind, layo
     assert skl.streamkl_paged_tree_attn_workspace_size(len(new), sum(new), HQ, HK, d, max(new), most) == 0
     _check(*ret[0], q, c, bits, new, lens, d ** -0.5, dt)
     assert torch.equal(ret[0][0], ret[1][0]) and torch.equal(ret[0][1], ret[1][1])
+
+
+def _wide(table, page, most):
+    """A table for sequences of up to `most` keys: behind the pages that are there, anything."""
+    out = torch.full((table.shape[0], -(-most // page)), 2 ** 30, dtype=torch.int32, device="cuda")
+    out[:, :table.shape[1]] = torch.where(table < 0, 2 ** 30, table)[:, :out.shape[1]]
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [4096, 16384, 1 << 17, 1 << 20])
+@pytest.mark.parametrize("new,lens,HQ,HK,d,page,dtype,kind,layout", [t for t in TREE if max(t[1]) > 100])
+def test_any_bound_of_the_lengths(new, lens, HQ, HK, d, page, dtype, kind, layout, most):
+    """max_kv_len decides how the work is dealt out (clusters, whole items, an even share; one or two row tiles), not what
+    comes out."""
+    dt = TYPES[dtype]
+    c = Cache(lens, HK, d, page, dt, layout=layout, seed=sum(lens))
+    q = torch.randn(sum(new), HQ, d, generator=torch.Generator().manual_seed(HQ + d)).to(dt).cuda()
+    bits = _masks(new, kind, seed=sum(new))
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_tree_attn(q, c.k, c.v, _wide(c.table, page, most), c.lens, _words(bits, -(-max(new) // 32)),
+                                          cu_seqlens=_cu(new), max_seqlen_q=max(new), max_kv_len=most, dev_status=st)
+    binding.raise_on_device_status(st)
+    _check(o, lse, q, c, bits, new, lens, d ** -0.5, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [4096, 1 << 17])
+@pytest.mark.parametrize("dtype,rise", [("fp16", 20.0), ("bf16", 100.0)])
+@pytest.mark.parametrize("d,n", [(128, 16), (64, 16), (128, 50), (64, 50), (128, 150), (64, 150)])
+def test_scores_that_rise_for_any_bound(d, n, dtype, rise, most):
+    """Keys far above all before them, within the drafted ones and before; key 3 is not seen by any row, its key is NaN."""
+    dt, L = TYPES[dtype], 900
+    g = torch.Generator().manual_seed(d + n)
+    u, w = _two_directions(d, g)
+    c = Cache([L], 1, d, 16, dt, fill=False)
+    k = 0.05 * torch.randn(L, 1, d, generator=g)
+    for i, at in enumerate(range(40, L, 37)):
+        k[at, 0] += (i % 7 + 1) * rise / d ** 0.5 * (u if i % 2 else w)
+    _put(c, 0, k.to(dt), torch.randn(L, 1, d, generator=g).to(dt))
+    q = torch.stack((u, w)).expand(n, 2, d).to(dt).cuda()
+    bits = _masks([n], "any", seed=n)
+    hidden = L - n + 3
+    bits[0][:, 3] = False
+    c.k[c.table[0, hidden // 16], 0, hidden % 16] = float("nan")
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_tree_attn(q, c.k, c.v, _wide(c.table, 16, most), c.lens, _words(bits, -(-n // 32)),
+                                          cu_seqlens=_cu([n]), max_seqlen_q=n, max_kv_len=most, dev_status=st)
+    binding.raise_on_device_status(st)
+    _check(o, lse, q, c, bits, [n], [L], d ** -0.5, dt)
 
 
 @pytest.mark.gpu
