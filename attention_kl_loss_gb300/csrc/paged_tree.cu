@@ -35,7 +35,8 @@
 //     24 sequences of up to 5,000 keys, up to 61 tokens, 8 heads 48 us, 3.2 TB/s.
 // No faster, each measured: softmax by two halves of the columns at d = 64 with two
 // row tiles (125 us for 104), barriers per row tile there (no change), two CTAs of one
-// row tile for more than 128 rows of d = 64 (200 for 189), the output's loops rolled.
+// row tile for more than 128 rows of d = 64 in large calls (200 for 189; small ones do
+// that), the output's loops rolled.
 #include <algorithm>
 #include <atomic>
 #include <climits>
