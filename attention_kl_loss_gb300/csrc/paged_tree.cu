@@ -658,11 +658,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
         const int i = base + idx_k(j);
         return warp_wait(kv_full(i % L::STAGES), (i / L::STAGES) & 1, wc);
       };
-      auto hand_back_s = [&](int j) {  // S has been read; K of the next tile comes with it
+      // S has been read; K of the next tile comes with it, landed as warp 6 has seen: the
+      // thread of the MMAs waits for nothing else of that tile, so the arrival releases
+      auto hand_back_s = [&](int j) {
         const bool got = warp != 6 || j + 1 == n_iter || landed_k(j + 1);
         tc_fence_before();
         __syncwarp();
-        if (got && lane == 0) mbar_arrive_relaxed(s_read);
+        if (got && lane == 0) mbar_arrive(s_read);
         return got;
       };
       // V of tile j (by warp 5, whose P comes with it); the slots past the last key
@@ -844,8 +846,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
           // S of this tile came from K's stage, the product of the V before it
           // has ended: both are free
           if ((warp & 3) == 0 && half == 0) {
-            if (j > 0) mbar_arrive_relaxed(kv_empty((base + idx_v(j - 1, n_iter)) % L::STAGES));
-            mbar_arrive_relaxed(kv_empty((base + idx_k(j)) % L::STAGES));
+            if (j > 0) mbar_arrive(kv_empty((base + idx_v(j - 1, n_iter)) % L::STAGES));
+            mbar_arrive(kv_empty((base + idx_k(j)) % L::STAGES));
           }
         }
         if (L::QBUFS == 2 && j == 0 && after.n_iter > 0) {
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
       if (!(ok = warp_wait(o_full(L::OWN_P ? 0 : t), it & 1, wc))) break;
       if (CLUSTER && !L::OWN_P && NT == 2 && !(ok = warp_wait(o_full(1 - t), it & 1, wc))) break;  // (the ring is free)
       tc_fence_after();
-      if ((warp & 3) == 0 && half == 0 && lane == 0) mbar_arrive_relaxed(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
+      if ((warp & 3) == 0 && half == 0 && lane == 0) mbar_arrive(kv_empty((base + idx_v(n_iter - 1, n_iter)) % L::STAGES));
       if (warp_live) {
         if constexpr (L::HALVES == 2) {
           float other;

@@ -392,3 +392,14 @@ def test_build_goes_on_without_the_native_module(compiler, tmp_path, monkeypatch
     lib = build.build()
     assert os.path.dirname(lib) == str(tmp_path) and os.path.getsize(lib) > 0
     assert not os.path.exists(old) and "ctypes" in capfd.readouterr().err
+
+
+def test_arrivals_of_the_tree_attention_release():
+    """The thread of the MMAs learns from other warps' arrivals alone that K and V have landed, and the loads that a stage
+    is free: without release nothing orders the copies and products behind them, and no run would show it reliably."""
+    text = open(os.path.join(ROOT, "attention_kl_loss_gb300", "csrc", "paged_tree.cu")).read()
+    assert "mbar_arrive(s_read)" in text and "mbar_arrive(kv_empty(" in text
+    assert not re.findall(r"mbar_arrive\w*relaxed\w*\(", text)
+    ptx = open(os.path.join(ROOT, "attention_kl_loss_gb300", "csrc", "ptx.cuh")).read()
+    body = re.search(r"void mbar_arrive\(uint32_t bar\) \{(.*?)\n\}", ptx, re.S).group(1)
+    assert "mbarrier.arrive.release.cta" in body
