@@ -6,7 +6,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
+#include <cstring>
 
 #include "streamkl.h"
 #include "host.h"
@@ -26,11 +28,13 @@ constexpr long long kMaxRows = 1LL << 30;  // rows (tokens x heads) of one tenso
 size_t elem_size(int dtype) { return dtype == STREAMKL_FP32 ? 4 : 2; }
 
 // The struct of a call, copied; false (with the error set) for another size.
+// `before`: its size without the fields that came later, which are then zero.
 template <typename A>
-bool take_args(A* to, const A* from) {
+bool take_args(A* to, const A* from, size_t before = sizeof(A)) {
   clear_error();
-  if (from && from->struct_size == sizeof(A)) {
-    *to = *from;
+  if (from && (from->struct_size == sizeof(A) || from->struct_size == before)) {
+    *to = A{};
+    std::memcpy(to, from, from->struct_size);
     return true;
   }
   fail(STREAMKL_ERR_INVALID_ARG, "struct_size is %zu, expected %zu", from ? from->struct_size : 0, sizeof(A));
@@ -681,7 +685,7 @@ streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream
 
 streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* stream) {
   streamkl_resize_args u;
-  if (!take_args(&u, args)) return STREAMKL_ERR_INVALID_ARG;
+  if (!take_args(&u, args, offsetof(streamkl_resize_args, step_lens))) return STREAMKL_ERR_INVALID_ARG;
   streamkl_status st = check_tables(u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.new_lens, "new_lens",
                                     u.dev_status, u.B, u.num_pages, u.max_pages);
   if (st != STREAMKL_OK) return st;
@@ -691,8 +695,10 @@ streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* st
   if (!aligned16(u.page_refs)) return fail(STREAMKL_ERR_INVALID_ARG, "page_refs is not 16-byte aligned");
   if (!u.copies || reinterpret_cast<uintptr_t>(u.copies) % 8)
     return fail(STREAMKL_ERR_INVALID_ARG, "copies must be an 8-byte aligned address");
+  if (u.step_lens && (u.step_lens == u.kv_lens || u.step_lens == u.new_lens))
+    return fail(STREAMKL_ERR_INVALID_ARG, "step_lens must be memory of its own");
   skl::ResizeArgs a{u.page_refs, u.block_table, u.table_stride, u.kv_lens, u.new_lens, reinterpret_cast<int2*>(u.copies), u.B,
-                    u.num_pages, u.max_pages, __builtin_ctz(static_cast<unsigned>(u.page_size)), 0, u.dev_status};
+                    u.num_pages, u.max_pages, __builtin_ctz(static_cast<unsigned>(u.page_size)), 0, u.dev_status, u.step_lens};
   cudaError_t e = skl::launch_resize(a, num_sms(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "resize launch");
 }

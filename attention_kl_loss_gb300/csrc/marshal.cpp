@@ -588,19 +588,23 @@ PyObject* fork(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
-// resize(entries, page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
+// resize(entries, page_refs, block_table, kv_lens, new_lens, page_size, dev_status, step_lens)
 PyObject* resize(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n == 7);
+    want(n == 8);
     Args a{argv};
     const Entries& lib = a.entries();
     const at::Tensor *refs = a.tensor(), *table = a.tensor(), *lens = a.tensor(), *to = a.tensor();
     streamkl_resize_args u{};
     u.page_size = a.integer();
-    const at::Tensor* status = a.tensor(true);
+    const at::Tensor *status = a.tensor(true), *step = a.tensor(true);
     const Home home(*table);
     table_args(&u, home, *refs, *table, *lens);
     home.list(*to, u.B, at::kInt);
+    if (step != nullptr) {
+      home.list(*step, u.B, at::kInt);
+      u.step_lens = static_cast<int*>(step->data_ptr());
+    }
     u.new_lens = static_cast<const int*>(to->data_ptr());
     const at::Tensor copies = home.make({u.B, 2}, at::kInt);
     u.copies = static_cast<int*>(copies.data_ptr());

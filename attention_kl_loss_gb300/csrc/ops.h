@@ -162,6 +162,7 @@ struct ResizeArgs {
   int B, num_pages, max_pages, page_shift;
   int released;              // set by the launcher: pages are given back by a kernel before
   int* dev_status;
+  int* step_lens;            // [B] or null: new lengths, 0 where there are no places
 };
 
 constexpr int kMaxTableRows = 4096;    // sequences of a fork or resize call

@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1) streamkl_paged_resize_kernel(const
       const bool is_served = served(b);
       if (last[b] < 0 || !is_served) a.copies[b] = make_int2(-1, -1);
       if (is_served && from[b] != to[b]) a.kv_lens[b] = to[b];
+      if (a.step_lens != nullptr) a.step_lens[b] = is_served ? to[b] : 0;
       if (!is_served) atomicCAS(a.dev_status, 0, kStatusNoPages);
     }
   }

@@ -42,7 +42,7 @@ _TREE = struct.Struct("N" + _ATTN.format + "Pqi0q")  # (0q: padded to 8 bytes)
 _COMPACT = struct.Struct("N" + 2 * _ROWS + "PqPPPqPP8i0q")
 _COPY = struct.Struct("N" + 2 * _ROWS + "PP6i0q")
 _FORK = struct.Struct("NPPqPPP3i0q")
-_RESIZE = struct.Struct("NPPqPPPP4i0q")
+_RESIZE = struct.Struct("NPPqPPPP4iP")
 
 
 def _pack(fields, *values):
@@ -644,7 +644,7 @@ def streamkl_paged_fork(page_refs, block_table, kv_lens, source, dev_status=None
 
 
 def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: int, out=None, dev_status=None,
-                          stream=None):
+                          stream=None, step_lens=None):
     """Sequences get the pages of new_lens int32 [B] tokens, or give back those
     behind them, in place (page_refs, block_table, kv_lens as for
     ``streamkl_paged_fork``; begin with zeros, -1 and zeros).
@@ -656,17 +656,21 @@ def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: 
     not suffice, sequences keep their lengths (that of the first one, and of all
     after it that ask for pages), and dev_status is STREAMKL_ERR_NO_PAGES: a word
     of its own where the step goes on, since attention does nothing after a failure.
-    Such a sequence has no places for new tokens: leave it out of the step (an
-    append would write over its last tokens)."""
+    Such a sequence has no places for new tokens, and an append at its length would
+    write over its last ones, in pages that others may hold: give the calls of the
+    step step_lens, int32 [B], in the place of kv_lens. It is written here: the new
+    lengths, 0 for sequences that were not served, which append and compact then
+    report and leave alone and whose rows of attention are zeros and -inf. (What is
+    kept of their tokens is none: num_kept * (step_lens > 0).)"""
     if out is None and stream is None and (native := load().native) is not None:
-        done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status)
+        done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status, step_lens)
         if done is not None:
             return done
     index = block_table.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_resize, block_table.device, stream, dict(
             page_refs=page_refs, block_table=block_table, kv_lens=kv_lens, new_lens=new_lens, page_size=page_size, out=out,
-            dev_status=dev_status))
+            dev_status=dev_status, step_lens=step_lens))
     B, tables, pages, width = _held(page_refs, block_table, kv_lens, index)
     if new_lens is None:
         raise ValueError("new_lens must be given")
@@ -675,10 +679,11 @@ def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: 
         out = torch.empty((B, 2), dtype=torch.int32, device=block_table.device)
     elif out.shape != (B, 2) or out.dtype is not torch.int32 or out.get_device() != index or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{B}, 2] on cuda:{index}")
+    step = _vector("step_lens", step_lens, B, torch.int32, index)
     status, _keep = _status(dev_status, index)
     if B == 0:
         return out
-    args = _pack(_RESIZE, *tables, at, out.data_ptr(), status, B, pages, width, page_size)
+    args = _pack(_RESIZE, *tables, at, out.data_ptr(), status, B, pages, width, page_size, step)
     st = load().streamkl_paged_resize(args, _raw_stream(index))
     if st:
         _check(st, "streamkl_paged_resize")

@@ -591,9 +591,17 @@ streamkl_status streamkl_paged_fork(const streamkl_fork_args* args, void* stream
  * and with it is there, or it asks for none (and grows into no shared page); the
  * others keep length and pages, and STREAMKL_ERR_NO_PAGES is set (in a word of its
  * own where the step goes on: attention that is given a word with a failure in it
- * does nothing). They have no places for new tokens: appended all the same, these
- * would be written over their last ones.
- * page_refs and copies are 16 and 8-byte aligned.
+ * does nothing). They have no places for new tokens: appended at their lengths
+ * all the same, these would be written over their last ones, in pages that others
+ * may hold.
+ *   step_lens [B], or NULL: the lengths for the calls of the step that follows, the
+ *   new ones; 0 for the sequences that were not served (and those whose numbers do
+ *   not fit). A sequence of length 0 that is given tokens is left alone by these
+ *   calls: append and compact report it and write nothing, attention gives its rows
+ *   zeros and -inf, so a captured step stays right whether pages suffice or not.
+ *   Memory of its own: not kv_lens, not new_lens.
+ * page_refs and copies are 16 and 8-byte aligned. The struct may end before
+ * step_lens (struct_size says so).
  */
 typedef struct {
   size_t struct_size;
@@ -605,6 +613,7 @@ typedef struct {
   int* copies;
   int* dev_status;
   int B, num_pages, max_pages, page_size;
+  int* step_lens;
 } streamkl_resize_args;
 
 streamkl_status streamkl_paged_resize(const streamkl_resize_args* args, void* stream);

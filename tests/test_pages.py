@@ -208,6 +208,36 @@ def test_captured_steps_replay():
         t.check()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("way", ["native", "ctypes"])
+@pytest.mark.parametrize("B,width,pages", [(1, 4, 3), (6, 8, 20), (300, 9, 1025), (1100, 6, 3001), (30, 9000, 100001)])
+def test_step_lens_are_the_new_lengths_or_zero(B, width, pages, way, monkeypatch):
+    """The lengths for the step's calls: what was asked for, 0 where there were no places or numbers do not fit."""
+    if way == "ctypes":
+        monkeypatch.setattr(binding.load(), "native", None)
+    rng = np.random.default_rng(B)
+    t = Tables(B, width, pages, 16)
+    step = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    short = 0
+    for _ in range(8):
+        if rng.random() < 0.4:
+            t.fork(rng.integers(0, B, B))
+        new = rng.integers(0, width * 16 + 1, B) if rng.random() < 0.5 else np.clip(t.lens + rng.integers(-9, 20, B), 0, width * 16)
+        t.resize(new, step_lens=step)
+        served = t.lens == new
+        short += not served.all()
+        assert np.array_equal(step.cpu().numpy(), np.where(served, new, 0))
+    assert short or B == 1
+    bad = t.lens.copy()
+    bad[0] = -1
+    skl.streamkl_paged_resize(t.d_refs, t.d_table, t.d_lens, _dev(bad), 16, dev_status=t.status, step_lens=step)
+    assert int(t.status.item()) == binding.STREAMKL_ERR_INVALID_ARG
+    assert step.tolist() == [0] + t.lens[1:].tolist()
+    for wrong in (t.d_lens, step.long(), torch.zeros(B + 1, dtype=torch.int32, device="cuda")):
+        with pytest.raises((ValueError, binding.StreamKLError), match="step_lens"):
+            skl.streamkl_paged_resize(t.d_refs, t.d_table, t.d_lens, _dev(t.lens), 16, step_lens=wrong)
+
+
 # ---------------------------------------------------------------- copy, compact
 def _caches(pages, HK, page, d, dt, layout, seed=0):
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -475,6 +505,18 @@ def test_fork_c_call_refuses(lib, over, status):
     (dict(page_size=24), 2), (dict(page_size=1024, max_pages=1 << 21, table_stride=1 << 21), 2)])
 def test_resize_c_call_refuses(lib, over, status):
     assert lib.streamkl_paged_resize(_raw(ResizeArgs, over), None) == status and lib.streamkl_last_error()
+
+
+def test_resize_takes_its_struct_with_and_without_step_lens(lib):
+    long = _struct("LongResizeArgs", *[(k[0], k[1]) for k in (
+        ("P", "page_refs block_table"), ("q", "table_stride"), ("P", "kv_lens new_lens copies dev_status"),
+        ("i", "B num_pages max_pages page_size"), ("P", "step_lens"))])
+    for over, status, text in ((dict(page_size=24, step_lens=8192), 2, b"page size"), (dict(), 1, b"step_lens"),  # (kv_lens)
+                               (dict(kv_lens=8192), 1, b"step_lens"), (dict(struct_size=ctypes.sizeof(long) + 8), 1, b"struct_size"),
+                               (dict(struct_size=ctypes.sizeof(long) - 16), 1, b"struct_size")):
+        assert lib.streamkl_paged_resize(_raw(long, over), None) == status and text in lib.streamkl_last_error()
+    assert ctypes.sizeof(long) == ctypes.sizeof(ResizeArgs) + 8
+    assert lib.streamkl_paged_resize(_raw(ResizeArgs, dict(page_size=24)), None) == 2
 
 
 def test_native_calls_leave_what_they_do_not_know(lib):

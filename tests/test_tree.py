@@ -627,6 +627,93 @@ def test_a_serving_loop(seed, HQ, HK, d, page, dtype):
     binding.raise_on_device_status(st)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("HQ,HK,d,dtype", [(4, 2, 64, "bf16"), (40, 2, 128, "fp16")])
+def test_a_captured_step_without_enough_pages_leaves_the_others_keys(HQ, HK, d, dtype):
+    """Sequences 0 and 1 hold the same partly filled last page and no page is free: neither gets places, nothing of theirs
+    changes, and 2, which needs no page, goes on. Once 3 has ended the same graph serves all."""
+    dt, page, pages, n = TYPES[dtype], 16, 5, 4
+    g = torch.Generator().manual_seed(d)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    table = torch.full((4, 3), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros(pages, HK, page, d, dtype=dt, device="cuda") for _ in range(2))
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def rows(count, heads):
+        return torch.randn(count, heads, d, generator=g).to(dt).cuda()
+
+    first = [20, 0, 22, 9]
+    skl.streamkl_paged_resize(refs, table, lens, i32(first), page)
+    x = rows(sum(first), HK), rows(sum(first), HK)
+    skl.streamkl_paged_append(*x, k, v, table, lens, cu_seqlens=_cu(first))
+    skl.streamkl_paged_fork(refs, table, lens, i32([0, 0, 2, 3]))
+    held = [[t[a:e] for t in x] for a, e in ((0, 20), (0, 20), (20, 42), (42, 51))]
+    assert lens.tolist() == [20, 20, 22, 9] and refs.tolist() == [2, 2, 1, 1, 1]
+    new, bits = [n, n, n, 0], _masks([n, n, n, 0], "causal")
+    mask, cu, q, x = _words(bits, 1).contiguous(), _cu(new), rows(3 * n, HQ), (rows(3 * n, HK), rows(3 * n, HK))
+    kept, wanted, step = i32([[0, 2]] * 4), i32([24, 24, 26, 9]), torch.full((4,), -9, dtype=torch.int32, device="cuda")
+    room, st = binding.new_status(), binding.new_status()
+
+    def one_step():
+        before = lens.clone()
+        copies = skl.streamkl_paged_resize(refs, table, lens, wanted, page, dev_status=room, step_lens=step)
+        skl.streamkl_paged_copy(k, v, copies, dev_status=st)
+        skl.streamkl_paged_append(*x, k, v, table, step, cu_seqlens=cu, dev_status=st)
+        out = skl.streamkl_paged_tree_attn(q, k, v, table, step, mask, cu_seqlens=cu, max_seqlen_q=n, max_kv_len=48, dev_status=st)
+        num = ((step > 0) * i32_two).to(torch.int32)
+        skl.streamkl_paged_compact(k, v, table, step, cu, kept, num, dev_status=st)
+        skl.streamkl_paged_resize(refs, table, lens, before + num, page, dev_status=st)
+        return out
+
+    def check_held():
+        t, ln = table.cpu().numpy(), lens.tolist()
+        for b in range(4):
+            assert ln[b] == len(held[b][0]), b
+            for cache, want in zip((k, v), held[b]):
+                got = [cache[t[b, p // page], :, p % page] for p in range(ln[b])]
+                assert ln[b] == 0 or torch.equal(torch.stack(got), want), b
+        orc.check_held(refs.cpu().numpy(), t, np.array(ln, dtype=np.int32), page)
+
+    i32_two = i32([2, 2, 2, 0])
+    side = [t.clone() for t in (refs, table, lens, k, v)]  # (the calls' first run, undone)
+    one_step()
+    for t, old in zip((refs, table, lens, k, v), side):
+        t.copy_(old)
+    for word in (room, st):
+        word.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = one_step()
+    check_held()
+
+    graph.replay()
+    assert int(room.item()) == binding.STREAMKL_ERR_NO_PAGES and step.tolist() == [0, 0, 26, 9]
+    assert int(st.item()) == binding.STREAMKL_ERR_INVALID_ARG  # tokens without places
+    o, lse = out
+    assert not o[:2 * n].any() and torch.all(torch.isneginf(lse[:2 * n]))
+    one = type("", (), {"rows": [[torch.cat((a, y[2 * n:])) for a, y in zip(held[2], x)]]})
+    _check(o[2 * n:], lse[2 * n:], q[2 * n:], one, [bits[2]], [n], [26], d ** -0.5, dt)
+    held[2] = [torch.cat((a, y[[2 * n, 2 * n + 2]])) for a, y in zip(held[2], x)]
+    check_held()
+
+    for word in (room, st):
+        word.zero_()
+    skl.streamkl_paged_resize(refs, table, lens, i32([20, 20, 24, 0]), page)
+    held[3] = [t[:0] for t in held[3]]
+    wanted.copy_(i32([24, 24, 28, 0]))
+    graph.replay()
+    for word in (room, st):
+        binding.raise_on_device_status(word)
+    assert step.tolist() == [24, 24, 28, 0]
+    all_rows = type("", (), {"rows": [[torch.cat((a, y[b * n:(b + 1) * n])) for a, y in zip(held[b], x)] for b in range(3)]})
+    _check(o, lse, q, all_rows, bits, [n] * 3, [24, 24, 28], d ** -0.5, dt)
+    held[:3] = [[torch.cat((a, y[[b * n, b * n + 2]])) for a, y in zip(held[b], x)] for b in range(3)]
+    check_held()
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib():
