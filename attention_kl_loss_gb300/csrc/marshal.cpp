@@ -10,7 +10,9 @@
 // tensor, outputs that the caller made, another current device, nothing to do,
 // any refusal of the C entry or exception on the way. ops.py then makes the call
 // itself and says what is wrong with it. So no refusal is worded here, and none
-// is left out: whatever passes here passes there.
+// is left out: whatever passes here passes there. A launch that failed is another
+// matter: a kernel of the call may run already, and some calls change their arguments
+// in place, so the status is returned, for ops.py to raise, and nothing made again.
 #include <Python.h>
 #include <dlfcn.h>
 
@@ -24,6 +26,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <utility>
 
 #include "streamkl.h"
 
@@ -147,6 +150,11 @@ struct Home {
   void* stream() const { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
 };
 
+// A launch that failed.
+struct Failed {
+  streamkl_status status;
+};
+
 // The launch, other threads running meanwhile; throws unless it went well.
 template <typename F, typename A>
 void launch(F entry, const A& args, const Home& home) {
@@ -154,6 +162,7 @@ void launch(F entry, const A& args, const Home& home) {
   PyThreadState* state = PyEval_SaveThread();
   const streamkl_status st = entry(&args, stream);
   PyEval_RestoreThread(state);
+  if (st == STREAMKL_ERR_CUDA) throw Failed{st};
   want(st == STREAMKL_OK);
 }
 
@@ -161,6 +170,9 @@ template <typename F>
 PyObject* guarded(F&& f) {
   try {
     return f();
+  } catch (const Failed& failed) {
+    PyErr_Clear();
+    return PyLong_FromLong(failed.status);
   } catch (...) {
     PyErr_Clear();
     Py_RETURN_NONE;
@@ -610,10 +622,14 @@ PyObject* resize(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     u.copies = static_cast<int*>(copies.data_ptr());
     at::Tensor word;
     u.dev_status = home.status(status, &word);
+    // (made before the launch: nothing may fail behind it)
+    struct Owned {
+      PyObject* o;
+      ~Owned() { Py_XDECREF(o); }
+    } out{THPVariable_Wrap(copies)};
+    want(out.o != nullptr);
     launch(lib.resize, u, home);
-    PyObject* o = THPVariable_Wrap(copies);
-    want(o != nullptr);
-    return o;
+    return std::exchange(out.o, nullptr);
   });
 }
 

@@ -14,7 +14,7 @@ PyTorch provides device memory and the current stream.
 
 Each call tries ``csrc/marshal.cpp`` first, which takes ordinary arguments in a
 third of the time and returns None for any others; these, and all refusals, are
-dealt with here.
+dealt with here. A launch that failed is not tried again.
 """
 from __future__ import annotations
 
@@ -104,6 +104,14 @@ def _status(dev_status, index):
     elif dev_status.dtype is not torch.int32 or dev_status.get_device() != index or dev_status.numel() < 1:
         raise ValueError(f"dev_status must be an int32 tensor on cuda:{index}")
     return dev_status.data_ptr(), dev_status
+
+
+def _done(done, where):
+    """What the native way gave. A status there is a launch that failed: the
+    call may have begun, so it is raised and the call not made again."""
+    if type(done) is int:
+        _check(done, where)
+    return done
 
 
 def _workspace(need, device, workspace):
@@ -229,7 +237,7 @@ def streamkl_qk_norm_rope_fwd(q, k, cos, sin, positions=None, k_positions=None, 
         done = native.rope_fwd(q, k, cos, sin, positions, k_positions, q_weight, k_weight, eps, interleaved, k_repeat,
                                dev_status)
         if done is not None:
-            return done
+            return _done(done, "streamkl_qk_norm_rope_fwd")
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
@@ -277,7 +285,7 @@ def streamkl_qk_norm_rope_bwd(q, k, dq_out, dk_out, cos, sin, positions=None, k_
         done = native.rope_bwd(q, k, dq_out, dk_out, cos, sin, positions, k_positions, q_weight, k_weight, eps, interleaved,
                                k_repeat, workspace, dev_status)
         if done is not None:
-            return done
+            return _done(done, "streamkl_qk_norm_rope_bwd")
     k_repeat = int(k_repeat)
     x, packed, k_pos = _rope_sizes(q, k, positions, k_positions, k_repeat)
     index = x.get_device()
@@ -372,8 +380,10 @@ def streamkl_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqle
     ``streamkl_qk_norm_rope_fwd``, None to leave out the rotation or the norm.
     Writes the caches in place and returns them."""
     if stream is None and (native := load().native) is not None:
-        if native.append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, cos, sin, k_weight, eps, interleaved,
-                         dev_status):
+        done = native.append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, cos, sin, k_weight, eps, interleaved,
+                             dev_status)
+        if done is not None:
+            _done(done, "streamkl_paged_append")
             return k_cache, v_cache
     index, dtype = k_cache.get_device(), k_cache.dtype
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
@@ -491,7 +501,7 @@ def streamkl_paged_attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=No
         done = native.attn(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_kv_len, scale, causal,
                            num_splits, workspace, dev_status)
         if done is not None:
-            return done
+            return _done(done, "streamkl_paged_attn")
     index = k_cache.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_attn, k_cache.device, stream, dict(
@@ -522,7 +532,7 @@ def streamkl_paged_tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mas
         done = native.tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len,
                                 scale, workspace, dev_status)
         if done is not None:
-            return done
+            return _done(done, "streamkl_paged_tree_attn")
     index = k_cache.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_tree_attn, k_cache.device, stream, dict(
@@ -546,7 +556,9 @@ def streamkl_paged_compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, k
     may have last tokens in the same page. Lengths are left to
     ``streamkl_paged_resize``. Returns the caches."""
     if stream is None and (native := load().native) is not None:
-        if native.compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status):
+        done = native.compact(k_cache, v_cache, block_table, kv_lens, cu_seqlens, kept, num_kept, dev_status)
+        if done is not None:
+            _done(done, "streamkl_paged_compact")
             return k_cache, v_cache
     index, dtype = k_cache.get_device(), k_cache.dtype
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
@@ -576,7 +588,9 @@ def streamkl_paged_copy(k_cache, v_cache, pairs, dev_status=None, stream=None):
     be the destination of two pairs, or of one and the source of another. What
     ``streamkl_paged_resize`` returns, once for each layer. Returns the caches."""
     if stream is None and (native := load().native) is not None:
-        if native.copy(k_cache, v_cache, pairs, dev_status):
+        done = native.copy(k_cache, v_cache, pairs, dev_status)
+        if done is not None:
+            _done(done, "streamkl_paged_copy")
             return k_cache, v_cache
     index, dtype = k_cache.get_device(), k_cache.dtype
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
@@ -624,7 +638,9 @@ def streamkl_paged_fork(page_refs, block_table, kv_lens, source, dev_status=None
     with -1 where an entry holds no page, kv_lens int32 [B]. Returns page_refs,
     block_table and kv_lens."""
     if stream is None and (native := load().native) is not None:
-        if native.fork(page_refs, block_table, kv_lens, source, dev_status):
+        done = native.fork(page_refs, block_table, kv_lens, source, dev_status)
+        if done is not None:
+            _done(done, "streamkl_paged_fork")
             return page_refs, block_table, kv_lens
     index = block_table.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
@@ -665,7 +681,7 @@ def streamkl_paged_resize(page_refs, block_table, kv_lens, new_lens, page_size: 
     if out is None and stream is None and (native := load().native) is not None:
         done = native.resize(page_refs, block_table, kv_lens, new_lens, page_size, dev_status, step_lens)
         if done is not None:
-            return done
+            return _done(done, "streamkl_paged_resize")
     index = block_table.get_device()
     if index >= 0 and (stream is not None or index != torch.cuda.current_device()):
         return _elsewhere(streamkl_paged_resize, block_table.device, stream, dict(

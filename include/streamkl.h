@@ -559,7 +559,8 @@ streamkl_status streamkl_paged_copy(const streamkl_page_copy_args* args, void* s
  * The two calls below keep that so; a table is filled by streamkl_paged_resize
  * from lengths of 0, counts of 0 and entries of -1. Both change their arguments
  * in place; a call that sets STREAMKL_ERR_INVALID_ARG has found numbers that do
- * not fit, left those out and done the rest. B is at most 4096, num_pages 2^23,
+ * not fit, left those out and done the rest. After STREAMKL_ERR_CUDA part of a
+ * call may have run, and the tables mean nothing. B is at most 4096, num_pages 2^23,
  * B * max_pages 2^30.
  *
  * streamkl_paged_fork: every sequence b becomes a copy of what source[b] was, for

@@ -567,3 +567,69 @@ def test_python_calls_refuse():
     skl.streamkl_paged_fork(refs, none, lens[:0], lens[:0])
     skl.streamkl_paged_copy(k, v, none)
     skl.streamkl_paged_compact(k, v, table, lens, cu, kept[:, :0], count)
+
+
+@pytest.mark.parametrize("call,args", [
+    ("rope_fwd", ("q", "q", "q", "q")), ("rope_bwd", ("q",) * 6), ("append", ("q",) * 6), ("attn", ("q",) * 5), ("tree_attn", ("q",) * 6),
+    ("compact", ("q",) * 7), ("copy", ("q",) * 3), ("fork", ("q",) * 4), ("resize", ("q",) * 4 + (16,))])
+def test_a_failed_launch_is_raised_and_not_made_again(lib, call, args, monkeypatch):
+    """The native way says that its launch failed: the call may have begun, and ctypes must not begin it again."""
+    name = {"rope_fwd": "streamkl_qk_norm_rope_fwd", "rope_bwd": "streamkl_qk_norm_rope_bwd"}.get(call, "streamkl_paged_" + call)
+
+    class Native:
+        def __getattr__(self, _):
+            return lambda *a: binding.STREAMKL_ERR_CUDA
+
+    def again(*a):
+        raise AssertionError("the call was made again")
+
+    monkeypatch.setattr(lib, "native", Native())
+    monkeypatch.setattr(lib, name, again)
+    x = torch.zeros(2, 2, 2, dtype=torch.int32)
+    with pytest.raises(binding.StreamKLError) as e:
+        getattr(skl, name)(*[x if a == "q" else a for a in args])
+    assert e.value.status == binding.STREAMKL_ERR_CUDA and name in str(e.value)
+
+
+@pytest.mark.gpu
+def test_the_native_way_returns_the_status_of_a_failed_launch(tmp_path):
+    """The entries of a library that refuses, or whose launches fail: None for the one, the status for the other, one
+    call each."""
+    import functools
+    import importlib.util
+    import subprocess
+    from attention_kl_loss_gb300 import build
+    names = [n for n in binding._SIGNATURES if n.startswith(("streamkl_paged", "streamkl_qk"))]
+    source = tmp_path / "entries.c"
+    source.write_text("int result, calls;\n" + "\n".join(
+        f"unsigned long {n}(void) {{ return 0; }}" if n.endswith("_size") else f"int {n}(void) {{ ++calls; return result; }}"
+        for n in names))
+    so = str(tmp_path / "entries.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", so, str(source)], check=True)
+    stub = ctypes.CDLL(so)
+    spec = importlib.util.spec_from_file_location("_marshal", build.marshal_path())
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    entries = module.entries(so)
+    k, v = _caches(8, 2, 16, 64, torch.bfloat16, "heads")
+    table, lens, cu, kept = _dev([[0, 1], [2, 3]]), _dev([20, 30]), _cu([5, 5]), _dev([[0, 1]] * 2)
+    refs, mask, q = _dev([1] * 4 + [0] * 4), torch.ones(10, 1, dtype=torch.int32, device="cuda"), torch.zeros(
+        10, 2, 64, dtype=torch.bfloat16, device="cuda")
+    calls = [functools.partial(getattr(module, n), entries, *a) for n, a in (
+        ("append", (q, q, k, v, table, lens, cu, None, None, None, 1e-6, False, None)),
+        ("attn", (q, k, v, table, lens, cu, 5, 32, None, True, 0, None, None)),
+        ("tree_attn", (q, k, v, table, lens, mask, cu, 5, 32, None, None, None)),
+        ("compact", (k, v, table, lens, cu, kept, _dev([2, 2]), None)), ("copy", (k, v, _dev([[0, 5]]), None)),
+        ("fork", (refs, table, lens, _dev([0, 1]), None)), ("resize", (refs, table, lens, lens.clone(), 16, None, None)))]
+    for status in range(6):
+        for i, call in enumerate(calls):
+            ctypes.c_int.in_dll(stub, "result").value = status
+            ctypes.c_int.in_dll(stub, "calls").value = 0
+            got = call()
+            assert ctypes.c_int.in_dll(stub, "calls").value == 1, i
+            if status == binding.STREAMKL_OK:
+                assert got is not None and type(got) is not int, i
+            elif status == binding.STREAMKL_ERR_CUDA:
+                assert got == status and type(got) is int, i
+            else:
+                assert got is None, (i, status)
