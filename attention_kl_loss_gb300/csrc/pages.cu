@@ -25,11 +25,12 @@ constexpr int kCopyThreads = 256, kCopyRun = 8, kCopyVectors = kCopyThreads * kC
 __global__ void __launch_bounds__(kCopyThreads) streamkl_page_copy_kernel(const __grid_constant__ PageCopyArgs a) {
   const int pair = static_cast<int>(blockIdx.x / a.chunks), chunk = static_cast<int>(blockIdx.x - pair * a.chunks);
   const int src = __ldg(a.pairs + 2LL * pair), dst = __ldg(a.pairs + 2LL * pair + 1);
-  if ((src < 0 && dst < 0) || src == dst) return;
+  if (src < 0 && dst < 0) return;
   if (src < 0 || dst < 0 || src >= a.num_pages || dst >= a.num_pages) {
     if (chunk == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
     return;
   }
+  if (src == dst) return;
   const CacheRows& c = a.cache[blockIdx.y];
   const uint4* from = static_cast<const uint4*>(c.data) + src * c.sp;
   uint4* to = static_cast<uint4*>(c.data) + dst * c.sp;

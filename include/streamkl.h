@@ -538,8 +538,8 @@ streamkl_status streamkl_paged_compact(const streamkl_compact_args* args, void* 
 /*
  * Copy pages of both caches: pairs [n, 2] of (source, destination), device,
  * 8-byte aligned. A pair of negative numbers copies nothing. No page may be the
- * destination of two pairs, or of one and the source of another. A pair with one
- * number that is no page is reported and not copied. At most 2^30 pairs and 2^36
+ * destination of two pairs, or of one and the source of another. Any other pair with
+ * a number that is no page is reported and not copied. At most 2^30 pairs and 2^36
  * rows (pairs, heads and slots of a page).
  */
 typedef struct {

@@ -288,6 +288,21 @@ def test_copy_reports_pairs_that_are_none_and_copies_the_rest():
         assert int(st.item()) == binding.STREAMKL_ERR_INVALID_ARG and _same(k, want[0]) and _same(v, want[1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("number", [8, 1 << 30, 2 ** 31 - 1])
+def test_copy_reports_a_number_that_is_no_page_onto_itself(number):
+    k, v = _caches(8, 2, 16, 64, torch.bfloat16, "heads")
+    want = [t.clone() for t in (k, v)]
+    for w in want:
+        w[3] = w[1]
+    st = binding.new_status()
+    skl.streamkl_paged_copy(k, v, _dev([(number, number), (5, 5), (1, 3)]), dev_status=st)
+    assert int(st.item()) == binding.STREAMKL_ERR_INVALID_ARG and _same(k, want[0]) and _same(v, want[1])
+    st.zero_()
+    skl.streamkl_paged_copy(k, v, _dev([(5, 5), (1, 3)]), dev_status=st)
+    assert int(st.item()) == 0
+
+
 COMPACT = [
     # lens, drafted, kept lists (None: random), HK, page, d, type, layout, most
     ([1], [1], [[0]], 1, 16, 64, "bf16", "heads", 1),
