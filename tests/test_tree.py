@@ -353,6 +353,70 @@ def test_long_and_many_sequences(B, n, L, HQ, HK, d, page, dtype):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])  # the same in every run
 
 
+def _plain_parts(q, k, v, scale, seen, G):
+    """fp64 on the device, one sequence: o, lse, sum_j p_j |v_j|, and scale sum |q k| at most."""
+    ks, vs = k.double().repeat_interleave(G, 0), v.double().repeat_interleave(G, 0)
+    x = torch.einsum("ihd,hjd->ihj", q.double(), ks) * scale
+    most = float(torch.einsum("ihd,hjd->ihj", q.double().abs(), ks.abs()).max()) * scale
+    x = x.masked_fill(~seen[:, None], float("-inf"))
+    lse = torch.logsumexp(x, -1)
+    p = (x - lse[..., None]).exp()
+    return torch.einsum("ihj,hjd->ihd", p, vs), lse, torch.einsum("ihj,hjd->ihd", p, vs.abs()), most
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,n,L,HQ,HK,d,page,dtype", [
+    (32, 8, 9000, 16, 4, 128, 16, "bf16"), (20, 16, 12000, 16, 4, 128, 32, "fp16"), (9, 61, 7000, 16, 8, 64, 16, "fp16"),
+    (3, 200, 15000, 8, 4, 128, 64, "bf16"), (1, 128, 40000, 1, 1, 128, 16, "bf16"), (2, 100, 30000, 8, 8, 64, 128, "bf16"),
+    (230, 40, 1500, 2, 2, 128, 16, "bf16"), (230, 150, 1500, 2, 2, 128, 32, "fp16"), (460, 40, 1500, 2, 2, 64, 16, "bf16"),
+    (230, 140, 1500, 2, 2, 64, 64, "bf16"), (6, 300, 9000, 4, 4, 64, 32, "fp16"), (2, 13, 50000, 8, 4, 64, 16, "bf16")])
+def test_every_row_has_a_key_of_its_own(B, n, L, HQ, HK, d, page, dtype):
+    """Long contexts and cut stretches, key by key: each row's query is one of the keys (of entries +-a, so that its own
+    score stands some ten nats above all others together), at a border of a tile or page, an end of the sequence, or among
+    the drafted tokens, hidden ones too. A key that is lost or leaks then is the whole row. Bounds per element as in
+    _check."""
+    dt = TYPES[dtype]
+    k, v, table, lens, new, q = _random(B, n, L, HQ, HK, d, page, dt, B + n)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    a = 1.5 if d == 128 else 2.0
+    k.copy_((torch.randint(0, 2, k.shape, generator=g, device="cuda") * 2 - 1) * a)
+    bits = _masks(new, "tree", seed=B)
+    rng = np.random.default_rng(B + L)
+    G, scale, ends = HQ // HK, d ** -0.5, np.cumsum([0] + new)
+    flat = [c.transpose(1, 2).reshape(-1, HK, d) for c in (k, v)]  # [page slots, heads, d]
+    rows = []  # of each sequence
+    for b, length in enumerate(lens.tolist()):
+        at = torch.arange(length, device="cuda")
+        rows.append(table[b].long()[at // page] * page + at % page)
+        m = new[b]
+        edges = [x for t in range(0, length + 1, min(128, page)) for x in (t - 1, t) if 0 <= x < length]
+        edges = edges + 8 * [x for x in (0, length - m - 1, length - m, length - 1) if x >= 0]
+        wanted = np.where(rng.random((m, HQ)) < 0.4, rng.integers(length - m, length, (m, HQ)), rng.choice(edges, (m, HQ)))
+        slots = rows[b][torch.from_numpy(wanted).cuda()]
+        q[ends[b]:ends[b + 1]] = flat[0][slots, torch.arange(HQ, device="cuda") // G]
+    st = binding.new_status()
+    o, lse = skl.streamkl_paged_tree_attn(q, k, v, table, lens, _words(bits, -(-n // 32)), cu_seqlens=_cu(new), max_seqlen_q=n,
+                                          max_kv_len=L, dev_status=st)
+    binding.raise_on_device_status(st)
+    half = torch.finfo(dt).eps / 2
+    own = total = 0
+    for b, length in enumerate(lens.tolist()):
+        r = slice(int(ends[b]), int(ends[b + 1]))
+        seen = torch.from_numpy(orc.seen_keys(bits[b], length)).cuda()
+        kk, vv = (c[rows[b]].transpose(0, 1) for c in flat)
+        ref, ref_lse, mag, S = _plain_parts(q[r], kk, vv, scale, seen, G)
+        E = 2 * ((d + 12) * 2.0 ** -23 * S + 2.0 ** -21) + length * 2.0 ** -23
+        tol = half * ref.abs() + (half + E) * mag
+        if dt == torch.float16:
+            tol = tol + length * 2.0 ** -25 * float(vv.abs().max()) + 2.0 ** -25
+        assert torch.all((o[r].double() - ref).abs() <= tol), b
+        assert torch.all((lse[r].double() - ref_lse).abs() <= E + 2.0 ** -22 * ref_lse.abs()), b
+        own += int((ref_lse > S - 1).sum())
+        total += ref_lse.numel()
+    # (of the inputs, by the fp64 sums: 0.6 of the rows are given a key at a border; short sequences hide many of those)
+    assert 0.3 * total < own < total
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,HQ", [(6, 4), (25, 4), (90, 4)])
 def test_one_bad_sequence_leaves_the_others_right(n, HQ):
