@@ -58,6 +58,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return TYPE == kTypeBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
+// The rows of a sequence without keys, by threads first, first + step, ..
+template <int D>
+__device__ __forceinline__ void empty_rows(const PagedAttnArgs& a, int tok0, int n, int first, int step) {
+  for (long long e = first; e < static_cast<long long>(n) * a.HQ * (D / 8); e += step) {
+    const int r = static_cast<int>(e / (D / 8)), i = static_cast<int>(e % (D / 8));
+    const int token = tok0 + r / a.HQ, head = r % a.HQ;
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh)[i] = make_uint4(0, 0, 0, 0);
+    if (i == 0) a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
+  }
+}
+
 // Rows of an item whose parts lie in the shared memory of a cluster's CTAs, joined by
 // their lse: O in fp32 [part_rows][D] from `part` on, a row's 16-byte pieces turned by
 // its number (^ row & 7), then the rows' lse in log2 units. Warp `at` of `warps` takes

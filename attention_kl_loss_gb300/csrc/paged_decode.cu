@@ -255,9 +255,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_relinquish();
   }
   // a sequence's numbers; its rows, where it has no key
+  bool empty = false;
   auto visit = [&](int b, const Seq& s, bool report, bool mine) {
     if (report && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
     if (s.n == 0 || s.tiles > 0 || !mine) return;
+    if constexpr (TREE) {  // (by the whole CTA, below)
+      empty = true;
+      return;
+    }
     for (int r = 0; r < s.n * a.HQ; ++r) {
       const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
       uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
@@ -298,7 +303,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         max(0LL, min(total - static_cast<long long>(blockIdx.x) * chunk, static_cast<long long>(chunk))));
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (TREE) {
+    if (__syncthreads_or(empty) && !*skip_flag) {
+      // this CTA's sequences, as they were met: its items', or every gridDim-th
+      const int heads = CLUSTER ? ranks * a.HK : a.whole ? a.HK : 1;
+      for (int i = static_cast<int>(blockIdx.x); i < a.B * heads; i += static_cast<int>(gridDim.x)) {
+        if (i % heads != 0) continue;
+        const Seq s = load_seq(a, i / heads);
+        if (s.tiles == 0) empty_rows<D>(a, s.tok0, s.n, static_cast<int>(threadIdx.x), kThreads);
+      }
+    }
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
   if (!a.whole) {

@@ -273,16 +273,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     tmem_relinquish();
   }
   // this CTA's stretch of the line of tiles, or whole items; sequences without a key on
-  // the way
+  // the way (those of a resize that found no pages, too)
+  bool empty = false;
   auto visit = [&](int b, const Seq& s) {
     if (blockIdx.x == 0 && !s.ok) atomicCAS(a.dev_status, 0, kStatusInvalidArg);
-    if (s.n == 0 || s.tiles > 0 || b % gridDim.x != blockIdx.x) return;
-    for (int r = 0; r < s.n * a.HQ; ++r) {
-      const int token = s.tok0 + r / a.HQ, head = r % a.HQ;
-      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + token * a.o_sn + head * a.o_sh);
-      for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-      a.lse[static_cast<long long>(token) * a.HQ + head] = -INFINITY;
-    }
+    empty = empty || (s.n > 0 && s.tiles == 0 && b % gridDim.x == blockIdx.x);
   };
   long long total = 0, chunk = 0;
   // With CLUSTER the CTAs of a cluster take the key tiles of one item in turn
@@ -305,7 +300,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::THREADS, TreeLayout<D, NT>:
     chunk = locate<L::THREADS>(a, kRows, scratch, start, &total, visit);
   }
   tc_fence_before();
-  __syncthreads();
+  // Empty rows by the whole CTA (4 sequences of 256 tokens, 32 heads, up to 16,384 keys,
+  // one of them empty: 122 us; by the thread that met it 880)
+  if (__syncthreads_or(empty) && !*skip_flag)
+    for (int b = static_cast<int>(blockIdx.x); b < a.B; b += static_cast<int>(gridDim.x)) {
+      const Seq s = load_seq(a, b, kRows);
+      if (s.tiles == 0) empty_rows<D>(a, s.tok0, s.n, static_cast<int>(threadIdx.x), L::THREADS);
+    }
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);  // (the same in every lane)
   ck.tmem = tmem;

@@ -219,6 +219,45 @@ def test_scores_that_rise_for_any_bound(d, n, dtype, rise, most):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,n,HQ,HK,d,most", [(B, n, HQ, HK, d, most) for n, HQ, HK, d in ((3, 8, 2, 128), (9, 6, 3, 64), (40, 4, 2, 128),
+                                                                                       (70, 8, 8, 64), (33, 16, 2, 128))
+                                              for B, most in ((2, 500), (2, 30000), (37, 130), (37, 4000), (330, 200), (330, 3000))])
+def test_sequences_without_keys(B, n, HQ, HK, d, most):
+    """Some sequences of length 0, among them the first and the last, however the work is dealt out: their rows are zeros
+    and -inf, the others' right, rows of none as they were."""
+    dt = torch.bfloat16
+    rng = np.random.default_rng(B + n)
+    lens = [0 if b in (0, B - 1) and B > 2 or rng.random() < 0.3 else int(rng.integers(1, min(most, 200))) for b in range(B)]
+    new = [n] + [int(x) for x in rng.integers(0, n + 1, B - 1)]
+    if B == 2:
+        lens[0] = 0
+    c = Cache(lens, HK, d, 16, dt, seed=n)
+    total = sum(new)
+    q = torch.randn(total + 3, HQ, d, generator=torch.Generator().manual_seed(B)).to(dt).cuda()
+    bits = _masks(new, "holes", seed=B)
+    o, lse = torch.full((total + 3, HQ, d), 3.0, dtype=dt, device="cuda"), torch.full((total + 3, HQ), 3.0, device="cuda")
+    st = binding.new_status()
+    skl.streamkl_paged_tree_attn(q, c.k, c.v, _wide(c.table, 16, most), c.lens, _words(bits, -(-n // 32), 3), cu_seqlens=_cu(new),
+                                 max_seqlen_q=n, max_kv_len=most, dev_status=st, out=(o, lse))
+    binding.raise_on_device_status(st)
+    assert torch.all(o[total:] == 3) and torch.all(lse[total:] == 3)
+    half, at, scale = torch.finfo(dt).eps / 2, 0, d ** -0.5
+    for b, (m, length) in enumerate(zip(new, lens)):  # (bounds as in _check)
+        r = slice(at, at + m)
+        at += m
+        if m == 0 or length == 0:
+            assert not o[r].any() and torch.all(lse[r].isneginf())
+            continue
+        seen = torch.from_numpy(orc.seen_keys(bits[b], length)).cuda()
+        ref, ref_lse, mag, S = _plain_parts(q[r], *(t.transpose(0, 1).cuda() for t in c.rows[b]), scale, seen, HQ // HK)
+        E = 2 * ((d + 12) * 2.0 ** -23 * S + 2.0 ** -21) + length * 2.0 ** -23
+        assert torch.all((o[r].double() - ref).abs() <= half * ref.abs() + (half + E) * mag), b
+        none = ref_lse.isneginf()
+        assert torch.equal(none, lse[r].isneginf()) and not o[r][none].any()
+        assert torch.all((lse[r].double() - ref_lse)[~none].abs() <= E + 2.0 ** -22 * ref_lse[~none].abs()), b
+
+
+@pytest.mark.gpu
 def test_single_tokens_without_offsets():
     """One drafted token a sequence: its bit says whether it sees itself."""
     lens = [1, 16, 17, 129, 400]
@@ -360,7 +399,7 @@ def _plain_parts(q, k, v, scale, seen, G):
     most = float(torch.einsum("ihd,hjd->ihj", q.double().abs(), ks.abs()).max()) * scale
     x = x.masked_fill(~seen[:, None], float("-inf"))
     lse = torch.logsumexp(x, -1)
-    p = (x - lse[..., None]).exp()
+    p = (x - lse.masked_fill(lse.isneginf(), 0)[..., None]).exp()  # (0 in a row that sees nothing)
     return torch.einsum("ihj,hjd->ihd", p, vs), lse, torch.einsum("ihj,hjd->ihd", p, vs.abs()), most
 
 
