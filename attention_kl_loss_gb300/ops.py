@@ -526,7 +526,9 @@ def streamkl_paged_tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mas
     guesses (append them first; their rotation goes by depth, not by place): each
     sees all keys before the drafted ones, and of these those that its row of
     tree_mask names: int32 [total, words], bit t % 32 of word t // 32 for its
-    sequence's drafted token t (itself and its ancestors, or any others).
+    sequence's drafted token t (itself and its ancestors, or any others). A hidden
+    token's key may hold anything; a value that is not finite reaches all rows of its
+    key tile, those that do not see it too.
     max_seqlen_q is at most 32 * words (and that, or every token, by default)."""
     if out is None and stream is None and (native := load().native) is not None:
         done = native.tree_attn(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens, max_seqlen_q, max_kv_len,

@@ -491,7 +491,11 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_attn_args* args, void* 
  * them (j < length - n) and those of them whose bit its mask has: bit t % 32 of
  * word t / 32 for the sequence's drafted token t, its own and its ancestors' in a
  * tree. Bits from n on say nothing. A row that sees no key gets zeros and -inf.
- * With fewer keys than drafted tokens the first of these have no key.
+ * With fewer keys than drafted tokens the first of these have no key. A hidden token's
+ * key may hold anything; a value of V that is not finite reaches every row whose key
+ * tile (128 keys from a multiple of 128 on) it lies in, those that it is hidden from
+ * too, as 0 x infinity in the product. The keys are cached as they are to be seen,
+ * rotated by their depth: streamkl_paged_append rotates by place.
  *   attn: the arguments of streamkl_paged_attn, struct_size and all; causal and
  *   num_splits must be 0. mask: device words [T, mask_words], rows mask_stride words apart, for
  *   the tokens in q's order; max_seqlen_q is at most 32 mask_words.
