@@ -209,6 +209,33 @@ def test_captured_steps_replay():
 
 
 @pytest.mark.gpu
+def test_captured_steps_of_large_tables_replay():
+    """Two kernels, the second launched beside the first's end, and a cluster of sixteen blocks, in a graph."""
+    B, width, page = 20, 40000, 16
+    t = Tables(B, width, 700000, page)
+    rng = np.random.default_rng(3)
+    t.resize(rng.integers(0, width * page // 2, B))
+    new, source = _dev(t.lens), _dev(np.arange(B))
+    step = torch.empty_like(new)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        copies = skl.streamkl_paged_resize(t.d_refs, t.d_table, t.d_lens, new, page, dev_status=t.status, step_lens=step)
+        skl.streamkl_paged_fork(t.d_refs, t.d_table, t.d_lens, source, dev_status=t.status)
+    for i in range(6):
+        to = rng.integers(0, width * page + 1, B) if i % 2 else np.clip(t.lens + rng.integers(-200000, 200000, B), 0, width * page)
+        beams = np.arange(B) if i % 3 == 0 else rng.integers(0, B, B)
+        new.copy_(_dev(to))
+        source.copy_(_dev(beams))
+        graph.replay()
+        want, fine = orc.resize(t.refs, t.table, t.lens, to, page)
+        assert np.array_equal(copies.cpu().numpy(), want) and int(t.status.item()) == (0 if fine else NO_PAGES)
+        assert np.array_equal(step.cpu().numpy(), np.where(t.lens == to, to, 0))
+        t.status.zero_()
+        orc.fork(t.refs, t.table, t.lens, beams.tolist())
+        t.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("way", ["native", "ctypes"])
 @pytest.mark.parametrize("B,width,pages", [(1, 4, 3), (6, 8, 20), (300, 9, 1025), (1100, 6, 3001), (30, 9000, 100001)])
 def test_step_lens_are_the_new_lengths_or_zero(B, width, pages, way, monkeypatch):

@@ -258,6 +258,25 @@ def test_sequences_without_keys(B, n, HQ, HK, d, most):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,HQ,d", [(3, 4, 128), (40, 4, 64), (200, 2, 128)])
+def test_no_keys_at_all(n, HQ, d):
+    """max_kv_len 0, and sequences without tokens only."""
+    c = Cache([0, 0, 0], 1, d, 16, torch.bfloat16)
+    new = [n, 0, 2]
+    q = torch.ones(sum(new), HQ, d, dtype=torch.bfloat16, device="cuda")
+    mask = _words(_masks(new, "causal"), -(-n // 32))
+    st = binding.new_status()
+    kw = dict(max_seqlen_q=n, dev_status=st)
+    for most in (0, 16):
+        o, lse = skl.streamkl_paged_tree_attn(q, c.k, c.v, c.table, c.lens, mask, cu_seqlens=_cu(new), max_kv_len=most, **kw)
+        assert not o.any() and torch.all(lse.isneginf())
+        o, lse = torch.full_like(q, 3.0), torch.full((sum(new), HQ), 3.0, device="cuda")
+        skl.streamkl_paged_tree_attn(q, c.k, c.v, c.table, c.lens, mask, cu_seqlens=_cu([0, 0, 0]), max_kv_len=most, out=(o, lse), **kw)
+        assert torch.all(o == 3) and torch.all(lse == 3)
+    binding.raise_on_device_status(st)
+
+
+@pytest.mark.gpu
 def test_single_tokens_without_offsets():
     """One drafted token a sequence: its bit says whether it sees itself."""
     lens = [1, 16, 17, 129, 400]
