@@ -308,7 +308,7 @@ AttnPlan tree_plan(int B, int HQ, int HK, int d, int max_q, int max_kv) {
   // have; whole items. From 200 shapes (1 to 16 sequences of up to 512 to 8,192 keys):
   // on average 0.7 % from the better way, 12 % at worst, 7 % under what it was without,
   // 1.4 times at best (8 ragged sequences of up to 1,024 keys, 240 rows of d = 128 31.6
-  // us -> 22.6)
+  // us -> 22.7)
   static constexpr double kTimes[2][2][9] = {
       {{6.1, 1.76, 6.1, 11.0, 12.1, 1.81, 0.97, 7.4, 1.08}, {6.2, 1.68, 7.0, 11.0, 11.65, 1.70, 1.0, 7.2, 1.33}},
       {{7.3, 1.44, 3.6, 11.2, 13.4, 1.74, 0.76, 6.2, 1.09}, {12.75, 1.47, 4.9, 12.9, 19.5, 1.62, 0.92, 8.3, 1.60}}};

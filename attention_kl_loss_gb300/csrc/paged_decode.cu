@@ -23,7 +23,7 @@
 // over 2,048 keys, 8 heads: 12.8 us both, 18.1 with four rows a warp and two tiles).
 // With CLUSTER (of these) up to 16 CTAs take an item's tiles in turn and join their
 // parts through shared memory: no search, no parts in HBM, no second kernel, the first
-// page numbers loaded beside the length. 10.7 us for the same; 4 sequences of 4,096 keys
+// page numbers loaded beside the length. 10.4 us for the same; 4 sequences of 4,096 keys
 // 19.9 for 25.8. Clusters of 16 with two CTAs on an SM wait for places (19.8 us where
 // those of 8 take 11.6).
 // CTA: warp 0 softmax and output (thread = row, TMEM lanes 0..31), warp 1 loads

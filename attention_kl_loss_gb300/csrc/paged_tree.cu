@@ -28,11 +28,13 @@
 //
 // What bounds it (one GB300, both kernels; a turn is one key tile of a CTA):
 //   d = 128, one row tile: HBM. 64 sequences of up to 16,384 keys, 16 drafted tokens,
-//     32 heads over 8: 451 us, 6.6 TB/s; 1.48 us a turn, some 20 us start, end and join.
+//     32 heads over 8: 456 us, 6.5 TB/s; 1.48 us a turn, some 20 us start, end and join.
 //   d = 128, two: the chain S, P, O of a row tile, 1.8 us a turn for 1.3 of products.
 //     4 sequences of up to 16,384 keys with 256 drafted tokens 131 us, 1.1 PFLOP/s.
 //   d = 64: the softmax, 0.80 us a turn of one row tile (two CTAs an SM), 1.35 of two.
-//     24 sequences of up to 5,000 keys, up to 61 tokens, 8 heads 48 us, 3.2 TB/s.
+//     24 sequences of up to 5,000 keys, up to 61 tokens, 8 heads 48 us, 3.2 TB/s. With
+//     two it is farthest from its bytes: 56 sequences of up to 1,023 keys, up to 339
+//     tokens, 10 heads 96 us for 18 at a plain copy's rate.
 // No faster, each measured: softmax by two halves of the columns at d = 64 with two
 // row tiles (125 us for 104), barriers per row tile there (no change), two CTAs of one
 // row tile for more than 128 rows of d = 64 in large calls (200 for 189; small ones do

@@ -19,7 +19,7 @@ namespace {
 // Page `dst` of both caches becomes page `src`, for each pair. A block moves
 // kCopyVectors vectors of one pair and cache: every lane has its 8 loads in flight
 // before the first store. Bound by HBM: 1,000 pages of 256 KB in each cache 152 us,
-// 6.9 TB/s; 16 of 32 KB 3.0 us, which is the launch.
+// 6.9 TB/s; 16 of 32 KB 2.9 us, which is the launch.
 constexpr int kCopyThreads = 256, kCopyRun = 8, kCopyVectors = kCopyThreads * kCopyRun;
 
 __global__ void __launch_bounds__(kCopyThreads) streamkl_page_copy_kernel(const __grid_constant__ PageCopyArgs a) {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kCopyThreads) streamkl_page_copy_kernel(const 
 // kept rows rise too, so row i is at most kept[i]: what a batch of rows writes lies
 // before all that later batches read, and within a batch every load comes before
 // the first store. Columns do not meet, so an item is one (sequence, cache, head). 64
-// sequences' up to 6 rows x 8 heads of 256 bytes: 3.1 us, the launch and the chain of
+// sequences' up to 6 rows x 8 heads of 256 bytes: 3.3 us, the launch and the chain of
 // offsets, list, page and row.
 constexpr int kCompactRun = 8;
 
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ?
 // every row: all of it is read before any is written, and other slabs do not meet
 // it. A page of the row b is afterwards held by as many rows more as there are
 // sequences that go on from b, less the row b itself: one atomic an entry, which is
-// what bounds a large call (512 sequences of up to 4,096 pages, 10.9 us for about a
-// million of them; 64 of 256 pages 2.8 us, the launch).
+// what bounds a large call (512 sequences of up to 4,096 pages, 11.0 us for about a
+// million of them; 64 of 256 pages 3.1 us, the launch).
 constexpr int kForkThreads = 256, kForkRun = 8;  // entries whose loads are in flight
 
 __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const __grid_constant__ ForkArgs a) {
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kForkThreads) streamkl_paged_fork_kernel(const
 // the sequences (every block makes them for itself) and over the free pages (the
 // blocks share them, one bit each, and exchange their counts). Between them lies what
 // has to be in that order: pages given back, the counts of last pages, free pages.
-// A step of 64 sequences takes 6.2 us, a chain of loads and barriers; 667,000 pages
+// A step of 64 sequences takes 6.6 us, a chain of loads and barriers; 667,000 pages
 // given back and 608,000 given out of two million 38 us: 9 give back, 7 look for free
 // pages and some 20 write them down, at what sixteen SMs store (a page's count and its
 // entry, in other lines for every warp).
